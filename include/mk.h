@@ -415,6 +415,113 @@ int mk_service_batch(mk_service* s, int64_t* ids, int32_t* seq_lens, int32_t* to
 /* Stop the loop (after the step in flight) and free the service. */
 void mk_service_destroy(mk_service* s);
 
+/* ---------------------------------------------------------------------
+ * 4-bit key/value cache: the paged pool of one layer held in 4 bits (4.5
+ * with its scales) instead of BF16's 16, its writer, its reader and the
+ * attention that reads it.
+ *
+ * A page of 16 tokens is [n_kv_heads] records of 18 * head_dim bytes (all KV
+ * heads of a page contiguous, as in the BF16 pools).  Dims are quantised in
+ * groups of 64 (NG = head_dim / 64 per token, KV head, key or value): a value
+ * reads back as step * code + low, code 0..15, step and low BF16:
+ *   low   the largest BF16 number not above the group's minimum
+ *   step  the smallest BF16 number with 15 step >= max - low, at least 2^-126;
+ *         0 if the group is constant
+ *   code  (x - low) / step to the nearest integer, ties to even, with x - low
+ *         rounded to fp32
+ * so a value is off by at most half a step (max - min) / 30, about.  A group
+ * with a NaN, an infinity or max - low past fp32 reads back as NaN.
+ * Record (byte offsets; d = head_dim; t = token, g = group):
+ *   0     key codes    dim 64 g + 16 c + n: nibble n of the 8 bytes at
+ *                      t d / 2 + 8 NG c + 8 g         (c 0..3, n 0..15)
+ *   8 d   value codes  dim 64 g + 8 c + 4 u + k: nibble k of the 2 bytes at
+ *                      8 d + (t / 2) d + 8 NG c + 8 g + 4 u + 2 (t % 2)
+ *                                                     (c 0..7, u 0..1, k 0..3)
+ *   16 d  key scales   step, then low at 16 d + 4 (t NG + g)
+ *   17 d  value scales step, then low at 17 d + 4 (t NG + g)
+ *
+ * These calls keep no state: everything they use is an argument, they run on
+ * `stream` (a cudaStream_t of the current device; NULL = default), return
+ * before the kernels have run, allocate nothing and may be captured into a
+ * graph.  Two calls may run at the same time unless one writes what the other
+ * uses (cache rows, outputs, workspace).  All pointers but the structs
+ * themselves are DEVICE pointers; pool, rows, q, out and workspace are 16-byte
+ * aligned, strides multiples of 16 bytes (else MK_ERR_BAD_ARG).
+ */
+enum mk_type { MK_TYPE_BF16 = 0, MK_TYPE_F32 = 1 };
+
+typedef struct {
+  void* pool;       /* [num_pages][mk_kvq_page_bytes]                            */
+  int num_pages;    /* 1 .. 2^27 - 1                                             */
+  int n_kv_heads;   /* 1 .. 1024                                                 */
+  int head_dim;     /* 64 or 128                                                 */
+  int32_t* status;  /* one int32, or NULL: a kernel that meets a bad index stores
+                       MK_ERR_BAD_PAGE there, a bad length MK_ERR_BAD_ARG; never
+                       cleared by a call                                         */
+} mk_kvq_cache;
+
+/* Keys and values outside the cache.  Element (token t of page p, KV head h,
+ * dim i) is at p * page_stride + t * row_stride + h * head_stride + i of k and
+ * of v (strides in elements).  With unit 1 a row index r is r * row_stride and
+ * page_stride is not used.  A BF16 pool [pages][hkv][16][d] has page_stride
+ * hkv 16 d, row_stride d, head_stride 16 d. */
+typedef struct {
+  void* k;
+  void* v;
+  int type;             /* enum mk_type                                          */
+  int count;            /* rows (unit 1) or pages (unit 16) there are            */
+  int64_t page_stride, row_stride, head_stride;
+} mk_kv_rows;
+
+/* Bytes of one page, all KV heads (18 * n_kv_heads * head_dim); 0 if the
+ * shape is not supported. */
+size_t mk_kvq_page_bytes(int n_kv_heads, int head_dim);
+
+/* Quantise n units into the cache: unit = 1 (tokens; a cache index is a slot
+ * page * 16 + row) or 16 (whole pages; a cache index is a page).  Unit i of
+ * the call is row (page) src_index[i] of src and goes to dst_index[i]; a NULL
+ * index is i.  Units with a negative index on either side are skipped (idle
+ * rows of a padded batch); one past the end is skipped and flagged in
+ * status.  The other rows of a page are left as they were.  No two units may
+ * name the same destination: the codes and scales left there would be a mix
+ * of both.  Errors: MK_ERR_BAD_CONFIG (cache shape), MK_ERR_BAD_ARG,
+ * MK_ERR_BAD_PAGE (NULL dst_index and n past the cache), MK_ERR_CUDA. */
+int mk_kvq_write(const mk_kvq_cache* c, const mk_kv_rows* src, const int32_t* src_index, const int32_t* dst_index,
+                 int n, int unit, void* stream);
+
+/* Read n units back: unit src_index[i] of the cache to row (page)
+ * dst_index[i] of dst, as step * code + low in fp32, rounded once to dst's
+ * type.  A negative src_index[i] gives zeros, a negative dst_index[i] is
+ * skipped, an index past the end is skipped and flagged in status.  No two
+ * units may name the same destination.  Errors as mk_kvq_write. */
+int mk_kvq_read(const mk_kvq_cache* c, const int32_t* src_index, const mk_kv_rows* dst, const int32_t* dst_index,
+                int n, int unit, void* stream);
+
+/* Workspace bytes of mk_kvq_attention for any lengths; 0 if the arguments are
+ * not supported. */
+size_t mk_kvq_workspace(const mk_kvq_cache* c, int n_q_heads, int batch);
+
+/* Attention of one query token per sequence over its cached tokens:
+ *   out[b][h] = sum_t softmax_t(scale q[b][h] . k_t) v_t,  t < seq_lens[b],
+ * with query head h reading KV head h / (n_q_heads / n_kv_heads).
+ *   q, out       [batch][n_q_heads][head_dim] of `type`, q_stride and
+ *                out_stride elements between sequences
+ *   page_tables  [batch][max_pages] physical pages; entries past a sequence's
+ *                length are not read
+ *   seq_lens     [batch] tokens attended to: 0 (the row is zeros: an idle slot
+ *                of a padded batch) .. 16 max_pages
+ * A sequence with a page outside the cache or a length outside its range gets
+ * a row of NaN and flags status.  fp32: scores and weights keep 22 bits;
+ * BF16: weights are rounded to 11 bits, sums stay in fp32, one rounding at
+ * the end.  Results do not depend on the other sequences' values and are the same from call
+ * to call.  Errors: MK_ERR_BAD_CONFIG (cache shape, n_q_heads no multiple of
+ * n_kv_heads or above 65536), MK_ERR_BATCH_TOO_LARGE (batch outside
+ * 0..65535), MK_ERR_BAD_ARG (also a workspace smaller than
+ * mk_kvq_workspace), MK_ERR_CUDA. */
+int mk_kvq_attention(const mk_kvq_cache* c, const void* q, int64_t q_stride, void* out, int64_t out_stride, int type,
+                     int n_q_heads, int batch, const int32_t* page_tables, int max_pages, const int32_t* seq_lens,
+                     float scale, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Library-owned device bytes (counters, scratch, queues, task lists). */
 size_t mk_device_bytes(const mk_handle* h);
 /* SMs the persistent grid uses. */

@@ -1,0 +1,424 @@
+// The 4-bit key/value cache: record layout, quantiser and the attention of one
+// page, shared by the cache operators (mk_kvq.cu) and whatever else reads a
+// page of it.
+//
+// A page of 16 tokens holds one record of 18 D bytes per KV head (D = 64 or
+// 128, NG = D / 64 groups of 64 dims): key codes (8 D bytes), value codes
+// (8 D), key scales (D), value scales (D).  A group is step * code + low.
+//
+// The orders inside a record are the tensor cores' own, so that a lane reads
+// its fragments with one wide load and no shuffle:
+//   keys    token t, column c (0..3): 8 NG bytes = dims 64 g + 16 c .. + 15 of
+//           every group g, dim n at nibble n.  Lane (row, c) of the A operand
+//           K[token][dim] takes one column; a 32-bit word masked to its nibbles
+//           0 and 4 (1 and 5, ...) is a pair of adjacent k elements.
+//   values  token pair t / 2, column c (0..7): 8 NG bytes = dims 64 g + 8 c ..
+//           + 7 of both tokens; 16-bit unit t % 2 of word u holds dims
+//           4 u .. 4 u + 3 of token t.  Masking a word gives one dim of two
+//           consecutive tokens: a k pair of the A operand V^T[dim][token].
+//   scales  token t, group g: (step, low) as two BF16 numbers in one word.
+// A nibble masked in place is an FP16 subnormal, code * 2^-24 (or, four bits
+// up, 16 code * 2^-24), which the FP16 tensor-core product takes exactly; the
+// power of two is undone in the fp32 result.  So a code needs half an
+// instruction to become an operand (values one more, to be centred) and is
+// never rounded.
+#pragma once
+#include <stdint.h>
+#include <float.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "mk_ptx.cuh"
+
+namespace mk {
+
+constexpr int kKvqPage = 16;    // tokens of a page
+constexpr int kKvqGroup = 64;   // dims that share a scale
+
+template <int D>
+struct KvqRec {
+  static constexpr int NG = D / kKvqGroup;
+  static constexpr int kBytes = 18 * D;
+  static constexpr int kVal = 8 * D, kKeyScale = 16 * D, kValScale = 17 * D;
+  static __device__ __forceinline__ int key_word(int t, int wi, int g) {   // dims 64 g + 8 wi .. + 7
+    return t * (D / 2) + (wi >> 1) * (8 * NG) + g * 8 + (wi & 1) * 4;
+  }
+  static __device__ __forceinline__ int val_half(int t, int wi, int g, int u) {   // dims 64 g + 8 wi + 4 u .. + 3
+    return kVal + (t >> 1) * D + wi * (8 * NG) + g * 8 + u * 4 + (t & 1) * 2;
+  }
+};
+
+// ---------------------------------------------------------------- quantiser
+
+__device__ __forceinline__ float fmin_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float fmax_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+struct KvqScale {
+  float low, step, inv;   // inv = 1 / step rounded, 0 with step 0
+  __device__ __forceinline__ uint32_t word() const {
+    return (__float_as_uint(step) >> 16) | (__float_as_uint(low) & 0xffff0000u);
+  }
+};
+
+// (step, low) of a group with minimum lo and maximum hi (NaN where the group
+// holds one): low = the largest BF16 number <= lo, step = the smallest BF16
+// number >= (hi - low) / 15, at least 2^-126, or 0 for a constant group.  15
+// times a BF16 number is exact in fp32, so one comparison settles the
+// rounding up.  A span that is not finite makes the whole group NaN.
+__device__ __forceinline__ KvqScale kvq_scale(float lo, float hi) {
+  KvqScale s;
+  uint32_t cut = __float_as_uint(lo) & 0xffff0000u;
+  if (cut != __float_as_uint(lo) && lo < 0.f) cut += 0x10000u;
+  s.low = __uint_as_float(cut) + 0.f;      // -0 becomes +0
+  const float span = hi - s.low;
+  cut = __float_as_uint(__fdiv_rn(span, 15.f)) & 0xffff0000u;
+  if (__uint_as_float(cut) * 15.f < span) cut += 0x10000u;
+  s.step = span == 0.f ? 0.f : fmaxf(__uint_as_float(cut), 1.17549435e-38f);
+  s.inv = span == 0.f ? 0.f : __frcp_rn(s.step);
+  if (!(fabsf(span) <= FLT_MAX)) {
+    s.low = __uint_as_float(0x7fc00000u);
+    s.step = s.inv = 0.f;
+  }
+  return s;
+}
+
+// code of x: (x - low) / step to the nearest integer, ties to even, the
+// difference rounded to fp32.  diff * inv is within 4e-6 of the quotient, so
+// away from the half-way points its rounding is the right one; next to one
+// the sign of diff - (k + 1/2) step decides, which one FMA gives exactly
+// ((k + 1/2) step has at most 13 bits).
+__device__ __forceinline__ uint32_t kvq_code(float x, const KvqScale& s) {
+  const float diff = x - s.low;
+  const float q = diff * s.inv;
+  float c = rintf(q);
+  if (fabsf(fabsf(q - c) - 0.5f) < 1e-4f) {
+    const float k = floorf(q);
+    const float r = fmaf(-(k + 0.5f), s.step, diff);
+    c = r > 0.f || (r == 0.f && ((int)k & 1)) ? k + 1.f : k;
+  }
+  return s.inv == 0.f ? 0u : (uint32_t)fminf(c, 15.f);
+}
+
+// ---------------------------------------------------------------- attention
+
+// D += A B, m16n8k16, FP16 in, fp32 out
+__device__ __forceinline__ void mma_f16(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// a + b, two FP16 numbers each, subnormals kept
+__device__ __forceinline__ uint32_t add_h2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("add.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float r;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// One warp's share of the attention of up to 8 query heads to one KV head,
+// page by page.
+//   x_t  = scale sum_i q_i k_ti = f sum_g step_tg (sum_{i in g} q'_i code_ti)
+//          + sum_g low_tg sq_g,   sq_g = scale sum_{i in g} q_i
+//   out  = sum_t p_t v_t / sum_t p_t,  p_t = 2^x_t (x in units of log2)
+//   sum_t p_t v_ti = sum_t (p_t step_tg) (code_ti - 8) + sum_t p_t mid_tg,
+//          mid_tg = low_tg + 8 step_tg: the two parts have the size of the
+//          values.  (With codes 0 .. 15 and low they are the size of the
+//          group's range and cancel in a mean over many tokens: 8 % off at
+//          256K tokens, measured.)
+// S^T = K Q^T takes the page's 16 tokens as M and the heads as N, O^T = V^T
+// P'^T the dims as M, 16 dims a tile, so no row of M is padding.  The weight
+// of a value code is P'_tg = p_t step_tg = 2^(x_t + log2 step_tg), kept per
+// group against its own running reference n_g: whatever the sizes of the
+// steps, the largest weight seen stays between 2^8 and 2^15, so that FP16
+// holds 11 bits of every weight down to 2^-22 of it.  A reference moves only
+// when a weight passes 2^15 (one vote a page); the sums l and sum p mid keep
+// theirs, r.
+// QT = 2 / PT = 2 split q and P' into FP16 high and low halves (22 bits) for
+// fp32 activations; with one half each P' is rounded to 11 bits, an eighth of
+// a BF16 result's own rounding, and BF16 q is exact.
+template <int D, int QT, int PT>
+struct KvqAttn {
+  using R = KvqRec<D>;
+  static constexpr int NG = R::NG;
+  static constexpr int NW = 2 * NG;        // code words of a lane per token / token pair
+  static constexpr int NT = 2 * NW;        // k-steps of S = 16-dim tiles of O
+
+  struct Page {
+    uint32_t k[2][NW];                     // keys of tokens gl, gl + 8
+    uint32_t v[2][NW];                     // values of token pairs cq, cq + 4
+    uint32_t ks[2][NG], vs[2][NG];         // scales of tokens gl, gl + 8
+  };
+
+  uint32_t q[QT][NT][2];
+  float f[2], sq[NG][2];                   // heads 2 cq, 2 cq + 1
+  float r[2], l[2], n[NG][2], om[NG][2];
+  float o[NT][4];
+
+  static constexpr float kHead = 8.f, kTop = 15.f;   // log2 of the weights' headroom and limit
+
+  template <int N>
+  static __device__ __forceinline__ void load_words(uint32_t* dst, const uint8_t* p) {
+    if constexpr (N == 4) {
+      const uint4 t = *(const uint4*)p;
+      dst[0] = t.x, dst[1] = t.y, dst[2] = t.z, dst[3] = t.w;
+    } else if constexpr (N == 2) {
+      const uint2 t = *(const uint2*)p;
+      dst[0] = t.x, dst[1] = t.y;
+    } else {
+      dst[0] = *(const uint32_t*)p;
+    }
+  }
+
+  static __device__ __forceinline__ void load(Page& pg, const uint8_t* rec, int lane) {
+    const int gl = lane >> 2, cq = lane & 3;
+#pragma unroll
+    for (int e = 0; e < 2; e++) {
+      load_words<NW>(pg.k[e], rec + (gl + 8 * e) * (D / 2) + cq * (8 * NG));
+      load_words<NW>(pg.v[e], rec + R::kVal + (cq + 4 * e) * D + gl * (8 * NG));
+      load_words<NG>(pg.ks[e], rec + R::kKeyScale + (gl + 8 * e) * (4 * NG));
+      load_words<NG>(pg.vs[e], rec + R::kValScale + (gl + 8 * e) * (4 * NG));
+    }
+  }
+
+  // x[g][16]: dims 64 g + 16 cq .. + 15 of query head gl (zeros where there is
+  // no such head); scale_log2 = softmax scale times log2 e
+  __device__ __forceinline__ void init(const float (*x)[16], float scale_log2, int lane) {
+    const int cq = lane & 3;
+    float top = 0.f, sum[NG];
+#pragma unroll
+    for (int g = 0; g < NG; g++) {
+      sum[g] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; i++) {
+        top = fmaxf(top, fabsf(x[g][i]));
+        sum[g] += x[g][i];
+      }
+    }
+#pragma unroll
+    for (int sh = 1; sh < 4; sh <<= 1) {
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, sh));
+#pragma unroll
+      for (int g = 0; g < NG; g++) sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], sh);
+    }
+    // a power of two takes the head's largest |q| to [2^13, 2^14): FP16 then
+    // holds every BF16 q exactly down to 2^-28 of it
+    const int e = top == 0.f ? 0 : min(126, 13 + 127 - (int)(__float_as_uint(top) >> 23));
+    const float up = __uint_as_float((uint32_t)(e + 127) << 23);
+    const float fh = scale_log2 * 16777216.f * __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+    for (int g = 0; g < NG; g++)
+#pragma unroll
+      for (int s = 0; s < 4; s++)          // word s / 2, nibbles 2 (s & 1) and + 1
+#pragma unroll
+        for (int hf = 0; hf < 2; hf++) {
+          const int i = (s >> 1) * 8 + (s & 1) * 2 + hf;
+          const float w = hf ? up * 0.0625f : up;   // the nibble four bits up counts 16 times
+          const float a = x[g][i] * w, b = x[g][i + 4] * w;
+          const uint32_t hi = pack_h2(a, b);
+          q[0][g * 4 + s][hf] = hi;
+          if constexpr (QT == 2) {
+            const float2 hv = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+            q[1][g * 4 + s][hf] = pack_h2(a - hv.x, b - hv.y);
+          }
+        }
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      const int src = (2 * cq + h) * 4;
+      f[h] = __shfl_sync(0xffffffffu, fh, src);
+#pragma unroll
+      for (int g = 0; g < NG; g++) {
+        sq[g][h] = __shfl_sync(0xffffffffu, sum[g] * scale_log2, src);
+        n[g][h] = -FLT_MAX;
+        om[g][h] = 0.f;
+      }
+      r[h] = -FLT_MAX;
+      l[h] = 0.f;
+    }
+#pragma unroll
+    for (int t = 0; t < NT; t++) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
+  }
+
+  // tokens [0, valid) of a page; valid is the same in every lane, 1..16
+  __device__ __forceinline__ void page(Page& pg, int valid, int lane) {
+    constexpr uint32_t M0 = 0x000f000fu, M1 = 0x00f000f0u;
+    constexpr uint32_t kMid0 = 0x80088008u, kMid1 = 0x80808080u;   // -8 2^-24, -128 2^-24
+    const int gl = lane >> 2;
+    float acc[NG][4];
+#pragma unroll
+    for (int g = 0; g < NG; g++) {
+      acc[g][0] = acc[g][1] = acc[g][2] = acc[g][3] = 0.f;
+#pragma unroll
+      for (int w = 0; w < 2; w++) {
+        const int j = 2 * g + w;
+        const uint32_t a = pg.k[0][j], b = pg.k[1][j], a8 = a >> 8, b8 = b >> 8;
+#pragma unroll
+        for (int t = 0; t < QT; t++) {
+          mma_f16(acc[g], a & M0, b & M0, a & M1, b & M1, q[t][2 * j][0], q[t][2 * j][1]);
+          mma_f16(acc[g], a8 & M0, b8 & M0, a8 & M1, b8 & M1, q[t][2 * j + 1][0], q[t][2 * j + 1][1]);
+        }
+      }
+    }
+    float x[2][2];                         // [token gl / gl + 8][head]
+#pragma unroll
+    for (int e = 0; e < 2; e++)
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        float dot = bf16lo(pg.ks[e][0]) * acc[0][2 * e + h], off = bf16hi(pg.ks[e][0]) * sq[0][h];
+#pragma unroll
+        for (int g = 1; g < NG; g++) {
+          dot = fmaf(bf16lo(pg.ks[e][g]), acc[g][2 * e + h], dot);
+          off = fmaf(bf16hi(pg.ks[e][g]), sq[g][h], off);
+        }
+        x[e][h] = fmaf(dot, f[h], off);
+      }
+    if (valid < kKvqPage) {
+      // rows past the sequence may hold anything, NaN scales included
+#pragma unroll
+      for (int e = 0; e < 2; e++)
+        if (gl + 8 * e >= valid) {
+          x[e][0] = x[e][1] = -INFINITY;
+#pragma unroll
+          for (int g = 0; g < NG; g++) pg.vs[e][g] = 0u;
+        }
+    }
+    float ls[2][NG], mid[2][NG];
+#pragma unroll
+    for (int e = 0; e < 2; e++)
+#pragma unroll
+      for (int g = 0; g < NG; g++) {
+        ls[e][g] = lg2(bf16lo(pg.vs[e][g]));
+        mid[e][g] = fmaf(8.f, bf16lo(pg.vs[e][g]), bf16hi(pg.vs[e][g]));
+      }
+    float top = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < 2; e++)
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        top = fmaxf(top, x[e][h] - r[h]);
+#pragma unroll
+        for (int g = 0; g < NG; g++) top = fmaxf(top, x[e][h] + ls[e][g] - n[g][h]);
+      }
+    if (__any_sync(0xffffffffu, top > kTop)) {
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        float m = fmaxf(x[0][h], x[1][h]), mg[NG];
+#pragma unroll
+        for (int g = 0; g < NG; g++) mg[g] = fmaxf(x[0][h] + ls[0][g], x[1][h] + ls[1][g]);
+#pragma unroll
+        for (int sh = 4; sh < 32; sh <<= 1) {
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, sh));
+#pragma unroll
+          for (int g = 0; g < NG; g++) mg[g] = fmaxf(mg[g], __shfl_xor_sync(0xffffffffu, mg[g], sh));
+        }
+        const float rn = fmaxf(r[h], m - kHead);
+        const float al = ex2(r[h] - rn);
+        r[h] = rn;
+        l[h] *= al;
+#pragma unroll
+        for (int g = 0; g < NG; g++) {
+          om[g][h] *= al;
+          const float nn = fmaxf(n[g][h], mg[g] - kHead);
+          const float be = ex2(n[g][h] - nn);
+          n[g][h] = nn;
+#pragma unroll
+          for (int t = 0; t < 4; t++) {
+            o[4 * g + t][h] *= be;
+            o[4 * g + t][2 + h] *= be;
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      const float p0 = ex2(x[0][h] - r[h]), p1 = ex2(x[1][h] - r[h]);
+      l[h] += p0 + p1;
+#pragma unroll
+      for (int g = 0; g < NG; g++) om[g][h] = fmaf(p1, mid[1][g], fmaf(p0, mid[0][g], om[g][h]));
+    }
+#pragma unroll
+    for (int g = 0; g < NG; g++) {
+      float w[2][2];
+#pragma unroll
+      for (int e = 0; e < 2; e++)
+#pragma unroll
+        for (int h = 0; h < 2; h++) w[e][h] = ex2(x[e][h] + ls[e][g] - n[g][h]);
+      // P'^T as the B operand: the score tiles [token][head] transposed
+      uint32_t b[PT][2];
+#pragma unroll
+      for (int e = 0; e < 2; e++) {
+        const uint32_t hi = pack_h2(w[e][0], w[e][1]);
+        b[0][e] = movm_trans(hi);
+        if constexpr (PT == 2) {
+          const float2 hv = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+          b[1][e] = movm_trans(pack_h2(w[e][0] - hv.x, w[e][1] - hv.y));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 2; u++) {
+        const int j = 2 * g + u;
+        const uint32_t a = pg.v[0][j], c = pg.v[1][j], a8 = a >> 8, c8 = c >> 8;
+        const uint32_t a0 = add_h2(a & M0, kMid0), a1 = add_h2(a & M1, kMid1);
+        const uint32_t a2 = add_h2(c & M0, kMid0), a3 = add_h2(c & M1, kMid1);
+        const uint32_t e0 = add_h2(a8 & M0, kMid0), e1 = add_h2(a8 & M1, kMid1);
+        const uint32_t e2 = add_h2(c8 & M0, kMid0), e3 = add_h2(c8 & M1, kMid1);
+#pragma unroll
+        for (int t = 0; t < PT; t++) {
+          mma_f16(o[2 * j], a0, a1, a2, a3, b[t][0], b[t][1]);
+          mma_f16(o[2 * j + 1], e0, e1, e2, e3, b[t][0], b[t][1]);
+        }
+      }
+    }
+  }
+
+  // the warp's sums against r: l over all its tokens, and v[g][h][8] = dims
+  // 64 g + 8 gl .. + 7 of head 2 cq + h
+  __device__ __forceinline__ void finish(float (*v)[2][8]) {
+#pragma unroll
+    for (int sh = 4; sh < 32; sh <<= 1)
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        l[h] += __shfl_xor_sync(0xffffffffu, l[h], sh);
+#pragma unroll
+        for (int g = 0; g < NG; g++) om[g][h] += __shfl_xor_sync(0xffffffffu, om[g][h], sh);
+      }
+#pragma unroll
+    for (int g = 0; g < NG; g++)
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        const float sc = ex2(n[g][h] - r[h]);
+#pragma unroll
+        for (int t = 0; t < 4; t++) {      // tile t: dims 2 t (as code 2^-24) and 2 t + 1 (16 times that)
+          v[g][h][2 * t] = fmaf(o[4 * g + t][h] * sc, 16777216.f, om[g][h]);
+          v[g][h][2 * t + 1] = fmaf(o[4 * g + t][2 + h] * sc, 1048576.f, om[g][h]);
+        }
+      }
+  }
+};
+
+}  // namespace mk

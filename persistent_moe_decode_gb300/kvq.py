@@ -1,0 +1,199 @@
+"""The 4-bit KV cache on torch tensors: checks, allocation and streams around
+the ``mk_kvq_*`` calls of include/mk.h (no arithmetic here).
+
+A :class:`QuantCache` is the paged pool of one layer, ``[pages][page bytes]``
+uint8, in the format include/mk.h documents: groups of 64 dims as
+``step * code + low``, 4.5 bits a value.  Rows are written as they are produced
+(``write``) or converted from a BF16 pool a page at a time (``write_pages``),
+read back (``read``, ``read_pages``) and attended to (``attention``).
+
+Every call runs on ``stream``, by default torch's current stream of the cache's
+device, and returns before the kernels have run; it can be captured into a CUDA
+graph.  Tensors last used on another stream are the caller's to order, as with
+any torch operation.  A call with tensors of another device, another type or a
+wrong shape raises; indexes and lengths are checked on the device (``check``).
+"""
+from __future__ import annotations
+
+import math
+
+import torch
+
+from . import mk
+
+PAGE_SIZE = 16
+_TYPES = {torch.bfloat16: mk.MK_TYPE_BF16, torch.float32: mk.MK_TYPE_F32}
+
+
+def page_bytes(n_kv_heads: int, head_dim: int) -> int:
+    """Bytes of one 16-token page of all KV heads; raises for a shape that is not supported."""
+    n = mk.mk_kvq_page_bytes(n_kv_heads, head_dim)
+    if n == 0:
+        raise ValueError(f"4-bit cache: {n_kv_heads} KV heads of {head_dim} dims are not supported "
+                         "(head_dim must be 64 or 128)")
+    return n
+
+
+class QuantCache:
+    """One layer's 4-bit paged KV cache (``pool``: uint8 ``[pages, page bytes]``, all zeros when new)."""
+
+    def __init__(self, n_pages: int, n_kv_heads: int, head_dim: int, device="cuda"):
+        self._attach(torch.zeros(n_pages, page_bytes(n_kv_heads, head_dim), dtype=torch.uint8, device=device),
+                     n_kv_heads, head_dim)
+
+    @classmethod
+    def from_pool(cls, pool: torch.Tensor, n_kv_heads: int, head_dim: int) -> "QuantCache":
+        """A cache over an existing pool (kept referenced, not copied)."""
+        self = cls.__new__(cls)
+        self._attach(pool, n_kv_heads, head_dim)
+        return self
+
+    def _attach(self, pool, n_kv_heads, head_dim):
+        if pool.dtype != torch.uint8 or pool.dim() != 2 or not pool.is_contiguous() \
+                or pool.shape[1] != page_bytes(n_kv_heads, head_dim) or pool.shape[0] < 1:
+            raise ValueError("4-bit cache: the pool is a contiguous uint8 [pages, "
+                             f"{page_bytes(n_kv_heads, head_dim)}] tensor, got {pool.dtype} {tuple(pool.shape)}")
+        if pool.device.type != "cuda":
+            raise ValueError(f"4-bit cache: the pool is on {pool.device}, not on a GPU")
+        self.pool, self.n_kv_heads, self.head_dim = pool, n_kv_heads, head_dim
+        self.status = torch.zeros(1, dtype=torch.int32, device=pool.device)
+        self._c = mk.mk_kvq_cache(pool=pool.data_ptr(), num_pages=pool.shape[0], n_kv_heads=n_kv_heads,
+                                  head_dim=head_dim, status=self.status.data_ptr())
+
+    @property
+    def n_pages(self) -> int:
+        return self.pool.shape[0]
+
+    def check(self) -> None:
+        """Raise MkError if a call so far met a page, slot or length out of range (synchronises);
+        clears the record."""
+        code = int(self.status.item())
+        if code:
+            self.status.zero_()
+            raise mk.MkError(code, "4-bit cache")
+
+    # ------------------------------------------------------------ arguments
+
+    def _index(self, t, name, n=None):
+        if t.dtype != torch.int32 or t.dim() != 1 or t.device != self.pool.device or (n is not None and t.numel() != n):
+            raise ValueError(f"{name}: an int32 vector{f' of {n}' if n is not None else ''} on {self.pool.device}, "
+                             f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+        return t.contiguous()
+
+    def _rows(self, k, v, shape, paged, out):
+        """mk_kv_rows of k and v, and the tensors it points into."""
+        for name, t in (("k", k), ("v", v)):
+            if t.dtype not in _TYPES or t.dtype != k.dtype:
+                raise ValueError(f"{name}: BF16 or fp32, k and v alike, got {t.dtype}")
+            if t.device != self.pool.device or t.shape[1:] != shape or t.shape[0] != k.shape[0]:
+                raise ValueError(f"{name}: [n, {', '.join(map(str, shape))}] on {self.pool.device}, "
+                                 f"got {tuple(t.shape)} on {t.device}")
+        q = 16 // k.element_size()
+        if k.stride() != v.stride() or k.stride(-1) != 1 or any(s % q for s in k.stride()[:-1]) \
+                or k.data_ptr() % 16 or v.data_ptr() % 16:
+            if out:
+                raise ValueError("k, v: rows of consecutive elements at 16-byte strides, k and v alike")
+            k, v = k.contiguous(), v.contiguous()
+            if k.data_ptr() % 16 or v.data_ptr() % 16:
+                k, v = k.clone(), v.clone()
+        s = k.stride()
+        r = mk.mk_kv_rows(k=k.data_ptr(), v=v.data_ptr(), type=_TYPES[k.dtype], count=k.shape[0],
+                          page_stride=s[0], row_stride=s[2] if paged else s[0], head_stride=s[1])
+        return r, (k, v)
+
+    def _on(self, stream):
+        return _On(self.pool.device, stream)
+
+    # ---------------------------------------------------------------- calls
+
+    def write(self, k, v, slots, stream=None) -> None:
+        """Quantise rows k, v ``[n, n_kv_heads, head_dim]`` (BF16 or fp32, any 16-byte strides) into slots
+        ``page * 16 + row`` (int32 ``[n]``, distinct; a negative one skips its row)."""
+        slots = self._index(slots, "slots", k.shape[0])
+        with self._on(stream) as st:
+            r, keep = self._rows(k, v, (self.n_kv_heads, self.head_dim), False, False)
+            mk.mk_kvq_write(self._c, r, None, slots.data_ptr(), k.shape[0], 1, st)
+
+    def read(self, slots, dtype=torch.bfloat16, stream=None):
+        """The keys and values ``[n, n_kv_heads, head_dim]`` at slots ``page * 16 + row``; zeros at a negative one."""
+        slots = self._index(slots, "slots")
+        if dtype not in _TYPES:
+            raise ValueError(f"dtype: BF16 or fp32, got {dtype}")
+        with self._on(stream) as st:
+            k, v = torch.empty(2, slots.numel(), self.n_kv_heads, self.head_dim, dtype=dtype, device=self.pool.device)
+            r, keep = self._rows(k, v, (self.n_kv_heads, self.head_dim), False, True)
+            mk.mk_kvq_read(self._c, slots.data_ptr(), r, None, slots.numel(), 1, st)
+        return k, v
+
+    def write_pages(self, k_pool, v_pool, src_pages, dst_pages, stream=None) -> None:
+        """Convert pages ``src_pages`` of BF16 (or fp32) pools ``[pages, n_kv_heads, 16, head_dim]`` into pages
+        ``dst_pages`` of the cache (int32 ``[n]``, destinations distinct; a negative index skips its page)."""
+        src, dst = self._index(src_pages, "src_pages"), self._index(dst_pages, "dst_pages", src_pages.numel())
+        with self._on(stream) as st:
+            r, keep = self._rows(k_pool, v_pool, (self.n_kv_heads, PAGE_SIZE, self.head_dim), True, False)
+            mk.mk_kvq_write(self._c, r, src.data_ptr(), dst.data_ptr(), src.numel(), PAGE_SIZE, st)
+
+    def read_pages(self, src_pages, k_pool, v_pool, dst_pages, stream=None) -> None:
+        """Read pages ``src_pages`` of the cache back into pages ``dst_pages`` of BF16 (or fp32) pools (int32
+        ``[n]``, destinations distinct; a negative source gives zeros, a negative destination skips its page)."""
+        src, dst = self._index(src_pages, "src_pages"), self._index(dst_pages, "dst_pages", src_pages.numel())
+        with self._on(stream) as st:
+            r, keep = self._rows(k_pool, v_pool, (self.n_kv_heads, PAGE_SIZE, self.head_dim), True, True)
+            mk.mk_kvq_read(self._c, src.data_ptr(), r, dst.data_ptr(), src.numel(), PAGE_SIZE, st)
+
+    def attention(self, q, page_tables, seq_lens, scale: float | None = None, out=None, stream=None):
+        """Attention of one query token per sequence, q ``[batch, n_q_heads, head_dim]`` (BF16 or fp32), over the
+        first ``seq_lens[b]`` cached tokens of ``page_tables[b]`` (int32 ``[batch]`` and ``[batch, max_pages]``).
+        ``scale`` defaults to head_dim ** -0.5.  A sequence of no tokens gives zeros.  Returns ``out``, a new tensor
+        like q unless given; it may be q itself only where q is not needed afterwards."""
+        dev = self.pool.device
+        if q.dim() != 3 or q.dtype not in _TYPES or q.device != dev or q.shape[2] != self.head_dim:
+            raise ValueError(f"q: BF16 or fp32 [batch, heads, {self.head_dim}] on {dev}, got {q.dtype} "
+                             f"{tuple(q.shape)} on {q.device}")
+        batch, hq = q.shape[:2]
+        if page_tables.dtype != torch.int32 or page_tables.dim() != 2 or page_tables.device != dev \
+                or page_tables.shape[0] != batch:
+            raise ValueError(f"page_tables: int32 [{batch}, max_pages] on {dev}, got {page_tables.dtype} "
+                             f"{tuple(page_tables.shape)} on {page_tables.device}")
+        seq_lens = self._index(seq_lens, "seq_lens", batch)
+        size = 16 // q.element_size()
+
+        def dense(t):
+            return t.stride(2) == 1 and t.stride(1) == self.head_dim and t.stride(0) % size == 0 \
+                and t.data_ptr() % 16 == 0
+
+        with self._on(stream) as st:
+            page_tables = page_tables.contiguous()
+            if not dense(q):
+                q = q.clone(memory_format=torch.contiguous_format)
+            if out is None:
+                out = torch.empty(batch, hq, self.head_dim, dtype=q.dtype, device=dev)
+            elif out.shape != q.shape or out.dtype != q.dtype or out.device != dev or not dense(out):
+                raise ValueError(f"out: {q.dtype} {tuple(q.shape)} on {dev}, rows of consecutive heads")
+            n = mk.mk_kvq_workspace(self._c, hq, batch)
+            ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+            mk.mk_kvq_attention(self._c, q.data_ptr(), q.stride(0), out.data_ptr(), out.stride(0), _TYPES[q.dtype],
+                                hq, batch, page_tables.data_ptr(), page_tables.shape[1], seq_lens.data_ptr(),
+                                1.0 / math.sqrt(self.head_dim) if scale is None else scale,
+                                ws.data_ptr() if n else None, n, st)
+        return out
+
+
+class _On:
+    """The cache's device and the call's stream current for the launches and
+    for torch's allocations, so that a call's temporaries belong to its stream."""
+
+    def __init__(self, device, stream):
+        self.device, self.stream = device, stream
+
+    def __enter__(self):
+        self.guard = torch.cuda.device(self.device)
+        self.guard.__enter__()
+        st = self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
+        self.inner = torch.cuda.stream(st)
+        self.inner.__enter__()
+        return st
+
+    def __exit__(self, *exc):
+        self.inner.__exit__(*exc)
+        self.guard.__exit__(*exc)

@@ -30,6 +30,7 @@ MK_ERR_DEVICE = -9
 
 MK_WAVES_DEFAULT, MK_WAVES_ATTN_FIRST, MK_WAVES_INTERLEAVED = 0, 1, 2
 MK_EXPERTS_BF16, MK_EXPERTS_FP8_E4M3 = 0, 1
+MK_TYPE_BF16, MK_TYPE_F32 = 0, 1
 (MK_SCRATCH_H, MK_SCRATCH_X, MK_SCRATCH_QKV, MK_SCRATCH_ATTN, MK_SCRATCH_ROUTER,
  MK_SCRATCH_OPROJ, MK_SCRATCH_MOE) = range(7)
 MK_DEBUG_ROUTE_GROUPS, MK_DEBUG_PAGE_GATHER, MK_DEBUG_NEW_SLOT = range(3)
@@ -40,7 +41,8 @@ EXPORTS = ("mk_create", "mk_schedule_step", "mk_decode_step", "mk_step_status", 
            "mk_step_upload_bytes", "mk_destroy", "mk_strerror", "mk_abi_version", "mk_read_trace",
            "mk_decode_step_static", "mk_plan_step", "mk_read_debug", "mk_service_create",
            "mk_service_submit", "mk_service_run", "mk_service_wait", "mk_service_result",
-           "mk_service_batch", "mk_service_destroy")
+           "mk_service_batch", "mk_service_destroy", "mk_kvq_page_bytes", "mk_kvq_write", "mk_kvq_read",
+           "mk_kvq_workspace", "mk_kvq_attention")
 
 
 class mk_config(C.Structure):
@@ -71,6 +73,16 @@ class mk_error(C.Structure):
 
     def as_dict(self):
         return {n: getattr(self, n) for n, _ in self._fields_}
+
+
+class mk_kvq_cache(C.Structure):
+    _fields_ = [("pool", C.c_void_p), ("num_pages", C.c_int), ("n_kv_heads", C.c_int),
+                ("head_dim", C.c_int), ("status", C.c_void_p)]
+
+
+class mk_kv_rows(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("type", C.c_int), ("count", C.c_int),
+                ("page_stride", C.c_int64), ("row_stride", C.c_int64), ("head_stride", C.c_int64)]
 
 
 class MkError(RuntimeError):
@@ -110,6 +122,15 @@ def lib():
             L.mk_service_batch.argtypes = [vp, vp, vp, vp, C.POINTER(i32)]
             L.mk_service_destroy.argtypes = [vp]
             L.mk_service_destroy.restype = None
+            kvc, kvr = C.POINTER(mk_kvq_cache), C.POINTER(mk_kv_rows)
+            L.mk_kvq_page_bytes.argtypes = [i32, i32]
+            L.mk_kvq_page_bytes.restype = C.c_size_t
+            L.mk_kvq_write.argtypes = [kvc, kvr, vp, vp, i32, i32, vp]
+            L.mk_kvq_read.argtypes = [kvc, vp, kvr, vp, i32, i32, vp]
+            L.mk_kvq_workspace.argtypes = [kvc, i32, i32]
+            L.mk_kvq_workspace.restype = C.c_size_t
+            L.mk_kvq_attention.argtypes = [kvc, vp, C.c_int64, vp, C.c_int64, i32, i32, i32, vp, i32, vp,
+                                           C.c_float, vp, C.c_size_t, vp]
             L.mk_device_bytes.argtypes = [vp]
             L.mk_device_bytes.restype = C.c_size_t
             L.mk_num_sms.argtypes = [vp]
@@ -310,6 +331,35 @@ def mk_service_batch(s, max_batch: int):
 def mk_service_destroy(s) -> None:
     if s:
         lib().mk_service_destroy(s)
+
+
+def mk_kvq_page_bytes(n_kv_heads: int, head_dim: int) -> int:
+    return int(lib().mk_kvq_page_bytes(int(n_kv_heads), int(head_dim)))
+
+
+def mk_kvq_write(cache: mk_kvq_cache, src: mk_kv_rows, src_index_ptr, dst_index_ptr, n: int, unit: int,
+                 stream=None) -> int:
+    return _check(lib().mk_kvq_write(C.byref(cache), C.byref(src), src_index_ptr, dst_index_ptr, int(n),
+                                     int(unit), _stream_ptr(stream)), "mk_kvq_write")
+
+
+def mk_kvq_read(cache: mk_kvq_cache, src_index_ptr, dst: mk_kv_rows, dst_index_ptr, n: int, unit: int,
+                stream=None) -> int:
+    return _check(lib().mk_kvq_read(C.byref(cache), src_index_ptr, C.byref(dst), dst_index_ptr, int(n),
+                                    int(unit), _stream_ptr(stream)), "mk_kvq_read")
+
+
+def mk_kvq_workspace(cache: mk_kvq_cache, n_q_heads: int, batch: int) -> int:
+    return int(lib().mk_kvq_workspace(C.byref(cache), int(n_q_heads), int(batch)))
+
+
+def mk_kvq_attention(cache: mk_kvq_cache, q_ptr: int, q_stride: int, out_ptr: int, out_stride: int, dtype: int,
+                     n_q_heads: int, batch: int, page_tables_ptr, max_pages: int, seq_lens_ptr, scale: float,
+                     workspace_ptr=None, workspace_bytes: int = 0, stream=None) -> int:
+    return _check(lib().mk_kvq_attention(C.byref(cache), q_ptr, int(q_stride), out_ptr, int(out_stride),
+                                         int(dtype), int(n_q_heads), int(batch), page_tables_ptr,
+                                         int(max_pages), seq_lens_ptr, float(scale), workspace_ptr,
+                                         int(workspace_bytes), _stream_ptr(stream)), "mk_kvq_attention")
 
 
 # ---------------------------------------------------------- convenience

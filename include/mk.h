@@ -497,8 +497,10 @@ int mk_kvq_write(const mk_kvq_cache* c, const mk_kv_rows* src, const int32_t* sr
 int mk_kvq_read(const mk_kvq_cache* c, const int32_t* src_index, const mk_kv_rows* dst, const int32_t* dst_index,
                 int n, int unit, void* stream);
 
-/* Workspace bytes of mk_kvq_attention for any lengths; 0 if the arguments are
- * not supported. */
+/* Workspace bytes of mk_kvq_attention on the current device, for any lengths
+ * and batch (about 2.6 MB); 0 if the arguments are not supported.  It needs no
+ * preparation.  Calls that may run at the same time, or two captured graphs
+ * that may, need a workspace each. */
 size_t mk_kvq_workspace(const mk_kvq_cache* c, int n_q_heads, int batch);
 
 /* Attention of one query token per sequence over its cached tokens:
@@ -512,12 +514,13 @@ size_t mk_kvq_workspace(const mk_kvq_cache* c, int n_q_heads, int batch);
  *                of a padded batch) .. 16 max_pages
  * A sequence with a page outside the cache or a length outside its range gets
  * a row of NaN and flags status.  fp32: scores and weights keep 22 bits;
- * BF16: weights are rounded to 11 bits, sums stay in fp32, one rounding at
- * the end.  Results do not depend on the other sequences' values and are the same from call
- * to call.  Errors: MK_ERR_BAD_CONFIG (cache shape, n_q_heads no multiple of
+ * BF16: weights are rounded to 11 bits; sums stay in fp32, one rounding at
+ * the end.  A call gives the same bits every time; where a long sequence is cut
+ * depends on the batch's lengths, and its sums then round differently.  out may
+ * be q.  Errors: MK_ERR_BAD_CONFIG (cache shape, n_q_heads no multiple of
  * n_kv_heads or above 65536), MK_ERR_BATCH_TOO_LARGE (batch outside
  * 0..65535), MK_ERR_BAD_ARG (also a workspace smaller than
- * mk_kvq_workspace), MK_ERR_CUDA. */
+ * mk_kvq_workspace; none is needed with max_pages <= 8), MK_ERR_CUDA. */
 int mk_kvq_attention(const mk_kvq_cache* c, const void* q, int64_t q_stride, void* out, int64_t out_stride, int type,
                      int n_q_heads, int batch, const int32_t* page_tables, int max_pages, const int32_t* seq_lens,
                      float scale, void* workspace, size_t workspace_bytes, void* stream);

@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "../../include/mk.h"
 #include "mk_kvq.cuh"
@@ -164,96 +165,396 @@ __global__ void __launch_bounds__(256) kvq_read_kernel(Cache c, const int32_t* s
   }
 }
 
+// ---------------------------------------------------------------- attention
+//
+// The pages of all tasks (sequence, KV head, 8 of its query heads) are cut
+// into segments by the blocks themselves from the lengths on the device, so
+// the host neither reads lengths nor launches for the longest one:
+//   few pages (less than kMinPages a block): segments of kMinPages pages, one
+//     page a warp, dealt to the blocks in turn;
+//   many: block i takes units T i / G .. T (i + 1) / G of the T pages of all
+//     tasks in order, so every block moves the same bytes whatever the mix of
+//     lengths.
+// A task that is one segment is written at once.  The segments of the others
+// leave (reference, sum, weighted sum) in workspace slots, at most two a block,
+// and a second kernel merges them in page order: no atomics, one result.
+
+constexpr int kAttnWarps = 8;
+constexpr int kAttnThreads = kAttnWarps * 32;
+// resident blocks: the fp32 kernel with 128 dims needs more than the 128
+// registers a thread that two blocks leave
+template <int D, class T>
+constexpr int kBlocksPerSm = D == 128 && sizeof(T) == 4 ? 1 : 2;
+constexpr int kMinPages = kAttnWarps;
+constexpr int kRing = 4;                   // pages of a warp in flight and in use
+
 struct AttnArgs {
   Cache c;
   const void* q;
   void* out;
   const int32_t* page_tables;
   const int32_t* seq_lens;
+  uint8_t* ws;                             // AttnWs
   long long q_stride, out_stride;          // elements between two sequences
-  int hq, grp, batch, max_pages;
+  int grp, tiles, batch, max_pages;        // tiles = ceil(grp / 8)
+  int split;                               // 0: every task is one segment
   float scale_log2;
 };
 
-constexpr int kAttnWarps = 8;
+// workspace: the slot count, a header per slot, then the slots
+struct AttnSlot {
+  int b, j;                                // sequence; KV head and head tile
+  int parts;                               // of the task, in its first slot; 0 in the others
+  int step;                                // 1: parts in consecutive slots; 2: in the even slots after the first
+};
+
+struct AttnWs {
+  int32_t* count;
+  AttnSlot* slots;
+  float* data;
+};
+
+__host__ __device__ inline size_t attn_slot_floats(int d) { return 8 * (size_t)d + 16; }
+
+__host__ __device__ inline size_t attn_ws_bytes(int blocks, int d) {
+  const size_t slots = 2 * (size_t)blocks;
+  return 16 + slots * sizeof(AttnSlot) + slots * attn_slot_floats(d) * 4;
+}
+
+__device__ __forceinline__ AttnWs attn_ws(uint8_t* p, int blocks) {
+  return {(int32_t*)p, (AttnSlot*)(p + 16), (float*)(p + 16 + 2 * (size_t)blocks * sizeof(AttnSlot))};
+}
 
 __device__ __forceinline__ void stf(uint16_t* p, float v) { *p = f2bf(v); }
 __device__ __forceinline__ void stf(float* p, float v) { *p = v; }
 
-// one block per (sequence, KV head, 8 of its query heads); its warps take the
-// sequence's pages in turn and merge at the end
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// pages of sequence b; -1 for a length out of range
+__device__ __forceinline__ int seq_pages(const AttnArgs& a, int b) {
+  const int len = a.seq_lens[b];
+  return len < 0 || len > a.max_pages * kKvqPage ? -1 : (len + kKvqPage - 1) / kKvqPage;
+}
+
+// Position in the list of sequences: the sums before sequence b of its pages
+// (or segments) and of its split segments
+struct Cursor {
+  int b;
+  long long units;
+  int split;
+};
+
+struct PlanSmem {
+  long long units[kAttnWarps];
+  int split[kAttnWarps];
+  Cursor found;
+};
+
+// The sequence, from `c` on, whose pages (seg: segments) hold number `target`;
+// batch if there is none.  All threads call it and get the same answer.
+__device__ Cursor find_sequence(const AttnArgs& a, PlanSmem& S, Cursor c, long long target, bool seg) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  while (c.b < a.batch) {
+    const int b = c.b + tid;
+    const int np = b < a.batch ? max(seq_pages(a, b), 0) : 0;
+    const int n = seg ? (np + kMinPages - 1) / kMinPages : np;
+    const int m = seg && n > 1 ? n : 0;
+    long long u = n;
+    int sp = m;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, u, o);
+      const int y = __shfl_up_sync(0xffffffffu, sp, o);
+      if (lane >= o) u += x, sp += y;
+    }
+    if (lane == 31) S.units[warp] = u, S.split[warp] = sp;
+    __syncthreads();
+    long long ub = c.units, ut = c.units;
+    int sb = c.split, st = c.split;
+    for (int w = 0; w < kAttnWarps; w++) {
+      if (w == warp) ub = ut, sb = st;
+      ut += S.units[w];
+      st += S.split[w];
+    }
+    const long long before = ub + u - n;
+    if (n > 0 && before <= target && target < before + n) S.found = {b, before, sb + sp - m};
+    __syncthreads();
+    if (target < ut) {
+      c = S.found;
+      __syncthreads();                     // the next call writes S again
+      return c;
+    }
+    c = {c.b + kAttnThreads, ut, st};
+  }
+  c.b = a.batch;
+  return c;
+}
+
+// output row of head h of task (b, j)
 template <int D, class T>
-__global__ void __launch_bounds__(kAttnWarps * 32, 2) kvq_attention_kernel(AttnArgs a) {
-  constexpr int TERMS = sizeof(T) == 4 ? 2 : 1;
+__device__ __forceinline__ T* out_row(const AttnArgs& a, int b, int j, int h) {
+  const int g = j / a.tiles, h0 = j % a.tiles * 8;
+  return (T*)a.out + b * a.out_stride + (long long)(g * a.grp + h0 + h) * D;
+}
+
+template <int D, class T>
+struct AttnBlock {
+  static constexpr int TERMS = sizeof(T) == 4 ? 2 : 1;
   using R = KvqRec<D>;
   using A = KvqAttn<D, TERMS, TERMS>;
-  constexpr int NG = R::NG;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gl = lane >> 2, cq = lane & 3;
-  const int tiles = (a.grp + 7) / 8, b = blockIdx.y, g = blockIdx.x / tiles, h0 = blockIdx.x % tiles * 8;
-  const int heads = min(8, a.grp - h0);
-  __shared__ float sm_o[kAttnWarps][8][D];
-  __shared__ float sm_r[kAttnWarps][8], sm_l[kAttnWarps][8];
+  static constexpr int NG = R::NG;
+  static constexpr int kPad = D + 8;       // row of the merge buffer: rows of one store fall in distinct banks
+  static constexpr size_t kRingBytes = (size_t)kAttnWarps * kRing * R::kBytes;
+  static constexpr size_t kMergeBytes = (size_t)kAttnWarps * 8 * (kPad + 2) * 4;
+  static constexpr size_t kSmem = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;
 
-  A at;
-  {
-    float x[NG][16];
-    const T* q = (const T*)a.q + b * a.q_stride + (long long)(g * a.grp + h0 + min(gl, heads - 1)) * D + cq * 16;
+  // pages [p0, p1) of task (b, j): its output row, or slot `slot` of the workspace
+  static __device__ void segment(const AttnArgs& a, uint8_t* smem, int b, int j, int p0, int p1, float* slot) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gl = lane >> 2, cq = lane & 3;
+    const int g = j / a.tiles, h0 = j % a.tiles * 8, heads = min(8, a.grp - h0);
+    const int len = a.seq_lens[b];
+    uint8_t* ring = smem + (size_t)warp * kRing * R::kBytes;
+    const int32_t* table = a.page_tables + (long long)b * a.max_pages + p0 + warp;
+    const int n = (p1 - p0 - warp + kAttnWarps - 1) / kAttnWarps;   // this warp's pages (may be <= 0)
+    bool bad = false;
+    // page numbers: 32 of the warp's pages at a time, a lane each
+    int ids = lane < n ? table[lane * kAttnWarps] : 0;
+    auto fetch = [&](int i) {              // page i of the warp into its ring slot
+      if (i < n) {
+        if (i && (i & 31) == 0) ids = i + lane < n ? table[(long long)(i + lane) * kAttnWarps] : 0;
+        int id = __shfl_sync(0xffffffffu, ids, i & 31);
+        if (id < 0 || id >= a.c.pages) {
+          bad = true;
+          id = 0;
+        }
+        const uint8_t* src = a.c.pool + ((long long)id * a.c.hkv + g) * R::kBytes;
+        uint8_t* dst = ring + (i % kRing) * R::kBytes;
 #pragma unroll
-    for (int k = 0; k < NG; k++) {
-      load8(x[k], q + k * kKvqGroup);
-      load8(x[k] + 8, q + k * kKvqGroup + 8);
-      if (gl >= heads)
+        for (int k = 0; k < (R::kBytes + 511) / 512; k++)
+          if (k * 512 + lane * 16 < R::kBytes) cp_async16(dst + k * 512 + lane * 16, src + k * 512 + lane * 16);
+      }
+      cp_async_commit();
+    };
 #pragma unroll
-        for (int i = 0; i < 16; i++) x[k][i] = 0.f;
-    }
-    at.init(x, a.scale_log2, lane);
-  }
-  int len = a.seq_lens[b];
-  bool bad = false;
-  if (len < 0 || len > a.max_pages * kKvqPage) {
-    if (threadIdx.x == 0) flag_bad(a.c, MK_ERR_BAD_ARG);
-    bad = true;
-    len = 0;
-  }
-  const int np = (len + kKvqPage - 1) / kKvqPage;
-  for (int p = warp; p < np; p += kAttnWarps) {
-    int id = a.page_tables[(long long)b * a.max_pages + p];
-    if (id < 0 || id >= a.c.pages) {
-      if (lane == 0) flag_bad(a.c, MK_ERR_BAD_PAGE);
-      bad = true;
-      id = 0;
-    }
-    typename A::Page pg;
-    A::load(pg, a.c.pool + ((long long)id * a.c.hkv + g) * R::kBytes, lane);
-    at.page(pg, min(kKvqPage, len - p * kKvqPage), lane);
-  }
-  float v[NG][2][8];
-  at.finish(v);
+    for (int i = 0; i < kRing - 1; i++) fetch(i);
+
+    A at;
+    {
+      float x[NG][16];
+      const T* q = (const T*)a.q + b * a.q_stride + (long long)(g * a.grp + h0 + min(gl, heads - 1)) * D + cq * 16;
 #pragma unroll
-  for (int h = 0; h < 2; h++) {
+      for (int k = 0; k < NG; k++) {
+        load8(x[k], q + k * kKvqGroup);
+        load8(x[k] + 8, q + k * kKvqGroup + 8);
+        if (gl >= heads)
 #pragma unroll
-    for (int k = 0; k < NG; k++) {
-      float* dst = &sm_o[warp][2 * cq + h][k * kKvqGroup + 8 * gl];
-      *(float4*)dst = make_float4(v[k][h][0], v[k][h][1], v[k][h][2], v[k][h][3]);
-      *(float4*)(dst + 4) = make_float4(v[k][h][4], v[k][h][5], v[k][h][6], v[k][h][7]);
+          for (int i = 0; i < 16; i++) x[k][i] = 0.f;
+      }
+      at.init(x, a.scale_log2, lane);
     }
-    if (gl == 0) {
-      sm_r[warp][2 * cq + h] = at.r[h];
-      sm_l[warp][2 * cq + h] = bad ? NAN : at.l[h];
+    for (int i = 0; i < n; i++) {
+      cp_async_wait<kRing - 2>();
+      __syncwarp();
+      typename A::Page pg;
+      A::load(pg, ring + (i % kRing) * R::kBytes, lane);
+      // the slot fetched into now was read in the iteration before
+      fetch(i + kRing - 1);
+      at.page(pg, min(kKvqPage, len - (p0 + warp + i * kAttnWarps) * kKvqPage), lane);
     }
+    cp_async_wait<0>();
+    if (bad && lane == 0) flag_bad(a.c, MK_ERR_BAD_PAGE);
+
+    float v[NG][2][8];
+    at.finish(v);
+    __syncthreads();                       // every warp is through its ring
+    float* mo = (float*)smem;              // [warp][8][kPad], then references and sums [warp][8] each
+    float* mr = mo + (size_t)kAttnWarps * 8 * kPad;
+    float* ml = mr + kAttnWarps * 8;
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+#pragma unroll
+      for (int k = 0; k < NG; k++) {
+        float* dst = mo + (warp * 8 + 2 * cq + h) * kPad + k * kKvqGroup + 8 * gl;
+        *(float4*)dst = make_float4(v[k][h][0], v[k][h][1], v[k][h][2], v[k][h][3]);
+        *(float4*)(dst + 4) = make_float4(v[k][h][4], v[k][h][5], v[k][h][6], v[k][h][7]);
+      }
+      if (gl == 0) {
+        mr[warp * 8 + 2 * cq + h] = at.r[h];
+        ml[warp * 8 + 2 * cq + h] = bad ? NAN : at.l[h];
+      }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < heads * (D / 4); i += kAttnThreads) {
+      const int h = i / (D / 4), dim = i % (D / 4) * 4;
+      float m = -FLT_MAX, den = 0.f, num[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < kAttnWarps; w++) m = fmaxf(m, mr[w * 8 + h]);
+#pragma unroll
+      for (int w = 0; w < kAttnWarps; w++) {
+        const float k = ex2(mr[w * 8 + h] - m);
+        const float4 o = *(const float4*)(mo + (w * 8 + h) * kPad + dim);
+        num[0] = fmaf(k, o.x, num[0]);
+        num[1] = fmaf(k, o.y, num[1]);
+        num[2] = fmaf(k, o.z, num[2]);
+        num[3] = fmaf(k, o.w, num[3]);
+        den = fmaf(k, ml[w * 8 + h], den);
+      }
+      if (slot) {
+        *(float4*)(slot + h * D + dim) = make_float4(num[0], num[1], num[2], num[3]);
+        if (dim == 0) {
+          slot[8 * D + h] = m;
+          slot[8 * D + 8 + h] = den;
+        }
+      } else {
+        T* dst = out_row<D, T>(a, b, j, h) + dim;
+#pragma unroll
+        for (int k = 0; k < 4; k++) stf(dst + k, num[k] / den);
+      }
+    }
+    __syncthreads();                       // the ring may be filled again
   }
+};
+
+template <int D, class T>
+__global__ void __launch_bounds__(kAttnThreads, kBlocksPerSm<D, T>) kvq_attention_kernel(AttnArgs a) {
+  using B = AttnBlock<D, T>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ PlanSmem S;
+  const int tid = threadIdx.x, G = gridDim.x, me = blockIdx.x, HT = a.c.hkv * a.tiles;
+
+  // all pages; rows of sequences without one
+  long long total = 0;
+  for (int b = tid; b < a.batch; b += kAttnThreads) total += max(seq_pages(a, b), 0);
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  if ((tid & 31) == 0) S.units[tid >> 5] = total;
   __syncthreads();
-  for (int i = threadIdx.x; i < heads * D; i += kAttnWarps * 32) {
-    const int h = i / D, dim = i % D;
-    float m = -FLT_MAX, num = 0.f, den = 0.f;
-    for (int w = 0; w < kAttnWarps; w++) m = fmaxf(m, sm_r[w][h]);
-    for (int w = 0; w < kAttnWarps; w++) {
-      const float k = ex2(sm_r[w][h] - m);
-      num = fmaf(k, sm_o[w][h][dim], num);
-      den = fmaf(k, sm_l[w][h], den);
+  total = 0;
+  for (int w = 0; w < kAttnWarps; w++) total += S.units[w];
+  __syncthreads();
+  for (int b = me; b < a.batch; b += G) {
+    const int np = seq_pages(a, b);
+    if (np > 0) continue;
+    if (np < 0 && tid == 0) flag_bad(a.c, MK_ERR_BAD_ARG);
+    for (int i = tid; i < a.c.hkv * a.grp * D; i += kAttnThreads)
+      stf((T*)a.out + b * a.out_stride + i, np < 0 ? NAN : 0.f);
+  }
+
+  const unsigned long long T0 = (unsigned long long)total * HT;
+  const AttnWs ws = attn_ws(a.ws, G);
+  if (!a.split || T0 < (unsigned long long)G * kMinPages) {
+    Cursor cur{0, 0, 0};
+    for (long long s = me;; s += G) {
+      cur = find_sequence(a, S, cur, s / HT, true);
+      if (cur.b >= a.batch) break;
+      const int np = seq_pages(a, cur.b), nc = (np + kMinPages - 1) / kMinPages;
+      const long long rem = s - cur.units * HT;
+      const int j = (int)(rem / nc), k = (int)(rem % nc);
+      const int slot = cur.split * HT + (int)rem;
+      if (nc > 1 && tid == 0) ws.slots[slot] = {cur.b, j, k == 0 ? nc : 0, 1};
+      B::segment(a, smem, cur.b, j, k * kMinPages, min(np, (k + 1) * kMinPages),
+                 nc > 1 ? ws.data + slot * attn_slot_floats(D) : nullptr);
     }
-    // no key at all: zeros
-    stf((T*)a.out + b * a.out_stride + (long long)(g * a.grp + h0 + h) * D + dim, den == 0.f ? 0.f : num / den);
+    if (a.split && me == 0 && tid == 0) *ws.count = cur.split * HT;
+  } else {
+    if (me == 0 && tid == 0) *ws.count = 2 * G;
+    unsigned long long u = T0 * me / G;
+    const unsigned long long end = T0 * (me + 1) / G;
+    Cursor cur{0, 0, 0};
+    bool first = true;
+    if (tid < 2) ws.slots[2 * me + tid].parts = 0;
+    __syncthreads();
+    while (u < end) {
+      cur = find_sequence(a, S, cur, (long long)(u / HT), false);
+      const int np = seq_pages(a, cur.b);
+      const unsigned long long rem = u - (unsigned long long)cur.units * HT;
+      const int j = (int)(rem / np), p0 = (int)(rem % np);
+      const unsigned long long task = u - p0;              // first unit of the task
+      const int p1 = (int)min((unsigned long long)np, p0 + (end - u));
+      const bool part = p0 > 0 || p1 < np;
+      const int slot = 2 * me + (first ? 0 : 1);
+      if (p0 == 0 && part && tid == 0) {
+        // the block that holds the task's last unit x: the largest i with T0 i / G <= x
+        const int last = (int)(((task + np) * G - 1) / T0);
+        ws.slots[slot] = {cur.b, j, last - me + 1, 2};
+      }
+      B::segment(a, smem, cur.b, j, p0, p1, part ? ws.data + slot * attn_slot_floats(D) : nullptr);
+      first = false;
+      u += p1 - p0;
+    }
+  }
+}
+
+constexpr int kMergeThreads = 256;
+constexpr int kMaxSlots = 1024;
+
+// Merges the parts of split tasks.  Every block lists the first slots, then
+// takes (task, head) pairs in turn: 8 parts at a time, a warp each.
+template <int D, class T>
+__global__ void __launch_bounds__(kMergeThreads) kvq_merge_kernel(AttnArgs a, int blocks) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int V = D / 32;                // dims of a lane
+  __shared__ int list[kMaxSlots], counts[8];
+  __shared__ float so[8][D], sr[8], sl[8];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const AttnWs ws = attn_ws(a.ws, blocks);
+  const int count = *ws.count;
+  int n = 0;
+  for (int s0 = 0; s0 < count; s0 += kMergeThreads) {
+    const int s = s0 + tid;
+    const bool is = s < count && ws.slots[s].parts > 0;
+    const unsigned m = __ballot_sync(0xffffffffu, is);
+    if (lane == 0) counts[warp] = __popc(m);
+    __syncthreads();
+    int at = n;
+    for (int w = 0; w < 8; w++) {
+      if (w < warp) at += counts[w];
+      n += counts[w];
+    }
+    if (is) list[at + __popc(m & ((1u << lane) - 1))] = s;
+    __syncthreads();
+  }
+  for (int w = blockIdx.x; w < n * 8; w += gridDim.x) {
+    const int s = list[w / 8], h = w % 8;
+    const AttnSlot t = ws.slots[s];
+    if (h >= min(8, a.grp - t.j % a.tiles * 8)) continue;
+    float m = -FLT_MAX, den = 0.f, num[V];
+#pragma unroll
+    for (int k = 0; k < V; k++) num[k] = 0.f;
+    for (int i = warp; i < t.parts; i += 8) {
+      const int slot = i == 0 ? s : t.step == 1 ? s + i : (s & ~1) + 2 * i;
+      const float* p = ws.data + slot * attn_slot_floats(D);
+      const float r = p[8 * D + h], l = p[8 * D + 8 + h];
+      float o[V];
+#pragma unroll
+      for (int k = 0; k < V; k++) o[k] = p[h * D + lane + 32 * k];
+      const float mn = fmaxf(m, r), ka = ex2(m - mn), kb = ex2(r - mn);
+      den = den * ka + l * kb;
+#pragma unroll
+      for (int k = 0; k < V; k++) num[k] = num[k] * ka + o[k] * kb;
+      m = mn;
+    }
+#pragma unroll
+    for (int k = 0; k < V; k++) so[warp][lane + 32 * k] = num[k];
+    if (lane == 0) sr[warp] = m, sl[warp] = den;
+    __syncthreads();
+    if (tid < D) {
+      float M = -FLT_MAX, sn = 0.f, sd = 0.f;
+      for (int i = 0; i < 8; i++) M = fmaxf(M, sr[i]);
+      for (int i = 0; i < 8; i++) {
+        const float k = ex2(sr[i] - M);
+        sn = fmaf(k, so[i][tid], sn);
+        sd = fmaf(k, sl[i], sd);
+      }
+      stf(out_row<D, T>(a, t.b, t.j, h) + tid, sn / sd);
+    }
+    __syncthreads();
   }
 }
 
@@ -298,6 +599,53 @@ int sm_count() {
     return 0;
   }
   return n;
+}
+
+int check_heads(const mk_kvq_cache* c, int n_q_heads, int batch) {
+  if (n_q_heads < 1 || n_q_heads % c->n_kv_heads || n_q_heads > 65536) return MK_ERR_BAD_CONFIG;
+  return batch < 0 || batch > 65535 ? MK_ERR_BATCH_TOO_LARGE : MK_OK;
+}
+
+// blocks that fill the GPU, two slots each
+int attn_blocks(int sms, int per_sm) { return std::min(sms * per_sm, kMaxSlots / 2); }
+
+template <int D, class T>
+int attention(const AttnArgs& a, int sms, cudaStream_t st) {
+  // the kernel's shared memory is raised once on each device
+  static std::atomic<unsigned long long> raised[2];
+  constexpr size_t smem = AttnBlock<D, T>::kSmem;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return MK_ERR_CUDA;
+  if (!(raised[dev / 64].load(std::memory_order_relaxed) >> (dev % 64) & 1)) {
+    if (cudaFuncSetAttribute(kvq_attention_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+        cudaSuccess) {
+      cudaGetLastError();
+      return MK_ERR_CUDA;
+    }
+    raised[dev / 64].fetch_or(1ull << (dev % 64), std::memory_order_relaxed);
+  }
+  // no more blocks than there can be segments, unless some rows are empty
+  const long long tasks = (long long)a.batch * a.c.hkv * a.tiles;
+  const long long most = tasks * std::max(1, (a.max_pages + kMinPages - 1) / kMinPages);
+  const int blocks = (int)std::min<long long>(attn_blocks(sms, kBlocksPerSm<D, T>), most);
+  kvq_attention_kernel<D, T><<<blocks, kAttnThreads, smem, st>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return MK_ERR_CUDA;
+  if (!a.split) return MK_OK;
+  // the merge is launched while the first kernel runs and waits for its end
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)std::min<long long>(sms, tasks * 8));
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.stream = st;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kvq_merge_kernel<D, T>, a, blocks) != cudaSuccess) {
+    cudaGetLastError();
+    return MK_ERR_CUDA;
+  }
+  return MK_OK;
 }
 
 int launched() { return cudaGetLastError() == cudaSuccess ? MK_OK : MK_ERR_CUDA; }
@@ -360,25 +708,26 @@ int mk_kvq_read(const mk_kvq_cache* c, const int32_t* src_index, const mk_kv_row
 }
 
 size_t mk_kvq_workspace(const mk_kvq_cache* c, int n_q_heads, int batch) {
-  (void)c, (void)n_q_heads, (void)batch;
-  return 0;
+  if (check_cache(c) || check_heads(c, n_q_heads, batch)) return 0;
+  const int sms = sm_count();
+  return sms ? attn_ws_bytes(attn_blocks(sms, 2), c->head_dim) : 0;
 }
 
 int mk_kvq_attention(const mk_kvq_cache* c, const void* q, int64_t q_stride, void* out, int64_t out_stride, int type,
                      int n_q_heads, int batch, const int32_t* page_tables, int max_pages, const int32_t* seq_lens,
                      float scale, void* workspace, size_t workspace_bytes, void* stream) {
-  (void)workspace, (void)workspace_bytes;
   int rc = check_cache(c);
+  if (!rc) rc = check_heads(c, n_q_heads, batch);
   if (rc) return rc;
-  if (n_q_heads < 1 || n_q_heads % c->n_kv_heads || n_q_heads > 65536) return MK_ERR_BAD_CONFIG;
   if (type != MK_TYPE_BF16 && type != MK_TYPE_F32) return MK_ERR_BAD_ARG;
-  if (batch < 0 || batch > 65535) return MK_ERR_BATCH_TOO_LARGE;
   if (max_pages < 0 || max_pages > 0x7fffffff / kKvqPage || !isfinite(scale)) return MK_ERR_BAD_ARG;
   if (batch == 0) return MK_OK;
   const int64_t v = type == MK_TYPE_BF16 ? 8 : 4;
   if (!q || !out || !seq_lens || (max_pages && !page_tables) || !aligned(q, 16) || !aligned(out, 16) ||
       q_stride % v || out_stride % v || (batch > 1 && out_stride < (int64_t)n_q_heads * c->head_dim))
     return MK_ERR_BAD_ARG;
+  const int sms = sm_count();
+  if (!sms) return MK_ERR_CUDA;
   AttnArgs a{};
   a.c = cache_of(c);
   a.q = q;
@@ -387,20 +736,21 @@ int mk_kvq_attention(const mk_kvq_cache* c, const void* q, int64_t q_stride, voi
   a.seq_lens = seq_lens;
   a.q_stride = q_stride;
   a.out_stride = out_stride;
-  a.hq = n_q_heads;
   a.grp = n_q_heads / c->n_kv_heads;
+  a.tiles = (a.grp + 7) / 8;
   a.batch = batch;
   a.max_pages = max_pages;
   a.scale_log2 = scale * 1.4426950408889634f;
-  const dim3 grid(c->n_kv_heads * ((a.grp + 7) / 8), batch);
+  a.split = max_pages > kMinPages;
+  if (a.split) {
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < attn_ws_bytes(attn_blocks(sms, 2), c->head_dim))
+      return MK_ERR_BAD_ARG;
+    a.ws = (uint8_t*)workspace;
+  }
   cudaStream_t st = (cudaStream_t)stream;
   if (c->head_dim == 128)
-    type == MK_TYPE_BF16 ? kvq_attention_kernel<128, uint16_t><<<grid, kAttnWarps * 32, 0, st>>>(a)
-                         : kvq_attention_kernel<128, float><<<grid, kAttnWarps * 32, 0, st>>>(a);
-  else
-    type == MK_TYPE_BF16 ? kvq_attention_kernel<64, uint16_t><<<grid, kAttnWarps * 32, 0, st>>>(a)
-                         : kvq_attention_kernel<64, float><<<grid, kAttnWarps * 32, 0, st>>>(a);
-  return launched();
+    return type == MK_TYPE_BF16 ? attention<128, uint16_t>(a, sms, st) : attention<128, float>(a, sms, st);
+  return type == MK_TYPE_BF16 ? attention<64, uint16_t>(a, sms, st) : attention<64, float>(a, sms, st);
 }
 
 }  // extern "C"

@@ -18,10 +18,8 @@
 //           consecutive tokens: a k pair of the A operand V^T[dim][token].
 //   scales  token t, group g: (step, low) as two BF16 numbers in one word.
 // A nibble masked in place is an FP16 subnormal, code * 2^-24 (or, four bits
-// up, 16 code * 2^-24), which the FP16 tensor-core product takes exactly; the
-// power of two is undone in the fp32 result.  So a code needs half an
-// instruction to become an operand (values one more, to be centred) and is
-// never rounded.
+// up, 16 code * 2^-24), an exact operand after half an instruction; with one
+// more it is the FP16 integer code - 8 (16 (code - 8)).  No code is rounded.
 #pragma once
 #include <stdint.h>
 #include <float.h>
@@ -110,12 +108,11 @@ __device__ __forceinline__ uint32_t kvq_code(float x, const KvqScale& s) {
 // ---------------------------------------------------------------- attention
 
 // D += A B, m16n8k16, FP16 in, fp32 out
-__device__ __forceinline__ void mma_f16(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, const uint32_t* b) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
@@ -160,7 +157,7 @@ __device__ __forceinline__ float lg2(float x) {
 // when a weight passes 2^15 (one vote a page); the sums l and sum p mid keep
 // theirs, r.
 // QT = 2 / PT = 2 split q and P' into FP16 high and low halves (22 bits) for
-// fp32 activations; with one half each P' is rounded to 11 bits, an eighth of
+// fp32 activations, with the key codes centred too; with one half each P' is rounded to 11 bits, an eighth of
 // a BF16 result's own rounding, and BF16 q is exact.
 template <int D, int QT, int PT>
 struct KvqAttn {
@@ -230,7 +227,7 @@ struct KvqAttn {
     // holds every BF16 q exactly down to 2^-28 of it
     const int e = top == 0.f ? 0 : min(126, 13 + 127 - (int)(__float_as_uint(top) >> 23));
     const float up = __uint_as_float((uint32_t)(e + 127) << 23);
-    const float fh = scale_log2 * 16777216.f * __uint_as_float((uint32_t)(127 - e) << 23);
+    const float fh = scale_log2 * (QT == 2 ? 1.f : 16777216.f) * __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
     for (int g = 0; g < NG; g++)
 #pragma unroll
@@ -264,36 +261,74 @@ struct KvqAttn {
     for (int t = 0; t < NT; t++) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
   }
 
+  // codes less 8 as FP16 integers (16 times that four bits up), from 1024 + n
+  // less 1032 (1152).  Integers and not subnormals: the tensor cores align
+  // their sums to the exponent a subnormal stands for, 2^-14, and would drop
+  // up to 10 bits of them.
+  static __device__ __forceinline__ uint32_t centred(uint32_t w) {
+    return add_h2((w & 0x000f000fu) | 0x64006400u, 0xe408e408u);
+  }
+  static __device__ __forceinline__ uint32_t centred16(uint32_t w) {
+    return add_h2((w & 0x00f000f0u) | 0x64006400u, 0xe480e480u);
+  }
+
+  // o += tile times weights.  The tensor cores cut their fp32 sums off rather
+  // than round them; for fp32 results a page's products are summed from zero
+  // (low halves first) and added with a rounding add
+  static __device__ __forceinline__ void add_tile(float* o, const uint32_t* c, const uint32_t (*b)[2]) {
+    if constexpr (PT == 1) {
+      mma_f16(o, c, b[0]);
+    } else {
+      float t[4] = {0.f, 0.f, 0.f, 0.f};
+      mma_f16(t, c, b[1]);
+      mma_f16(t, c, b[0]);
+#pragma unroll
+      for (int e = 0; e < 4; e++) o[e] += t[e];
+    }
+  }
+
   // tokens [0, valid) of a page; valid is the same in every lane, 1..16
   __device__ __forceinline__ void page(Page& pg, int valid, int lane) {
     constexpr uint32_t M0 = 0x000f000fu, M1 = 0x00f000f0u;
-    constexpr uint32_t kMid0 = 0x80088008u, kMid1 = 0x80808080u;   // -8 2^-24, -128 2^-24
     const int gl = lane >> 2;
     float acc[NG][4];
 #pragma unroll
     for (int g = 0; g < NG; g++) {
       acc[g][0] = acc[g][1] = acc[g][2] = acc[g][3] = 0.f;
+      [[maybe_unused]] float low[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int w = 0; w < 2; w++) {
         const int j = 2 * g + w;
         const uint32_t a = pg.k[0][j], b = pg.k[1][j], a8 = a >> 8, b8 = b >> 8;
-#pragma unroll
-        for (int t = 0; t < QT; t++) {
-          mma_f16(acc[g], a & M0, b & M0, a & M1, b & M1, q[t][2 * j][0], q[t][2 * j][1]);
-          mma_f16(acc[g], a8 & M0, b8 & M0, a8 & M1, b8 & M1, q[t][2 * j + 1][0], q[t][2 * j + 1][1]);
+        if constexpr (QT == 2) {
+          const uint32_t c0[4] = {centred(a), centred(b), centred16(a), centred16(b)};
+          const uint32_t c1[4] = {centred(a8), centred(b8), centred16(a8), centred16(b8)};
+          mma_f16(low, c0, q[1][2 * j]);
+          mma_f16(low, c1, q[1][2 * j + 1]);
+          mma_f16(acc[g], c0, q[0][2 * j]);
+          mma_f16(acc[g], c1, q[0][2 * j + 1]);
+        } else {
+          const uint32_t c0[4] = {a & M0, b & M0, a & M1, b & M1};
+          const uint32_t c1[4] = {a8 & M0, b8 & M0, a8 & M1, b8 & M1};
+          mma_f16(acc[g], c0, q[0][2 * j]);
+          mma_f16(acc[g], c1, q[0][2 * j + 1]);
         }
       }
+      if constexpr (QT == 2)
+#pragma unroll
+        for (int e = 0; e < 4; e++) acc[g][e] += low[e];
     }
     float x[2][2];                         // [token gl / gl + 8][head]
 #pragma unroll
     for (int e = 0; e < 2; e++)
 #pragma unroll
       for (int h = 0; h < 2; h++) {
-        float dot = bf16lo(pg.ks[e][0]) * acc[0][2 * e + h], off = bf16hi(pg.ks[e][0]) * sq[0][h];
+        float dot = 0.f, off = 0.f;
 #pragma unroll
-        for (int g = 1; g < NG; g++) {
-          dot = fmaf(bf16lo(pg.ks[e][g]), acc[g][2 * e + h], dot);
-          off = fmaf(bf16hi(pg.ks[e][g]), sq[g][h], off);
+        for (int g = 0; g < NG; g++) {
+          const float step = bf16lo(pg.ks[e][g]), base = bf16hi(pg.ks[e][g]);
+          dot = fmaf(step, acc[g][2 * e + h], dot);
+          off = fmaf(QT == 2 ? fmaf(8.f, step, base) : base, sq[g][h], off);
         }
         x[e][h] = fmaf(dot, f[h], off);
       }
@@ -383,15 +418,10 @@ struct KvqAttn {
       for (int u = 0; u < 2; u++) {
         const int j = 2 * g + u;
         const uint32_t a = pg.v[0][j], c = pg.v[1][j], a8 = a >> 8, c8 = c >> 8;
-        const uint32_t a0 = add_h2(a & M0, kMid0), a1 = add_h2(a & M1, kMid1);
-        const uint32_t a2 = add_h2(c & M0, kMid0), a3 = add_h2(c & M1, kMid1);
-        const uint32_t e0 = add_h2(a8 & M0, kMid0), e1 = add_h2(a8 & M1, kMid1);
-        const uint32_t e2 = add_h2(c8 & M0, kMid0), e3 = add_h2(c8 & M1, kMid1);
-#pragma unroll
-        for (int t = 0; t < PT; t++) {
-          mma_f16(o[2 * j], a0, a1, a2, a3, b[t][0], b[t][1]);
-          mma_f16(o[2 * j + 1], e0, e1, e2, e3, b[t][0], b[t][1]);
-        }
+        const uint32_t c0[4] = {centred(a), centred16(a), centred(c), centred16(c)};
+        const uint32_t c1[4] = {centred(a8), centred16(a8), centred(c8), centred16(c8)};
+        add_tile(o[2 * j], c0, b);
+        add_tile(o[2 * j + 1], c1, b);
       }
     }
   }
@@ -413,9 +443,9 @@ struct KvqAttn {
       for (int h = 0; h < 2; h++) {
         const float sc = ex2(n[g][h] - r[h]);
 #pragma unroll
-        for (int t = 0; t < 4; t++) {      // tile t: dims 2 t (as code 2^-24) and 2 t + 1 (16 times that)
-          v[g][h][2 * t] = fmaf(o[4 * g + t][h] * sc, 16777216.f, om[g][h]);
-          v[g][h][2 * t + 1] = fmaf(o[4 * g + t][2 + h] * sc, 1048576.f, om[g][h]);
+        for (int t = 0; t < 4; t++) {      // tile t: dims 2 t and (16 times its codes) 2 t + 1
+          v[g][h][2 * t] = fmaf(o[4 * g + t][h], sc, om[g][h]);
+          v[g][h][2 * t + 1] = fmaf(o[4 * g + t][2 + h] * 0.0625f, sc, om[g][h]);
         }
       }
   }

@@ -15,8 +15,6 @@ wrong shape raises; indexes and lengths are checked on the device (``check``).
 """
 from __future__ import annotations
 
-import math
-
 import torch
 
 from . import mk
@@ -56,6 +54,7 @@ class QuantCache:
         if pool.device.type != "cuda":
             raise ValueError(f"4-bit cache: the pool is on {pool.device}, not on a GPU")
         self.pool, self.n_kv_heads, self.head_dim = pool, n_kv_heads, head_dim
+        self._dev, self._ws_bytes = pool.device.index, None
         self.status = torch.zeros(1, dtype=torch.int32, device=pool.device)
         self._c = mk.mk_kvq_cache(pool=pool.data_ptr(), num_pages=pool.shape[0], n_kv_heads=n_kv_heads,
                                   head_dim=head_dim, status=self.status.data_ptr())
@@ -75,13 +74,15 @@ class QuantCache:
     # ------------------------------------------------------------ arguments
 
     def _index(self, t, name, n=None):
-        if t.dtype != torch.int32 or t.dim() != 1 or t.device != self.pool.device or (n is not None and t.numel() != n):
+        if t.dtype != torch.int32 or t.dim() != 1 or t.device != self.pool.device \
+                or (n is not None and t.shape[0] != n):
             raise ValueError(f"{name}: an int32 vector{f' of {n}' if n is not None else ''} on {self.pool.device}, "
                              f"got {t.dtype} {tuple(t.shape)} on {t.device}")
         return t.contiguous()
 
-    def _rows(self, k, v, shape, paged, out):
+    def _rows(self, k, v, unit, out):
         """mk_kv_rows of k and v, and the tensors it points into."""
+        shape = (self.n_kv_heads, self.head_dim) if unit == 1 else (self.n_kv_heads, PAGE_SIZE, self.head_dim)
         for name, t in (("k", k), ("v", v)):
             if t.dtype not in _TYPES or t.dtype != k.dtype:
                 raise ValueError(f"{name}: BF16 or fp32, k and v alike, got {t.dtype}")
@@ -89,111 +90,100 @@ class QuantCache:
                 raise ValueError(f"{name}: [n, {', '.join(map(str, shape))}] on {self.pool.device}, "
                                  f"got {tuple(t.shape)} on {t.device}")
         q = 16 // k.element_size()
-        if k.stride() != v.stride() or k.stride(-1) != 1 or any(s % q for s in k.stride()[:-1]) \
-                or k.data_ptr() % 16 or v.data_ptr() % 16:
+        s = k.stride()
+        if s != v.stride() or s[-1] != 1 or any(x % q for x in s[:-1]) or k.data_ptr() % 16 or v.data_ptr() % 16:
             if out:
                 raise ValueError("k, v: rows of consecutive elements at 16-byte strides, k and v alike")
-            k, v = k.contiguous(), v.contiguous()
-            if k.data_ptr() % 16 or v.data_ptr() % 16:
-                k, v = k.clone(), v.clone()
-        s = k.stride()
-        r = mk.mk_kv_rows(k=k.data_ptr(), v=v.data_ptr(), type=_TYPES[k.dtype], count=k.shape[0],
-                          page_stride=s[0], row_stride=s[2] if paged else s[0], head_stride=s[1])
-        return r, (k, v)
+            k, v = (t.clone(memory_format=torch.contiguous_format) for t in (k, v))
+            s = k.stride()
+        return mk.mk_kv_rows(k=k.data_ptr(), v=v.data_ptr(), type=_TYPES[k.dtype], count=k.shape[0], page_stride=s[0],
+                             row_stride=s[0] if unit == 1 else s[2], head_stride=s[1]), (k, v)
 
-    def _on(self, stream):
-        return _On(self.pool.device, stream)
+    def _dense(self, t):
+        s = t.stride()
+        return s[2] == 1 and s[1] == self.head_dim and s[0] * t.element_size() % 16 == 0 and t.data_ptr() % 16 == 0
+
+    def _run(self, fn, stream, *args):
+        """fn(stream pointer, ...) with the cache's device and the call's stream current, for torch's own
+        allocations and copies too."""
+        if stream is None and torch.cuda.current_device() == self._dev:
+            return fn(torch.cuda.current_stream().cuda_stream, *args)
+        with torch.cuda.device(self._dev), torch.cuda.stream(stream):    # None: the device's current one
+            return fn(torch.cuda.current_stream().cuda_stream, *args)
 
     # ---------------------------------------------------------------- calls
 
     def write(self, k, v, slots, stream=None) -> None:
         """Quantise rows k, v ``[n, n_kv_heads, head_dim]`` (BF16 or fp32, any 16-byte strides) into slots
         ``page * 16 + row`` (int32 ``[n]``, distinct; a negative one skips its row)."""
-        slots = self._index(slots, "slots", k.shape[0])
-        with self._on(stream) as st:
-            r, keep = self._rows(k, v, (self.n_kv_heads, self.head_dim), False, False)
-            mk.mk_kvq_write(self._c, r, None, slots.data_ptr(), k.shape[0], 1, st)
+        self._run(self._write, stream, k, v, None, slots, 1)
 
     def read(self, slots, dtype=torch.bfloat16, stream=None):
         """The keys and values ``[n, n_kv_heads, head_dim]`` at slots ``page * 16 + row``; zeros at a negative one."""
-        slots = self._index(slots, "slots")
-        if dtype not in _TYPES:
-            raise ValueError(f"dtype: BF16 or fp32, got {dtype}")
-        with self._on(stream) as st:
-            k, v = torch.empty(2, slots.numel(), self.n_kv_heads, self.head_dim, dtype=dtype, device=self.pool.device)
-            r, keep = self._rows(k, v, (self.n_kv_heads, self.head_dim), False, True)
-            mk.mk_kvq_read(self._c, slots.data_ptr(), r, None, slots.numel(), 1, st)
-        return k, v
+        return self._run(self._read_rows, stream, slots, dtype)
 
     def write_pages(self, k_pool, v_pool, src_pages, dst_pages, stream=None) -> None:
         """Convert pages ``src_pages`` of BF16 (or fp32) pools ``[pages, n_kv_heads, 16, head_dim]`` into pages
         ``dst_pages`` of the cache (int32 ``[n]``, destinations distinct; a negative index skips its page)."""
-        src, dst = self._index(src_pages, "src_pages"), self._index(dst_pages, "dst_pages", src_pages.numel())
-        with self._on(stream) as st:
-            r, keep = self._rows(k_pool, v_pool, (self.n_kv_heads, PAGE_SIZE, self.head_dim), True, False)
-            mk.mk_kvq_write(self._c, r, src.data_ptr(), dst.data_ptr(), src.numel(), PAGE_SIZE, st)
+        self._run(self._write, stream, k_pool, v_pool, src_pages, dst_pages, PAGE_SIZE)
 
     def read_pages(self, src_pages, k_pool, v_pool, dst_pages, stream=None) -> None:
         """Read pages ``src_pages`` of the cache back into pages ``dst_pages`` of BF16 (or fp32) pools (int32
         ``[n]``, destinations distinct; a negative source gives zeros, a negative destination skips its page)."""
-        src, dst = self._index(src_pages, "src_pages"), self._index(dst_pages, "dst_pages", src_pages.numel())
-        with self._on(stream) as st:
-            r, keep = self._rows(k_pool, v_pool, (self.n_kv_heads, PAGE_SIZE, self.head_dim), True, True)
-            mk.mk_kvq_read(self._c, src.data_ptr(), r, dst.data_ptr(), src.numel(), PAGE_SIZE, st)
+        self._run(self._read, stream, src_pages, k_pool, v_pool, dst_pages, PAGE_SIZE)
 
     def attention(self, q, page_tables, seq_lens, scale: float | None = None, out=None, stream=None):
         """Attention of one query token per sequence, q ``[batch, n_q_heads, head_dim]`` (BF16 or fp32), over the
         first ``seq_lens[b]`` cached tokens of ``page_tables[b]`` (int32 ``[batch]`` and ``[batch, max_pages]``).
         ``scale`` defaults to head_dim ** -0.5.  A sequence of no tokens gives zeros.  Returns ``out``, a new tensor
-        like q unless given; it may be q itself only where q is not needed afterwards."""
-        dev = self.pool.device
-        if q.dim() != 3 or q.dtype not in _TYPES or q.device != dev or q.shape[2] != self.head_dim:
-            raise ValueError(f"q: BF16 or fp32 [batch, heads, {self.head_dim}] on {dev}, got {q.dtype} "
+        like q unless given; it may be q."""
+        return self._run(self._attention, stream, q, page_tables, seq_lens, scale, out)
+
+    def _write(self, st, k, v, src, dst, unit):
+        dst = self._index(dst, "slots" if unit == 1 else "dst_pages", k.shape[0] if unit == 1 else None)
+        if src is not None:
+            src = self._index(src, "src_pages", dst.numel())
+        r, keep = self._rows(k, v, unit, False)
+        mk.mk_kvq_write(self._c, r, None if src is None else src.data_ptr(), dst.data_ptr(), dst.numel(), unit, st)
+
+    def _read(self, st, src, k, v, dst, unit):
+        src = self._index(src, "slots" if unit == 1 else "src_pages")
+        if dst is not None:
+            dst = self._index(dst, "dst_pages", src.numel())
+        r, keep = self._rows(k, v, unit, True)
+        mk.mk_kvq_read(self._c, src.data_ptr(), r, None if dst is None else dst.data_ptr(), src.numel(), unit, st)
+
+    def _read_rows(self, st, slots, dtype):
+        if dtype not in _TYPES:
+            raise ValueError(f"dtype: BF16 or fp32, got {dtype}")
+        k, v = torch.empty((2, slots.numel(), self.n_kv_heads, self.head_dim), dtype=dtype, device=self.pool.device)
+        self._read(st, slots, k, v, None, 1)
+        return k, v
+
+    def _attention(self, st, q, page_tables, seq_lens, scale, out):
+        dev, d = self.pool.device, self.head_dim
+        if q.dim() != 3 or q.dtype not in _TYPES or q.device != dev or q.shape[2] != d:
+            raise ValueError(f"q: BF16 or fp32 [batch, heads, {d}] on {dev}, got {q.dtype} "
                              f"{tuple(q.shape)} on {q.device}")
-        batch, hq = q.shape[:2]
+        batch, hq = q.shape[0], q.shape[1]
         if page_tables.dtype != torch.int32 or page_tables.dim() != 2 or page_tables.device != dev \
                 or page_tables.shape[0] != batch:
             raise ValueError(f"page_tables: int32 [{batch}, max_pages] on {dev}, got {page_tables.dtype} "
                              f"{tuple(page_tables.shape)} on {page_tables.device}")
         seq_lens = self._index(seq_lens, "seq_lens", batch)
-        size = 16 // q.element_size()
-
-        def dense(t):
-            return t.stride(2) == 1 and t.stride(1) == self.head_dim and t.stride(0) % size == 0 \
-                and t.data_ptr() % 16 == 0
-
-        with self._on(stream) as st:
-            page_tables = page_tables.contiguous()
-            if not dense(q):
-                q = q.clone(memory_format=torch.contiguous_format)
-            if out is None:
-                out = torch.empty(batch, hq, self.head_dim, dtype=q.dtype, device=dev)
-            elif out.shape != q.shape or out.dtype != q.dtype or out.device != dev or not dense(out):
-                raise ValueError(f"out: {q.dtype} {tuple(q.shape)} on {dev}, rows of consecutive heads")
-            n = mk.mk_kvq_workspace(self._c, hq, batch)
-            ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-            mk.mk_kvq_attention(self._c, q.data_ptr(), q.stride(0), out.data_ptr(), out.stride(0), _TYPES[q.dtype],
-                                hq, batch, page_tables.data_ptr(), page_tables.shape[1], seq_lens.data_ptr(),
-                                1.0 / math.sqrt(self.head_dim) if scale is None else scale,
-                                ws.data_ptr() if n else None, n, st)
+        page_tables = page_tables.contiguous()
+        max_pages = page_tables.shape[1]
+        if not self._dense(q):
+            q = q.clone(memory_format=torch.contiguous_format)
+        if out is None:
+            out = torch.empty((batch, hq, d), dtype=q.dtype, device=dev)
+        elif out.shape != q.shape or out.dtype != q.dtype or out.device != dev or not self._dense(out):
+            raise ValueError(f"out: {q.dtype} {tuple(q.shape)} on {dev}, rows of consecutive heads at 16-byte strides")
+        # the workspace belongs to this call's stream, or to the graph that captures it
+        if self._ws_bytes is None:
+            self._ws_bytes = mk.mk_kvq_workspace(self._c, self.n_kv_heads, 1)
+        ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=dev)
+        mk.mk_kvq_attention(self._c, q.data_ptr(), q.stride(0), out.data_ptr(), out.stride(0), _TYPES[q.dtype], hq,
+                            batch, page_tables.data_ptr(), max_pages, seq_lens.data_ptr(),
+                            d ** -0.5 if scale is None else scale, ws.data_ptr(), self._ws_bytes, st)
         return out
-
-
-class _On:
-    """The cache's device and the call's stream current for the launches and
-    for torch's allocations, so that a call's temporaries belong to its stream."""
-
-    def __init__(self, device, stream):
-        self.device, self.stream = device, stream
-
-    def __enter__(self):
-        self.guard = torch.cuda.device(self.device)
-        self.guard.__enter__()
-        st = self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
-        self.inner = torch.cuda.stream(st)
-        self.inner.__enter__()
-        return st
-
-    def __exit__(self, *exc):
-        self.inner.__exit__(*exc)
-        self.guard.__exit__(*exc)

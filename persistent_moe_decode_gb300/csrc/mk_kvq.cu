@@ -31,138 +31,310 @@ __device__ __forceinline__ void flag_bad(const Cache& c, int code) {
   if (c.status) *c.status = code;          // every writer stores a code of an error
 }
 
-// eight consecutive elements
-__device__ __forceinline__ void load8(float* x, const uint16_t* p) {
-  const uint4 t = __ldg((const uint4*)p);
-  const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+// ------------------------------------------------------------ write and read
+//
+// Both are bound by bytes: d (size + 9/16) a value each way.  Tokens come in
+// any order, so a token's row is eight values a thread and the eight threads
+// of a scale group side by side.  Whole pages (unit 16) go a page and head a
+// warp: codes of both tokens of a pair meet in one lane, and every record is
+// moved in 16-byte pieces.
+
+// eight consecutive elements as they lie in memory, moved 16 bytes at a time
+template <class T>
+struct Raw8 {
+  static constexpr int W = 2 * (int)sizeof(T);
+  uint32_t w[W];
+  __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-  for (int i = 0; i < 4; i++) {
-    x[2 * i] = bf16lo(w[i]);
-    x[2 * i + 1] = bf16hi(w[i]);
+    for (int i = 0; i < W; i += 4) {
+      const uint4 t = __ldg((const uint4*)p + i / 4);
+      w[i] = t.x, w[i + 1] = t.y, w[i + 2] = t.z, w[i + 3] = t.w;
+    }
   }
-}
-__device__ __forceinline__ void load8(float* x, const float* p) {
-  const float4 a = __ldg((const float4*)p), b = __ldg((const float4*)p + 1);
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-  x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-__device__ __forceinline__ void store8(uint16_t* p, const float* x) {
-  *(uint4*)p = make_uint4(pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3]), pack_bf2(x[4], x[5]), pack_bf2(x[6], x[7]));
-}
-__device__ __forceinline__ void store8(float* p, const float* x) {
-  *(float4*)p = make_float4(x[0], x[1], x[2], x[3]);
-  *((float4*)p + 1) = make_float4(x[4], x[5], x[6], x[7]);
-}
-
-// Token `i` of a call whose indexes count units of 1 token or of a page:
-// the row of the outside view and the slot of the cache it goes with, or < 0.
-__device__ __forceinline__ long long unit_token(const int32_t* index, int i, int unit) {
-  const int u = i / unit;
-  const int at = index ? index[u] : u;
-  return at < 0 ? -1 : (long long)at * unit + i % unit;
-}
-
-// Eight dims a thread, the eight threads of a scale group side by side: group
-// octet e = ((token hkv + head) 2 + key / value) NG + group.
-struct Octet {
-  int i, head, val, group;
-};
-template <int D>
-__device__ __forceinline__ Octet octet(long long e, int hkv) {
-  constexpr int NG = D / kKvqGroup;
-  Octet o;
-  o.group = (int)(e % NG);
-  e /= NG;
-  o.val = (int)(e & 1);
-  e >>= 1;
-  o.head = (int)(e % hkv);
-  o.i = (int)(e / hkv);
-  return o;
-}
-
-template <int D, class T>
-__global__ void __launch_bounds__(256) kvq_write_kernel(Cache c, Rows src, const int32_t* src_index,
-                                                        const int32_t* dst_index, int tokens, int unit) {
-  using R = KvqRec<D>;
-  const long long octets = (long long)tokens * c.hkv * 2 * R::NG;
-  const int wi = threadIdx.x & 7;
-  const unsigned mask = 0xffu << (threadIdx.x & 24);
-  for (long long e = (blockIdx.x * 256ll + threadIdx.x) >> 3; e < octets; e += gridDim.x * 32ll) {
-    const Octet o = octet<D>(e, c.hkv);
-    const long long from = unit_token(src_index, o.i, unit), to = unit_token(dst_index, o.i, unit);
-    if (from < 0 || to < 0) continue;
-    if (from >= (long long)src.count * unit || to >= (long long)c.pages * kKvqPage) {
-      flag_bad(c, MK_ERR_BAD_PAGE);
-      continue;
-    }
-    const T* row = (const T*)(o.val ? src.v : src.k) + from / kKvqPage * src.page + from % kKvqPage * src.row +
-                   o.head * src.head + o.group * kKvqGroup + wi * 8;
-    float x[8];
-    load8(x, row);
-    float lo = x[0], hi = x[0];
+  __device__ __forceinline__ void store(T* p) const {
 #pragma unroll
-    for (int i = 1; i < 8; i++) {
-      lo = fmin_nan(lo, x[i]);
-      hi = fmax_nan(hi, x[i]);
-    }
-#pragma unroll
-    for (int sh = 1; sh < 8; sh <<= 1) {
-      lo = fmin_nan(lo, __shfl_xor_sync(mask, lo, sh));
-      hi = fmax_nan(hi, __shfl_xor_sync(mask, hi, sh));
-    }
-    const KvqScale s = kvq_scale(lo, hi);
-    uint32_t word = 0;
-#pragma unroll
-    for (int i = 0; i < 8; i++) word |= kvq_code(x[i], s) << (4 * i);
-    const int t = (int)(to % kKvqPage);
-    uint8_t* rec = c.pool + ((to / kKvqPage) * c.hkv + o.head) * R::kBytes;
-    if (o.val) {
-      *(uint16_t*)(rec + R::val_half(t, wi, o.group, 0)) = (uint16_t)word;
-      *(uint16_t*)(rec + R::val_half(t, wi, o.group, 1)) = (uint16_t)(word >> 16);
-    } else {
-      *(uint32_t*)(rec + R::key_word(t, wi, o.group)) = word;
-    }
-    if (wi == 0)
-      *(uint32_t*)(rec + (o.val ? R::kValScale : R::kKeyScale) + 4 * (t * R::NG + o.group)) = s.word();
+    for (int i = 0; i < W; i += 4) *((uint4*)p + i / 4) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
   }
-}
-
-template <int D, class T>
-__global__ void __launch_bounds__(256) kvq_read_kernel(Cache c, const int32_t* src_index, Rows dst,
-                                                       const int32_t* dst_index, int tokens, int unit) {
-  using R = KvqRec<D>;
-  const long long octets = (long long)tokens * c.hkv * 2 * R::NG;
-  const int wi = threadIdx.x & 7;
-  for (long long e = (blockIdx.x * 256ll + threadIdx.x) >> 3; e < octets; e += gridDim.x * 32ll) {
-    const Octet o = octet<D>(e, c.hkv);
-    const long long from = unit_token(src_index, o.i, unit), to = unit_token(dst_index, o.i, unit);
-    if (to < 0) continue;
-    if (from >= (long long)c.pages * kKvqPage || to >= (long long)dst.count * unit) {
-      flag_bad(c, MK_ERR_BAD_PAGE);
-      continue;
-    }
-    float x[8];
-    if (from < 0) {
+  __device__ __forceinline__ void get(float* x) const {
 #pragma unroll
-      for (int i = 0; i < 8; i++) x[i] = 0.f;
-    } else {
-      const int t = (int)(from % kKvqPage);
-      const uint8_t* rec = c.pool + ((from / kKvqPage) * c.hkv + o.head) * R::kBytes;
-      uint32_t word;
-      if (o.val)
-        word = *(const uint16_t*)(rec + R::val_half(t, wi, o.group, 0)) |
-               ((uint32_t)*(const uint16_t*)(rec + R::val_half(t, wi, o.group, 1)) << 16);
+    for (int i = 0; i < W; i++)
+      if constexpr (sizeof(T) == 2) {
+        x[2 * i] = bf16lo(w[i]);
+        x[2 * i + 1] = bf16hi(w[i]);
+      } else {
+        x[i] = __uint_as_float(w[i]);
+      }
+  }
+  __device__ __forceinline__ void set(const float* x) {
+#pragma unroll
+    for (int i = 0; i < W; i++)
+      if constexpr (sizeof(T) == 2)
+        w[i] = pack_bf2(x[2 * i], x[2 * i + 1]);
       else
-        word = *(const uint32_t*)(rec + R::key_word(t, wi, o.group));
-      const uint32_t s =
-          *(const uint32_t*)(rec + (o.val ? R::kValScale : R::kKeyScale) + 4 * (t * R::NG + o.group));
-#pragma unroll
-      for (int i = 0; i < 8; i++) x[i] = fmaf((float)((word >> (4 * i)) & 15u), bf16lo(s), bf16hi(s));
-    }
-    T* row = (T*)(o.val ? dst.v : dst.k) + to / kKvqPage * dst.page + to % kKvqPage * dst.row + o.head * dst.head +
-             o.group * kKvqGroup + wi * 8;
-    store8(row, x);
+        w[i] = __float_as_uint(x[i]);
   }
+};
+
+template <class T>
+__device__ __forceinline__ void load8(float* x, const T* p) {
+  Raw8<T> r;
+  r.load(p);
+  r.get(x);
+}
+
+// scale of a group whose values lie eight a thread in eight neighbouring
+// threads, all of which (`mask`) call it
+__device__ __forceinline__ KvqScale group_scale(const float* x, unsigned mask) {
+  float lo = x[0], hi = x[0];
+#pragma unroll
+  for (int i = 1; i < 8; i++) {
+    lo = fmin_nan(lo, x[i]);
+    hi = fmax_nan(hi, x[i]);
+  }
+#pragma unroll
+  for (int sh = 1; sh < 8; sh <<= 1) {
+    lo = fmin_nan(lo, __shfl_xor_sync(mask, lo, sh));
+    hi = fmax_nan(hi, __shfl_xor_sync(mask, hi, sh));
+  }
+  return kvq_scale(lo, hi);
+}
+
+// values of the eight codes of a word: step * code + low in fp32.  A nibble
+// under the exponent of 2^23 is 2^23 + code; both operations that follow are
+// exact up to the last.
+__device__ __forceinline__ void kvq_values(float* x, uint32_t word, uint32_t scale) {
+  const float step = bf16lo(scale), low = bf16hi(scale);
+#pragma unroll
+  for (int i = 0; i < 8; i++)
+    x[i] = fmaf(__uint_as_float((word >> (4 * i) & 15u) | 0x4b000000u) - 8388608.f, step, low);
+}
+
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t* w, const uint8_t* p) {
+  if constexpr (N == 4) {
+    const uint4 t = __ldcs((const uint4*)p);
+    w[0] = t.x, w[1] = t.y, w[2] = t.z, w[3] = t.w;
+  } else if constexpr (N == 2) {
+    const uint2 t = __ldcs((const uint2*)p);
+    w[0] = t.x, w[1] = t.y;
+  } else {
+    w[0] = __ldcs((const uint32_t*)p);
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_words(uint8_t* p, const uint32_t* w) {
+  if constexpr (N == 4)
+    *(uint4*)p = make_uint4(w[0], w[1], w[2], w[3]);
+  else if constexpr (N == 2)
+    *(uint2*)p = make_uint2(w[0], w[1]);
+  else
+    *(uint32_t*)p = w[0];
+}
+
+// a unit of the call: its indexes on the two sides, false if it is skipped
+__device__ __forceinline__ bool unit_pair(const Cache& c, const int32_t* src_index, int src_count,
+                                          const int32_t* dst_index, int dst_count, int i, int& from, int& to) {
+  from = src_index ? src_index[i] : i;
+  to = dst_index ? dst_index[i] : i;
+  if (to < 0) return false;
+  if (from >= src_count || to >= dst_count) {
+    flag_bad(c, MK_ERR_BAD_PAGE);
+    return false;
+  }
+  return true;
+}
+
+constexpr int kCopyThreads = 256;
+
+// The thread's eight dims of a token call: block (x, y) takes kTokens tokens of
+// head y, eight threads a (token, key or value, group)
+template <int D>
+struct TokenLane {
+  static constexpr int NG = D / kKvqGroup;
+  static constexpr int kTokens = kCopyThreads / 8 / (2 * NG);
+  int wi, group, val, i;
+  __device__ __forceinline__ TokenLane() {
+    const int o = threadIdx.x >> 3;
+    wi = threadIdx.x & 7;
+    group = o % NG;
+    val = o / NG & 1;
+    i = blockIdx.x * kTokens + o / (2 * NG);
+  }
+};
+
+template <int D, class T>
+__global__ void __launch_bounds__(kCopyThreads) kvq_write_kernel(Cache c, Rows src, const int32_t* src_index,
+                                                                 const int32_t* dst_index, int n) {
+  using R = KvqRec<D>;
+  const TokenLane<D> o;
+  const int head = blockIdx.y;
+  int from, to;
+  if (o.i >= n || !unit_pair(c, src_index, src.count, dst_index, c.pages * kKvqPage, o.i, from, to) || from < 0)
+    return;                                // all eight threads of a group alike
+  Raw8<T> raw;
+  raw.load((const T*)(o.val ? src.v : src.k) + from * src.row + head * src.head + o.group * kKvqGroup + o.wi * 8);
+  float x[8];
+  raw.get(x);
+  const KvqScale s = group_scale(x, 0xffu << (threadIdx.x & 24));
+  const uint32_t word = kvq_codes(x, s);
+  const int t = to % kKvqPage;
+  uint8_t* rec = c.pool + ((long long)(to / kKvqPage) * c.hkv + head) * R::kBytes;
+  if (o.val) {
+    *(uint16_t*)(rec + R::val_half(t, o.wi, o.group, 0)) = (uint16_t)word;
+    *(uint16_t*)(rec + R::val_half(t, o.wi, o.group, 1)) = (uint16_t)(word >> 16);
+  } else {
+    *(uint32_t*)(rec + R::key_word(t, o.wi, o.group)) = word;
+  }
+  if (o.wi == 0) *(uint32_t*)(rec + (o.val ? R::kValScale : R::kKeyScale) + 4 * (t * R::NG + o.group)) = s.word();
+}
+
+template <int D, class T>
+__global__ void __launch_bounds__(kCopyThreads) kvq_read_kernel(Cache c, const int32_t* src_index, Rows dst,
+                                                                const int32_t* dst_index, int n) {
+  using R = KvqRec<D>;
+  const TokenLane<D> o;
+  const int head = blockIdx.y;
+  int from, to;
+  if (o.i >= n || !unit_pair(c, src_index, c.pages * kKvqPage, dst_index, dst.count, o.i, from, to)) return;
+  float x[8] = {};
+  if (from >= 0) {
+    const int t = from % kKvqPage;
+    const uint8_t* rec = c.pool + ((long long)(from / kKvqPage) * c.hkv + head) * R::kBytes;
+    uint32_t word;
+    if (o.val)
+      word = *(const uint16_t*)(rec + R::val_half(t, o.wi, o.group, 0)) |
+             ((uint32_t)*(const uint16_t*)(rec + R::val_half(t, o.wi, o.group, 1)) << 16);
+    else
+      word = *(const uint32_t*)(rec + R::key_word(t, o.wi, o.group));
+    kvq_values(x, word, *(const uint32_t*)(rec + (o.val ? R::kValScale : R::kKeyScale) + 4 * (t * R::NG + o.group)));
+  }
+  Raw8<T> raw;
+  raw.set(x);
+  raw.store((T*)(o.val ? dst.v : dst.k) + to * dst.row + head * dst.head + o.group * kKvqGroup + o.wi * 8);
+}
+
+template <int D, class T>
+__global__ void __launch_bounds__(kCopyThreads) kvq_write_pages_kernel(Cache c, Rows src, const int32_t* src_index,
+                                                                       const int32_t* dst_index, int n) {
+  using R = KvqRec<D>;
+  constexpr int NG = R::NG;
+  const int lane = threadIdx.x & 31, head = blockIdx.y;
+  const int i = blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5);
+  int from, to;
+  if (i >= n || !unit_pair(c, src_index, src.count, dst_index, c.pages, i, from, to) || from < 0) return;
+  const T* kb = (const T*)src.k + from * src.page + head * src.head;
+  const T* vb = (const T*)src.v + from * src.page + head * src.head;
+  uint8_t* rec = c.pool + ((long long)to * c.hkv + head) * R::kBytes;
+  const int pr = lane >> 3, wi = lane & 7;
+  Raw8<T> kr[4][NG], vr[2][2][NG];         // tokens pr + 4 e; tokens 2 (pr + 4 e) and + 1; dims 64 g + 8 wi ..
+#pragma unroll
+  for (int g = 0; g < NG; g++) {
+#pragma unroll
+    for (int e = 0; e < 4; e++) kr[e][g].load(kb + (pr + 4 * e) * src.row + g * kKvqGroup + wi * 8);
+#pragma unroll
+    for (int e = 0; e < 4; e++)
+      vr[e / 2][e % 2][g].load(vb + (2 * (pr + e / 2 * 4) + e % 2) * src.row + g * kKvqGroup + wi * 8);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; e++) {
+    uint32_t w[NG], sw[NG];
+#pragma unroll
+    for (int g = 0; g < NG; g++) {
+      float x[8];
+      kr[e][g].get(x);
+      const KvqScale s = group_scale(x, 0xffffffffu);
+      w[g] = kvq_codes(x, s);
+      sw[g] = s.word();
+    }
+    const int t = pr + 4 * e;
+    if constexpr (NG == 2) {
+      // a column's 16 bytes are both words of group 0, then of group 1: two threads hold one of each
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, wi & 1 ? w[0] : w[1], 1);
+      if (wi & 1)
+        w[0] = got;
+      else
+        w[1] = got;
+    }
+    store_words<NG>(rec + t * (D / 2) + wi * 4 * NG, w);
+    if (wi == 0) store_words<NG>(rec + R::kKeyScale + t * 4 * NG, sw);
+  }
+#pragma unroll
+  for (int e = 0; e < 2; e++) {
+    uint32_t w[2 * NG], sw[2 * NG];
+#pragma unroll
+    for (int g = 0; g < NG; g++) {
+      uint32_t c8[2];
+#pragma unroll
+      for (int t = 0; t < 2; t++) {
+        float x[8];
+        vr[e][t][g].get(x);
+        const KvqScale s = group_scale(x, 0xffffffffu);
+        c8[t] = kvq_codes(x, s);
+        sw[t * NG + g] = s.word();
+      }
+      w[2 * g] = __byte_perm(c8[0], c8[1], 0x5410);
+      w[2 * g + 1] = __byte_perm(c8[0], c8[1], 0x7632);
+    }
+    const int pair = pr + 4 * e;
+    store_words<2 * NG>(rec + R::kVal + pair * D + wi * 8 * NG, w);
+    if (wi == 0) store_words<2 * NG>(rec + R::kValScale + pair * 8 * NG, sw);
+  }
+}
+
+template <int D, class T>
+__global__ void __launch_bounds__(kCopyThreads) kvq_read_pages_kernel(Cache c, const int32_t* src_index, Rows dst,
+                                                                      const int32_t* dst_index, int n) {
+  using R = KvqRec<D>;
+  constexpr int NG = R::NG;
+  const int lane = threadIdx.x & 31, head = blockIdx.y;
+  const int i = blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5);
+  int from, to;
+  if (i >= n || !unit_pair(c, src_index, c.pages, dst_index, dst.count, i, from, to)) return;
+  T* kb = (T*)dst.k + to * dst.page + head * dst.head;
+  T* vb = (T*)dst.v + to * dst.page + head * dst.head;
+  const int pr = lane >> 3, wi = lane & 7;
+  uint32_t kw[4][NG] = {}, ks[4][NG] = {}, vw[2][2 * NG] = {}, vs[2][2 * NG] = {};   // no source: zeros
+  if (from >= 0) {
+    const uint8_t* rec = c.pool + ((long long)from * c.hkv + head) * R::kBytes;
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+      load_words<NG>(kw[e], rec + (pr + 4 * e) * (D / 2) + wi * 4 * NG);
+      load_words<NG>(ks[e], rec + R::kKeyScale + (pr + 4 * e) * 4 * NG);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; e++) {
+      load_words<2 * NG>(vw[e], rec + R::kVal + (pr + 4 * e) * D + wi * 8 * NG);
+      load_words<2 * NG>(vs[e], rec + R::kValScale + (pr + 4 * e) * 8 * NG);
+    }
+  }
+  float x[8];
+  Raw8<T> raw;
+#pragma unroll
+  for (int e = 0; e < 4; e++) {
+    if constexpr (NG == 2) {               // as in the write, the other way round
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, wi & 1 ? kw[e][0] : kw[e][1], 1);
+      if (wi & 1)
+        kw[e][0] = got;
+      else
+        kw[e][1] = got;
+    }
+#pragma unroll
+    for (int g = 0; g < NG; g++) {
+      kvq_values(x, kw[e][g], ks[e][g]);
+      raw.set(x);
+      raw.store(kb + (pr + 4 * e) * dst.row + g * kKvqGroup + wi * 8);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 2; e++)
+#pragma unroll
+    for (int t = 0; t < 2; t++)
+#pragma unroll
+      for (int g = 0; g < NG; g++) {
+        kvq_values(x, __byte_perm(vw[e][2 * g], vw[e][2 * g + 1], t ? 0x7632 : 0x5410), vs[e][t * NG + g]);
+        raw.set(x);
+        raw.store(vb + (2 * (pr + 4 * e) + t) * dst.row + g * kKvqGroup + wi * 8);
+      }
 }
 
 // ---------------------------------------------------------------- attention
@@ -170,11 +342,11 @@ __global__ void __launch_bounds__(256) kvq_read_kernel(Cache c, const int32_t* s
 // The pages of all tasks (sequence, KV head, 8 of its query heads) are cut
 // into segments by the blocks themselves from the lengths on the device, so
 // the host neither reads lengths nor launches for the longest one:
-//   few pages (less than kMinPages a block): segments of kMinPages pages, one
-//     page a warp, dealt to the blocks in turn;
-//   many: block i takes units T i / G .. T (i + 1) / G of the T pages of all
-//     tasks in order, so every block moves the same bytes whatever the mix of
-//     lengths.
+//   few pages (less than two segments a block): segments of kMinPages pages,
+//     one page a warp, dealt to the blocks in turn;
+//   many: block i takes units T i / G .. T (i + 1) / G of the T units of all
+//     tasks in order (a unit is a page, a task's last segment rounded up), so
+//     every block moves the same bytes whatever the mix of lengths.
 // A task that is one segment is written at once.  The segments of the others
 // leave (reference, sum, weighted sum) in workspace slots, at most two a block,
 // and a second kernel merges them in page order: no atomics, one result.
@@ -228,8 +400,8 @@ __device__ __forceinline__ AttnWs attn_ws(uint8_t* p, int blocks) {
 __device__ __forceinline__ void stf(uint16_t* p, float v) { *p = f2bf(v); }
 __device__ __forceinline__ void stf(float* p, float v) { *p = v; }
 
-__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -243,10 +415,11 @@ __device__ __forceinline__ int seq_pages(const AttnArgs& a, int b) {
   return len < 0 || len > a.max_pages * kKvqPage ? -1 : (len + kKvqPage - 1) / kKvqPage;
 }
 
-// Position in the list of sequences: the sums before sequence b of its pages
-// (or segments) and of its split segments
-struct Cursor {
-  int b;
+// A place in the list of sequences: the pages of sequence b and what comes
+// before it, in units (kMinPages for each started kMinPages pages of one head:
+// a short task costs a block about that much) and in chunks of split tasks
+struct Place {
+  int b, np;
   long long units;
   int split;
 };
@@ -254,47 +427,68 @@ struct Cursor {
 struct PlanSmem {
   long long units[kAttnWarps];
   int split[kAttnWarps];
-  Cursor found;
+  Place found;
+  // the window: a sequence a thread, and the units and chunks before each
+  int np[kAttnThreads], split_before[kAttnThreads];
+  long long before[kAttnThreads];
+  int b0, split_end;
+  long long end;                           // before the next window
 };
 
-// The sequence, from `c` on, whose pages (seg: segments) hold number `target`;
-// batch if there is none.  All threads call it and get the same answer.
-__device__ Cursor find_sequence(const AttnArgs& a, PlanSmem& S, Cursor c, long long target, bool seg) {
+__device__ __forceinline__ int seq_units(int np) { return (np + kMinPages - 1) / kMinPages * kMinPages; }
+
+// Sums over the sequences, a window of one sequence a thread at a time (in
+// shared memory: between segments nothing stays in registers).  All threads
+// of the block make every call together.
+__device__ void plan_window(const AttnArgs& a, PlanSmem& S, int first, long long end, int split_end) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  while (c.b < a.batch) {
-    const int b = c.b + tid;
-    const int np = b < a.batch ? max(seq_pages(a, b), 0) : 0;
-    const int n = seg ? (np + kMinPages - 1) / kMinPages : np;
-    const int m = seg && n > 1 ? n : 0;
-    long long u = n;
-    int sp = m;
+  const int np = first + tid < a.batch ? max(seq_pages(a, first + tid), 0) : 0;
+  const int n = seq_units(np), m = n > kMinPages ? n / kMinPages : 0;
+  long long u = n;
+  int sp = m;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, u, o);
-      const int y = __shfl_up_sync(0xffffffffu, sp, o);
-      if (lane >= o) u += x, sp += y;
-    }
-    if (lane == 31) S.units[warp] = u, S.split[warp] = sp;
-    __syncthreads();
-    long long ub = c.units, ut = c.units;
-    int sb = c.split, st = c.split;
-    for (int w = 0; w < kAttnWarps; w++) {
-      if (w == warp) ub = ut, sb = st;
-      ut += S.units[w];
-      st += S.split[w];
-    }
-    const long long before = ub + u - n;
-    if (n > 0 && before <= target && target < before + n) S.found = {b, before, sb + sp - m};
-    __syncthreads();
-    if (target < ut) {
-      c = S.found;
-      __syncthreads();                     // the next call writes S again
-      return c;
-    }
-    c = {c.b + kAttnThreads, ut, st};
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, u, o);
+    const int y = __shfl_up_sync(0xffffffffu, sp, o);
+    if (lane >= o) u += x, sp += y;
   }
-  c.b = a.batch;
-  return c;
+  if (lane == 31) S.units[warp] = u, S.split[warp] = sp;
+  __syncthreads();
+  long long before = end + u - n;
+  int split_before = split_end + sp - m;
+  for (int w = 0; w < kAttnWarps; w++) {
+    if (w < warp) before += S.units[w], split_before += S.split[w];
+    end += S.units[w];
+    split_end += S.split[w];
+  }
+  S.np[tid] = np;
+  S.before[tid] = before;
+  S.split_before[tid] = split_before;
+  if (tid == 0) S.b0 = first, S.end = end, S.split_end = split_end;
+  __syncthreads();
+}
+
+// the next window, false after the last
+__device__ bool plan_next(const AttnArgs& a, PlanSmem& S) {
+  const int first = S.b0 + kAttnThreads, split_end = S.split_end;
+  const long long end = S.end;
+  __syncthreads();
+  if (first >= a.batch) return false;
+  plan_window(a, S, first, end, split_end);
+  return true;
+}
+
+// the sequence that holds unit `target`, not before the window; false past the last
+__device__ bool plan_find(const AttnArgs& a, PlanSmem& S, long long target, Place& at) {
+  while (target >= S.end)
+    if (!plan_next(a, S)) return false;
+  const int tid = threadIdx.x, np = S.np[tid];
+  const long long before = S.before[tid];
+  if (before <= target && target < before + seq_units(np)) S.found = {S.b0 + tid, np, before, S.split_before[tid]};
+  __syncthreads();
+  at = S.found;
+  __syncthreads();                         // the next call writes it again
+  return true;
 }
 
 // output row of head h of task (b, j)
@@ -310,6 +504,7 @@ struct AttnBlock {
   using R = KvqRec<D>;
   using A = KvqAttn<D, TERMS, TERMS>;
   static constexpr int NG = R::NG;
+  static constexpr int kChunks = (R::kBytes / 16 + 31) / 32;
   static constexpr int kPad = D + 8;       // row of the merge buffer: rows of one store fall in distinct banks
   static constexpr size_t kRingBytes = (size_t)kAttnWarps * kRing * R::kBytes;
   static constexpr size_t kMergeBytes = (size_t)kAttnWarps * 8 * (kPad + 2) * 4;
@@ -325,25 +520,34 @@ struct AttnBlock {
     const int n = (p1 - p0 - warp + kAttnWarps - 1) / kAttnWarps;   // this warp's pages (may be <= 0)
     bool bad = false;
     // page numbers: 32 of the warp's pages at a time, a lane each
-    int ids = lane < n ? table[lane * kAttnWarps] : 0;
-    auto fetch = [&](int i) {              // page i of the warp into its ring slot
-      if (i < n) {
-        if (i && (i & 31) == 0) ids = i + lane < n ? table[(long long)(i + lane) * kAttnWarps] : 0;
-        int id = __shfl_sync(0xffffffffu, ids, i & 31);
-        if (id < 0 || id >= a.c.pages) {
+    int ids = lane < n ? table[lane * kAttnWarps] : 0, fetched = 0;
+    const uint8_t* base = a.c.pool + (long long)g * R::kBytes + lane * 16;
+    const long long page_bytes = (long long)a.c.hkv * R::kBytes;
+    // the lane's 16-byte chunks lie 512 bytes apart, in the ring slot too: value chunks from one place (32 of
+    // them are whole fours of token pairs), the others from another
+    constexpr int kVal0 = R::kVal / 512, kVal1 = R::kKeyScale / 512;
+    const uint32_t line = smem_u32(ring) + lane * 16;
+    const uint32_t line_v = smem_u32(ring) + A::staged(R::kVal / 16 + lane) * 16 - R::kVal;
+    auto fetch = [&](uint32_t slot) {      // the warp's next page into the ring, `slot` bytes in
+      if (fetched < n) {
+        if (fetched && (fetched & 31) == 0)
+          ids = fetched + lane < n ? table[(long long)(fetched + lane) * kAttnWarps] : 0;
+        int id = __shfl_sync(0xffffffffu, ids, fetched & 31);
+        if ((unsigned)id >= (unsigned)a.c.pages) {
           bad = true;
           id = 0;
         }
-        const uint8_t* src = a.c.pool + ((long long)id * a.c.hkv + g) * R::kBytes;
-        uint8_t* dst = ring + (i % kRing) * R::kBytes;
+        const uint8_t* src = base + id * page_bytes;
 #pragma unroll
-        for (int k = 0; k < (R::kBytes + 511) / 512; k++)
-          if (k * 512 + lane * 16 < R::kBytes) cp_async16(dst + k * 512 + lane * 16, src + k * 512 + lane * 16);
+        for (int k = 0; k < kChunks; k++)
+          if (k * 32 + 32 <= R::kBytes / 16 || k * 32 + lane < R::kBytes / 16) 
+            cp_async16((k >= kVal0 && k < kVal1 ? line_v : line) + slot + k * 512, src + k * 512);
+        fetched++;
       }
       cp_async_commit();
     };
 #pragma unroll
-    for (int i = 0; i < kRing - 1; i++) fetch(i);
+    for (int i = 0; i < kRing - 1; i++) fetch(i * R::kBytes);
 
     A at;
     {
@@ -359,14 +563,16 @@ struct AttnBlock {
       }
       at.init(x, a.scale_log2, lane);
     }
+    int left = len - (p0 + warp) * kKvqPage;   // tokens from the page on
+    uint32_t rd = 0, wr = (kRing - 1) * R::kBytes;
     for (int i = 0; i < n; i++) {
       cp_async_wait<kRing - 2>();
       __syncwarp();
-      typename A::Page pg;
-      A::load(pg, ring + (i % kRing) * R::kBytes, lane);
-      // the slot fetched into now was read in the iteration before
-      fetch(i + kRing - 1);
-      at.page(pg, min(kKvqPage, len - (p0 + warp + i * kAttnWarps) * kKvqPage), lane);
+      fetch(wr);                           // into the slot read in the iteration before
+      wr = wr == (kRing - 1) * R::kBytes ? 0 : wr + R::kBytes;
+      at.template page<true>(ring + rd, left, lane);
+      rd = rd == (kRing - 1) * R::kBytes ? 0 : rd + R::kBytes;
+      left -= kAttnWarps * kKvqPage;
     }
     cp_async_wait<0>();
     if (bad && lane == 0) flag_bad(a.c, MK_ERR_BAD_PAGE);
@@ -428,65 +634,64 @@ __global__ void __launch_bounds__(kAttnThreads, kBlocksPerSm<D, T>) kvq_attentio
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ PlanSmem S;
   const int tid = threadIdx.x, G = gridDim.x, me = blockIdx.x, HT = a.c.hkv * a.tiles;
+  // the merge may be set up as soon as there is room for it
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // all pages; rows of sequences without one
-  long long total = 0;
-  for (int b = tid; b < a.batch; b += kAttnThreads) total += max(seq_pages(a, b), 0);
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  if ((tid & 31) == 0) S.units[tid >> 5] = total;
-  __syncthreads();
-  total = 0;
-  for (int w = 0; w < kAttnWarps; w++) total += S.units[w];
-  __syncthreads();
   for (int b = me; b < a.batch; b += G) {
     const int np = seq_pages(a, b);
-    if (np > 0) continue;
+    if (np > 0) continue;                  // rows of sequences without a page
     if (np < 0 && tid == 0) flag_bad(a.c, MK_ERR_BAD_ARG);
     for (int i = tid; i < a.c.hkv * a.grp * D; i += kAttnThreads)
       stf((T*)a.out + b * a.out_stride + i, np < 0 ? NAN : 0.f);
   }
+  plan_window(a, S, 0, 0, 0);
+  while (plan_next(a, S)) {}
+  const unsigned long long total = (unsigned long long)S.end * HT;
+  if (me == 0 && tid == 0 && a.split) *attn_ws(a.ws, G).count = S.split_end * HT;   // changed below with whole shares
+  if (a.batch > kAttnThreads) {
+    __syncthreads();
+    plan_window(a, S, 0, 0, 0);
+  }
 
-  const unsigned long long T0 = (unsigned long long)total * HT;
   const AttnWs ws = attn_ws(a.ws, G);
-  if (!a.split || T0 < (unsigned long long)G * kMinPages) {
-    Cursor cur{0, 0, 0};
-    for (long long s = me;; s += G) {
-      cur = find_sequence(a, S, cur, s / HT, true);
-      if (cur.b >= a.batch) break;
-      const int np = seq_pages(a, cur.b), nc = (np + kMinPages - 1) / kMinPages;
-      const long long rem = s - cur.units * HT;
+  Place at;
+  if (!a.split || total < 2ull * G * kMinPages) {
+    // segment s is the s-th chunk of kMinPages pages
+    for (long long s = me; plan_find(a, S, s / HT * kMinPages, at); s += G) {
+      const int nc = seq_units(at.np) / kMinPages;
+      const long long rem = s - at.units / kMinPages * HT;
       const int j = (int)(rem / nc), k = (int)(rem % nc);
-      const int slot = cur.split * HT + (int)rem;
-      if (nc > 1 && tid == 0) ws.slots[slot] = {cur.b, j, k == 0 ? nc : 0, 1};
-      B::segment(a, smem, cur.b, j, k * kMinPages, min(np, (k + 1) * kMinPages),
+      const int slot = at.split * HT + (int)rem;
+      if (nc > 1 && tid == 0) ws.slots[slot] = {at.b, j, k == 0 ? nc : 0, 1};
+      B::segment(a, smem, at.b, j, k * kMinPages, min(at.np, (k + 1) * kMinPages),
                  nc > 1 ? ws.data + slot * attn_slot_floats(D) : nullptr);
     }
-    if (a.split && me == 0 && tid == 0) *ws.count = cur.split * HT;
   } else {
     if (me == 0 && tid == 0) *ws.count = 2 * G;
-    unsigned long long u = T0 * me / G;
-    const unsigned long long end = T0 * (me + 1) / G;
-    Cursor cur{0, 0, 0};
+    if (tid == 0) ws.slots[2 * me].parts = ws.slots[2 * me + 1].parts = 0;
+    unsigned long long u = total * me / G;
+    const unsigned long long end = total * (me + 1) / G;
     bool first = true;
-    if (tid < 2) ws.slots[2 * me + tid].parts = 0;
-    __syncthreads();
     while (u < end) {
-      cur = find_sequence(a, S, cur, (long long)(u / HT), false);
-      const int np = seq_pages(a, cur.b);
-      const unsigned long long rem = u - (unsigned long long)cur.units * HT;
-      const int j = (int)(rem / np), p0 = (int)(rem % np);
+      plan_find(a, S, (long long)(u / HT), at);
+      const int nu = seq_units(at.np);
+      const unsigned long long rem = u - (unsigned long long)at.units * HT;
+      const int j = (int)(rem / nu), p0 = (int)(rem % nu);
       const unsigned long long task = u - p0;              // first unit of the task
-      const int p1 = (int)min((unsigned long long)np, p0 + (end - u));
-      const bool part = p0 > 0 || p1 < np;
-      const int slot = 2 * me + (first ? 0 : 1);
-      if (p0 == 0 && part && tid == 0) {
-        // the block that holds the task's last unit x: the largest i with T0 i / G <= x
-        const int last = (int)(((task + np) * G - 1) / T0);
-        ws.slots[slot] = {cur.b, j, last - me + 1, 2};
+      const int step = (int)min((unsigned long long)(nu - p0), end - u);
+      const int p1 = min(at.np, p0 + step);
+      if (p0 < at.np) {                    // else the run begins behind the task's last page
+        const bool part = p0 > 0 || p1 < at.np;
+        const int slot = 2 * me + (first ? 0 : 1);
+        if (p0 == 0 && part && tid == 0) {
+          // the block that holds the task's last page, unit x: the largest i with total i / G <= x
+          const int last = (int)(((task + at.np) * G - 1) / total);
+          ws.slots[slot] = {at.b, j, last - me + 1, 2};
+        }
+        B::segment(a, smem, at.b, j, p0, p1, part ? ws.data + slot * attn_slot_floats(D) : nullptr);
       }
-      B::segment(a, smem, cur.b, j, p0, p1, part ? ws.data + slot * attn_slot_floats(D) : nullptr);
       first = false;
-      u += p1 - p0;
+      u += step;
     }
   }
 }
@@ -495,49 +700,76 @@ constexpr int kMergeThreads = 256;
 constexpr int kMaxSlots = 1024;
 
 // Merges the parts of split tasks.  Every block lists the first slots, then
-// takes (task, head) pairs in turn: 8 parts at a time, a warp each.
+// takes (task, head) pairs in turn: a warp each eighth part, kBatch of them in
+// flight (one load after the other, 76 parts of a 256K context took 11 us).
 template <int D, class T>
 __global__ void __launch_bounds__(kMergeThreads) kvq_merge_kernel(AttnArgs a, int blocks) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  constexpr int V = D / 32;                // dims of a lane
-  __shared__ int list[kMaxSlots], counts[8];
+  constexpr int V = D / 32, kBatch = 5;    // dims of a lane
+  __shared__ int list[kMaxSlots], n_list;
   __shared__ float so[8][D], sr[8], sl[8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const AttnWs ws = attn_ws(a.ws, blocks);
   const int count = *ws.count;
-  int n = 0;
-  for (int s0 = 0; s0 < count; s0 += kMergeThreads) {
-    const int s = s0 + tid;
-    const bool is = s < count && ws.slots[s].parts > 0;
-    const unsigned m = __ballot_sync(0xffffffffu, is);
-    if (lane == 0) counts[warp] = __popc(m);
-    __syncthreads();
-    int at = n;
-    for (int w = 0; w < 8; w++) {
-      if (w < warp) at += counts[w];
-      n += counts[w];
+  if (warp == 0) {
+    // the first slots in order
+    int n = 0;
+#pragma unroll 1
+    for (int s0 = 0; s0 < count; s0 += 32 * 10) {
+      bool is[10];
+#pragma unroll
+      for (int i = 0; i < 10; i++) {
+        const int s = s0 + 32 * i + lane;
+        is[i] = s < count && ws.slots[s].parts > 0;
+      }
+#pragma unroll
+      for (int i = 0; i < 10; i++) {
+        const unsigned m = __ballot_sync(0xffffffffu, is[i]);
+        if (is[i]) list[n + __popc(m & ((1u << lane) - 1))] = s0 + 32 * i + lane;
+        n += __popc(m);
+      }
     }
-    if (is) list[at + __popc(m & ((1u << lane) - 1))] = s;
-    __syncthreads();
+    if (lane == 0) n_list = n;
   }
-  for (int w = blockIdx.x; w < n * 8; w += gridDim.x) {
+  __syncthreads();
+  for (int w = blockIdx.x; w < n_list * 8; w += gridDim.x) {
     const int s = list[w / 8], h = w % 8;
     const AttnSlot t = ws.slots[s];
     if (h >= min(8, a.grp - t.j % a.tiles * 8)) continue;
     float m = -FLT_MAX, den = 0.f, num[V];
 #pragma unroll
     for (int k = 0; k < V; k++) num[k] = 0.f;
-    for (int i = warp; i < t.parts; i += 8) {
-      const int slot = i == 0 ? s : t.step == 1 ? s + i : (s & ~1) + 2 * i;
-      const float* p = ws.data + slot * attn_slot_floats(D);
-      const float r = p[8 * D + h], l = p[8 * D + 8 + h];
-      float o[V];
+    for (int i0 = warp; i0 < t.parts; i0 += 8 * kBatch) {
+      float r[kBatch], l[kBatch], o[kBatch][V];
 #pragma unroll
-      for (int k = 0; k < V; k++) o[k] = p[h * D + lane + 32 * k];
-      const float mn = fmaxf(m, r), ka = ex2(m - mn), kb = ex2(r - mn);
-      den = den * ka + l * kb;
+      for (int u = 0; u < kBatch; u++) {
+        const int i = i0 + 8 * u;
+        const int slot = i == 0 ? s : t.step == 1 ? s + i : (s & ~1) + 2 * i;
+        const float* p = ws.data + slot * attn_slot_floats(D);
+        r[u] = -FLT_MAX, l[u] = 0.f;
 #pragma unroll
-      for (int k = 0; k < V; k++) num[k] = num[k] * ka + o[k] * kb;
+        for (int k = 0; k < V; k++) o[u][k] = 0.f;
+        if (i < t.parts) {
+          r[u] = p[8 * D + h];
+          l[u] = p[8 * D + 8 + h];
+#pragma unroll
+          for (int k = 0; k < V; k++) o[u][k] = p[h * D + lane + 32 * k];
+        }
+      }
+      float mn = m;
+#pragma unroll
+      for (int u = 0; u < kBatch; u++) mn = fmaxf(mn, r[u]);
+      const float keep = ex2(m - mn);
+      den *= keep;
+#pragma unroll
+      for (int k = 0; k < V; k++) num[k] *= keep;
+#pragma unroll
+      for (int u = 0; u < kBatch; u++) {
+        const float c = ex2(r[u] - mn);
+        den = fmaf(l[u], c, den);
+#pragma unroll
+        for (int k = 0; k < V; k++) num[k] = fmaf(o[u][k], c, num[k]);
+      }
       m = mn;
     }
 #pragma unroll
@@ -546,7 +778,9 @@ __global__ void __launch_bounds__(kMergeThreads) kvq_merge_kernel(AttnArgs a, in
     __syncthreads();
     if (tid < D) {
       float M = -FLT_MAX, sn = 0.f, sd = 0.f;
+#pragma unroll
       for (int i = 0; i < 8; i++) M = fmaxf(M, sr[i]);
+#pragma unroll
       for (int i = 0; i < 8; i++) {
         const float k = ex2(sr[i] - M);
         sn = fmaf(k, so[i][tid], sn);
@@ -586,10 +820,8 @@ int check_rows(const mk_kv_rows* r, const mk_kvq_cache* c, int n, int unit, cons
 
 Cache cache_of(const mk_kvq_cache* c) { return Cache{(uint8_t*)c->pool, c->status, c->num_pages, c->n_kv_heads}; }
 
-Rows rows_of(const mk_kv_rows* r, int unit) {
-  // a row index counts tokens with unit 1: page and row strides then agree
-  return Rows{r->k, r->v, unit == 1 ? r->row_stride * kKvqPage : r->page_stride, r->row_stride, r->head_stride,
-              r->count};
+dim3 copy_grid(int n, int per_block, const mk_kvq_cache* c) {
+  return dim3((unsigned)(((long long)n + per_block - 1) / per_block), (unsigned)c->n_kv_heads);
 }
 
 int sm_count() {
@@ -664,22 +896,24 @@ int mk_kvq_write(const mk_kvq_cache* c, const mk_kv_rows* src, const int32_t* sr
   int rc = check_cache(c);
   if (!rc) rc = check_rows(src, c, n, unit, src_index, dst_index);
   if (rc || n == 0) return rc;
-  const int sms = sm_count();
-  if (!sms) return MK_ERR_CUDA;
-  const int tokens = n * unit;
-  const long long threads = (long long)tokens * c->n_kv_heads * (c->head_dim / 4);
-  const int blocks = (int)std::min<long long>((threads + 255) / 256, sms * 8ll);
   const Cache cc = cache_of(c);
-  const Rows rr = rows_of(src, unit);
+  const Rows rr{src->k, src->v, src->page_stride, src->row_stride, src->head_stride, src->count};
   cudaStream_t st = (cudaStream_t)stream;
-  if (c->head_dim == 128)
-    src->type == MK_TYPE_BF16
-        ? kvq_write_kernel<128, uint16_t><<<blocks, 256, 0, st>>>(cc, rr, src_index, dst_index, tokens, unit)
-        : kvq_write_kernel<128, float><<<blocks, 256, 0, st>>>(cc, rr, src_index, dst_index, tokens, unit);
-  else
-    src->type == MK_TYPE_BF16
-        ? kvq_write_kernel<64, uint16_t><<<blocks, 256, 0, st>>>(cc, rr, src_index, dst_index, tokens, unit)
-        : kvq_write_kernel<64, float><<<blocks, 256, 0, st>>>(cc, rr, src_index, dst_index, tokens, unit);
+#define WRITE(D, T)                                                                                               \
+  do {                                                                                                            \
+    if (unit == 1)                                                                                                \
+      kvq_write_kernel<D, T><<<copy_grid(n, TokenLane<D>::kTokens, c), kCopyThreads, 0, st>>>(cc, rr, src_index,  \
+                                                                                              dst_index, n);      \
+    else                                                                                                          \
+      kvq_write_pages_kernel<D, T><<<copy_grid(n, kCopyThreads / 32, c), kCopyThreads, 0, st>>>(cc, rr, src_index, \
+                                                                                                dst_index, n);    \
+  } while (0)
+  if (c->head_dim == 128) {
+    if (src->type == MK_TYPE_BF16) WRITE(128, uint16_t); else WRITE(128, float);
+  } else {
+    if (src->type == MK_TYPE_BF16) WRITE(64, uint16_t); else WRITE(64, float);
+  }
+#undef WRITE
   return launched();
 }
 
@@ -688,22 +922,24 @@ int mk_kvq_read(const mk_kvq_cache* c, const int32_t* src_index, const mk_kv_row
   int rc = check_cache(c);
   if (!rc) rc = check_rows(dst, c, n, unit, dst_index, src_index);
   if (rc || n == 0) return rc;
-  const int sms = sm_count();
-  if (!sms) return MK_ERR_CUDA;
-  const int tokens = n * unit;
-  const long long threads = (long long)tokens * c->n_kv_heads * (c->head_dim / 4);
-  const int blocks = (int)std::min<long long>((threads + 255) / 256, sms * 8ll);
   const Cache cc = cache_of(c);
-  const Rows rr = rows_of(dst, unit);
+  const Rows rr{dst->k, dst->v, dst->page_stride, dst->row_stride, dst->head_stride, dst->count};
   cudaStream_t st = (cudaStream_t)stream;
-  if (c->head_dim == 128)
-    dst->type == MK_TYPE_BF16
-        ? kvq_read_kernel<128, uint16_t><<<blocks, 256, 0, st>>>(cc, src_index, rr, dst_index, tokens, unit)
-        : kvq_read_kernel<128, float><<<blocks, 256, 0, st>>>(cc, src_index, rr, dst_index, tokens, unit);
-  else
-    dst->type == MK_TYPE_BF16
-        ? kvq_read_kernel<64, uint16_t><<<blocks, 256, 0, st>>>(cc, src_index, rr, dst_index, tokens, unit)
-        : kvq_read_kernel<64, float><<<blocks, 256, 0, st>>>(cc, src_index, rr, dst_index, tokens, unit);
+#define READ(D, T)                                                                                                \
+  do {                                                                                                            \
+    if (unit == 1)                                                                                                \
+      kvq_read_kernel<D, T><<<copy_grid(n, TokenLane<D>::kTokens, c), kCopyThreads, 0, st>>>(cc, src_index, rr,   \
+                                                                                             dst_index, n);       \
+    else                                                                                                          \
+      kvq_read_pages_kernel<D, T><<<copy_grid(n, kCopyThreads / 32, c), kCopyThreads, 0, st>>>(cc, src_index, rr, \
+                                                                                               dst_index, n);     \
+  } while (0)
+  if (c->head_dim == 128) {
+    if (dst->type == MK_TYPE_BF16) READ(128, uint16_t); else READ(128, float);
+  } else {
+    if (dst->type == MK_TYPE_BF16) READ(64, uint16_t); else READ(64, float);
+  }
+#undef READ
   return launched();
 }
 

@@ -88,11 +88,9 @@ __device__ __forceinline__ KvqScale kvq_scale(float lo, float hi) {
   return s;
 }
 
-// code of x: (x - low) / step to the nearest integer, ties to even, the
-// difference rounded to fp32.  diff * inv is within 4e-6 of the quotient, so
-// away from the half-way points its rounding is the right one; next to one
-// the sign of diff - (k + 1/2) step decides, which one FMA gives exactly
-// ((k + 1/2) step has at most 13 bits).
+// code of x where the quotient may be next to a half-way point k + 1/2: the
+// sign of diff - (k + 1/2) step decides, which one FMA gives exactly ((k + 1/2)
+// step has at most 13 bits)
 __device__ __forceinline__ uint32_t kvq_code(float x, const KvqScale& s) {
   const float diff = x - s.low;
   const float q = diff * s.inv;
@@ -102,14 +100,48 @@ __device__ __forceinline__ uint32_t kvq_code(float x, const KvqScale& s) {
     const float r = fmaf(-(k + 0.5f), s.step, diff);
     c = r > 0.f || (r == 0.f && ((int)k & 1)) ? k + 1.f : k;
   }
-  return s.inv == 0.f ? 0u : (uint32_t)fminf(c, 15.f);
+  return (uint32_t)c;
+}
+
+// Codes of eight values, nibble i of the word that of x[i]: (x - low) / step to
+// the nearest integer, ties to even, the difference rounded to fp32.  Adding
+// 1.5 2^23 rounds diff * inv to an integer in the low mantissa bits; eight such
+// patterns, shifted and added, leave the codes and one constant.  diff * inv is
+// within 3e-6 of the quotient, so only a value within 1e-5 of a half-way point
+// needs the exact decision.
+__device__ __forceinline__ uint32_t kvq_codes(const float* x, const KvqScale& s) {
+  constexpr float kMagic = 12582912.f;     // 0x4b400000
+  float worst = 0.f;
+  uint32_t word = 0;
+#pragma unroll
+  for (int i = 7; i >= 0; i--) {
+    const float q = (x[i] - s.low) * s.inv;
+    const float t = q + kMagic;
+    worst = fmaxf(worst, fabsf(q - (t - kMagic)));
+    word = word * 16u + __float_as_uint(t);
+  }
+  word -= 0x4b400000u * 0x11111111u;
+  if (worst > 0.49999f) {
+    word = 0;
+#pragma unroll
+    for (int i = 7; i >= 0; i--) word = word * 16u + kvq_code(x[i], s);
+  }
+  return s.inv == 0.f ? 0u : word;
 }
 
 // ---------------------------------------------------------------- attention
 
-// D += A B, m16n8k16, FP16 in, fp32 out
+// D = A B, m16n8k16, FP16 in, fp32 out
+__device__ __forceinline__ void mma_f16_first(float* d, const uint32_t* a, const uint32_t* b) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.f));
+}
+
+// D += A B
 __device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, const uint32_t* b) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
@@ -129,15 +161,9 @@ __device__ __forceinline__ uint32_t add_h2(uint32_t a, uint32_t b) {
 
 __device__ __forceinline__ float ex2(float x) {
   float r;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ float lg2(float x) {
-  float r;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
 // One warp's share of the attention of up to 8 query heads to one KV head,
 // page by page.
 //   x_t  = scale sum_i q_i k_ti = f sum_g step_tg (sum_{i in g} q'_i code_ti)
@@ -149,16 +175,16 @@ __device__ __forceinline__ float lg2(float x) {
 //          group's range and cancel in a mean over many tokens: 8 % off at
 //          256K tokens, measured.)
 // S^T = K Q^T takes the page's 16 tokens as M and the heads as N, O^T = V^T
-// P'^T the dims as M, 16 dims a tile, so no row of M is padding.  The weight
-// of a value code is P'_tg = p_t step_tg = 2^(x_t + log2 step_tg), kept per
-// group against its own running reference n_g: whatever the sizes of the
-// steps, the largest weight seen stays between 2^8 and 2^15, so that FP16
-// holds 11 bits of every weight down to 2^-22 of it.  A reference moves only
-// when a weight passes 2^15 (one vote a page); the sums l and sum p mid keep
-// theirs, r.
-// QT = 2 / PT = 2 split q and P' into FP16 high and low halves (22 bits) for
-// fp32 activations, with the key codes centred too; with one half each P' is rounded to 11 bits, an eighth of
-// a BF16 result's own rounding, and BF16 q is exact.
+// W^T the dims as M, 16 dims a tile, so no row of M is padding.  The weight of
+// a value code is w_tg = p_t step_tg sc_g with p_t = 2^(x_t - r).  The reference
+// r and each group's power of two sc_g move only when a p or w passes 2^15
+// (one vote a page), and then so that the largest seen is 2^8: whatever the
+// sizes of scores and steps, FP16 holds 11 bits of every weight down to 2^-22
+// of the largest.
+// QT = 2 / PT = 2 split q and w into FP16 high and low halves (22 bits) for
+// fp32 activations, with the key codes centred too.  With one half each w is
+// rounded to 11 bits, an eighth of a BF16 result's own rounding, and BF16 q is
+// exact.
 template <int D, int QT, int PT>
 struct KvqAttn {
   using R = KvqRec<D>;
@@ -166,18 +192,13 @@ struct KvqAttn {
   static constexpr int NW = 2 * NG;        // code words of a lane per token / token pair
   static constexpr int NT = 2 * NW;        // k-steps of S = 16-dim tiles of O
 
-  struct Page {
-    uint32_t k[2][NW];                     // keys of tokens gl, gl + 8
-    uint32_t v[2][NW];                     // values of token pairs cq, cq + 4
-    uint32_t ks[2][NG], vs[2][NG];         // scales of tokens gl, gl + 8
-  };
-
   uint32_t q[QT][NT][2];
   float f[2], sq[NG][2];                   // heads 2 cq, 2 cq + 1
-  float r[2], l[2], n[NG][2], om[NG][2];
+  float r[2], l[2], sc[NG][2], om[NG][2];
   float o[NT][4];
 
-  static constexpr float kHead = 8.f, kTop = 15.f;   // log2 of the weights' headroom and limit
+  // the largest weight after the references move (log2, and itself), the limit before; sc's own limit
+  static constexpr float kHead = 8.f, kHeadW = 256.f, kTop = 32768.f, kScMax = 0x1p120f;
 
   template <int N>
   static __device__ __forceinline__ void load_words(uint32_t* dst, const uint8_t* p) {
@@ -192,14 +213,37 @@ struct KvqAttn {
     }
   }
 
-  static __device__ __forceinline__ void load(Page& pg, const uint8_t* rec, int lane) {
+  // Place of the record's 16-byte chunk c in a copy of it in shared memory: the
+  // value chunks of four token pairs side by side, so that the eight lanes of
+  // one 128-byte read (two columns, four pairs) take eight neighbouring chunks
+  // and not eight that share their banks.
+  static __device__ __forceinline__ int staged(int c) {
+    constexpr int V0 = R::kVal / 16, V1 = R::kKeyScale / 16, W = D / 16;   // value chunks, chunks of a pair
+    if (c < V0 || c >= V1) return c;
+    const int v = c - V0, pair = v / W, col = v % W;
+    return V0 + (pair / 4) * (4 * W) + col * 4 + pair % 4;
+  }
+
+  // a lane's part of a record's keys or values (tokens gl, gl + 8; token pairs
+  // cq, cq + 4); STAGED: of a copy in the order of staged()
+  struct Half {
+    uint32_t w[2][NW], sc[2][NG];          // codes; scales of tokens gl, gl + 8
+  };
+  static __device__ __forceinline__ void load_keys(Half& k, const uint8_t* rec, int lane) {
+#pragma unroll
+    for (int e = 0; e < 2; e++) {
+      load_words<NW>(k.w[e], rec + ((lane >> 2) + 8 * e) * (D / 2) + (lane & 3) * (8 * NG));
+      load_words<NG>(k.sc[e], rec + R::kKeyScale + ((lane >> 2) + 8 * e) * (4 * NG));
+    }
+  }
+  template <bool STAGED>
+  static __device__ __forceinline__ void load_values(Half& v, const uint8_t* rec, int lane) {
     const int gl = lane >> 2, cq = lane & 3;
 #pragma unroll
     for (int e = 0; e < 2; e++) {
-      load_words<NW>(pg.k[e], rec + (gl + 8 * e) * (D / 2) + cq * (8 * NG));
-      load_words<NW>(pg.v[e], rec + R::kVal + (cq + 4 * e) * D + gl * (8 * NG));
-      load_words<NG>(pg.ks[e], rec + R::kKeyScale + (gl + 8 * e) * (4 * NG));
-      load_words<NG>(pg.vs[e], rec + R::kValScale + (gl + 8 * e) * (4 * NG));
+      load_words<NW>(v.w[e], rec + R::kVal + e * 4 * D +
+                                 (STAGED ? (gl * NG / 2 * 4 + cq) * 16 + gl * NG % 2 * 8 : cq * D + gl * (8 * NG)));
+      load_words<NG>(v.sc[e], rec + R::kValScale + (gl + 8 * e) * (4 * NG));
     }
   }
 
@@ -251,7 +295,7 @@ struct KvqAttn {
 #pragma unroll
       for (int g = 0; g < NG; g++) {
         sq[g][h] = __shfl_sync(0xffffffffu, sum[g] * scale_log2, src);
-        n[g][h] = -FLT_MAX;
+        sc[g][h] = kScMax;
         om[g][h] = 0.f;
       }
       r[h] = -FLT_MAX;
@@ -279,38 +323,40 @@ struct KvqAttn {
     if constexpr (PT == 1) {
       mma_f16(o, c, b[0]);
     } else {
-      float t[4] = {0.f, 0.f, 0.f, 0.f};
-      mma_f16(t, c, b[1]);
+      float t[4];
+      mma_f16_first(t, c, b[1]);
       mma_f16(t, c, b[0]);
 #pragma unroll
       for (int e = 0; e < 4; e++) o[e] += t[e];
     }
   }
 
-  // tokens [0, valid) of a page; valid is the same in every lane, 1..16
-  __device__ __forceinline__ void page(Page& pg, int valid, int lane) {
+  // tokens [0, valid) of a page; valid is the same in every lane, 1 or more
+  template <bool STAGED>
+  __device__ __forceinline__ void page(const uint8_t* rec, int valid, int lane) {
     constexpr uint32_t M0 = 0x000f000fu, M1 = 0x00f000f0u;
     const int gl = lane >> 2;
+    Half ky;
+    load_keys(ky, rec, lane);
     float acc[NG][4];
 #pragma unroll
     for (int g = 0; g < NG; g++) {
-      acc[g][0] = acc[g][1] = acc[g][2] = acc[g][3] = 0.f;
-      [[maybe_unused]] float low[4] = {0.f, 0.f, 0.f, 0.f};
+      [[maybe_unused]] float low[4];
 #pragma unroll
       for (int w = 0; w < 2; w++) {
         const int j = 2 * g + w;
-        const uint32_t a = pg.k[0][j], b = pg.k[1][j], a8 = a >> 8, b8 = b >> 8;
+        const uint32_t a = ky.w[0][j], b = ky.w[1][j], a8 = a >> 8, b8 = b >> 8;
         if constexpr (QT == 2) {
           const uint32_t c0[4] = {centred(a), centred(b), centred16(a), centred16(b)};
           const uint32_t c1[4] = {centred(a8), centred(b8), centred16(a8), centred16(b8)};
-          mma_f16(low, c0, q[1][2 * j]);
+          w == 0 ? mma_f16_first(low, c0, q[1][2 * j]) : mma_f16(low, c0, q[1][2 * j]);
           mma_f16(low, c1, q[1][2 * j + 1]);
-          mma_f16(acc[g], c0, q[0][2 * j]);
+          w == 0 ? mma_f16_first(acc[g], c0, q[0][2 * j]) : mma_f16(acc[g], c0, q[0][2 * j]);
           mma_f16(acc[g], c1, q[0][2 * j + 1]);
         } else {
           const uint32_t c0[4] = {a & M0, b & M0, a & M1, b & M1};
           const uint32_t c1[4] = {a8 & M0, b8 & M0, a8 & M1, b8 & M1};
-          mma_f16(acc[g], c0, q[0][2 * j]);
+          w == 0 ? mma_f16_first(acc[g], c0, q[0][2 * j]) : mma_f16(acc[g], c0, q[0][2 * j]);
           mma_f16(acc[g], c1, q[0][2 * j + 1]);
         }
       }
@@ -318,6 +364,8 @@ struct KvqAttn {
 #pragma unroll
         for (int e = 0; e < 4; e++) acc[g][e] += low[e];
     }
+    Half vl;
+    load_values<STAGED>(vl, rec, lane);
     float x[2][2];                         // [token gl / gl + 8][head]
 #pragma unroll
     for (int e = 0; e < 2; e++)
@@ -326,9 +374,10 @@ struct KvqAttn {
         float dot = 0.f, off = 0.f;
 #pragma unroll
         for (int g = 0; g < NG; g++) {
-          const float step = bf16lo(pg.ks[e][g]), base = bf16hi(pg.ks[e][g]);
-          dot = fmaf(step, acc[g][2 * e + h], dot);
-          off = fmaf(QT == 2 ? fmaf(8.f, step, base) : base, sq[g][h], off);
+          const float step = bf16lo(ky.sc[e][g]);
+          const float base = QT == 2 ? fmaf(8.f, step, bf16hi(ky.sc[e][g])) : bf16hi(ky.sc[e][g]);
+          dot = g == 0 ? step * acc[g][2 * e + h] : fmaf(step, acc[g][2 * e + h], dot);
+          off = g == 0 ? base * sq[g][h] : fmaf(base, sq[g][h], off);
         }
         x[e][h] = fmaf(dot, f[h], off);
       }
@@ -339,38 +388,36 @@ struct KvqAttn {
         if (gl + 8 * e >= valid) {
           x[e][0] = x[e][1] = -INFINITY;
 #pragma unroll
-          for (int g = 0; g < NG; g++) pg.vs[e][g] = 0u;
+          for (int g = 0; g < NG; g++) vl.sc[e][g] = 0u;
         }
     }
-    float ls[2][NG], mid[2][NG];
+    float p[2][2], w[NG][2][2];
+    auto weights = [&]() {
 #pragma unroll
-    for (int e = 0; e < 2; e++)
+      for (int e = 0; e < 2; e++)
 #pragma unroll
-      for (int g = 0; g < NG; g++) {
-        ls[e][g] = lg2(bf16lo(pg.vs[e][g]));
-        mid[e][g] = fmaf(8.f, bf16lo(pg.vs[e][g]), bf16hi(pg.vs[e][g]));
-      }
-    float top = -INFINITY;
+        for (int h = 0; h < 2; h++) {
+          p[e][h] = ex2(x[e][h] - r[h]);
+#pragma unroll
+          for (int g = 0; g < NG; g++) w[g][e][h] = p[e][h] * bf16lo(vl.sc[e][g]) * sc[g][h];
+        }
+    };
+    weights();
+    float top = 0.f;
 #pragma unroll
     for (int e = 0; e < 2; e++)
 #pragma unroll
       for (int h = 0; h < 2; h++) {
-        top = fmaxf(top, x[e][h] - r[h]);
+        top = fmaxf(top, p[e][h]);
 #pragma unroll
-        for (int g = 0; g < NG; g++) top = fmaxf(top, x[e][h] + ls[e][g] - n[g][h]);
+        for (int g = 0; g < NG; g++) top = fmaxf(top, w[g][e][h]);
       }
     if (__any_sync(0xffffffffu, top > kTop)) {
 #pragma unroll
       for (int h = 0; h < 2; h++) {
-        float m = fmaxf(x[0][h], x[1][h]), mg[NG];
+        float m = fmaxf(x[0][h], x[1][h]);
 #pragma unroll
-        for (int g = 0; g < NG; g++) mg[g] = fmaxf(x[0][h] + ls[0][g], x[1][h] + ls[1][g]);
-#pragma unroll
-        for (int sh = 4; sh < 32; sh <<= 1) {
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, sh));
-#pragma unroll
-          for (int g = 0; g < NG; g++) mg[g] = fmaxf(mg[g], __shfl_xor_sync(0xffffffffu, mg[g], sh));
-        }
+        for (int sh = 4; sh < 32; sh <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, sh));
         const float rn = fmaxf(r[h], m - kHead);
         const float al = ex2(r[h] - rn);
         r[h] = rn;
@@ -378,46 +425,49 @@ struct KvqAttn {
 #pragma unroll
         for (int g = 0; g < NG; g++) {
           om[g][h] *= al;
-          const float nn = fmaxf(n[g][h], mg[g] - kHead);
-          const float be = ex2(n[g][h] - nn);
-          n[g][h] = nn;
+          float t = fmaxf(ex2(x[0][h] - rn) * bf16lo(vl.sc[0][g]), ex2(x[1][h] - rn) * bf16lo(vl.sc[1][g]));
 #pragma unroll
-          for (int t = 0; t < 4; t++) {
-            o[4 * g + t][h] *= be;
-            o[4 * g + t][2 + h] *= be;
+          for (int sh = 4; sh < 32; sh <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, sh));
+          // at most what keeps the old weights where they were, and this page's within the headroom; a power
+          // of two (the exponent alone), so that it rounds nothing
+          float s = fminf(fminf(sc[g][h] / al, kHeadW / t), kScMax);
+          s = __uint_as_float(__float_as_uint(s) & 0x7f800000u);
+          const float be = al == 0.f ? 0.f : al * (s / sc[g][h]);
+          sc[g][h] = s;
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            o[4 * g + i][h] *= be;
+            o[4 * g + i][2 + h] *= be;
           }
         }
       }
+      weights();
     }
 #pragma unroll
     for (int h = 0; h < 2; h++) {
-      const float p0 = ex2(x[0][h] - r[h]), p1 = ex2(x[1][h] - r[h]);
-      l[h] += p0 + p1;
+      l[h] += p[0][h] + p[1][h];
 #pragma unroll
-      for (int g = 0; g < NG; g++) om[g][h] = fmaf(p1, mid[1][g], fmaf(p0, mid[0][g], om[g][h]));
+      for (int g = 0; g < NG; g++)
+        om[g][h] = fmaf(p[1][h], fmaf(8.f, bf16lo(vl.sc[1][g]), bf16hi(vl.sc[1][g])),
+                        fmaf(p[0][h], fmaf(8.f, bf16lo(vl.sc[0][g]), bf16hi(vl.sc[0][g])), om[g][h]));
     }
 #pragma unroll
     for (int g = 0; g < NG; g++) {
-      float w[2][2];
-#pragma unroll
-      for (int e = 0; e < 2; e++)
-#pragma unroll
-        for (int h = 0; h < 2; h++) w[e][h] = ex2(x[e][h] + ls[e][g] - n[g][h]);
-      // P'^T as the B operand: the score tiles [token][head] transposed
+      // W^T as the B operand: the score tiles [token][head] transposed
       uint32_t b[PT][2];
 #pragma unroll
       for (int e = 0; e < 2; e++) {
-        const uint32_t hi = pack_h2(w[e][0], w[e][1]);
+        const uint32_t hi = pack_h2(w[g][e][0], w[g][e][1]);
         b[0][e] = movm_trans(hi);
         if constexpr (PT == 2) {
           const float2 hv = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-          b[1][e] = movm_trans(pack_h2(w[e][0] - hv.x, w[e][1] - hv.y));
+          b[1][e] = movm_trans(pack_h2(w[g][e][0] - hv.x, w[g][e][1] - hv.y));
         }
       }
 #pragma unroll
       for (int u = 0; u < 2; u++) {
         const int j = 2 * g + u;
-        const uint32_t a = pg.v[0][j], c = pg.v[1][j], a8 = a >> 8, c8 = c >> 8;
+        const uint32_t a = vl.w[0][j], c = vl.w[1][j], a8 = a >> 8, c8 = c >> 8;
         const uint32_t c0[4] = {centred(a), centred16(a), centred(c), centred16(c)};
         const uint32_t c1[4] = {centred(a8), centred16(a8), centred(c8), centred16(c8)};
         add_tile(o[2 * j], c0, b);
@@ -441,11 +491,11 @@ struct KvqAttn {
     for (int g = 0; g < NG; g++)
 #pragma unroll
       for (int h = 0; h < 2; h++) {
-        const float sc = ex2(n[g][h] - r[h]);
+        const float un = 1.f / sc[g][h];
 #pragma unroll
         for (int t = 0; t < 4; t++) {      // tile t: dims 2 t and (16 times its codes) 2 t + 1
-          v[g][h][2 * t] = fmaf(o[4 * g + t][h], sc, om[g][h]);
-          v[g][h][2 * t + 1] = fmaf(o[4 * g + t][2 + h] * 0.0625f, sc, om[g][h]);
+          v[g][h][2 * t] = fmaf(o[4 * g + t][h], un, om[g][h]);
+          v[g][h][2 * t + 1] = fmaf(o[4 * g + t][2 + h] * 0.0625f, un, om[g][h]);
         }
       }
   }

@@ -54,7 +54,8 @@ class QuantCache:
         if pool.device.type != "cuda":
             raise ValueError(f"4-bit cache: the pool is on {pool.device}, not on a GPU")
         self.pool, self.n_kv_heads, self.head_dim = pool, n_kv_heads, head_dim
-        self._dev, self._ws_bytes = pool.device.index, None
+        self._dev, self._ws_bytes = pool.get_device(), None
+        self._inner = {1: (n_kv_heads, head_dim), PAGE_SIZE: (n_kv_heads, PAGE_SIZE, head_dim)}
         self.status = torch.zeros(1, dtype=torch.int32, device=pool.device)
         self._c = mk.mk_kvq_cache(pool=pool.data_ptr(), num_pages=pool.shape[0], n_kv_heads=n_kv_heads,
                                   head_dim=head_dim, status=self.status.data_ptr())
@@ -74,40 +75,40 @@ class QuantCache:
     # ------------------------------------------------------------ arguments
 
     def _index(self, t, name, n=None):
-        if t.dtype != torch.int32 or t.dim() != 1 or t.device != self.pool.device \
+        if t.dtype is not torch.int32 or t.dim() != 1 or t.get_device() != self._dev \
                 or (n is not None and t.shape[0] != n):
             raise ValueError(f"{name}: an int32 vector{f' of {n}' if n is not None else ''} on {self.pool.device}, "
                              f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-        return t.contiguous()
+        return t if t.is_contiguous() else t.contiguous()
 
     def _rows(self, k, v, unit, out):
         """mk_kv_rows of k and v, and the tensors it points into."""
-        shape = (self.n_kv_heads, self.head_dim) if unit == 1 else (self.n_kv_heads, PAGE_SIZE, self.head_dim)
+        inner, shape = self._inner[unit], k.shape
         for name, t in (("k", k), ("v", v)):
-            if t.dtype not in _TYPES or t.dtype != k.dtype:
+            if t.dtype not in _TYPES or t.dtype is not k.dtype:
                 raise ValueError(f"{name}: BF16 or fp32, k and v alike, got {t.dtype}")
-            if t.device != self.pool.device or t.shape[1:] != shape or t.shape[0] != k.shape[0]:
-                raise ValueError(f"{name}: [n, {', '.join(map(str, shape))}] on {self.pool.device}, "
+            if t.get_device() != self._dev or t.shape[1:] != inner or t.shape != shape:
+                raise ValueError(f"{name}: [n, {', '.join(map(str, inner))}] on {self.pool.device}, "
                                  f"got {tuple(t.shape)} on {t.device}")
-        q = 16 // k.element_size()
-        s = k.stride()
-        if s != v.stride() or s[-1] != 1 or any(x % q for x in s[:-1]) or k.data_ptr() % 16 or v.data_ptr() % 16:
+        q = 8 if k.dtype is torch.bfloat16 else 4
+        s, kp, vp = k.stride(), k.data_ptr(), v.data_ptr()
+        if s != v.stride() or s[-1] != 1 or any(x % q for x in s[:-1]) or (kp | vp) & 15:
             if out:
                 raise ValueError("k, v: rows of consecutive elements at 16-byte strides, k and v alike")
             k, v = (t.clone(memory_format=torch.contiguous_format) for t in (k, v))
-            s = k.stride()
-        return mk.mk_kv_rows(k=k.data_ptr(), v=v.data_ptr(), type=_TYPES[k.dtype], count=k.shape[0], page_stride=s[0],
-                             row_stride=s[0] if unit == 1 else s[2], head_stride=s[1]), (k, v)
+            s, kp, vp = k.stride(), k.data_ptr(), v.data_ptr()
+        return mk.mk_kv_rows(kp, vp, _TYPES[k.dtype], shape[0], s[0], s[0] if unit == 1 else s[2], s[1]), (k, v)
 
     def _dense(self, t):
         s = t.stride()
-        return s[2] == 1 and s[1] == self.head_dim and s[0] * t.element_size() % 16 == 0 and t.data_ptr() % 16 == 0
+        return s[2] == 1 and s[1] == self.head_dim and s[0] % (8 if t.dtype is torch.bfloat16 else 4) == 0 \
+            and t.data_ptr() % 16 == 0
 
     def _run(self, fn, stream, *args):
         """fn(stream pointer, ...) with the cache's device and the call's stream current, for torch's own
         allocations and copies too."""
         if stream is None and torch.cuda.current_device() == self._dev:
-            return fn(torch.cuda.current_stream().cuda_stream, *args)
+            return fn(torch._C._cuda_getCurrentRawStream(self._dev), *args)   # current_stream() costs 2 us more
         with torch.cuda.device(self._dev), torch.cuda.stream(stream):    # None: the device's current one
             return fn(torch.cuda.current_stream().cuda_stream, *args)
 
@@ -156,34 +157,36 @@ class QuantCache:
     def _read_rows(self, st, slots, dtype):
         if dtype not in _TYPES:
             raise ValueError(f"dtype: BF16 or fp32, got {dtype}")
-        k, v = torch.empty((2, slots.numel(), self.n_kv_heads, self.head_dim), dtype=dtype, device=self.pool.device)
+        k = torch.empty((slots.shape[0], *self._inner[1]), dtype=dtype, device=self.pool.device)
+        v = torch.empty_like(k)
         self._read(st, slots, k, v, None, 1)
         return k, v
 
     def _attention(self, st, q, page_tables, seq_lens, scale, out):
-        dev, d = self.pool.device, self.head_dim
-        if q.dim() != 3 or q.dtype not in _TYPES or q.device != dev or q.shape[2] != d:
-            raise ValueError(f"q: BF16 or fp32 [batch, heads, {d}] on {dev}, got {q.dtype} "
-                             f"{tuple(q.shape)} on {q.device}")
-        batch, hq = q.shape[0], q.shape[1]
-        if page_tables.dtype != torch.int32 or page_tables.dim() != 2 or page_tables.device != dev \
+        dev, d, dtype, shape = self._dev, self.head_dim, q.dtype, q.shape
+        if len(shape) != 3 or dtype not in _TYPES or q.get_device() != dev or shape[2] != d:
+            raise ValueError(f"q: BF16 or fp32 [batch, heads, {d}] on {self.pool.device}, got {dtype} "
+                             f"{tuple(shape)} on {q.device}")
+        batch, hq, _ = shape
+        if page_tables.dtype is not torch.int32 or page_tables.dim() != 2 or page_tables.get_device() != dev \
                 or page_tables.shape[0] != batch:
-            raise ValueError(f"page_tables: int32 [{batch}, max_pages] on {dev}, got {page_tables.dtype} "
-                             f"{tuple(page_tables.shape)} on {page_tables.device}")
+            raise ValueError(f"page_tables: int32 [{batch}, max_pages] on {self.pool.device}, got "
+                             f"{page_tables.dtype} {tuple(page_tables.shape)} on {page_tables.device}")
         seq_lens = self._index(seq_lens, "seq_lens", batch)
-        page_tables = page_tables.contiguous()
-        max_pages = page_tables.shape[1]
+        if not page_tables.is_contiguous():
+            page_tables = page_tables.contiguous()
         if not self._dense(q):
             q = q.clone(memory_format=torch.contiguous_format)
         if out is None:
-            out = torch.empty((batch, hq, d), dtype=q.dtype, device=dev)
-        elif out.shape != q.shape or out.dtype != q.dtype or out.device != dev or not self._dense(out):
-            raise ValueError(f"out: {q.dtype} {tuple(q.shape)} on {dev}, rows of consecutive heads at 16-byte strides")
+            out = torch.empty(shape, dtype=dtype, device=q.device)
+        elif out.shape != shape or out.dtype is not dtype or out.get_device() != dev or not self._dense(out):
+            raise ValueError(f"out: {dtype} {tuple(shape)} on {self.pool.device}, rows of consecutive heads at "
+                             "16-byte strides")
         # the workspace belongs to this call's stream, or to the graph that captures it
         if self._ws_bytes is None:
             self._ws_bytes = mk.mk_kvq_workspace(self._c, self.n_kv_heads, 1)
-        ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=dev)
-        mk.mk_kvq_attention(self._c, q.data_ptr(), q.stride(0), out.data_ptr(), out.stride(0), _TYPES[q.dtype], hq,
-                            batch, page_tables.data_ptr(), max_pages, seq_lens.data_ptr(),
+        ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=q.device)
+        mk.mk_kvq_attention(self._c, q.data_ptr(), q.stride(0), out.data_ptr(), out.stride(0), _TYPES[dtype], hq,
+                            batch, page_tables.data_ptr(), page_tables.shape[1], seq_lens.data_ptr(),
                             d ** -0.5 if scale is None else scale, ws.data_ptr(), self._ws_bytes, st)
         return out

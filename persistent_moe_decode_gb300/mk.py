@@ -339,27 +339,26 @@ def mk_kvq_page_bytes(n_kv_heads: int, head_dim: int) -> int:
 
 def mk_kvq_write(cache: mk_kvq_cache, src: mk_kv_rows, src_index_ptr, dst_index_ptr, n: int, unit: int,
                  stream=None) -> int:
-    return _check(lib().mk_kvq_write(C.byref(cache), C.byref(src), src_index_ptr, dst_index_ptr, int(n),
-                                     int(unit), _stream_ptr(stream)), "mk_kvq_write")
+    return _check(lib().mk_kvq_write(cache, src, src_index_ptr, dst_index_ptr, n, unit, _stream_ptr(stream)),
+                  "mk_kvq_write")
 
 
 def mk_kvq_read(cache: mk_kvq_cache, src_index_ptr, dst: mk_kv_rows, dst_index_ptr, n: int, unit: int,
                 stream=None) -> int:
-    return _check(lib().mk_kvq_read(C.byref(cache), src_index_ptr, C.byref(dst), dst_index_ptr, int(n),
-                                    int(unit), _stream_ptr(stream)), "mk_kvq_read")
+    return _check(lib().mk_kvq_read(cache, src_index_ptr, dst, dst_index_ptr, n, unit, _stream_ptr(stream)),
+                  "mk_kvq_read")
 
 
 def mk_kvq_workspace(cache: mk_kvq_cache, n_q_heads: int, batch: int) -> int:
-    return int(lib().mk_kvq_workspace(C.byref(cache), int(n_q_heads), int(batch)))
+    return int(lib().mk_kvq_workspace(cache, n_q_heads, batch))
 
 
 def mk_kvq_attention(cache: mk_kvq_cache, q_ptr: int, q_stride: int, out_ptr: int, out_stride: int, dtype: int,
                      n_q_heads: int, batch: int, page_tables_ptr, max_pages: int, seq_lens_ptr, scale: float,
                      workspace_ptr=None, workspace_bytes: int = 0, stream=None) -> int:
-    return _check(lib().mk_kvq_attention(C.byref(cache), q_ptr, int(q_stride), out_ptr, int(out_stride),
-                                         int(dtype), int(n_q_heads), int(batch), page_tables_ptr,
-                                         int(max_pages), seq_lens_ptr, float(scale), workspace_ptr,
-                                         int(workspace_bytes), _stream_ptr(stream)), "mk_kvq_attention")
+    return _check(lib().mk_kvq_attention(cache, q_ptr, q_stride, out_ptr, out_stride, dtype, n_q_heads, batch,
+                                         page_tables_ptr, max_pages, seq_lens_ptr, scale, workspace_ptr,
+                                         workspace_bytes, _stream_ptr(stream)), "mk_kvq_attention")
 
 
 # ---------------------------------------------------------- convenience

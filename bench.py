@@ -153,10 +153,10 @@ class ClockSampler:
                 "reasons": sorted(reasons), "samples": len(sm)}
 
 
-def step_bytes(dims, routing_idx, keys_per_seq, expert_format="bf16"):
+def step_bytes(dims, routing_idx, keys_per_seq, expert_format="bf16", kv_format="bf16"):
     from persistent_moe_decode_gb300.configs import algorithmic_bytes
     distinct = [len(set(routing_idx[l].reshape(-1).tolist())) for l in range(dims.n_layers)]
-    return algorithmic_bytes(dims, distinct, keys_per_seq, expert_format)
+    return algorithmic_bytes(dims, distinct, keys_per_seq, expert_format, kv_format)
 
 
 class CpuSample:
@@ -319,7 +319,7 @@ def device_timed(run, wl, args, stream, tok_seq, dist=None, clocks=None):
 
 def roofline_of(run, wl, kern_ms, keys, traffic_key):
     idx, _ = run.dec.routing()
-    bytes_step = step_bytes(wl.dims, idx, keys, wl.expert_format)
+    bytes_step = step_bytes(wl.dims, idx, keys, wl.expert_format, wl.kv_format)
     peak, peak_kind = load_peaks()
     achieved = bytes_step / (kern_ms / 1000.0) / 1e9
     return bytes_step, {"bound": "hbm", "achieved": achieved, "peak": peak, "unit": "GB/s",
@@ -448,7 +448,8 @@ def main():
     e2e = None if args.no_e2e else e2e_timed(run, wl, args, stream, world, dist)
 
     cpu = None
-    if rank == 0 and world == 1 and not args.no_cpu_baseline:
+    # (the oracle's cache is BF16: no CPU time beside a 4-bit one)
+    if rank == 0 and world == 1 and not args.no_cpu_baseline and wl.kv_format == "bf16":
         try:
             cpu = CpuSample(run.model, run.k_pool, run.v_pool, state, wl,
                             min(4 if B == 1 else 2, dims.n_layers)).measure(args.cpu_seconds)
@@ -478,7 +479,8 @@ def main():
         "metric": METRIC, "value": tok_s, "unit": "tok/s", "n_gpus": world, "steps": args.steps,
         "warmup": args.warmup, "ms_per_step": elapsed_ms / args.steps, "higher_is_better": True,
         "scaling": "weak", "vs_baseline": None,
-        "dtype": "bf16" if wl.expert_format == "bf16" else "bf16 (routed experts e4m3 + fp32 row scales)",
+        "dtype": ("bf16" if wl.expert_format == "bf16" else "bf16 (routed experts e4m3 + fp32 row scales)")
+                 + ("" if wl.kv_format == "bf16" else " (KV cache in 4 bits + BF16 scales)"),
         "data": "synthetic",
         "config": {"workload": wl.name + (f" (first {args.layers} layers)" if args.layers else ""),
                    "batch": B, "context": context_of(state[1]),

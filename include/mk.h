@@ -122,7 +122,19 @@ typedef struct {
                              shares below; -1 = each expert-branch SM takes an
                              equal share of the routed experts' rows.
                              Results are identical either way.              */
+  int kv_format;          /* enum mk_kv_format: how k_pool / v_pool hold the
+                             cached keys and values                           */
 } mk_config;
+
+/* Format of the KV pools (mk_config.kv_format).
+ *   MK_KV_BF16  k_pool and v_pool are BF16 (below).
+ *   MK_KV_INT4  k_pool[l] is layer l's 4-bit pool, keys and values together:
+ *               [num_kv_pages][mk_kvq_page_bytes], the format of the mk_kvq_*
+ *               calls below; v_pool is not used (may be NULL).  The step
+ *               quantises the new token's fp32 K (post-RoPE) and V into it and
+ *               attends to what it then holds.  28 % of the BF16 cache's
+ *               bytes. */
+enum mk_kv_format { MK_KV_BF16 = 0, MK_KV_INT4 = 1 };
 
 /* Weight format of the routed experts (mk_config.expert_format).
  *   MK_EXPERTS_BF16     w_gate / w_up / w_down are BF16 (below).
@@ -156,7 +168,8 @@ enum mk_expert_format { MK_EXPERTS_BF16 = 0, MK_EXPERTS_FP8_E4M3 = 1 };
  *                    matrices above then hold E4M3 bytes in the same
  *                    layouts); NULL with BF16 experts
  *   k_pool[l], v_pool[l]  [num_kv_pages][hkv][page_size][d]  (written: the
- *                    step stores its new K/V, post-RoPE, at position seq_len)
+ *                    step stores its new K/V, post-RoPE, at position seq_len);
+ *                    with MK_KV_INT4 see there
  * Every pointer must be 16-byte aligned.
  */
 typedef struct {

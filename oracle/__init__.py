@@ -232,6 +232,9 @@ def route(logits, top_k: int):
 
 # ------------------------------------------------------------ the model
 
+ORC_KV_F32 = 16
+
+
 class Oracle:
     """Host model: BF16 weights (uint16 views, stacked over layers) + its own KV pools.
 
@@ -239,7 +242,8 @@ class Oracle:
     w_router, w_gate, w_up, w_down to uint16 arrays with the layouts given in
     oracle.h (stacked over a leading layer axis where per-layer).  ``k_pool`` /
     ``v_pool`` are [L, pages, hkv, P, d] uint16 arrays that the oracle appends
-    the new K/V to (the caller keeps ownership).
+    the new K/V to (the caller keeps ownership), or float32 arrays of that shape
+    that hold the new token's K/V already and are only read (ORC_KV_F32).
 
     ``fp8``, if given, maps q_gate, q_up, q_down (uint8 E4M3 codes, [L, E, I,
     H] / [L, E, H, I]) and s_gate, s_up, s_down (float32 per-row scales, [L,
@@ -258,8 +262,9 @@ class Oracle:
             for n in ("w_gate", "w_up", "w_down"):
                 weights.setdefault(n, np.zeros((self.dims["n_layers"], 1), dtype=np.uint16))
         self.w = {n: _u16(a) for n, a in weights.items()}
-        self.k_pool = _u16(k_pool)
-        self.v_pool = _u16(v_pool)
+        self._flags = ORC_KV_F32 if k_pool.dtype == np.float32 else 0
+        self.k_pool, self.v_pool = (np.ascontiguousarray(a) if self._flags else _u16(a) for a in (k_pool, v_pool))
+        assert self.k_pool.dtype == self.v_pool.dtype
         L = self.dims["n_layers"]
         self.num_pages = int(self.k_pool.shape[1])
         self._dm = _dims(self.dims, self.num_pages)
@@ -306,6 +311,7 @@ class Oracle:
                     force=None):
         """One step; ``force`` = (idx int32 [L, B, k], mask bool [L, B]) imposes
         those experts where mask is set (orc_decode_step_forced)."""
+        flags |= self._flags
         d = self.dims
         B = len(tokens)
         L, H, E, K = d["n_layers"], d["hidden"], d["n_experts"], d["top_k"]
@@ -341,6 +347,7 @@ class Oracle:
         return (logits, out) if trace else logits
 
     def run_layers(self, l0: int, l1: int, h, seq_lens, page_tables, flags: int = 0) -> np.ndarray:
+        flags |= self._flags
         h = _f64(h).copy()
         sl = np.ascontiguousarray(seq_lens, dtype=np.int32)
         pt = np.ascontiguousarray(page_tables, dtype=np.int32)

@@ -175,6 +175,33 @@ int orc_paged_attention(const orc_dims* dm, const uint16_t* k_pool, const uint16
   return ORC_OK;
 }
 
+int orc_paged_attention_f32(const orc_dims* dm, const float* k_pool, const float* v_pool,
+                            const int32_t* page_table, int n_keys, int kv_head,
+                            const double* q, double* out) {
+  const int d = dm->head_dim, P = dm->page_size, hkv = dm->n_kv_heads;
+  if (n_keys <= 0) return ORC_ERR_ARG;
+  double* s = (double*)malloc(sizeof(double) * (size_t)n_keys);
+  if (!s) return ORC_ERR_NOMEM;
+  double mx = -INFINITY, den = 0.0;
+  for (int p = 0; p < n_keys; p++) {
+    int32_t pg = page_table[p / P];
+    if (pg < 0 || pg >= dm->num_pages) { free(s); return ORC_ERR_PAGE; }
+    const float* k = k_pool + (((size_t)pg * hkv + kv_head) * P + (p % P)) * d;
+    s[p] = 0.0;
+    for (int i = 0; i < d; i++) s[p] += q[i] * (double)k[i];
+    s[p] /= sqrt((double)d);
+    if (s[p] > mx) mx = s[p];
+  }
+  for (int p = 0; p < n_keys; p++) { s[p] = exp(s[p] - mx); den += s[p]; }
+  for (int i = 0; i < d; i++) out[i] = 0.0;
+  for (int p = 0; p < n_keys; p++) {
+    const float* v = v_pool + (((size_t)page_table[p / P] * hkv + kv_head) * P + (p % P)) * d;
+    for (int i = 0; i < d; i++) out[i] += s[p] / den * (double)v[i];
+  }
+  free(s);
+  return ORC_OK;
+}
+
 /* ------------------------------------------------------------- routing
  * §Tasks, ROUTER_GEMM / ROUTER_TOPK: score the experts, keep the top-k per
  * token; routing weights = softmax over all experts, renormalised over the
@@ -291,7 +318,7 @@ static int layer_body(const orc_dims* dm, const orc_model* m, int l, int B,
     if (pidx >= max_pages) return ORC_ERR_PAGE;
     int32_t pg = page_tables[(size_t)b * max_pages + pidx];
     if (pg < 0 || pg >= dm->num_pages) return ORC_ERR_PAGE;
-    for (int g = 0; g < hkv; g++) {
+    for (int g = 0; g < hkv && !(flags & ORC_KV_F32); g++) {
       size_t off = (((size_t)pg * hkv + g) * P + (pos % P)) * d;
       for (int i = 0; i < d; i++) {
         m->k_pool[l][off + i] = orc_double_to_bf16(k[g * d + i]);
@@ -309,9 +336,12 @@ static int layer_body(const orc_dims* dm, const orc_model* m, int l, int B,
       for (int hh = 0; hh < hq; hh++) {
         const double* q = qkv + (size_t)b * R + (size_t)hh * d;
         double* o = att + (size_t)b * QD + (size_t)hh * d;
-        int e2 = orc_paged_attention(dm, m->k_pool[l], m->v_pool[l],
-                                     page_tables + (size_t)b * max_pages, seq_lens[b] + 1,
-                                     hh / grp, q, o);
+        const int32_t* pt = page_tables + (size_t)b * max_pages;
+        int e2 = flags & ORC_KV_F32
+                     ? orc_paged_attention_f32(dm, (const float*)(const void*)m->k_pool[l],
+                                               (const float*)(const void*)m->v_pool[l], pt, seq_lens[b] + 1,
+                                               hh / grp, q, o)
+                     : orc_paged_attention(dm, m->k_pool[l], m->v_pool[l], pt, seq_lens[b] + 1, hh / grp, q, o);
         if (e2 != ORC_OK) {
 #pragma omp critical
           err = e2;

@@ -29,7 +29,11 @@ enum {
   ORC_BF16_X = 1,     /* normalised input of each layer and of the LM head  */
   ORC_BF16_Q = 2,     /* query after RoPE                                    */
   ORC_BF16_ATTN = 4,  /* attention output entering O-proj                    */
-  ORC_BF16_A = 8      /* expert hidden SiLU(g)*u entering the down projection */
+  ORC_BF16_A = 8,     /* expert hidden SiLU(g)*u entering the down projection */
+  /* not a rounding: k_pool / v_pool hold fp32 values in the same layout (what a
+   * cache of another format reads back as), the new token's among them: the
+   * step appends nothing and attends to what is there */
+  ORC_KV_F32 = 16
 };
 
 typedef struct {
@@ -106,6 +110,10 @@ void orc_matvec_e4m3(int rows, int cols, const uint8_t* q, const float* scale, c
 int orc_paged_attention(const orc_dims* dm, const uint16_t* k_pool, const uint16_t* v_pool,
                         const int32_t* page_table, int n_keys, int kv_head,
                         const double* q, double* out);
+/* the same over fp32 pools */
+int orc_paged_attention_f32(const orc_dims* dm, const float* k_pool, const float* v_pool,
+                            const int32_t* page_table, int n_keys, int kv_head,
+                            const double* q, double* out);
 void orc_route(int n_experts, int top_k, const double* logits, int32_t* idx, double* w,
                double* gap);
 void orc_moe(const orc_dims* dm, const orc_model* m, int layer, const double* x, int n_sel,

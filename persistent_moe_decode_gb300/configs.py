@@ -50,9 +50,11 @@ class ModelDims:
             return 3 * self.moe_inter * self.hidden + 4 * (2 * self.moe_inter + self.hidden)
         return 2 * 3 * self.moe_inter * self.hidden
 
-    def kv_bytes_per_token(self) -> int:
-        """BF16 K+V bytes one cached token costs across all layers."""
-        return self.n_layers * 2 * self.n_kv_heads * self.head_dim * 2
+    def kv_bytes_per_token(self, kv_format: str = "bf16") -> int:
+        """K+V bytes one cached token costs across all layers: BF16, or 4-bit
+        codes plus two BF16 scales for each 64 dims."""
+        per_dim = 0.5 + 4 / 64 if kv_format == "int4" else 2
+        return int(self.n_layers * 2 * self.n_kv_heads * self.head_dim * per_dim)
 
     def total_weight_bytes(self) -> int:
         return (self.n_layers * (self.layer_dense_bytes()
@@ -75,6 +77,7 @@ class Workload:
     seed: int = 0
     extra: dict = field(default_factory=dict)
     expert_format: str = "bf16"   # "bf16", or "fp8": routed experts in E4M3 + per-row scales
+    kv_format: str = "bf16"       # "bf16", or "int4": KV pools of 4-bit codes + scales (kvq)
 
     def with_(self, **kw) -> "Workload":
         return replace(self, **kw)
@@ -144,11 +147,25 @@ WORKLOADS = {
     "mid_dense": Workload("mid_dense", MID_DENSE, batch=1, context=8192, steps=32),
     # a dense FFN model whose one expert is 8-bit
     "tiny_dense_fp8": Workload("tiny_dense_fp8", TINY_DENSE, batch=1, context=64, steps=8, expert_format="fp8"),
+    # the KV cache held in 4 bits: tiny and mid models for parity (batch 1 and
+    # continuous batching), the 30B/3.3B shape at 8K, 256K and batch 16
+    "tiny_kv4": Workload("tiny_kv4", TINY, batch=1, context=64, steps=8, kv_format="int4"),
+    "tiny_b5_kv4": Workload("tiny_b5_kv4", TINY, batch=5, context=0, steps=6, ragged=(10, 300),
+                            churn=True, join_context=40, kv_format="int4"),
+    "tiny_fp8_kv4": Workload("tiny_fp8_kv4", TINY, batch=1, context=64, steps=8, expert_format="fp8",
+                             kv_format="int4"),
+    "mid_8k_kv4": Workload("mid_8k_kv4", MID, batch=1, context=8192, steps=32, kv_format="int4"),
+    "mid_b16_kv4": Workload("mid_b16_kv4", MID, batch=16, context=0, steps=3, ragged=(64, 2048),
+                            churn=True, join_context=100, kv_format="int4"),
+    "a3b_8k_kv4": Workload("a3b_8k_kv4", A3B, batch=1, context=8192, steps=128, kv_format="int4"),
+    "a3b_256k_kv4": Workload("a3b_256k_kv4", A3B, batch=1, context=262144, steps=32, kv_format="int4"),
+    "a3b_b16_kv4": Workload("a3b_b16_kv4", A3B, batch=16, context=0, steps=128, ragged=(1024, 32768),
+                            churn=True, join_context=1024, kv_format="int4"),
 }
 
 
 def algorithmic_bytes(dims: ModelDims, n_distinct_experts_per_layer, keys_per_seq,
-                      expert_format: str = "bf16") -> int:
+                      expert_format: str = "bf16", kv_format: str = "bf16") -> int:
     """Bytes one decode step must move (the Speed-of-Light numerator).
 
     Dense weights of every layer, the distinct routed experts of every layer,
@@ -158,7 +175,6 @@ def algorithmic_bytes(dims: ModelDims, n_distinct_experts_per_layer, keys_per_se
     """
     dense = dims.n_layers * dims.layer_dense_bytes() + 2 * dims.hidden
     experts = sum(int(n) for n in n_distinct_experts_per_layer) * dims.expert_bytes(expert_format)
-    per_tok = dims.n_layers * 2 * dims.n_kv_heads * dims.head_dim * 2
-    kv = sum(int(n) for n in keys_per_seq) * per_tok
+    kv = sum(int(n) for n in keys_per_seq) * dims.kv_bytes_per_token(kv_format)
     lm = 2 * dims.vocab * dims.hidden
     return dense + experts + kv + lm

@@ -488,8 +488,11 @@ int mk_create(const mk_config* cfg, const mk_weights* w, mk_handle** out) {
     TRY(upload_ptrs(h, (const void* const*)w->s_down, L, (const void* const**)&p.s_down));
   }
   TRY(upload_ptrs(h, (const void* const*)w->k_pool, L, (const void* const**)&p.k_pool));
-  TRY(upload_ptrs(h, (const void* const*)w->v_pool, L, (const void* const**)&p.v_pool));
-  TRY(make_kv_maps(h, w, &p.kv_maps));
+  p.q4 = c.kv_format == MK_KV_INT4;
+  if (!p.q4) {
+    TRY(upload_ptrs(h, (const void* const*)w->v_pool, L, (const void* const**)&p.v_pool));
+    TRY(make_kv_maps(h, w, &p.kv_maps));
+  }
   TRY(make_weight_maps(h, w, &p.w_maps));
   TRY(make_down_maps(h, w, &p.wd_maps));
 

@@ -64,6 +64,7 @@
 
 #include "mk_layout.h"
 #include "mk_ptx.cuh"
+#include "mk_kvq.cuh"
 
 namespace mk {
 
@@ -146,7 +147,7 @@ __device__ __forceinline__ bool stopped(const Params& p) {
   return *(volatile uint32_t*)&p.err[E_CODE] != 0;
 }
 
-__device__ __noinline__ void report(const Params& p, uint32_t code, int task, int op, int bar, uint32_t val,
+static __device__ __noinline__ void report(const Params& p, uint32_t code, int task, int op, int bar, uint32_t val,
                        uint32_t tgt) {
   if (atomicCAS(&p.err[E_CODE], 0u, code) == 0u) {
     p.err[E_SM] = blockIdx.x;
@@ -215,6 +216,18 @@ __device__ __forceinline__ int attn_page_bytes(const Params& p) { return p.hkv *
 __device__ __forceinline__ int attn_pps(const Params& p) {
   const int pb = attn_page_bytes(p);
   return pb >= kStageBytes / 2 ? 1 : (kStageBytes / 2) / pb;
+}
+// 4-bit cache: a page is the records of all KV heads (keys, values and scales
+// together); as many as fit a stage, 1, 2, 4 or 8 of them
+__device__ __forceinline__ int attn_page_bytes_q4(const Params& p) { return p.hkv * 18 * p.d; }
+template <bool Q4>
+__device__ __forceinline__ int attn_stage_pages(const Params& p) {
+  if constexpr (!Q4) {
+    return attn_pps(p);
+  } else {
+    const int n = kStageBytes / attn_page_bytes_q4(p);
+    return n >= 8 ? 8 : n >= 4 ? 4 : n >= 2 ? 2 : 1;
+  }
 }
 
 // share of slice s of n in [0, total); total * n < 2^32 for every device-side
@@ -307,7 +320,7 @@ __device__ __forceinline__ void route_one(const Params& p, RouteTab& rt, int l, 
 // weight / KV stages.
 // ONE: the batch has one token; TR: the task timeline is recorded (kernel
 // instance); F8: the routed experts are 8-bit (E4M3)
-template <bool ONE, bool TR, bool F8 = false>
+template <bool ONE, bool TR, bool F8 = false, bool Q4 = false>
 struct Prod {
   const Params& p;
   Smem& S;
@@ -434,10 +447,10 @@ struct Prod {
   // pages, each as d / 64 swizzled boxes of (hkv * P rows) x 128 bytes.  The
   // page ids are read 32 at a time (lane k holds page c0 + k), the next 32
   // requested while the current ones stream, so no stage waits on a
-  // page-table read.
+  // page-table read.  4-bit cache: a page is one contiguous copy.
   __device__ __forceinline__ bool stream_attn(int b, int pg0, int npages) {
-    const int pb = attn_page_bytes(p);
-    const int pps = attn_pps(p);                 // a power of two <= 8: divides 32
+    const int pb = Q4 ? attn_page_bytes_q4(p) : attn_page_bytes(p);
+    const int pps = attn_stage_pages<Q4>(p);     // a power of two <= 8: divides 32
     const int rows = p.hkv * p.P;
     const int nbox = p.d / 64;
     const uint8_t* km = p.kv_maps + (size_t)l * 2 * 128;
@@ -460,9 +473,13 @@ struct Prod {
         }
         uint32_t slot;
         if (!acquire_stage(slot)) return false;
-        if (lane == 0) mbar_arrive_expect_tx(&S.full[slot], (uint32_t)(2 * n * pb));
+        if (lane == 0) mbar_arrive_expect_tx(&S.full[slot], (uint32_t)((Q4 ? n : 2 * n) * pb));
         __syncwarp();
-        if (lane < 2 * n) {
+        if constexpr (Q4) {
+          if (lane < n)
+            bulk_g2s_hint(&S.stage[slot][lane * pb], (const uint8_t*)p.k_pool[l] + (size_t)pg * pb, (uint32_t)pb,
+                          &S.full[slot], policy_evict_first());
+        } else if (lane < 2 * n) {
           const bool is_k = lane < n;
           uint8_t* dst = &S.stage[slot][(is_k ? lane : pps + lane - n) * pb];
           for (int bx = 0; bx < nbox; bx++)
@@ -640,7 +657,7 @@ struct Prod {
   }
 
   __device__ __forceinline__ bool do_attn() {
-    const int pps = attn_pps(p);
+    const int pps = attn_stage_pages<Q4>(p);
     const int sm = blockIdx.x;
     const int i0 = p.attn_sm_off[sm], i1 = p.attn_sm_off[sm + 1];
     for (int item = i0; item < i1; item++) {
@@ -2715,6 +2732,163 @@ struct Cons {
     return signal(bar_index(p, l, p.bl.items + b), 1);
   }
 
+  // ATTN item over the 4-bit cache: KvqAttn's products on the staged records,
+  // a warp a (page, KV head) as above.  A lane's dims of its query head hold
+  // whole RoPE pairs (head_dim 128) or one half of each (64), so the query
+  // goes from the QKV output to its fragments without shared memory.  q keeps
+  // 22 bits; a weight is rounded to 11 (its error is random from token to
+  // token and averages out; the cache's own rounding is 4 bits).
+  template <int D>
+  __device__ __forceinline__ bool attn_q4() {
+    using A = KvqAttn<D, 2, 1>;
+    using R = KvqRec<D>;
+    constexpr int NG = R::NG;
+    const int hkv = p.hkv, grp = p.grp, P = p.P, hq = p.hq;
+    const int NWG = kConsumerWarps / hkv;
+    const int g = warp % hkv, jw = warp / hkv;
+    const int l = t[R_LAYER], b = t[R_B];
+    const int tt0 = t[R_TT0], tt1 = t[R_TT1], pos = t[R_POS];
+    const int pb = hkv * R::kBytes;
+    const int pps = attn_stage_pages<true>(p);
+    if (!wait_counter(bar_index(p, l, p.bl.p1), p.n_sm)) return false;
+    const float* qraw = p.qkv + ((size_t)l * p.Bmax + b) * p.qkv_rows;
+    const float* rope = p.rope + (size_t)b * (D / 2) * 2;
+    A at;
+    {
+      const float* qr = qraw + (size_t)(g * grp + min(gl, grp - 1)) * D;
+      float x[NG][16];
+#pragma unroll
+      for (int i = 0; i < 16; i++) {
+        const int k = (16 * cq + i) & (D / 2 - 1);     // the pair
+        const float x1 = __ldcg(qr + k), x2 = __ldcg(qr + k + D / 2);
+        const float c = rope[2 * k], s = rope[2 * k + 1];
+        const float y1 = x1 * c - x2 * s, y2 = x2 * c + x1 * s;
+        if constexpr (D == 128) {
+          x[0][i] = gl < grp ? y1 : 0.f;
+          x[NG - 1][i] = gl < grp ? y2 : 0.f;
+        } else {
+          x[0][i] = gl < grp ? (cq < 2 ? y1 : y2) : 0.f;
+        }
+      }
+      at.init(x, p.attn_scale_log2, lane);
+    }
+
+    const int pg0 = tt0 / P;
+    const int npages = (tt1 + P - 1) / P - pg0;
+    const int nst = t[R_NST];
+    for (int st = 0; st < nst; st++) {
+      uint32_t slot;
+      if (!stage_full(slot)) return false;
+      if (TR && tid == 0 && st == 0) S.t_mark[0] = gtime_ns();
+      for (int qi = 0; qi < pps; qi++) {
+        const int page = st * pps + qi;
+        if (page >= npages) break;
+        if (page % NWG != jw) continue;
+        uint8_t* rec = S.stage[slot] + qi * pb + g * R::kBytes;
+        const int tk0 = (pg0 + page) * P;
+        const bool has_new = pos >= tk0 && pos < tk0 + P;
+        // the new token's row (RoPE applied here) is quantised from fp32 into
+        // the staged record and into the cache: eight dims a lane, keys in
+        // the first D / 8 lanes, values in the next
+        if (has_new) {
+          const int row = pos - tk0, wi = lane & 7, o = lane >> 3, k8 = o % NG, val = o / NG;
+          const int pg = p.page_tables[(size_t)b * p.max_pages + pos / P];
+          if (TR && p.dbg && l == 0 && g == 0 && lane == 0)
+            p.dbg[(size_t)p.L * kDbgRouteWords + (size_t)p.Bmax * p.max_pages + b] = pg * P + row;
+          const float* kr = qraw + (size_t)(hq + g) * D;
+          const float* vr = qraw + (size_t)(hq + hkv + g) * D + k8 * kKvqGroup + wi * 8;
+          float y[8];
+#pragma unroll
+          for (int i = 0; i < 8; i++) {
+            const int dim = k8 * kKvqGroup + wi * 8 + i, k = dim & (D / 2 - 1);
+            const float x1 = __ldcg(kr + k), x2 = __ldcg(kr + k + D / 2);
+            const float c = rope[2 * k], s = rope[2 * k + 1];
+            y[i] = val ? __ldcg(vr + i) : dim < D / 2 ? x1 * c - x2 * s : x2 * c + x1 * s;
+          }
+          const KvqScale sc = kvq_group_scale(y, 0xffffffffu);
+          const uint32_t word = kvq_codes(y, sc);
+          if (val < 2) {
+            uint8_t* out = (uint8_t*)p.k_pool[l] + ((size_t)pg * hkv + g) * R::kBytes;
+            kvq_store_row<D>(rec, row, wi, k8, val, word, sc);
+            kvq_store_row<D>(out, row, wi, k8, val, word, sc);
+          }
+          __syncwarp();
+        }
+        at.template page<false>(rec, tt1 - tk0, lane);
+        if (has_new) fence_proxy_async_smem();
+        __syncwarp();
+      }
+      stage_release(slot);
+    }
+    if (TR && tid == 0) S.t_mark[1] = gtime_ns();
+
+    // merge the NWG warps of each group as above; a lane holds dims
+    // 64 k + 8 gl .. + 7 of heads 2 cq, 2 cq + 1
+    float v[NG][2][8];
+    at.finish(v);
+    float* mo = S.red;   // [hkv][D][8]
+    if (!csync()) return false;
+    for (int r = 1; r < NWG; r++) {
+      if (jw == r) {
+#pragma unroll
+        for (int k = 0; k < NG; k++)
+#pragma unroll
+          for (int i = 0; i < 8; i++)
+            *(float2*)(mo + ((size_t)g * D + k * kKvqGroup + 8 * gl + i) * 8 + 2 * cq) =
+                make_float2(v[k][0][i], v[k][1][i]);
+        if (gl == 0)
+#pragma unroll
+          for (int h = 0; h < 2; h++) {
+            S.nred[warp][2 * cq + h] = at.r[h];
+            S.nred[warp][8 + 2 * cq + h] = at.l[h];
+          }
+      }
+      if (!csync()) return false;
+      if (jw == 0) {
+        const int src = r * hkv + g;
+        float own[2], add[2];
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          const float pm = S.nred[src][2 * cq + h], M = fmaxf(at.r[h], pm);
+          own[h] = ex2(at.r[h] - M);
+          add[h] = ex2(pm - M);
+          at.l[h] = at.l[h] * own[h] + S.nred[src][8 + 2 * cq + h] * add[h];
+          at.r[h] = M;
+        }
+#pragma unroll
+        for (int k = 0; k < NG; k++)
+#pragma unroll
+          for (int i = 0; i < 8; i++) {
+            const float2 u = *(const float2*)(mo + ((size_t)g * D + k * kKvqGroup + 8 * gl + i) * 8 + 2 * cq);
+            v[k][0][i] = v[k][0][i] * own[0] + u.x * add[0];
+            v[k][1][i] = v[k][1][i] * own[1] + u.y * add[1];
+          }
+      }
+      if (!csync()) return false;
+    }
+    if (jw == 0) {
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        const int hh = 2 * cq + h;
+        if (hh < grp) {
+          const size_t it = ((size_t)t[R_ITEM] * hkv + g) * grp + hh;
+#pragma unroll
+          for (int k = 0; k < NG; k++) {
+            float4* dst = (float4*)(p.attn_part + it * D + k * kKvqGroup + 8 * gl);
+            __stcg(dst, make_float4(v[k][h][0], v[k][h][1], v[k][h][2], v[k][h][3]));
+            __stcg(dst + 1, make_float4(v[k][h][4], v[k][h][5], v[k][h][6], v[k][h][7]));
+          }
+          if (gl == 0) {
+            __stcg(p.attn_ml + it * 2 + 0, at.r[h]);
+            __stcg(p.attn_ml + it * 2 + 1, at.l[h]);
+          }
+        }
+      }
+    }
+    if (TR && tid == 0) S.t_mark[2] = gtime_ns();
+    return signal(bar_index(p, l, p.bl.items + b), 1);
+  }
+
   // ATTN_COMBINE of units [u0, u1) (unit = sequence b, query head h): merge the
   // sequence's split-KV partials in one pass.  Warp w takes splits w, w + 8,
   // ... (four loads in flight), lane l dims DPL l .. DPL l + DPL - 1, and keeps
@@ -2927,10 +3101,14 @@ __device__ __forceinline__ bool op_route(const Params& p, Smem& S, const int32_t
   return ok;
 }
 
-template <bool ONE, bool TR, int D>
+template <bool ONE, bool TR, bool Q4, int D>
 __device__ __forceinline__ bool op_attn(const Params& p, Smem& S, const int32_t* t) {
   Cons<ONE, TR> c(p, S, t);
-  const bool ok = c.template attn<D>();
+  bool ok;
+  if constexpr (Q4)
+    ok = c.template attn_q4<D>();
+  else
+    ok = c.template attn<D>();
   c.save();
   return ok;
 }
@@ -2947,8 +3125,8 @@ __device__ __forceinline__ bool op_combine(const Params& p, Smem& S, const int32
 // ONE: the batch has one token (one-token GEMV paths only; a separate kernel
 // instance keeps each instance's union of inlined paths within registers).
 // TR: the timeline is recorded (an instance of its own, so the timed
-// instances carry no clock reads).
-template <bool ONE, bool TR, bool F8>
+// instances carry no clock reads).  Q4: the KV cache is held in 4 bits.
+template <bool ONE, bool TR, bool F8, bool Q4>
 __device__ __forceinline__ void consumer_loop(const Params& p, Smem& S) {
   const int tid = threadIdx.x, lane = tid & 31;
   uint32_t task_seq = 0;
@@ -2988,7 +3166,7 @@ __device__ __forceinline__ void consumer_loop(const Params& p, Smem& S) {
         break;
       }
       case OP_ROUTE: ok = op_route<ONE, TR>(p, S, t); break;
-      case OP_ATTN: ok = (p.d == 128) ? op_attn<ONE, TR, 128>(p, S, t) : op_attn<ONE, TR, 64>(p, S, t); break;
+      case OP_ATTN: ok = (p.d == 128) ? op_attn<ONE, TR, Q4, 128>(p, S, t) : op_attn<ONE, TR, Q4, 64>(p, S, t); break;
       case OP_COMBINE: ok = (p.d == 128) ? op_combine<ONE, TR, 128>(p, S, t) : op_combine<ONE, TR, 64>(p, S, t); break;
       default: ok = false; break;
     }
@@ -3022,7 +3200,7 @@ __device__ __forceinline__ void consumer_loop(const Params& p, Smem& S) {
   }
 }
 
-template <bool ONE, bool TR, bool F8 = false>
+template <bool ONE, bool TR, bool F8 = false, bool Q4 = false>
 __global__ void __launch_bounds__(kThreads, 1) mk_step_kernel(const __grid_constant__ Params p) {
   static_assert(kThreads == 384 && kLaunchRegs == 168, "register split assumes 384 threads x 168");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -3055,31 +3233,48 @@ __global__ void __launch_bounds__(kThreads, 1) mk_step_kernel(const __grid_const
     // registers back
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs) : "memory");
     if (wid == kConsumerWarps) {
-      Prod<ONE, TR, F8> pr(p, S);
+      Prod<ONE, TR, F8, Q4> pr(p, S);
       pr.run();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs) : "memory");
-    consumer_loop<ONE, TR, F8>(p, S);
+    consumer_loop<ONE, TR, F8, Q4>(p, S);
   }
 }
 
-// the four kernel instances: (one token, several) x (timeline off, on)
+// the kernel instances: (one token, several) x (timeline off, on)
 // and, for one token with 8-bit experts, two more (timeline off, on), so that
-// the BF16 instances carry none of the 8-bit paths
+// the BF16 instances carry none of the 8-bit paths; and the same six over the
+// 4-bit cache, compiled in a translation unit of their own
+// (mk_kernel_q4.cu) beside these
 constexpr int kNumStepKernels = 6;
+#ifndef MK_STEP_Q4
+#define MK_STEP_Q4 false
+#endif
+#if !defined(MK_STEP_Q4_UNIT)
+extern const void* const kStepKernelsQ4[kNumStepKernels];
 static const void* const kStepKernels[kNumStepKernels] = {
-    (const void*)mk_step_kernel<false, false>, (const void*)mk_step_kernel<true, false>,
-    (const void*)mk_step_kernel<false, true>, (const void*)mk_step_kernel<true, true>,
-    (const void*)mk_step_kernel<true, false, true>, (const void*)mk_step_kernel<true, true, true>};
+#else
+extern const void* const kStepKernelsQ4[kNumStepKernels];
+const void* const kStepKernelsQ4[kNumStepKernels] = {
+#endif
+    (const void*)mk_step_kernel<false, false, false, MK_STEP_Q4>,
+    (const void*)mk_step_kernel<true, false, false, MK_STEP_Q4>,
+    (const void*)mk_step_kernel<false, true, false, MK_STEP_Q4>,
+    (const void*)mk_step_kernel<true, true, false, MK_STEP_Q4>,
+    (const void*)mk_step_kernel<true, false, true, MK_STEP_Q4>,
+    (const void*)mk_step_kernel<true, true, true, MK_STEP_Q4>};
+
+#ifndef MK_STEP_Q4_UNIT
+static const void* step_kernel(int i) { return i < kNumStepKernels ? kStepKernels[i] : kStepKernelsQ4[i - kNumStepKernels]; }
 
 // registers per thread every kernel instance was built with (the split above
 // needs kLaunchRegs); -1 if they differ or cannot be read
 int step_kernel_regs() {
   int regs = -1;
-  for (int i = 0; i < kNumStepKernels; i++) {
+  for (int i = 0; i < 2 * kNumStepKernels; i++) {
     cudaFuncAttributes a;
-    if (cudaFuncGetAttributes(&a, kStepKernels[i]) != cudaSuccess) {
+    if (cudaFuncGetAttributes(&a, step_kernel(i)) != cudaSuccess) {
       cudaGetLastError();
       return -1;
     }
@@ -3149,8 +3344,8 @@ cudaError_t configure_step_kernels() {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 0 && dev < kMaxDev && configured[dev].load(std::memory_order_acquire)) return cudaSuccess;
-  for (int i = 0; i < kNumStepKernels; i++) {
-    e = cudaFuncSetAttribute(kStepKernels[i], cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+  for (int i = 0; i < 2 * kNumStepKernels; i++) {
+    e = cudaFuncSetAttribute(step_kernel(i), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
     if (e != cudaSuccess) return e;
   }
   if (dev >= 0 && dev < kMaxDev) configured[dev].store(true, std::memory_order_release);
@@ -3170,10 +3365,13 @@ cudaError_t launch_step(const Params& p, int n_sm, cudaStream_t stream) {
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const void* k = p.fp8 ? kStepKernels[4 + (p.trace != nullptr ? 1 : 0)]
-                        : kStepKernels[(p.B == 1 ? 1 : 0) + (p.trace != nullptr ? 2 : 0)];
+  const void* k = step_kernel((p.q4 ? kNumStepKernels : 0) +
+                              (p.fp8 ? 4 + (p.trace != nullptr ? 1 : 0)
+                                     : (p.B == 1 ? 1 : 0) + (p.trace != nullptr ? 2 : 0)));
   void* args[1] = {(void*)&p};
   return cudaLaunchKernelExC(&cfg, k, args);
 }
+
+#endif  // MK_STEP_Q4_UNIT
 
 }  // namespace mk

@@ -82,23 +82,6 @@ __device__ __forceinline__ void load8(float* x, const T* p) {
   r.get(x);
 }
 
-// scale of a group whose values lie eight a thread in eight neighbouring
-// threads, all of which (`mask`) call it
-__device__ __forceinline__ KvqScale group_scale(const float* x, unsigned mask) {
-  float lo = x[0], hi = x[0];
-#pragma unroll
-  for (int i = 1; i < 8; i++) {
-    lo = fmin_nan(lo, x[i]);
-    hi = fmax_nan(hi, x[i]);
-  }
-#pragma unroll
-  for (int sh = 1; sh < 8; sh <<= 1) {
-    lo = fmin_nan(lo, __shfl_xor_sync(mask, lo, sh));
-    hi = fmax_nan(hi, __shfl_xor_sync(mask, hi, sh));
-  }
-  return kvq_scale(lo, hi);
-}
-
 // values of the eight codes of a word: step * code + low in fp32.  A nibble
 // under the exponent of 2^23 is 2^23 + code; both operations that follow are
 // exact up to the last.
@@ -175,17 +158,11 @@ __global__ void __launch_bounds__(kCopyThreads) kvq_write_kernel(Cache c, Rows s
   raw.load((const T*)(o.val ? src.v : src.k) + from * src.row + head * src.head + o.group * kKvqGroup + o.wi * 8);
   float x[8];
   raw.get(x);
-  const KvqScale s = group_scale(x, 0xffu << (threadIdx.x & 24));
+  const KvqScale s = kvq_group_scale(x, 0xffu << (threadIdx.x & 24));
   const uint32_t word = kvq_codes(x, s);
   const int t = to % kKvqPage;
   uint8_t* rec = c.pool + ((long long)(to / kKvqPage) * c.hkv + head) * R::kBytes;
-  if (o.val) {
-    *(uint16_t*)(rec + R::val_half(t, o.wi, o.group, 0)) = (uint16_t)word;
-    *(uint16_t*)(rec + R::val_half(t, o.wi, o.group, 1)) = (uint16_t)(word >> 16);
-  } else {
-    *(uint32_t*)(rec + R::key_word(t, o.wi, o.group)) = word;
-  }
-  if (o.wi == 0) *(uint32_t*)(rec + (o.val ? R::kValScale : R::kKeyScale) + 4 * (t * R::NG + o.group)) = s.word();
+  kvq_store_row<D>(rec, t, o.wi, o.group, o.val, word, s);
 }
 
 template <int D, class T>
@@ -242,7 +219,7 @@ __global__ void __launch_bounds__(kCopyThreads) kvq_write_pages_kernel(Cache c, 
     for (int g = 0; g < NG; g++) {
       float x[8];
       kr[e][g].get(x);
-      const KvqScale s = group_scale(x, 0xffffffffu);
+      const KvqScale s = kvq_group_scale(x, 0xffffffffu);
       w[g] = kvq_codes(x, s);
       sw[g] = s.word();
     }
@@ -268,7 +245,7 @@ __global__ void __launch_bounds__(kCopyThreads) kvq_write_pages_kernel(Cache c, 
       for (int t = 0; t < 2; t++) {
         float x[8];
         vr[e][t][g].get(x);
-        const KvqScale s = group_scale(x, 0xffffffffu);
+        const KvqScale s = kvq_group_scale(x, 0xffffffffu);
         c8[t] = kvq_codes(x, s);
         sw[t * NG + g] = s.word();
       }
@@ -374,7 +351,7 @@ struct AttnArgs {
 };
 
 // workspace: the slot count, a header per slot, then the slots
-struct AttnSlot {
+struct __align__(16) AttnSlot {
   int b, j;                                // sequence; KV head and head tile
   int parts;                               // of the task, in its first slot; 0 in the others
   int step;                                // 1: parts in consecutive slots; 2: in the even slots after the first
@@ -706,26 +683,30 @@ template <int D, class T>
 __global__ void __launch_bounds__(kMergeThreads) kvq_merge_kernel(AttnArgs a, int blocks) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int V = D / 32, kBatch = 5;    // dims of a lane
-  __shared__ int list[kMaxSlots], n_list;
+  __shared__ int list[kMaxSlots], n_list;  // first slots
+  __shared__ AttnSlot head[kMaxSlots];     // and what they say
   __shared__ float so[8][D], sr[8], sl[8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const AttnWs ws = attn_ws(a.ws, blocks);
-  const int count = *ws.count;
   if (warp == 0) {
-    // the first slots in order
+    // the first slots in order; nothing past the count is used, but it is read with it
+    const int count = *ws.count;
     int n = 0;
-#pragma unroll 1
-    for (int s0 = 0; s0 < count; s0 += 32 * 10) {
-      bool is[10];
+    for (int s0 = 0; s0 < 2 * blocks; s0 += 32 * 10) {
+      AttnSlot t[10];
 #pragma unroll
       for (int i = 0; i < 10; i++) {
         const int s = s0 + 32 * i + lane;
-        is[i] = s < count && ws.slots[s].parts > 0;
+        t[i].parts = 0;
+        if (s < 2 * blocks) *(int4*)&t[i] = *(const int4*)&ws.slots[s];
       }
 #pragma unroll
       for (int i = 0; i < 10; i++) {
-        const unsigned m = __ballot_sync(0xffffffffu, is[i]);
-        if (is[i]) list[n + __popc(m & ((1u << lane) - 1))] = s0 + 32 * i + lane;
+        const int s = s0 + 32 * i + lane;
+        const bool is = s < count && t[i].parts > 0;
+        const unsigned m = __ballot_sync(0xffffffffu, is);
+        const int at = n + __popc(m & ((1u << lane) - 1));
+        if (is) list[at] = s, head[at] = t[i];
         n += __popc(m);
       }
     }
@@ -734,7 +715,7 @@ __global__ void __launch_bounds__(kMergeThreads) kvq_merge_kernel(AttnArgs a, in
   __syncthreads();
   for (int w = blockIdx.x; w < n_list * 8; w += gridDim.x) {
     const int s = list[w / 8], h = w % 8;
-    const AttnSlot t = ws.slots[s];
+    const AttnSlot t = head[w / 8];
     if (h >= min(8, a.grp - t.j % a.tiles * 8)) continue;
     float m = -FLT_MAX, den = 0.f, num[V];
 #pragma unroll

@@ -129,6 +129,38 @@ __device__ __forceinline__ uint32_t kvq_codes(const float* x, const KvqScale& s)
   return s.inv == 0.f ? 0u : word;
 }
 
+// scale of a group whose values lie eight a thread in eight neighbouring
+// threads, all of which (`mask`) call it
+__device__ __forceinline__ KvqScale kvq_group_scale(const float* x, unsigned mask) {
+  float lo = x[0], hi = x[0];
+#pragma unroll
+  for (int i = 1; i < 8; i++) {
+    lo = fmin_nan(lo, x[i]);
+    hi = fmax_nan(hi, x[i]);
+  }
+#pragma unroll
+  for (int sh = 1; sh < 8; sh <<= 1) {
+    lo = fmin_nan(lo, __shfl_xor_sync(mask, lo, sh));
+    hi = fmax_nan(hi, __shfl_xor_sync(mask, hi, sh));
+  }
+  return kvq_scale(lo, hi);
+}
+
+// codes of dims 64 g + 8 wi .. + 7 of token t and, from one thread of the
+// group, its scale into a record
+template <int D>
+__device__ __forceinline__ void kvq_store_row(uint8_t* rec, int t, int wi, int g, int val, uint32_t word,
+                                              const KvqScale& s) {
+  using R = KvqRec<D>;
+  if (val) {
+    *(uint16_t*)(rec + R::val_half(t, wi, g, 0)) = (uint16_t)word;
+    *(uint16_t*)(rec + R::val_half(t, wi, g, 1)) = (uint16_t)(word >> 16);
+  } else {
+    *(uint32_t*)(rec + R::key_word(t, wi, g)) = word;
+  }
+  if (wi == 0) *(uint32_t*)(rec + (val ? R::kValScale : R::kKeyScale) + 4 * (t * R::NG + g)) = s.word();
+}
+
 // ---------------------------------------------------------------- attention
 
 // D = A B, m16n8k16, FP16 in, fp32 out

@@ -182,8 +182,9 @@ struct Params {
   const uint16_t* const* w_gate;
   const uint16_t* const* w_up;
   const uint16_t* const* w_down;
-  uint16_t* const* k_pool;
-  uint16_t* const* v_pool;
+  uint16_t* const* k_pool;     // q4: the 4-bit pool, [pages][hkv][18 d] bytes
+  uint16_t* const* v_pool;     // q4: not used
+  int q4;                      // the KV cache is held in 4 bits (mk_kvq.cuh)
   // 8-bit experts (E4M3): w_gate / w_up / w_down hold bytes (same layouts),
   // weight = scale[row] * e4m3(byte); fp32 per-row scales [E][I], [E][I], [E][H]
   int fp8;

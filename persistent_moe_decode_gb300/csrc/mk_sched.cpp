@@ -58,6 +58,7 @@ int validate_config(const mk_config& c) {
   if (c.moe_stage_depth < 0 || c.moe_stage_depth > kStages) return MK_ERR_BAD_CONFIG;
   if (c.wave_order < MK_WAVES_DEFAULT || c.wave_order > MK_WAVES_INTERLEAVED) return MK_ERR_BAD_CONFIG;
   if (c.expert_format != MK_EXPERTS_BF16 && c.expert_format != MK_EXPERTS_FP8_E4M3) return MK_ERR_BAD_CONFIG;
+  if (c.kv_format != MK_KV_BF16 && c.kv_format != MK_KV_INT4) return MK_ERR_BAD_CONFIG;
   if (c.moe_claim_rows < -1 || (c.moe_claim_rows > 0 && c.moe_claim_rows % 16)) return MK_ERR_BAD_CONFIG;
   // 8-bit experts: the one-token path (tensor-core rows of 2048 bytes, or
   // CUDA-core rows of 256, 512 or 1024 bytes in 16-byte lane chunks; a whole

@@ -30,6 +30,7 @@ MK_ERR_DEVICE = -9
 
 MK_WAVES_DEFAULT, MK_WAVES_ATTN_FIRST, MK_WAVES_INTERLEAVED = 0, 1, 2
 MK_EXPERTS_BF16, MK_EXPERTS_FP8_E4M3 = 0, 1
+MK_KV_BF16, MK_KV_INT4 = 0, 1
 MK_TYPE_BF16, MK_TYPE_F32 = 0, 1
 (MK_SCRATCH_H, MK_SCRATCH_X, MK_SCRATCH_QKV, MK_SCRATCH_ATTN, MK_SCRATCH_ROUTER,
  MK_SCRATCH_OPROJ, MK_SCRATCH_MOE) = range(7)
@@ -54,7 +55,7 @@ class mk_config(C.Structure):
                 ("max_attn_items", C.c_int), ("wave_order", C.c_int), ("n_attn_claimers", C.c_int),
                 ("n_moe_claimers", C.c_int), ("kv_split_tokens", C.c_int), ("sm_cap", C.c_int),
                 ("timeout_ms", C.c_int), ("trace_records", C.c_int), ("moe_stage_depth", C.c_int),
-                ("expert_format", C.c_int), ("moe_claim_rows", C.c_int)]
+                ("expert_format", C.c_int), ("moe_claim_rows", C.c_int), ("kv_format", C.c_int)]
 
 
 _VPP = C.POINTER(C.c_void_p)
@@ -380,7 +381,10 @@ class Decoder:
     """Owns one mk handle over caller-owned device tensors (weights, KV pools).
 
     ``model`` has the stacked BF16 device tensors of ``synth.SynthModel``;
-    ``k_pool`` / ``v_pool`` are [L, pages, hkv, P, d] BF16 device tensors.
+    ``k_pool`` / ``v_pool`` are [L, pages, hkv, P, d] BF16 device tensors, or
+    ``k_pool`` is the 4-bit pools of all layers, [L, pages, page bytes] uint8
+    (:class:`persistent_moe_decode_gb300.kvq.QuantCache` pools), and ``v_pool``
+    None.
     The tensors are kept referenced for the lifetime of the decoder.
     """
 
@@ -391,6 +395,12 @@ class Decoder:
         fp8 = getattr(model, "fp8", None)
         if fp8 is not None:
             cfg_kw = {**cfg_kw, "expert_format": MK_EXPERTS_FP8_E4M3}
+        if v_pool is None:
+            if k_pool.dim() != 3 or k_pool.element_size() != 1 \
+                    or k_pool.shape[2] != mk_kvq_page_bytes(self.dims.n_kv_heads, self.dims.head_dim):
+                raise ValueError("4-bit KV pools: uint8 [layers, pages, page bytes], got "
+                                 f"{k_pool.dtype} {tuple(k_pool.shape)}")
+            cfg_kw = {**cfg_kw, "kv_format": MK_KV_INT4}
         self.cfg = make_config(self.dims, max_batch, max_pages_per_seq, k_pool.shape[1], **cfg_kw)
         self._keep = []
 
@@ -405,7 +415,9 @@ class Decoder:
                                   attn_norm=arr(model.attn_norm), w_qkv=arr(model.w_qkv),
                                   w_o=arr(model.w_o), w_router=arr(model.w_router),
                                   w_gate=arr(ex["q_gate"]), w_up=arr(ex["q_up"]),
-                                  w_down=arr(ex["q_down"]), k_pool=arr(k_pool), v_pool=arr(v_pool))
+                                  w_down=arr(ex["q_down"]), k_pool=arr(k_pool))
+        if v_pool is not None:
+            self.weights.v_pool = arr(v_pool)
         if fp8 is not None:
             self.weights.s_gate = arr(fp8["s_gate"])
             self.weights.s_up = arr(fp8["s_up"])

@@ -170,6 +170,12 @@ def make_model(dims: ModelDims, seed: int = 0, device="cpu", expert_format: str 
     )
 
 
+def kv_layer(dims: ModelDims, num_pages: int, kv_std: float, seed: int, layer: int, device="cpu"):
+    """One layer's K and V pools, each [num_pages, hkv, P, d] BF16 of N(0, kv_std^2)."""
+    shape = (num_pages, dims.n_kv_heads, dims.page_size, dims.head_dim)
+    return tuple(_normal_bf16(shape, _seed_for(seed, n, layer), device, kv_std) for n in ("k_pool", "v_pool"))
+
+
 def make_kv_pools(dims: ModelDims, num_pages: int, kv_std: float, seed: int = 0,
                   device="cpu"):
     """K and V pools, each [L, num_pages, hkv, P, d] BF16 of N(0, kv_std^2)."""
@@ -178,8 +184,7 @@ def make_kv_pools(dims: ModelDims, num_pages: int, kv_std: float, seed: int = 0,
     k = torch.empty((L,) + shape, dtype=torch.bfloat16, device=device)
     v = torch.empty((L,) + shape, dtype=torch.bfloat16, device=device)
     for l in range(L):
-        k[l] = _normal_bf16(shape, _seed_for(seed, "k_pool", l), device, kv_std)
-        v[l] = _normal_bf16(shape, _seed_for(seed, "v_pool", l), device, kv_std)
+        k[l], v[l] = kv_layer(dims, num_pages, kv_std, seed, l, device)
     return k, v
 
 
@@ -259,6 +264,13 @@ class DecodeBatch:
         self.seq_ids[slot] = self.next_seq_id
         self.next_seq_id += 1
         return slot, added
+
+
+def refill_rows(dims: ModelDims, n_pages: int, kv_std: float, seed: int, step: int, layer: int, device):
+    """Fresh K and V pages of one layer, [n_pages, hkv, P, d] BF16 of N(0, kv_std^2)."""
+    shape = (n_pages, dims.n_kv_heads, dims.page_size, dims.head_dim)
+    return tuple(_normal_bf16(shape, _seed_for(seed, "kv_refill", layer, 2 * step + i), device, kv_std)
+                 for i in range(2))
 
 
 def refill_pages(k_pool: torch.Tensor, v_pool: torch.Tensor, pages, kv_std: float,

@@ -156,3 +156,34 @@ def test_the_restated_store_and_load_agree_within_half_a_step(d):
         g = x.reshape(n, hkv, -1, 64)
         span = g.max(-1) - g.min(-1)
         assert (step.reshape(n, hkv, -1, 64)[..., 0] <= (span + 2.0 ** -7 * np.abs(g.min(-1))) / 15 * (1 + 2.0 ** -7)).all()
+
+
+def test_the_step_refuses_unknown_cache_formats_and_shapes(lib):
+    from persistent_moe_decode_gb300.configs import TINY
+    w = mk.mk_weights()
+    for bad in (2, -1):
+        cfg = mk.make_config(TINY, 1, 8, 16, kv_format=bad)
+        h = C.c_void_p()
+        assert lib.mk_create(C.byref(cfg), C.byref(w), C.byref(h)) == mk.MK_ERR_BAD_CONFIG
+
+    class Model:
+        dims, fp8 = TINY, None
+        w_gate = w_up = w_down = None
+
+    for pool in (torch.zeros(2, 4, 100, dtype=torch.uint8), torch.zeros(4, 2 * 1152, dtype=torch.uint8),
+                 torch.zeros(2, 4, 2 * 1152)):
+        with pytest.raises(ValueError):
+            mk.Decoder(Model, pool, None, 1, 4)
+
+
+def test_bytes_of_a_cached_token():
+    """4.5 bits a value: the record's 18 bytes for every 32 values, keys and values together."""
+    from persistent_moe_decode_gb300.configs import A3B, TINY, WORKLOADS, algorithmic_bytes
+    for d in (TINY, A3B):
+        page = mk.mk_kvq_page_bytes(d.n_kv_heads, d.head_dim)
+        assert d.kv_bytes_per_token("int4") * 16 == d.n_layers * page
+        assert d.kv_bytes_per_token() == d.n_layers * 4 * d.n_kv_heads * d.head_dim
+        n = [d.top_k] * d.n_layers
+        assert algorithmic_bytes(d, n, [100], kv_format="int4") - algorithmic_bytes(d, n, [99], kv_format="int4") \
+            == d.kv_bytes_per_token("int4")
+    assert WORKLOADS["a3b_256k_kv4"].kv_format == "int4"

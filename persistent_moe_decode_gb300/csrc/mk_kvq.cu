@@ -335,7 +335,7 @@ constexpr int kAttnThreads = kAttnWarps * 32;
 template <int D, class T>
 constexpr int kBlocksPerSm = D == 128 && sizeof(T) == 4 ? 1 : 2;
 constexpr int kMinPages = kAttnWarps;
-constexpr int kRing = 4;                   // pages of a warp in flight and in use
+constexpr int kRing = 4;                   // pages of a warp, in flight and in use
 
 struct AttnArgs {
   Cache c;
@@ -496,8 +496,7 @@ struct AttnBlock {
     const int32_t* table = a.page_tables + (long long)b * a.max_pages + p0 + warp;
     const int n = (p1 - p0 - warp + kAttnWarps - 1) / kAttnWarps;   // this warp's pages (may be <= 0)
     bool bad = false;
-    // page numbers: 32 of the warp's pages at a time, a lane each
-    int ids = lane < n ? table[lane * kAttnWarps] : 0, fetched = 0;
+    int fetched = 0, id = n > 0 ? table[0] : 0;   // the next page to fetch, read an iteration ahead
     const uint8_t* base = a.c.pool + (long long)g * R::kBytes + lane * 16;
     const long long page_bytes = (long long)a.c.hkv * R::kBytes;
     // the lane's 16-byte chunks lie 512 bytes apart, in the ring slot too: value chunks from one place (32 of
@@ -507,19 +506,14 @@ struct AttnBlock {
     const uint32_t line_v = smem_u32(ring) + A::staged(R::kVal / 16 + lane) * 16 - R::kVal;
     auto fetch = [&](uint32_t slot) {      // the warp's next page into the ring, `slot` bytes in
       if (fetched < n) {
-        if (fetched && (fetched & 31) == 0)
-          ids = fetched + lane < n ? table[(long long)(fetched + lane) * kAttnWarps] : 0;
-        int id = __shfl_sync(0xffffffffu, ids, fetched & 31);
-        if ((unsigned)id >= (unsigned)a.c.pages) {
-          bad = true;
-          id = 0;
-        }
-        const uint8_t* src = base + id * page_bytes;
+        const bool ok = (unsigned)id < (unsigned)a.c.pages;
+        bad |= !ok;
+        const uint8_t* src = base + (ok ? id : 0) * page_bytes;
 #pragma unroll
         for (int k = 0; k < kChunks; k++)
-          if (k * 32 + 32 <= R::kBytes / 16 || k * 32 + lane < R::kBytes / 16) 
+          if (k * 32 + 32 <= R::kBytes / 16 || k * 32 + lane < R::kBytes / 16)
             cp_async16((k >= kVal0 && k < kVal1 ? line_v : line) + slot + k * 512, src + k * 512);
-        fetched++;
+        if (++fetched < n) id = table[(long long)fetched * kAttnWarps];
       }
       cp_async_commit();
     };
@@ -540,16 +534,26 @@ struct AttnBlock {
       }
       at.init(x, a.scale_log2, lane);
     }
-    int left = len - (p0 + warp) * kKvqPage;   // tokens from the page on
     uint32_t rd = 0, wr = (kRing - 1) * R::kBytes;
-    for (int i = 0; i < n; i++) {
+    auto next = [&]() {                    // the next page has arrived; another goes into the slot read before it
       cp_async_wait<kRing - 2>();
       __syncwarp();
-      fetch(wr);                           // into the slot read in the iteration before
+      fetch(wr);
       wr = wr == (kRing - 1) * R::kBytes ? 0 : wr + R::kBytes;
-      at.template page<true>(ring + rd, left, lane);
+      const uint8_t* rec = ring + rd;
       rd = rd == (kRing - 1) * R::kBytes ? 0 : rd + R::kBytes;
-      left -= kAttnWarps * kKvqPage;
+      return rec;
+    };
+    // only the sequence's last page can have rows past its end
+    const int tail = len - (p0 + warp + (n - 1) * kAttnWarps) * kKvqPage;
+    const int full = tail >= kKvqPage ? n : n - 1;
+    for (int i = 0; i < full; i++) {
+      const uint8_t* const rec[1] = {next()};
+      at.template pages<1, true, false>(rec, {kKvqPage}, lane);
+    }
+    if (n > 0 && full < n) {
+      const uint8_t* const rec[1] = {next()};
+      at.template pages<1, true, true>(rec, {tail}, lane);
     }
     cp_async_wait<0>();
     if (bad && lane == 0) flag_bad(a.c, MK_ERR_BAD_PAGE);

@@ -256,27 +256,25 @@ struct KvqAttn {
     return V0 + (pair / 4) * (4 * W) + col * 4 + pair % 4;
   }
 
-  // a lane's part of a record's keys or values (tokens gl, gl + 8; token pairs
-  // cq, cq + 4); STAGED: of a copy in the order of staged()
-  struct Half {
-    uint32_t w[2][NW], sc[2][NG];          // codes; scales of tokens gl, gl + 8
+  // keys of tokens gl, gl + 8 and their scales
+  struct Keys {
+    uint32_t w[2][NW], sc[2][NG];
   };
-  static __device__ __forceinline__ void load_keys(Half& k, const uint8_t* rec, int lane) {
+  static __device__ __forceinline__ void load_keys(Keys& k, const uint8_t* rec, int lane) {
 #pragma unroll
     for (int e = 0; e < 2; e++) {
       load_words<NW>(k.w[e], rec + ((lane >> 2) + 8 * e) * (D / 2) + (lane & 3) * (8 * NG));
       load_words<NG>(k.sc[e], rec + R::kKeyScale + ((lane >> 2) + 8 * e) * (4 * NG));
     }
   }
+  // values of token pairs cq, cq + 4; STAGED: of a copy in the order of staged()
   template <bool STAGED>
-  static __device__ __forceinline__ void load_values(Half& v, const uint8_t* rec, int lane) {
+  static __device__ __forceinline__ void load_values(uint32_t (*v)[NW], const uint8_t* rec, int lane) {
     const int gl = lane >> 2, cq = lane & 3;
 #pragma unroll
-    for (int e = 0; e < 2; e++) {
-      load_words<NW>(v.w[e], rec + R::kVal + e * 4 * D +
-                                 (STAGED ? (gl * NG / 2 * 4 + cq) * 16 + gl * NG % 2 * 8 : cq * D + gl * (8 * NG)));
-      load_words<NG>(v.sc[e], rec + R::kValScale + (gl + 8 * e) * (4 * NG));
-    }
+    for (int e = 0; e < 2; e++)
+      load_words<NW>(v[e], rec + R::kVal + e * 4 * D +
+                               (STAGED ? (gl * NG / 2 * 4 + cq) * 16 + gl * NG % 2 * 8 : cq * D + gl * (8 * NG)));
   }
 
   // x[g][16]: dims 64 g + 16 cq .. + 15 of query head gl (zeros where there is
@@ -363,12 +361,11 @@ struct KvqAttn {
     }
   }
 
-  // tokens [0, valid) of a page; valid is the same in every lane, 1 or more
-  template <bool STAGED>
-  __device__ __forceinline__ void page(const uint8_t* rec, int valid, int lane) {
+  // scores (in units of log2) of tokens gl, gl + 8 of a page for heads 2 cq,
+  // 2 cq + 1
+  __device__ __forceinline__ void scores(float (*x)[2], const uint8_t* rec, int lane) {
     constexpr uint32_t M0 = 0x000f000fu, M1 = 0x00f000f0u;
-    const int gl = lane >> 2;
-    Half ky;
+    Keys ky;
     load_keys(ky, rec, lane);
     float acc[NG][4];
 #pragma unroll
@@ -396,9 +393,6 @@ struct KvqAttn {
 #pragma unroll
         for (int e = 0; e < 4; e++) acc[g][e] += low[e];
     }
-    Half vl;
-    load_values<STAGED>(vl, rec, lane);
-    float x[2][2];                         // [token gl / gl + 8][head]
 #pragma unroll
     for (int e = 0; e < 2; e++)
 #pragma unroll
@@ -413,41 +407,65 @@ struct KvqAttn {
         }
         x[e][h] = fmaf(dot, f[h], off);
       }
-    if (valid < kKvqPage) {
-      // rows past the sequence may hold anything, NaN scales included
+  }
+
+  // Tokens [0, valid[n]) of N pages (MASK; else all 16 of each); valid is the
+  // same in every lane and may be 0 or less (a page that is not there; its
+  // record is read but not used).  N = 2 gives the scheduler two independent
+  // chains and one vote for both.
+  template <int N, bool STAGED, bool MASK>
+  __device__ __forceinline__ void pages(const uint8_t* const (&rec)[N], const int (&valid)[N], int lane) {
+    const int gl = lane >> 2;
+    float x[N][2][2];                      // [page][token gl / gl + 8][head]
 #pragma unroll
-      for (int e = 0; e < 2; e++)
-        if (gl + 8 * e >= valid) {
-          x[e][0] = x[e][1] = -INFINITY;
+    for (int n = 0; n < N; n++) scores(x[n], rec[n], lane);
+    uint32_t vs[N][2][NG];                 // value scales of tokens gl, gl + 8
 #pragma unroll
-          for (int g = 0; g < NG; g++) vl.sc[e][g] = 0u;
-        }
+    for (int n = 0; n < N; n++) {
+#pragma unroll
+      for (int e = 0; e < 2; e++) load_words<NG>(vs[n][e], rec[n] + R::kValScale + (gl + 8 * e) * (4 * NG));
+      if (MASK && valid[n] < kKvqPage) {
+        // rows past the sequence may hold anything, NaN scales included
+#pragma unroll
+        for (int e = 0; e < 2; e++)
+          if (gl + 8 * e >= valid[n]) {
+            x[n][e][0] = x[n][e][1] = -INFINITY;
+#pragma unroll
+            for (int g = 0; g < NG; g++) vs[n][e][g] = 0u;
+          }
+      }
     }
-    float p[2][2], w[NG][2][2];
+    float p[N][2][2], top;
+    uint32_t wt[PT][N][NG][2];             // weights of both heads, FP16 (high halves, low halves)
     auto weights = [&]() {
+      top = 0.f;
 #pragma unroll
-      for (int e = 0; e < 2; e++)
+      for (int n = 0; n < N; n++)
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-          p[e][h] = ex2(x[e][h] - r[h]);
+        for (int e = 0; e < 2; e++) {
+          p[n][e][0] = ex2(x[n][e][0] - r[0]);
+          p[n][e][1] = ex2(x[n][e][1] - r[1]);
+          top = fmaxf(fmaxf(top, p[n][e][0]), p[n][e][1]);
 #pragma unroll
-          for (int g = 0; g < NG; g++) w[g][e][h] = p[e][h] * bf16lo(vl.sc[e][g]) * sc[g][h];
+          for (int g = 0; g < NG; g++) {
+            const float w0 = p[n][e][0] * bf16lo(vs[n][e][g]) * sc[g][0], w1 = p[n][e][1] * bf16lo(vs[n][e][g]) * sc[g][1];
+            top = fmaxf(fmaxf(top, w0), w1);
+            const uint32_t hi = pack_h2(w0, w1);
+            wt[0][n][g][e] = hi;
+            if constexpr (PT == 2) {
+              const float2 hv = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+              wt[1][n][g][e] = pack_h2(w0 - hv.x, w1 - hv.y);
+            }
+          }
         }
     };
     weights();
-    float top = 0.f;
-#pragma unroll
-    for (int e = 0; e < 2; e++)
-#pragma unroll
-      for (int h = 0; h < 2; h++) {
-        top = fmaxf(top, p[e][h]);
-#pragma unroll
-        for (int g = 0; g < NG; g++) top = fmaxf(top, w[g][e][h]);
-      }
     if (__any_sync(0xffffffffu, top > kTop)) {
 #pragma unroll
       for (int h = 0; h < 2; h++) {
-        float m = fmaxf(x[0][h], x[1][h]);
+        float m = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < N; n++) m = fmaxf(m, fmaxf(x[n][0][h], x[n][1][h]));
 #pragma unroll
         for (int sh = 4; sh < 32; sh <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, sh));
         const float rn = fmaxf(r[h], m - kHead);
@@ -457,7 +475,11 @@ struct KvqAttn {
 #pragma unroll
         for (int g = 0; g < NG; g++) {
           om[g][h] *= al;
-          float t = fmaxf(ex2(x[0][h] - rn) * bf16lo(vl.sc[0][g]), ex2(x[1][h] - rn) * bf16lo(vl.sc[1][g]));
+          float t = 0.f;
+#pragma unroll
+          for (int n = 0; n < N; n++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) t = fmaxf(t, ex2(x[n][e][h] - rn) * bf16lo(vs[n][e][g]));
 #pragma unroll
           for (int sh = 4; sh < 32; sh <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, sh));
           // at most what keeps the old weights where they were, and this page's within the headroom; a power
@@ -476,34 +498,36 @@ struct KvqAttn {
       weights();
     }
 #pragma unroll
-    for (int h = 0; h < 2; h++) {
-      l[h] += p[0][h] + p[1][h];
+    for (int n = 0; n < N; n++)
 #pragma unroll
-      for (int g = 0; g < NG; g++)
-        om[g][h] = fmaf(p[1][h], fmaf(8.f, bf16lo(vl.sc[1][g]), bf16hi(vl.sc[1][g])),
-                        fmaf(p[0][h], fmaf(8.f, bf16lo(vl.sc[0][g]), bf16hi(vl.sc[0][g])), om[g][h]));
-    }
+      for (int h = 0; h < 2; h++) {
+        l[h] += p[n][0][h] + p[n][1][h];
 #pragma unroll
-    for (int g = 0; g < NG; g++) {
-      // W^T as the B operand: the score tiles [token][head] transposed
-      uint32_t b[PT][2];
-#pragma unroll
-      for (int e = 0; e < 2; e++) {
-        const uint32_t hi = pack_h2(w[g][e][0], w[g][e][1]);
-        b[0][e] = movm_trans(hi);
-        if constexpr (PT == 2) {
-          const float2 hv = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-          b[1][e] = movm_trans(pack_h2(w[g][e][0] - hv.x, w[g][e][1] - hv.y));
-        }
+        for (int g = 0; g < NG; g++)
+          om[g][h] = fmaf(p[n][1][h], fmaf(8.f, bf16lo(vs[n][1][g]), bf16hi(vs[n][1][g])),
+                          fmaf(p[n][0][h], fmaf(8.f, bf16lo(vs[n][0][g]), bf16hi(vs[n][0][g])), om[g][h]));
       }
 #pragma unroll
-      for (int u = 0; u < 2; u++) {
-        const int j = 2 * g + u;
-        const uint32_t a = vl.w[0][j], c = vl.w[1][j], a8 = a >> 8, c8 = c >> 8;
-        const uint32_t c0[4] = {centred(a), centred16(a), centred(c), centred16(c)};
-        const uint32_t c1[4] = {centred(a8), centred16(a8), centred(c8), centred16(c8)};
-        add_tile(o[2 * j], c0, b);
-        add_tile(o[2 * j + 1], c1, b);
+    for (int n = 0; n < N; n++) {
+      uint32_t v[2][NW];
+      load_values<STAGED>(v, rec[n], lane);
+#pragma unroll
+      for (int g = 0; g < NG; g++) {
+        // W^T as the B operand: the score tiles [token][head] transposed
+        uint32_t b[PT][2];
+#pragma unroll
+        for (int t = 0; t < PT; t++)
+#pragma unroll
+          for (int e = 0; e < 2; e++) b[t][e] = movm_trans(wt[t][n][g][e]);
+#pragma unroll
+        for (int u = 0; u < 2; u++) {
+          const int j = 2 * g + u;
+          const uint32_t a = v[0][j], c = v[1][j], a8 = a >> 8, c8 = c >> 8;
+          const uint32_t c0[4] = {centred(a), centred16(a), centred(c), centred16(c)};
+          const uint32_t c1[4] = {centred(a8), centred16(a8), centred(c8), centred16(c8)};
+          add_tile(o[2 * j], c0, b);
+          add_tile(o[2 * j + 1], c1, b);
+        }
       }
     }
   }

@@ -106,8 +106,13 @@ int attention_sms(const mk_config& c, int n_sm, int batch, const int32_t* seq_le
   // on the 30B/3.3B model: 40 attention SMs at batch 1 with 8K context
   // (w = 1.6), 128 at 256K, 20-24 at batch 4 with 8K, 22-26 at batch 16 with
   // contexts of 1K-32K.
+  // The 4-bit cache moves 28 % of the bytes, but its attention is bound by
+  // instructions, about as many a token as over BF16: the same byte count with
+  // a fit of its own (56 attention SMs at 8K, the best of 40 .. 88; 128 at 256K,
+  // the best of 96 .. 140; 52 at batch 16, the best of 28 .. 72).
+  const bool q4 = c.kv_format == MK_KV_INT4;
   const double mean_ctx = keys / batch;
-  const double w = 1.6 * pow(8192.0 / mean_ctx, 0.22) / pow((double)batch, 0.45);
+  const double w = (q4 ? 2.6 : 1.6) * pow(8192.0 / mean_ctx, q4 ? 0.36 : 0.22) / pow((double)batch, 0.45);
   double ideal = n_sm * w * kv / (w * kv + moe);
   // several tokens: at least 16 % of the SMs on the attention branch, 23 %
   // from 8 tokens up.  As the contexts of a continuous batch shrink (short
@@ -115,7 +120,8 @@ int attention_sms(const mk_config& c, int n_sm, int batch, const int32_t* seq_le
   // branch's per-byte cost (its multi-token GEMVs) does not follow; with the
   // expert tiles claimed, 36 of 152 SMs (32 within 0.5 %) were the best
   // fixed split over whole batch-16 runs and 24 over batch-4 runs.
-  if (batch > 1) ideal = std::max(ideal, (batch >= 8 ? 0.23 : 0.16) * n_sm);
+  // With the 4-bit cache the best at batch 16 is 0.34, 1.5 times that.
+  if (batch > 1) ideal = std::max(ideal, (batch >= 8 ? (q4 ? 0.34 : 0.23) : (q4 ? 0.24 : 0.16)) * n_sm);
   // in steps of 4 SMs on a large GPU: each split has its own task lists,
   // built and uploaded the first time it is used, and the contexts of a
   // continuous batch move the ideal split by a few SMs every step

@@ -130,15 +130,18 @@ def attention(q, keys, values, hkv, scale):
     return out, spread, score
 
 
-def attention_tolerance(out, spread, score, n, d, f32):
+def attention_tolerance(out, spread, score, n, d, f32, q_bits=24):
     """How far the kernel may be from ``out``, from its roundings:
     a weight is 2^(x + log2 step): x sums d products in fp32 (at most d + 8 roundings, each at most 2^-23 of the
     sum of absolute terms: the tensor cores may truncate), fp32 queries carry 22 bits; 2^x and log2 are good to
     2^-21; a weight is rounded to 11 bits (BF16 call) or 22 (fp32); the sums over n tokens round once per page
     and once per merge, each at most 2^-22 of the sum of absolute terms; the result is rounded to its type.  Errors
-    of numerator and denominator add up: the factor 2."""
+    of numerator and denominator add up: the factor 2.  q_bits = 11: the query was rounded to 11 bits, each of its
+    elements by at most 2^-11."""
     weight = np.log(2) * ((d + 8) * 2.0 ** -23 + 2.0 ** -22) * score + 2.0 ** -20
     weight = weight + (2.0 ** -21 if f32 else 2.0 ** -11)
+    if q_bits == 11:
+        weight = weight + np.log(2) * 2.0 ** -11 * score
     sums = (n / PAGE + 512) * 2.0 ** -22
     half_step = 2.0 ** -24 if f32 else 2.0 ** -8
     return half_step * np.abs(out) + 2 * (weight[:, None] + sums) * spread + 1e-38

@@ -95,8 +95,8 @@ def check_cache_and_attention(run, before, lens, tables, layers):
                 # the steps are the smallest that cover the group: low and step each round by less than 2^-7
                 assert (15 * s <= (span + 2.0 ** -7 * np.abs(g.min(-1))[..., None]) * (1 + 2.0 ** -6) + 1e-30).all()
             ref, spread, score = _kvq.attention(q, keys, values, hkv, dim ** -0.5)
-            # as the BF16 call's weights, but an fp32 result
-            tol = _kvq.attention_tolerance(ref, spread, score, n + 1, dim, False) - 2.0 ** -8 * np.abs(ref) \
+            # weights as in a BF16 call, q rounded to 11 bits, an fp32 result
+            tol = _kvq.attention_tolerance(ref, spread, score, n + 1, dim, False, 11) - 2.0 ** -8 * np.abs(ref) \
                 + 2.0 ** -23 * np.abs(ref)
             assert (np.abs(att[b] - ref) <= tol).all(), (l, b, float((np.abs(att[b] - ref) / tol).max()))
 

@@ -510,11 +510,12 @@ int mk_kvq_write(const mk_kvq_cache* c, const mk_kv_rows* src, const int32_t* sr
 int mk_kvq_read(const mk_kvq_cache* c, const int32_t* src_index, const mk_kv_rows* dst, const int32_t* dst_index,
                 int n, int unit, void* stream);
 
-/* Workspace bytes of mk_kvq_attention on the current device, for any lengths
- * and batch (about 2.6 MB); 0 if the arguments are not supported.  It needs no
- * preparation.  Calls that may run at the same time, or two captured graphs
- * that may, need a workspace each. */
-size_t mk_kvq_workspace(const mk_kvq_cache* c, int n_q_heads, int batch);
+/* Workspace bytes of mk_kvq_attention with these arguments on the current
+ * device, for any lengths: 0 (none: NULL will do) where the page tables are
+ * short, else about 2.6 MB; also 0 if the arguments are not supported.  It
+ * needs no preparation.  Calls that may run at the same time, or two captured
+ * graphs that may, need a workspace each. */
+size_t mk_kvq_workspace(const mk_kvq_cache* c, int type, int n_q_heads, int batch, int max_pages);
 
 /* Attention of one query token per sequence over its cached tokens:
  *   out[b][h] = sum_t softmax_t(scale q[b][h] . k_t) v_t,  t < seq_lens[b],
@@ -533,7 +534,7 @@ size_t mk_kvq_workspace(const mk_kvq_cache* c, int n_q_heads, int batch);
  * be q.  Errors: MK_ERR_BAD_CONFIG (cache shape, n_q_heads no multiple of
  * n_kv_heads or above 65536), MK_ERR_BATCH_TOO_LARGE (batch outside
  * 0..65535), MK_ERR_BAD_ARG (also a workspace smaller than
- * mk_kvq_workspace; none is needed with max_pages <= 8), MK_ERR_CUDA. */
+ * mk_kvq_workspace), MK_ERR_CUDA. */
 int mk_kvq_attention(const mk_kvq_cache* c, const void* q, int64_t q_stride, void* out, int64_t out_stride, int type,
                      int n_q_heads, int batch, const int32_t* page_tables, int max_pages, const int32_t* seq_lens,
                      float scale, void* workspace, size_t workspace_bytes, void* stream);

@@ -130,18 +130,27 @@ __device__ __forceinline__ bool unit_pair(const Cache& c, const int32_t* src_ind
 constexpr int kCopyThreads = 256;
 
 // The thread's eight dims of a token call: block (x, y) takes kTokens tokens of
-// head y, eight threads a (token, key or value, group)
+// head y, eight threads a (token, key or value, group).  The call's tokens 2 k
+// and 2 k + 1 are kPartner lanes apart in a warp: where they lie side by side
+// in the cache (a prompt's do), their value codes, 16 bits of a word each, are
+// exchanged and moved as whole words.
 template <int D>
 struct TokenLane {
-  static constexpr int NG = D / kKvqGroup;
+  static constexpr int NG = D / kKvqGroup, kPartner = 8 * NG;
   static constexpr int kTokens = kCopyThreads / 8 / (2 * NG);
-  int wi, group, val, i;
+  int wi, group, val, odd, i;
   __device__ __forceinline__ TokenLane() {
     const int o = threadIdx.x >> 3;
     wi = threadIdx.x & 7;
     group = o % NG;
-    val = o / NG & 1;
-    i = blockIdx.x * kTokens + o / (2 * NG);
+    odd = o / NG & 1;
+    val = o / (2 * NG) & 1;
+    i = blockIdx.x * kTokens + o / (4 * NG) * 2 + odd;
+  }
+  // this thread's slot and its partner's are the two halves of a pair
+  __device__ __forceinline__ bool paired(int slot) const {
+    const int other = __shfl_xor_sync(0xffffffffu, slot, kPartner);
+    return val && slot >= 0 && other == (slot ^ 1) && (slot & 1) == odd;
   }
 };
 
@@ -151,18 +160,25 @@ __global__ void __launch_bounds__(kCopyThreads) kvq_write_kernel(Cache c, Rows s
   using R = KvqRec<D>;
   const TokenLane<D> o;
   const int head = blockIdx.y;
-  int from, to;
-  if (o.i >= n || !unit_pair(c, src_index, src.count, dst_index, c.pages * kKvqPage, o.i, from, to) || from < 0)
-    return;                                // all eight threads of a group alike
-  Raw8<T> raw;
-  raw.load((const T*)(o.val ? src.v : src.k) + from * src.row + head * src.head + o.group * kKvqGroup + o.wi * 8);
-  float x[8];
-  raw.get(x);
-  const KvqScale s = kvq_group_scale(x, 0xffu << (threadIdx.x & 24));
+  int from = -1, to = -1;
+  const bool live = o.i < n &&
+                    unit_pair(c, src_index, src.count, dst_index, c.pages * kKvqPage, o.i, from, to) && from >= 0;
+  float x[8] = {};
+  if (live) load8(x, (const T*)(o.val ? src.v : src.k) + from * src.row + head * src.head + o.group * kKvqGroup + o.wi * 8);
+  const KvqScale s = kvq_group_scale(x, 0xffffffffu);
   const uint32_t word = kvq_codes(x, s);
+  const bool pair = o.paired(live ? to : -1);
+  const uint32_t other = __shfl_xor_sync(0xffffffffu, word, TokenLane<D>::kPartner);
+  if (!live) return;
   const int t = to % kKvqPage;
   uint8_t* rec = c.pool + ((long long)(to / kKvqPage) * c.hkv + head) * R::kBytes;
-  kvq_store_row<D>(rec, t, o.wi, o.group, o.val, word, s);
+  if (pair) {
+    *(uint32_t*)(rec + R::val_half(t & ~1, o.wi, o.group, o.odd)) =
+        o.odd ? __byte_perm(other, word, 0x7632) : __byte_perm(word, other, 0x5410);
+    if (o.wi == 0) *(uint32_t*)(rec + R::kValScale + 4 * (t * R::NG + o.group)) = s.word();
+  } else {
+    kvq_store_row<D>(rec, t, o.wi, o.group, o.val, word, s);
+  }
 }
 
 template <int D, class T>
@@ -171,20 +187,29 @@ __global__ void __launch_bounds__(kCopyThreads) kvq_read_kernel(Cache c, const i
   using R = KvqRec<D>;
   const TokenLane<D> o;
   const int head = blockIdx.y;
-  int from, to;
-  if (o.i >= n || !unit_pair(c, src_index, c.pages * kKvqPage, dst_index, dst.count, o.i, from, to)) return;
-  float x[8] = {};
+  int from = -1, to = -1;
+  const bool live =
+      o.i < n && unit_pair(c, src_index, c.pages * kKvqPage, dst_index, dst.count, o.i, from, to);
+  if (!live) from = -1;
+  const bool pair = o.paired(from);
+  uint32_t word = 0, scale = 0;            // no source: zeros
   if (from >= 0) {
     const int t = from % kKvqPage;
     const uint8_t* rec = c.pool + ((long long)(from / kKvqPage) * c.hkv + head) * R::kBytes;
-    uint32_t word;
-    if (o.val)
+    if (pair)
+      word = *(const uint32_t*)(rec + R::val_half(t & ~1, o.wi, o.group, o.odd));
+    else if (o.val)
       word = *(const uint16_t*)(rec + R::val_half(t, o.wi, o.group, 0)) |
              ((uint32_t)*(const uint16_t*)(rec + R::val_half(t, o.wi, o.group, 1)) << 16);
     else
       word = *(const uint32_t*)(rec + R::key_word(t, o.wi, o.group));
-    kvq_values(x, word, *(const uint32_t*)(rec + (o.val ? R::kValScale : R::kKeyScale) + 4 * (t * R::NG + o.group)));
+    scale = *(const uint32_t*)(rec + (o.val ? R::kValScale : R::kKeyScale) + 4 * (t * R::NG + o.group));
   }
+  const uint32_t other = __shfl_xor_sync(0xffffffffu, word, TokenLane<D>::kPartner);
+  if (!live) return;
+  if (pair) word = o.odd ? __byte_perm(other, word, 0x7632) : __byte_perm(word, other, 0x5410);
+  float x[8];
+  kvq_values(x, word, scale);
   Raw8<T> raw;
   raw.set(x);
   raw.store((T*)(o.val ? dst.v : dst.k) + to * dst.row + head * dst.head + o.group * kKvqGroup + o.wi * 8);
@@ -319,8 +344,8 @@ __global__ void __launch_bounds__(kCopyThreads) kvq_read_pages_kernel(Cache c, c
 // The pages of all tasks (sequence, KV head, 8 of its query heads) are cut
 // into segments by the blocks themselves from the lengths on the device, so
 // the host neither reads lengths nor launches for the longest one:
-//   few pages (less than two segments a block): segments of kMinPages pages,
-//     one page a warp, dealt to the blocks in turn;
+//   few pages (no more than a segment a block): segments of kMinPages pages,
+//     one page a warp;
 //   many: block i takes units T i / G .. T (i + 1) / G of the T units of all
 //     tasks in order (a unit is a page, a task's last segment rounded up), so
 //     every block moves the same bytes whatever the mix of lengths.
@@ -332,8 +357,9 @@ constexpr int kAttnWarps = 8;
 constexpr int kAttnThreads = kAttnWarps * 32;
 // resident blocks: the fp32 kernel with 128 dims needs more than the 128
 // registers a thread that two blocks leave
+constexpr int attn_per_sm(int d, int type) { return d == 128 && type == MK_TYPE_F32 ? 1 : 2; }
 template <int D, class T>
-constexpr int kBlocksPerSm = D == 128 && sizeof(T) == 4 ? 1 : 2;
+constexpr int kBlocksPerSm = attn_per_sm(D, sizeof(T) == 4 ? MK_TYPE_F32 : MK_TYPE_BF16);
 constexpr int kMinPages = kAttnWarps;
 constexpr int kRing = 4;                   // pages of a warp, in flight and in use
 
@@ -346,7 +372,6 @@ struct AttnArgs {
   uint8_t* ws;                             // AttnWs
   long long q_stride, out_stride;          // elements between two sequences
   int grp, tiles, batch, max_pages;        // tiles = ceil(grp / 8)
-  int split;                               // 0: every task is one segment
   float scale_log2;
 };
 
@@ -363,9 +388,9 @@ struct AttnWs {
   float* data;
 };
 
-__host__ __device__ inline size_t attn_slot_floats(int d) { return 8 * (size_t)d + 16; }
+__host__ __device__ constexpr size_t attn_slot_floats(int d) { return 8 * (size_t)d + 16; }
 
-__host__ __device__ inline size_t attn_ws_bytes(int blocks, int d) {
+__host__ __device__ constexpr size_t attn_ws_bytes(int blocks, int d) {
   const size_t slots = 2 * (size_t)blocks;
   return 16 + slots * sizeof(AttnSlot) + slots * attn_slot_floats(d) * 4;
 }
@@ -377,8 +402,9 @@ __device__ __forceinline__ AttnWs attn_ws(uint8_t* p, int blocks) {
 __device__ __forceinline__ void stf(uint16_t* p, float v) { *p = f2bf(v); }
 __device__ __forceinline__ void stf(float* p, float v) { *p = v; }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// 16 bytes, of which `bytes` (16 or 0) are read and the rest are zeros
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -497,6 +523,7 @@ struct AttnBlock {
     const int n = (p1 - p0 - warp + kAttnWarps - 1) / kAttnWarps;   // this warp's pages (may be <= 0)
     bool bad = false;
     int fetched = 0, id = n > 0 ? table[0] : 0;   // the next page to fetch, read an iteration ahead
+    const int last = max(n - 1, 0) * kAttnWarps;
     const uint8_t* base = a.c.pool + (long long)g * R::kBytes + lane * 16;
     const long long page_bytes = (long long)a.c.hkv * R::kBytes;
     // the lane's 16-byte chunks lie 512 bytes apart, in the ring slot too: value chunks from one place (32 of
@@ -504,17 +531,18 @@ struct AttnBlock {
     constexpr int kVal0 = R::kVal / 512, kVal1 = R::kKeyScale / 512;
     const uint32_t line = smem_u32(ring) + lane * 16;
     const uint32_t line_v = smem_u32(ring) + A::staged(R::kVal / 16 + lane) * 16 - R::kVal;
-    auto fetch = [&](uint32_t slot) {      // the warp's next page into the ring, `slot` bytes in
-      if (fetched < n) {
-        const bool ok = (unsigned)id < (unsigned)a.c.pages;
-        bad |= !ok;
-        const uint8_t* src = base + (ok ? id : 0) * page_bytes;
+    // the warp's next page into the ring, `slot` bytes in; without branches: past the warp's last page nothing is read
+    auto fetch = [&](uint32_t slot) {
+      const bool live = fetched < n, ok = (unsigned)id < (unsigned)a.c.pages;
+      bad |= live && !ok;
+      const uint8_t* src = base + (ok ? id : 0) * page_bytes;
+      const int bytes = live ? 16 : 0;
 #pragma unroll
-        for (int k = 0; k < kChunks; k++)
-          if (k * 32 + 32 <= R::kBytes / 16 || k * 32 + lane < R::kBytes / 16)
-            cp_async16((k >= kVal0 && k < kVal1 ? line_v : line) + slot + k * 512, src + k * 512);
-        if (++fetched < n) id = table[(long long)fetched * kAttnWarps];
-      }
+      for (int k = 0; k < kChunks; k++)
+        if (k * 32 + 32 <= R::kBytes / 16 || k * 32 + lane < R::kBytes / 16)
+          cp_async16((k >= kVal0 && k < kVal1 ? line_v : line) + slot + k * 512, src + k * 512, bytes);
+      fetched++;
+      if (n > 0) id = table[min(fetched * kAttnWarps, last)];
       cp_async_commit();
     };
 #pragma unroll
@@ -628,7 +656,7 @@ __global__ void __launch_bounds__(kAttnThreads, kBlocksPerSm<D, T>) kvq_attentio
   plan_window(a, S, 0, 0, 0);
   while (plan_next(a, S)) {}
   const unsigned long long total = (unsigned long long)S.end * HT;
-  if (me == 0 && tid == 0 && a.split) *attn_ws(a.ws, G).count = S.split_end * HT;   // changed below with whole shares
+  if (me == 0 && tid == 0) *attn_ws(a.ws, G).count = S.split_end * HT;   // changed below with whole shares
   if (a.batch > kAttnThreads) {
     __syncthreads();
     plan_window(a, S, 0, 0, 0);
@@ -636,7 +664,7 @@ __global__ void __launch_bounds__(kAttnThreads, kBlocksPerSm<D, T>) kvq_attentio
 
   const AttnWs ws = attn_ws(a.ws, G);
   Place at;
-  if (!a.split || total < 2ull * G * kMinPages) {
+  if (total <= (unsigned long long)G * kMinPages) {
     // segment s is the s-th chunk of kMinPages pages
     for (long long s = me; plan_find(a, S, s / HT * kMinPages, at); s += G) {
       const int nc = seq_units(at.np) / kMinPages;
@@ -675,6 +703,75 @@ __global__ void __launch_bounds__(kAttnThreads, kBlocksPerSm<D, T>) kvq_attentio
       u += step;
     }
   }
+}
+
+// Short page tables: a cluster of up to kMaxCluster blocks takes a task, page
+// ranges of equal length, and merges over distributed shared memory: one
+// launch, no workspace, no plan (attn_cluster below has the rule).
+constexpr int kMaxCluster = 16;
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
+template <int D, class T>
+__global__ void __launch_bounds__(kAttnThreads, kBlocksPerSm<D, T>) kvq_attention_cluster_kernel(AttnArgs a, int blocks) {
+  using B = AttnBlock<D, T>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(16) float part[attn_slot_floats(D)];
+  const int tid = threadIdx.x, HT = a.c.hkv * a.tiles, rank = blockIdx.x % blocks;
+  const long long task = blockIdx.x / blocks;
+  const int b = (int)(task / HT), j = (int)(task % HT);
+  const int np = seq_pages(a, b), n = max(np, 0);
+  if (np < 0 && rank == 0 && tid == 0) flag_bad(a.c, MK_ERR_BAD_ARG);
+  if (n > 0) B::segment(a, smem, b, j, (int)((long long)n * rank / blocks), (int)((long long)n * (rank + 1) / blocks), part);
+  cluster_sync();
+  const int heads = min(8, a.grp - j % a.tiles * 8);
+  for (int i = rank + blocks * tid; i < heads * (D / 4); i += blocks * kAttnThreads) {
+    const int h = i / (D / 4), dim = i % (D / 4) * 4;
+    float m = -FLT_MAX, den = 0.f, num[4] = {0.f, 0.f, 0.f, 0.f};
+    if (n > 0) {
+      constexpr int W = 8;                 // peers' loads in flight
+      for (int k0 = 0; k0 < blocks; k0 += W) {
+        float r[W], l[W];
+        float4 o[W];
+#pragma unroll
+        for (int k = 0; k < W; k++) {
+          r[k] = -FLT_MAX, l[k] = 0.f, o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (k0 + k < blocks) {
+            uint32_t peer;
+            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer) : "r"(smem_u32(part)), "r"(k0 + k));
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(r[k]) : "r"(peer + (8 * D + h) * 4));
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(l[k]) : "r"(peer + (8 * D + 8 + h) * 4));
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(o[k].x), "=f"(o[k].y), "=f"(o[k].z), "=f"(o[k].w)
+                         : "r"(peer + (h * D + dim) * 4));
+          }
+        }
+        float mn = m;
+#pragma unroll
+        for (int k = 0; k < W; k++) mn = fmaxf(mn, r[k]);
+        const float keep = ex2(m - mn);
+        m = mn;
+        den *= keep;
+#pragma unroll
+        for (int e = 0; e < 4; e++) num[e] *= keep;
+#pragma unroll
+        for (int k = 0; k < W; k++) {
+          const float c = ex2(r[k] - m);
+          num[0] = fmaf(c, o[k].x, num[0]);
+          num[1] = fmaf(c, o[k].y, num[1]);
+          num[2] = fmaf(c, o[k].z, num[2]);
+          num[3] = fmaf(c, o[k].w, num[3]);
+          den = fmaf(c, l[k], den);
+        }
+      }
+    }
+    T* dst = out_row<D, T>(a, b, j, h) + dim;
+#pragma unroll
+    for (int k = 0; k < 4; k++) stf(dst + k, n > 0 ? num[k] / den : np < 0 ? NAN : 0.f);
+  }
+  cluster_sync();                          // a block's shared memory stays until its peers have read it
 }
 
 constexpr int kMergeThreads = 256;
@@ -826,38 +923,78 @@ int check_heads(const mk_kvq_cache* c, int n_q_heads, int batch) {
 // blocks that fill the GPU, two slots each
 int attn_blocks(int sms, int per_sm) { return std::min(sms * per_sm, kMaxSlots / 2); }
 
+// Blocks of the cluster that takes a whole task, or 0: the two kernels with a
+// workspace.  The cluster is the largest power of two with which all tasks run
+// at once (half of the slots where it spans 8 SMs or more: a GPC holds two of
+// those at best).  Its warps then have `mine` pages each of the longest
+// sequence the page tables can hold, with all blocks sharing every page evenly
+// it would be `even`; a page costs a warp about a microsecond, the second
+// kernel and the plan about seven, and a batch with one long sequence among
+// short ones must not wait for one cluster.  Measured, cluster against two
+// kernels, 32 query and 4 KV heads of 128 dims: one sequence of 512 7.5 : 9.0 us, 8K
+// 10.2 : 12.7, 16K 12.3 : 20.4; four of 8K 17.5 : 19.6, sixteen up to 2K 12.9 : 23.2.
+int attn_cluster(long long tasks, int max_pages, int sms, int per_sm) {
+  const long long slots = (long long)sms * per_sm;
+  int n = 1;
+  while (n < kMaxCluster && n * kAttnWarps < max_pages && 2 * n * tasks <= (2 * n >= 8 * per_sm ? slots / 2 : slots))
+    n *= 2;
+  const long long mine = (max_pages + n * kAttnWarps - 1) / (n * kAttnWarps);
+  const long long even = tasks * max_pages / (slots * kAttnWarps);
+  return mine <= 12 && mine - even <= 8 && tasks * n <= 0x7fffffff ? n : 0;
+}
+
 template <int D, class T>
-int attention(const AttnArgs& a, int sms, cudaStream_t st) {
-  // the kernel's shared memory is raised once on each device
+int attention(AttnArgs& a, void* workspace, size_t workspace_bytes, int sms, cudaStream_t st) {
+  // the kernels' shared memory is raised once on each device
   static std::atomic<unsigned long long> raised[2];
   constexpr size_t smem = AttnBlock<D, T>::kSmem;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return MK_ERR_CUDA;
   if (!(raised[dev / 64].load(std::memory_order_relaxed) >> (dev % 64) & 1)) {
     if (cudaFuncSetAttribute(kvq_attention_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-        cudaSuccess) {
+            cudaSuccess ||
+        cudaFuncSetAttribute(kvq_attention_cluster_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)smem) != cudaSuccess ||
+        cudaFuncSetAttribute(kvq_attention_cluster_kernel<D, T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+            cudaSuccess) {
       cudaGetLastError();
       return MK_ERR_CUDA;
     }
     raised[dev / 64].fetch_or(1ull << (dev % 64), std::memory_order_relaxed);
   }
-  // no more blocks than there can be segments, unless some rows are empty
   const long long tasks = (long long)a.batch * a.c.hkv * a.tiles;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at{};
+  cfg.stream = st;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  const int cluster = attn_cluster(tasks, a.max_pages, sms, kBlocksPerSm<D, T>);
+  if (cluster) {
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = (unsigned)cluster;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)(tasks * cluster));
+    cfg.blockDim = dim3(kAttnThreads);
+    cfg.dynamicSmemBytes = smem;
+    if (cudaLaunchKernelEx(&cfg, kvq_attention_cluster_kernel<D, T>, a, cluster) != cudaSuccess) {
+      cudaGetLastError();
+      return MK_ERR_CUDA;
+    }
+    return MK_OK;
+  }
+  if (!workspace || !aligned(workspace, 16) || workspace_bytes < attn_ws_bytes(attn_blocks(sms, 2), D))
+    return MK_ERR_BAD_ARG;
+  a.ws = (uint8_t*)workspace;
+  // no more blocks than there can be segments
   const long long most = tasks * std::max(1, (a.max_pages + kMinPages - 1) / kMinPages);
   const int blocks = (int)std::min<long long>(attn_blocks(sms, kBlocksPerSm<D, T>), most);
   kvq_attention_kernel<D, T><<<blocks, kAttnThreads, smem, st>>>(a);
   if (cudaGetLastError() != cudaSuccess) return MK_ERR_CUDA;
-  if (!a.split) return MK_OK;
   // the merge is launched while the first kernel runs and waits for its end
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3((unsigned)std::min<long long>(sms, tasks * 8));
   cfg.blockDim = dim3(kMergeThreads);
-  cfg.stream = st;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, kvq_merge_kernel<D, T>, a, blocks) != cudaSuccess) {
     cudaGetLastError();
     return MK_ERR_CUDA;
@@ -928,10 +1065,14 @@ int mk_kvq_read(const mk_kvq_cache* c, const int32_t* src_index, const mk_kv_row
   return launched();
 }
 
-size_t mk_kvq_workspace(const mk_kvq_cache* c, int n_q_heads, int batch) {
-  if (check_cache(c) || check_heads(c, n_q_heads, batch)) return 0;
+size_t mk_kvq_workspace(const mk_kvq_cache* c, int type, int n_q_heads, int batch, int max_pages) {
+  if (check_cache(c) || check_heads(c, n_q_heads, batch) || max_pages < 0 || batch == 0) return 0;
   const int sms = sm_count();
-  return sms ? attn_ws_bytes(attn_blocks(sms, 2), c->head_dim) : 0;
+  if (!sms) return 0;
+  const int grp = n_q_heads / c->n_kv_heads;
+  const long long tasks = (long long)batch * c->n_kv_heads * ((grp + 7) / 8);
+  return attn_cluster(tasks, max_pages, sms, attn_per_sm(c->head_dim, type)) ? 0
+                                                                             : attn_ws_bytes(attn_blocks(sms, 2), c->head_dim);
 }
 
 int mk_kvq_attention(const mk_kvq_cache* c, const void* q, int64_t q_stride, void* out, int64_t out_stride, int type,
@@ -962,16 +1103,12 @@ int mk_kvq_attention(const mk_kvq_cache* c, const void* q, int64_t q_stride, voi
   a.batch = batch;
   a.max_pages = max_pages;
   a.scale_log2 = scale * 1.4426950408889634f;
-  a.split = max_pages > kMinPages;
-  if (a.split) {
-    if (!workspace || !aligned(workspace, 16) || workspace_bytes < attn_ws_bytes(attn_blocks(sms, 2), c->head_dim))
-      return MK_ERR_BAD_ARG;
-    a.ws = (uint8_t*)workspace;
-  }
   cudaStream_t st = (cudaStream_t)stream;
   if (c->head_dim == 128)
-    return type == MK_TYPE_BF16 ? attention<128, uint16_t>(a, sms, st) : attention<128, float>(a, sms, st);
-  return type == MK_TYPE_BF16 ? attention<64, uint16_t>(a, sms, st) : attention<64, float>(a, sms, st);
+    return type == MK_TYPE_BF16 ? attention<128, uint16_t>(a, workspace, workspace_bytes, sms, st)
+                                : attention<128, float>(a, workspace, workspace_bytes, sms, st);
+  return type == MK_TYPE_BF16 ? attention<64, uint16_t>(a, workspace, workspace_bytes, sms, st)
+                              : attention<64, float>(a, workspace, workspace_bytes, sms, st);
 }
 
 }  // extern "C"

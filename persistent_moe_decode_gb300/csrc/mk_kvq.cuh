@@ -460,7 +460,7 @@ struct KvqAttn {
         }
     };
     weights();
-    if (__any_sync(0xffffffffu, top > kTop)) {
+    if (__builtin_expect(__any_sync(0xffffffffu, top > kTop), 0)) {
 #pragma unroll
       for (int h = 0; h < 2; h++) {
         float m = -INFINITY;

@@ -54,7 +54,7 @@ class QuantCache:
         if pool.device.type != "cuda":
             raise ValueError(f"4-bit cache: the pool is on {pool.device}, not on a GPU")
         self.pool, self.n_kv_heads, self.head_dim = pool, n_kv_heads, head_dim
-        self._dev, self._ws_bytes = pool.get_device(), None
+        self._dev, self._ws_bytes = pool.get_device(), {}
         self._inner = {1: (n_kv_heads, head_dim), PAGE_SIZE: (n_kv_heads, PAGE_SIZE, head_dim)}
         self.status = torch.zeros(1, dtype=torch.int32, device=pool.device)
         self._c = mk.mk_kvq_cache(pool=pool.data_ptr(), num_pages=pool.shape[0], n_kv_heads=n_kv_heads,
@@ -183,10 +183,14 @@ class QuantCache:
             raise ValueError(f"out: {dtype} {tuple(shape)} on {self.pool.device}, rows of consecutive heads at "
                              "16-byte strides")
         # the workspace belongs to this call's stream, or to the graph that captures it
-        if self._ws_bytes is None:
-            self._ws_bytes = mk.mk_kvq_workspace(self._c, self.n_kv_heads, 1)
-        ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=q.device)
-        mk.mk_kvq_attention(self._c, q.data_ptr(), q.stride(0), out.data_ptr(), out.stride(0), _TYPES[dtype], hq,
-                            batch, page_tables.data_ptr(), page_tables.shape[1], seq_lens.data_ptr(),
-                            d ** -0.5 if scale is None else scale, ws.data_ptr(), self._ws_bytes, st)
+        max_pages, kind = page_tables.shape[1], _TYPES[dtype]
+        n = self._ws_bytes.get((kind, hq, batch, max_pages))     # a function of these alone
+        if n is None:
+            if len(self._ws_bytes) >= 1024:
+                self._ws_bytes.clear()
+            n = self._ws_bytes[kind, hq, batch, max_pages] = mk.mk_kvq_workspace(self._c, kind, hq, batch, max_pages)
+        ws = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+        mk.mk_kvq_attention(self._c, q.data_ptr(), q.stride(0), out.data_ptr(), out.stride(0), kind, hq, batch,
+                            page_tables.data_ptr(), max_pages, seq_lens.data_ptr(), d ** -0.5 if scale is None else scale,
+                            ws.data_ptr() if n else None, n, st)
         return out

@@ -128,7 +128,7 @@ def lib():
             L.mk_kvq_page_bytes.restype = C.c_size_t
             L.mk_kvq_write.argtypes = [kvc, kvr, vp, vp, i32, i32, vp]
             L.mk_kvq_read.argtypes = [kvc, vp, kvr, vp, i32, i32, vp]
-            L.mk_kvq_workspace.argtypes = [kvc, i32, i32]
+            L.mk_kvq_workspace.argtypes = [kvc, i32, i32, i32, i32]
             L.mk_kvq_workspace.restype = C.c_size_t
             L.mk_kvq_attention.argtypes = [kvc, vp, C.c_int64, vp, C.c_int64, i32, i32, i32, vp, i32, vp,
                                            C.c_float, vp, C.c_size_t, vp]
@@ -350,8 +350,8 @@ def mk_kvq_read(cache: mk_kvq_cache, src_index_ptr, dst: mk_kv_rows, dst_index_p
                   "mk_kvq_read")
 
 
-def mk_kvq_workspace(cache: mk_kvq_cache, n_q_heads: int, batch: int) -> int:
-    return int(lib().mk_kvq_workspace(cache, n_q_heads, batch))
+def mk_kvq_workspace(cache: mk_kvq_cache, dtype: int, n_q_heads: int, batch: int, max_pages: int) -> int:
+    return int(lib().mk_kvq_workspace(cache, dtype, n_q_heads, batch, max_pages))
 
 
 def mk_kvq_attention(cache: mk_kvq_cache, q_ptr: int, q_stride: int, out_ptr: int, out_stride: int, dtype: int,

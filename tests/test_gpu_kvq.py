@@ -257,6 +257,29 @@ def test_attention_of_long_and_uneven_contexts(hkv, grp, d, lens, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("spare", [40, 300, 3001])
+@pytest.mark.parametrize("lens", [[1], [17, 0, 1], [700, 128, 129, 0], [0, 0], [5, 2000, 64, 0, 1023], [16] * 70],
+                         ids=lambda x: "-".join(map(str, x[:5])))
+def test_attention_with_wide_page_tables(lens, spare, d, dtype):
+    """Room for far longer sequences than there are: every way of cutting the pages, at every length."""
+    rng = np.random.default_rng(spare + d)
+    pool, table, q = attention_case(rng, 2, 4, d, lens, dtype, spare=spare)
+    check_attention(run_attention(pool, table, q, lens, 2), pool, table, q, lens, 2)
+
+
+@pytest.mark.parametrize("batch,n", [(300, 40), (700, 0), (1500, 20)])
+def test_attention_of_a_large_batch(batch, n):
+    """More sequences than one window of the plan, idle ones and one long one among them."""
+    rng = np.random.default_rng(batch)
+    lens = rng.integers(0, n + 1, size=batch)
+    lens[rng.random(batch) < 0.2] = 0
+    lens[batch // 2 + 7] = 3000
+    pool, table, q = attention_case(rng, 1, 2, 64, [int(x) for x in lens], torch.bfloat16)
+    check_attention(run_attention(pool, table, q, [int(x) for x in lens], 1), pool, table, q, lens, 1)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("kw", [
     dict(qmul=30.0),                                                # one key takes nearly all
     dict(qmul=1e-3),                                                # nearly uniform weights
@@ -310,6 +333,17 @@ def test_attention_scale_strides_and_output_rows():
     same = q.cuda()
     c.attention(same, tb, ln, scale=0.3, out=same)
     assert torch.equal(same, got)
+    # a workspace that is missing, short or misaligned is refused; short page tables need none
+    from persistent_moe_decode_gb300 import mk
+    need = mk.mk_kvq_workspace(c._c, mk.MK_TYPE_BF16, 8, 3, 5000)
+    ws = torch.empty(need + 16, dtype=torch.uint8, device="cuda")
+    args = (c._c, q.cuda().data_ptr(), 8 * d, got.data_ptr(), 8 * d, mk.MK_TYPE_BF16, 8, 3, tb.data_ptr(), 5000,
+            ln.data_ptr(), 0.3)
+    for ptr, n in ((None, need), (ws.data_ptr(), need - 1), (ws.data_ptr() + 8, need)):
+        with pytest.raises(mk.MkError) as e:
+            mk.mk_kvq_attention(*args, ptr, n)
+        assert e.value.code == mk.MK_ERR_BAD_ARG
+    assert need > 0 and mk.mk_kvq_workspace(c._c, mk.MK_TYPE_BF16, 8, 3, tb.shape[1]) == 0
     # nothing to do
     assert c.attention(q.cuda()[:0], tb[:0], ln[:0]).shape == (0, 8, d)
     none = c.attention(q.cuda(), tb[:, :0], torch.zeros_like(ln))

@@ -73,7 +73,7 @@ def test_bad_caches(lib, bad, code):
     assert lib.mk_kvq_write(C.byref(c), C.byref(r), P, P, 1, 1, None) == code
     assert lib.mk_kvq_read(C.byref(c), P, C.byref(r), P, 1, 1, None) == code
     assert lib.mk_kvq_attention(C.byref(c), P, 256, P, 256, 0, 4, 1, P, 4, P, 1.0, None, 0, None) == code
-    assert mk.mk_kvq_workspace(c, 4, 1) == 0
+    assert mk.mk_kvq_workspace(c, 0, 4, 1, 4000) == 0
 
 
 @pytest.mark.parametrize("bad", [dict(k=None), dict(v=None), dict(k=P + 8), dict(type=2), dict(count=-1),

@@ -229,8 +229,9 @@ struct KvqAttn {
   float r[2], l[2], sc[NG][2], om[NG][2];
   float o[NT][4];
 
-  // the largest weight after the references move (log2, and itself), the limit before; sc's own limit
-  static constexpr float kHead = 8.f, kHeadW = 256.f, kTop = 32768.f, kScMax = 0x1p120f;
+  // log2 of the largest weight after the references move, the limit before; sc's own limit and its exponent field
+  static constexpr float kHead = 8.f, kTop = 32768.f, kScMax = 0x1p120f;
+  static constexpr int kScMaxExp = 247;
 
   template <int N>
   static __device__ __forceinline__ void load_words(uint32_t* dst, const uint8_t* p) {
@@ -469,7 +470,7 @@ struct KvqAttn {
 #pragma unroll
         for (int sh = 4; sh < 32; sh <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, sh));
         const float rn = fmaxf(r[h], m - kHead);
-        const float al = ex2(r[h] - rn);
+        const float al = ex2(r[h] - rn), up = ex2(rn - r[h]);
         r[h] = rn;
         l[h] *= al;
 #pragma unroll
@@ -482,11 +483,12 @@ struct KvqAttn {
             for (int e = 0; e < 2; e++) t = fmaxf(t, ex2(x[n][e][h] - rn) * bf16lo(vs[n][e][g]));
 #pragma unroll
           for (int sh = 4; sh < 32; sh <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, sh));
-          // at most what keeps the old weights where they were, and this page's within the headroom; a power
-          // of two (the exponent alone), so that it rounds nothing
-          float s = fminf(fminf(sc[g][h] / al, kHeadW / t), kScMax);
+          // at most what keeps the old weights where they were, and this page's within 2^8; a power of two (the
+          // exponent alone), so that it rounds nothing, and its inverse is another exponent
+          const float fit = __uint_as_float((uint32_t)min(kScMaxExp, 261 - (int)(__float_as_uint(t) >> 23)) << 23);
+          float s = fminf(sc[g][h] * up, fit);
           s = __uint_as_float(__float_as_uint(s) & 0x7f800000u);
-          const float be = al == 0.f ? 0.f : al * (s / sc[g][h]);
+          const float be = al == 0.f ? 0.f : al * (s * __uint_as_float(0x7f000000u - __float_as_uint(sc[g][h])));
           sc[g][h] = s;
 #pragma unroll
           for (int i = 0; i < 4; i++) {

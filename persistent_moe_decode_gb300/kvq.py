@@ -157,8 +157,7 @@ class QuantCache:
     def _read_rows(self, st, slots, dtype):
         if dtype not in _TYPES:
             raise ValueError(f"dtype: BF16 or fp32, got {dtype}")
-        k = torch.empty((slots.shape[0], *self._inner[1]), dtype=dtype, device=self.pool.device)
-        v = torch.empty_like(k)
+        k, v = torch.empty((2, slots.shape[0], *self._inner[1]), dtype=dtype, device=self.pool.device).unbind()
         self._read(st, slots, k, v, None, 1)
         return k, v
 

@@ -75,6 +75,14 @@ struct Raw8 {
   }
 };
 
+// scale of the group of which a thread holds `raw`, as fp32 x
+__device__ __forceinline__ KvqScale row_scale(const Raw8<uint16_t>& raw, const float*, unsigned mask) {
+  return kvq_group_scale(raw.w, mask);
+}
+__device__ __forceinline__ KvqScale row_scale(const Raw8<float>&, const float* x, unsigned mask) {
+  return kvq_group_scale(x, mask);
+}
+
 template <class T>
 __device__ __forceinline__ void load8(float* x, const T* p) {
   Raw8<T> r;
@@ -163,9 +171,11 @@ __global__ void __launch_bounds__(kCopyThreads) kvq_write_kernel(Cache c, Rows s
   int from = -1, to = -1;
   const bool live = o.i < n &&
                     unit_pair(c, src_index, src.count, dst_index, c.pages * kKvqPage, o.i, from, to) && from >= 0;
-  float x[8] = {};
-  if (live) load8(x, (const T*)(o.val ? src.v : src.k) + from * src.row + head * src.head + o.group * kKvqGroup + o.wi * 8);
-  const KvqScale s = kvq_group_scale(x, 0xffffffffu);
+  Raw8<T> raw = {};
+  if (live) raw.load((const T*)(o.val ? src.v : src.k) + from * src.row + head * src.head + o.group * kKvqGroup + o.wi * 8);
+  float x[8];
+  raw.get(x);
+  const KvqScale s = row_scale(raw, x, 0xffffffffu);
   const uint32_t word = kvq_codes(x, s);
   const bool pair = o.paired(live ? to : -1);
   const uint32_t other = __shfl_xor_sync(0xffffffffu, word, TokenLane<D>::kPartner);
@@ -216,7 +226,7 @@ __global__ void __launch_bounds__(kCopyThreads) kvq_read_kernel(Cache c, const i
 }
 
 template <int D, class T>
-__global__ void __launch_bounds__(kCopyThreads) kvq_write_pages_kernel(Cache c, Rows src, const int32_t* src_index,
+__global__ void __launch_bounds__(kCopyThreads, sizeof(T) == 2 ? 3 : 1) kvq_write_pages_kernel(Cache c, Rows src, const int32_t* src_index,
                                                                        const int32_t* dst_index, int n) {
   using R = KvqRec<D>;
   constexpr int NG = R::NG;
@@ -244,7 +254,7 @@ __global__ void __launch_bounds__(kCopyThreads) kvq_write_pages_kernel(Cache c, 
     for (int g = 0; g < NG; g++) {
       float x[8];
       kr[e][g].get(x);
-      const KvqScale s = kvq_group_scale(x, 0xffffffffu);
+      const KvqScale s = row_scale(kr[e][g], x, 0xffffffffu);
       w[g] = kvq_codes(x, s);
       sw[g] = s.word();
     }
@@ -270,7 +280,7 @@ __global__ void __launch_bounds__(kCopyThreads) kvq_write_pages_kernel(Cache c, 
       for (int t = 0; t < 2; t++) {
         float x[8];
         vr[e][t][g].get(x);
-        const KvqScale s = kvq_group_scale(x, 0xffffffffu);
+        const KvqScale s = row_scale(vr[e][t][g], x, 0xffffffffu);
         c8[t] = kvq_codes(x, s);
         sw[t * NG + g] = s.word();
       }

@@ -60,7 +60,7 @@ __device__ __forceinline__ float fmax_nan(float a, float b) {
 }
 
 struct KvqScale {
-  float low, step, inv;   // inv = 1 / step rounded, 0 with step 0
+  float low, step, inv;   // inv = 1 / step to 2^-23, 0 with step 0
   __device__ __forceinline__ uint32_t word() const {
     return (__float_as_uint(step) >> 16) | (__float_as_uint(low) & 0xffff0000u);
   }
@@ -68,69 +68,77 @@ struct KvqScale {
 
 // (step, low) of a group with minimum lo and maximum hi (NaN where the group
 // holds one): low = the largest BF16 number <= lo, step = the smallest BF16
-// number >= (hi - low) / 15, at least 2^-126, or 0 for a constant group.  15
-// times a BF16 number is exact in fp32, so one comparison settles the
-// rounding up.  A span that is not finite makes the whole group NaN.
+// number >= (hi - low) / 15, at least 2^-126, or 0 for a constant group.  The
+// product with 1 / 15, cut to BF16, is that number or one of the two below it;
+// 15 times a BF16 number is exact in fp32, so two comparisons settle it (a
+// division took three times as long).  A span that is not finite makes the
+// whole group NaN.  BF: lo is a BF16 number.
+template <bool BF = false>
 __device__ __forceinline__ KvqScale kvq_scale(float lo, float hi) {
   KvqScale s;
-  uint32_t cut = __float_as_uint(lo) & 0xffff0000u;
-  if (cut != __float_as_uint(lo) && lo < 0.f) cut += 0x10000u;
+  uint32_t cut = __float_as_uint(lo);
+  if constexpr (!BF) {
+    cut &= 0xffff0000u;
+    if (cut != __float_as_uint(lo) && lo < 0.f) cut += 0x10000u;
+  }
   s.low = __uint_as_float(cut) + 0.f;      // -0 becomes +0
   const float span = hi - s.low;
-  cut = __float_as_uint(__fdiv_rn(span, 15.f)) & 0xffff0000u;
+  cut = __float_as_uint(span * (1.f / 15.f)) & 0xffff0000u;
   if (__uint_as_float(cut) * 15.f < span) cut += 0x10000u;
-  s.step = span == 0.f ? 0.f : fmaxf(__uint_as_float(cut), 1.17549435e-38f);
-  s.inv = span == 0.f ? 0.f : __frcp_rn(s.step);
-  if (!(fabsf(span) <= FLT_MAX)) {
-    s.low = __uint_as_float(0x7fc00000u);
-    s.step = s.inv = 0.f;
-  }
+  if (__uint_as_float(cut) * 15.f < span) cut += 0x10000u;
+  s.step = fmaxf(__uint_as_float(cut), 1.17549435e-38f);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.inv) : "f"(s.step));
+  const bool bad = !(span <= FLT_MAX);     // NaN included; span >= 0
+  if (span == 0.f || bad) s.step = s.inv = 0.f;
+  if (bad) s.low = __uint_as_float(0x7fc00000u);
   return s;
-}
-
-// code of x where the quotient may be next to a half-way point k + 1/2: the
-// sign of diff - (k + 1/2) step decides, which one FMA gives exactly ((k + 1/2)
-// step has at most 13 bits)
-__device__ __forceinline__ uint32_t kvq_code(float x, const KvqScale& s) {
-  const float diff = x - s.low;
-  const float q = diff * s.inv;
-  float c = rintf(q);
-  if (fabsf(fabsf(q - c) - 0.5f) < 1e-4f) {
-    const float k = floorf(q);
-    const float r = fmaf(-(k + 0.5f), s.step, diff);
-    c = r > 0.f || (r == 0.f && ((int)k & 1)) ? k + 1.f : k;
-  }
-  return (uint32_t)c;
 }
 
 // Codes of eight values, nibble i of the word that of x[i]: (x - low) / step to
 // the nearest integer, ties to even, the difference rounded to fp32.  Adding
-// 1.5 2^23 rounds diff * inv to an integer in the low mantissa bits; eight such
-// patterns, shifted and added, leave the codes and one constant.  diff * inv is
-// within 3e-6 of the quotient, so only a value within 1e-5 of a half-way point
-// needs the exact decision.
+// 1.5 2^23 rounds diff * inv to an integer c in the low mantissa bits.  The
+// product is within 5e-6 of the quotient, so c is the nearest integer or, next
+// to a half-way point, its neighbour; diff - c step, which one FMA gives
+// exactly (c step has at most 12 bits), tells: c moves by one where that is
+// beyond half a step, or at it with an odd c (the limit is then the number
+// below half a step).  BF16 values with BF16 steps tie often, one in a few
+// hundred, so a branch around the correction would nearly always be taken by
+// some lane (it cost 200 us instead of 174 for a 256K prefix).  Eight patterns,
+// shifted and added, leave the codes and one constant.
 __device__ __forceinline__ uint32_t kvq_codes(const float* x, const KvqScale& s) {
   constexpr float kMagic = 12582912.f;     // 0x4b400000
-  float worst = 0.f;
+  const int half = __float_as_int(0.5f * s.step);
   uint32_t word = 0;
 #pragma unroll
   for (int i = 7; i >= 0; i--) {
-    const float q = (x[i] - s.low) * s.inv;
-    const float t = q + kMagic;
-    worst = fmaxf(worst, fabsf(q - (t - kMagic)));
-    word = word * 16u + __float_as_uint(t);
+    const float diff = x[i] - s.low;
+    const float t = fmaf(diff, s.inv, kMagic);
+    const float r = fmaf(kMagic - t, s.step, diff);
+    const float limit = __int_as_float(half - (__float_as_int(t) & 1));
+    const float moved = fabsf(r) > limit ? t + copysignf(1.f, r) : t;
+    word = word * 16u + __float_as_uint(moved);
   }
-  word -= 0x4b400000u * 0x11111111u;
-  if (worst > 0.49999f) {
-    word = 0;
-#pragma unroll
-    for (int i = 7; i >= 0; i--) word = word * 16u + kvq_code(x[i], s);
-  }
-  return s.inv == 0.f ? 0u : word;
+  return s.inv == 0.f ? 0u : word - 0x4b400000u * 0x11111111u;
 }
 
 // scale of a group whose values lie eight a thread in eight neighbouring
-// threads, all of which (`mask`) call it
+// threads, all of which (`mask`) call it; of BF16 pairs, minimum and negated
+// maximum travel in one register
+__device__ __forceinline__ KvqScale kvq_group_scale(const uint32_t (&w)[4], unsigned mask) {
+  using B2 = __nv_bfloat162;
+  const B2* v = reinterpret_cast<const B2*>(w);
+  const B2 mn = __hmin2_nan(__hmin2_nan(v[0], v[1]), __hmin2_nan(v[2], v[3]));
+  const B2 mx = __hmax2_nan(__hmax2_nan(v[0], v[1]), __hmax2_nan(v[2], v[3]));
+  B2 m = __halves2bfloat162(__hmin_nan(mn.x, mn.y), __hneg(__hmax_nan(mx.x, mx.y)));
+#pragma unroll
+  for (int sh = 1; sh < 8; sh <<= 1) {
+    const uint32_t o = __shfl_xor_sync(mask, *reinterpret_cast<const uint32_t*>(&m), sh);
+    m = __hmin2_nan(m, *reinterpret_cast<const B2*>(&o));
+  }
+  return kvq_scale<true>(__low2float(m), -__high2float(m));
+}
+
+// the same of fp32 values
 __device__ __forceinline__ KvqScale kvq_group_scale(const float* x, unsigned mask) {
   float lo = x[0], hi = x[0];
 #pragma unroll

@@ -131,7 +131,7 @@ class QuantCache:
     def read_pages(self, src_pages, k_pool, v_pool, dst_pages, stream=None) -> None:
         """Read pages ``src_pages`` of the cache back into pages ``dst_pages`` of BF16 (or fp32) pools (int32
         ``[n]``, destinations distinct; a negative source gives zeros, a negative destination skips its page)."""
-        self._run(self._read, stream, src_pages, k_pool, v_pool, dst_pages, PAGE_SIZE)
+        self._run(self._read_pages, stream, src_pages, k_pool, v_pool, dst_pages)
 
     def attention(self, q, page_tables, seq_lens, scale: float | None = None, out=None, stream=None):
         """Attention of one query token per sequence, q ``[batch, n_q_heads, head_dim]`` (BF16 or fp32), over the
@@ -147,18 +147,21 @@ class QuantCache:
         r, keep = self._rows(k, v, unit, False)
         mk.mk_kvq_write(self._c, r, None if src is None else src.data_ptr(), dst.data_ptr(), dst.numel(), unit, st)
 
-    def _read(self, st, src, k, v, dst, unit):
-        src = self._index(src, "slots" if unit == 1 else "src_pages")
-        if dst is not None:
-            dst = self._index(dst, "dst_pages", src.numel())
-        r, keep = self._rows(k, v, unit, True)
-        mk.mk_kvq_read(self._c, src.data_ptr(), r, None if dst is None else dst.data_ptr(), src.numel(), unit, st)
+    def _read_pages(self, st, src, k, v, dst):
+        src = self._index(src, "src_pages")
+        dst = self._index(dst, "dst_pages", src.numel())
+        r, keep = self._rows(k, v, PAGE_SIZE, True)
+        mk.mk_kvq_read(self._c, src.data_ptr(), r, dst.data_ptr(), src.numel(), PAGE_SIZE, st)
 
     def _read_rows(self, st, slots, dtype):
         if dtype not in _TYPES:
             raise ValueError(f"dtype: BF16 or fp32, got {dtype}")
-        k, v = torch.empty((2, slots.shape[0], *self._inner[1]), dtype=dtype, device=self.pool.device).unbind()
-        self._read(st, slots, k, v, None, 1)
+        slots = self._index(slots, "slots")
+        n, (hkv, d) = slots.shape[0], self._inner[1]
+        k = torch.empty((n, hkv, d), dtype=dtype, device=slots.device)
+        v = torch.empty_like(k)
+        r = mk.mk_kv_rows(k.data_ptr(), v.data_ptr(), _TYPES[dtype], n, hkv * d, hkv * d, d)
+        mk.mk_kvq_read(self._c, slots.data_ptr(), r, None, n, 1, st)
         return k, v
 
     def _attention(self, st, q, page_tables, seq_lens, scale, out):

@@ -33,11 +33,15 @@ __device__ __forceinline__ void flag_bad(const Cache& c, int code) {
 
 // ------------------------------------------------------------ write and read
 //
-// Both are bound by bytes: d (size + 9/16) a value each way.  Tokens come in
-// any order, so a token's row is eight values a thread and the eight threads
-// of a scale group side by side.  Whole pages (unit 16) go a page and head a
-// warp: codes of both tokens of a pair meet in one lane, and every record is
-// moved in 16-byte pieces.
+// Each moves 2 (or 4) bytes and 9/16 of a byte a value.  Tokens come in any
+// order, so a token's row is eight values a thread and the eight threads of a
+// scale group side by side.  Whole pages (unit 16) go a page and head a warp:
+// codes of both tokens of a pair meet in one lane, and every record is moved in
+// 16-byte pieces.  262,144 tokens of 4 heads of 128 dims in BF16, 688 MB: read 104 us
+// (98 % of the measured copy rate), written 157 us (65 %; bound by
+// instructions, about 35 a value pair: the exact rounding of every code and the
+// reduction for every scale).  8191 tokens by row: 8 us written, 6 read, bound
+// by instructions too (the indexes and addresses of short rows).
 
 // eight consecutive elements as they lie in memory, moved 16 bytes at a time
 template <class T>
@@ -137,8 +141,10 @@ __device__ __forceinline__ bool unit_pair(const Cache& c, const int32_t* src_ind
 
 constexpr int kCopyThreads = 256;
 
-// The thread's eight dims of a token call: block (x, y) takes kTokens tokens of
-// head y, eight threads a (token, key or value, group).  The call's tokens 2 k
+// The thread's eight dims of a token call: block (x, y) takes kTokens tokens
+// and `heads` KV heads from y heads on, eight threads a (token, key or value,
+// group); one head a block where there are few tokens, several where the
+// indexes and addresses would cost more than the row.  The call's tokens 2 k
 // and 2 k + 1 are kPartner lanes apart in a warp: where they lie side by side
 // in the cache (a prompt's do), their value codes, 16 bits of a word each, are
 // exchanged and moved as whole words.
@@ -164,70 +170,77 @@ struct TokenLane {
 
 template <int D, class T>
 __global__ void __launch_bounds__(kCopyThreads) kvq_write_kernel(Cache c, Rows src, const int32_t* src_index,
-                                                                 const int32_t* dst_index, int n) {
+                                                                 const int32_t* dst_index, int n, int heads) {
   using R = KvqRec<D>;
   const TokenLane<D> o;
-  const int head = blockIdx.y;
+  const int h0 = blockIdx.y * heads, h1 = min(c.hkv, h0 + heads);
   int from = -1, to = -1;
   const bool live = o.i < n &&
                     unit_pair(c, src_index, src.count, dst_index, c.pages * kKvqPage, o.i, from, to) && from >= 0;
-  Raw8<T> raw = {};
-  if (live) raw.load((const T*)(o.val ? src.v : src.k) + from * src.row + head * src.head + o.group * kKvqGroup + o.wi * 8);
-  float x[8];
-  raw.get(x);
-  const KvqScale s = row_scale(raw, x, 0xffffffffu);
-  const uint32_t word = kvq_codes(x, s);
-  const bool pair = o.paired(live ? to : -1);
-  const uint32_t other = __shfl_xor_sync(0xffffffffu, word, TokenLane<D>::kPartner);
-  if (!live) return;
-  const int t = to % kKvqPage;
-  uint8_t* rec = c.pool + ((long long)(to / kKvqPage) * c.hkv + head) * R::kBytes;
-  if (pair) {
-    *(uint32_t*)(rec + R::val_half(t & ~1, o.wi, o.group, o.odd)) =
-        o.odd ? __byte_perm(other, word, 0x7632) : __byte_perm(word, other, 0x5410);
-    if (o.wi == 0) *(uint32_t*)(rec + R::kValScale + 4 * (t * R::NG + o.group)) = s.word();
-  } else {
-    kvq_store_row<D>(rec, t, o.wi, o.group, o.val, word, s);
+  if (!live) from = 0, to = -1;
+  const bool pair = o.paired(to);
+  const int t = max(to, 0) % kKvqPage;
+  const T* row = (const T*)(o.val ? src.v : src.k) + from * src.row + h0 * src.head + o.group * kKvqGroup + o.wi * 8;
+  uint8_t* rec = c.pool + ((long long)(max(to, 0) / kKvqPage) * c.hkv + h0) * R::kBytes;
+#pragma unroll 2
+  for (int h = h0; h < h1; h++, row += src.head, rec += R::kBytes) {
+    Raw8<T> raw = {};
+    if (live) raw.load(row);
+    float x[8];
+    raw.get(x);
+    const KvqScale s = row_scale(raw, x, 0xffffffffu);
+    const uint32_t word = kvq_codes(x, s);
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, word, TokenLane<D>::kPartner);
+    if (pair) {
+      *(uint32_t*)(rec + R::val_half(t & ~1, o.wi, o.group, o.odd)) =
+          o.odd ? __byte_perm(other, word, 0x7632) : __byte_perm(word, other, 0x5410);
+      if (o.wi == 0) *(uint32_t*)(rec + R::kValScale + 4 * (t * R::NG + o.group)) = s.word();
+    } else if (live) {
+      kvq_store_row<D>(rec, t, o.wi, o.group, o.val, word, s);
+    }
   }
 }
 
 template <int D, class T>
 __global__ void __launch_bounds__(kCopyThreads) kvq_read_kernel(Cache c, const int32_t* src_index, Rows dst,
-                                                                const int32_t* dst_index, int n) {
+                                                                const int32_t* dst_index, int n, int heads) {
   using R = KvqRec<D>;
   const TokenLane<D> o;
-  const int head = blockIdx.y;
+  const int h0 = blockIdx.y * heads, h1 = min(c.hkv, h0 + heads);
   int from = -1, to = -1;
   const bool live =
       o.i < n && unit_pair(c, src_index, c.pages * kKvqPage, dst_index, dst.count, o.i, from, to);
-  if (!live) from = -1;
+  if (!live) from = -1, to = 0;
   const bool pair = o.paired(from);
-  uint32_t word = 0, scale = 0;            // no source: zeros
-  if (from >= 0) {
-    const int t = from % kKvqPage;
-    const uint8_t* rec = c.pool + ((long long)(from / kKvqPage) * c.hkv + head) * R::kBytes;
-    if (pair)
-      word = *(const uint32_t*)(rec + R::val_half(t & ~1, o.wi, o.group, o.odd));
-    else if (o.val)
-      word = *(const uint16_t*)(rec + R::val_half(t, o.wi, o.group, 0)) |
-             ((uint32_t)*(const uint16_t*)(rec + R::val_half(t, o.wi, o.group, 1)) << 16);
-    else
-      word = *(const uint32_t*)(rec + R::key_word(t, o.wi, o.group));
-    scale = *(const uint32_t*)(rec + (o.val ? R::kValScale : R::kKeyScale) + 4 * (t * R::NG + o.group));
+  const int t = max(from, 0) % kKvqPage;
+  const uint8_t* rec = c.pool + ((long long)(max(from, 0) / kKvqPage) * c.hkv + h0) * R::kBytes;
+  T* row = (T*)(o.val ? dst.v : dst.k) + to * dst.row + h0 * dst.head + o.group * kKvqGroup + o.wi * 8;
+#pragma unroll 2
+  for (int h = h0; h < h1; h++, row += dst.head, rec += R::kBytes) {
+    uint32_t word = 0, scale = 0;          // no source: zeros
+    if (from >= 0) {
+      if (pair)
+        word = *(const uint32_t*)(rec + R::val_half(t & ~1, o.wi, o.group, o.odd));
+      else if (o.val)
+        word = *(const uint16_t*)(rec + R::val_half(t, o.wi, o.group, 0)) |
+               ((uint32_t)*(const uint16_t*)(rec + R::val_half(t, o.wi, o.group, 1)) << 16);
+      else
+        word = *(const uint32_t*)(rec + R::key_word(t, o.wi, o.group));
+      scale = *(const uint32_t*)(rec + (o.val ? R::kValScale : R::kKeyScale) + 4 * (t * R::NG + o.group));
+    }
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, word, TokenLane<D>::kPartner);
+    if (pair) word = o.odd ? __byte_perm(other, word, 0x7632) : __byte_perm(word, other, 0x5410);
+    float x[8];
+    kvq_values(x, word, scale);
+    Raw8<T> raw;
+    raw.set(x);
+    if (live) raw.store(row);
   }
-  const uint32_t other = __shfl_xor_sync(0xffffffffu, word, TokenLane<D>::kPartner);
-  if (!live) return;
-  if (pair) word = o.odd ? __byte_perm(other, word, 0x7632) : __byte_perm(word, other, 0x5410);
-  float x[8];
-  kvq_values(x, word, scale);
-  Raw8<T> raw;
-  raw.set(x);
-  raw.store((T*)(o.val ? dst.v : dst.k) + to * dst.row + head * dst.head + o.group * kKvqGroup + o.wi * 8);
 }
 
 template <int D, class T>
-__global__ void __launch_bounds__(kCopyThreads, sizeof(T) == 2 ? 3 : 1) kvq_write_pages_kernel(Cache c, Rows src, const int32_t* src_index,
-                                                                       const int32_t* dst_index, int n) {
+__global__ void __launch_bounds__(kCopyThreads, sizeof(T) == 2 ? 3 : 1)
+    kvq_write_pages_kernel(Cache c, Rows src, const int32_t* src_index, const int32_t* dst_index, int n) {
   using R = KvqRec<D>;
   constexpr int NG = R::NG;
   const int lane = threadIdx.x & 31, head = blockIdx.y;
@@ -362,6 +375,16 @@ __global__ void __launch_bounds__(kCopyThreads) kvq_read_pages_kernel(Cache c, c
 // A task that is one segment is written at once.  The segments of the others
 // leave (reference, sum, weighted sum) in workspace slots, at most two a block,
 // and a second kernel merges them in page order: no atomics, one result.
+// A warp takes every eighth page of a segment through a ring of four in shared
+// memory (three on their way: 110 KB an SM, twice what the latency needs).
+// 32 query and 4 KV heads of 128 dims, BF16: 262,144 tokens in 41 us, 39 of them
+// in the first kernel, against 22 us for its 151 MB at the measured copy rate;
+// 16 sequences of 1K-32K in 51 us (152 MB).  What bounds it is issuing
+// instructions, about 365 a page and head (4096 codes): 40 to mask key codes,
+// 72 to mask and centre value codes, 60 for scales, 45 for weights and
+// references, 25 to fetch; ALU pipe 53 %, tensor pipe 20 %.  Slower: two pages a
+// warp at a time (49 us, registers spill), 18 warps an SM at 96 registers
+// (60 us), shifts as multiplications (43 us).
 
 constexpr int kAttnWarps = 8;
 constexpr int kAttnThreads = kAttnWarps * 32;
@@ -912,8 +935,18 @@ int check_rows(const mk_kv_rows* r, const mk_kvq_cache* c, int n, int unit, cons
 
 Cache cache_of(const mk_kvq_cache* c) { return Cache{(uint8_t*)c->pool, c->status, c->num_pages, c->n_kv_heads}; }
 
-dim3 copy_grid(int n, int per_block, const mk_kvq_cache* c) {
-  return dim3((unsigned)(((long long)n + per_block - 1) / per_block), (unsigned)c->n_kv_heads);
+dim3 copy_grid(int n, int per_block, const mk_kvq_cache* c, int heads = 1) {
+  return dim3((unsigned)(((long long)n + per_block - 1) / per_block), (unsigned)((c->n_kv_heads + heads - 1) / heads));
+}
+
+// KV heads of a block of a token call: as many as leave every SM the six
+// blocks it can hold, in equal parts (8191 tokens of 4 heads stored and read
+// back: 14 us with several heads a block, 16 with one)
+int token_heads(int n, int per_block, const mk_kvq_cache* c, int sms) {
+  const long long blocks = ((long long)n + per_block - 1) / per_block * c->n_kv_heads;
+  const int most = (int)std::max(1ll, std::min<long long>(c->n_kv_heads, blocks / (6ll * sms)));
+  const int parts = (c->n_kv_heads + most - 1) / most;
+  return (c->n_kv_heads + parts - 1) / parts;
 }
 
 int sm_count() {
@@ -1014,6 +1047,44 @@ int attention(AttnArgs& a, void* workspace, size_t workspace_bytes, int sms, cud
 
 int launched() { return cudaGetLastError() == cudaSuccess ? MK_OK : MK_ERR_CUDA; }
 
+Rows rows_of(const mk_kv_rows* r) { return Rows{r->k, r->v, r->page_stride, r->row_stride, r->head_stride, r->count}; }
+
+template <int D, class T>
+int write_rows(const mk_kvq_cache* c, const mk_kv_rows* src, const int32_t* src_index, const int32_t* dst_index, int n,
+               int unit, void* stream) {
+  constexpr int kTokens = TokenLane<D>::kTokens;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (unit == 1) {
+    const int sms = sm_count();
+    if (!sms) return MK_ERR_CUDA;
+    const int heads = token_heads(n, kTokens, c, sms);
+    kvq_write_kernel<D, T><<<copy_grid(n, kTokens, c, heads), kCopyThreads, 0, st>>>(cache_of(c), rows_of(src), src_index,
+                                                                                    dst_index, n, heads);
+  } else {
+    kvq_write_pages_kernel<D, T><<<copy_grid(n, kCopyThreads / 32, c), kCopyThreads, 0, st>>>(
+        cache_of(c), rows_of(src), src_index, dst_index, n);
+  }
+  return launched();
+}
+
+template <int D, class T>
+int read_rows(const mk_kvq_cache* c, const int32_t* src_index, const mk_kv_rows* dst, const int32_t* dst_index, int n,
+              int unit, void* stream) {
+  constexpr int kTokens = TokenLane<D>::kTokens;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (unit == 1) {
+    const int sms = sm_count();
+    if (!sms) return MK_ERR_CUDA;
+    const int heads = token_heads(n, kTokens, c, sms);
+    kvq_read_kernel<D, T><<<copy_grid(n, kTokens, c, heads), kCopyThreads, 0, st>>>(cache_of(c), src_index, rows_of(dst),
+                                                                                   dst_index, n, heads);
+  } else {
+    kvq_read_pages_kernel<D, T><<<copy_grid(n, kCopyThreads / 32, c), kCopyThreads, 0, st>>>(
+        cache_of(c), src_index, rows_of(dst), dst_index, n);
+  }
+  return launched();
+}
+
 }  // namespace
 
 extern "C" {
@@ -1028,25 +1099,11 @@ int mk_kvq_write(const mk_kvq_cache* c, const mk_kv_rows* src, const int32_t* sr
   int rc = check_cache(c);
   if (!rc) rc = check_rows(src, c, n, unit, src_index, dst_index);
   if (rc || n == 0) return rc;
-  const Cache cc = cache_of(c);
-  const Rows rr{src->k, src->v, src->page_stride, src->row_stride, src->head_stride, src->count};
-  cudaStream_t st = (cudaStream_t)stream;
-#define WRITE(D, T)                                                                                               \
-  do {                                                                                                            \
-    if (unit == 1)                                                                                                \
-      kvq_write_kernel<D, T><<<copy_grid(n, TokenLane<D>::kTokens, c), kCopyThreads, 0, st>>>(cc, rr, src_index,  \
-                                                                                              dst_index, n);      \
-    else                                                                                                          \
-      kvq_write_pages_kernel<D, T><<<copy_grid(n, kCopyThreads / 32, c), kCopyThreads, 0, st>>>(cc, rr, src_index, \
-                                                                                                dst_index, n);    \
-  } while (0)
-  if (c->head_dim == 128) {
-    if (src->type == MK_TYPE_BF16) WRITE(128, uint16_t); else WRITE(128, float);
-  } else {
-    if (src->type == MK_TYPE_BF16) WRITE(64, uint16_t); else WRITE(64, float);
-  }
-#undef WRITE
-  return launched();
+  if (c->head_dim == 128)
+    return src->type == MK_TYPE_BF16 ? write_rows<128, uint16_t>(c, src, src_index, dst_index, n, unit, stream)
+                                     : write_rows<128, float>(c, src, src_index, dst_index, n, unit, stream);
+  return src->type == MK_TYPE_BF16 ? write_rows<64, uint16_t>(c, src, src_index, dst_index, n, unit, stream)
+                                   : write_rows<64, float>(c, src, src_index, dst_index, n, unit, stream);
 }
 
 int mk_kvq_read(const mk_kvq_cache* c, const int32_t* src_index, const mk_kv_rows* dst, const int32_t* dst_index,
@@ -1054,25 +1111,11 @@ int mk_kvq_read(const mk_kvq_cache* c, const int32_t* src_index, const mk_kv_row
   int rc = check_cache(c);
   if (!rc) rc = check_rows(dst, c, n, unit, dst_index, src_index);
   if (rc || n == 0) return rc;
-  const Cache cc = cache_of(c);
-  const Rows rr{dst->k, dst->v, dst->page_stride, dst->row_stride, dst->head_stride, dst->count};
-  cudaStream_t st = (cudaStream_t)stream;
-#define READ(D, T)                                                                                                \
-  do {                                                                                                            \
-    if (unit == 1)                                                                                                \
-      kvq_read_kernel<D, T><<<copy_grid(n, TokenLane<D>::kTokens, c), kCopyThreads, 0, st>>>(cc, src_index, rr,   \
-                                                                                             dst_index, n);       \
-    else                                                                                                          \
-      kvq_read_pages_kernel<D, T><<<copy_grid(n, kCopyThreads / 32, c), kCopyThreads, 0, st>>>(cc, src_index, rr, \
-                                                                                               dst_index, n);     \
-  } while (0)
-  if (c->head_dim == 128) {
-    if (dst->type == MK_TYPE_BF16) READ(128, uint16_t); else READ(128, float);
-  } else {
-    if (dst->type == MK_TYPE_BF16) READ(64, uint16_t); else READ(64, float);
-  }
-#undef READ
-  return launched();
+  if (c->head_dim == 128)
+    return dst->type == MK_TYPE_BF16 ? read_rows<128, uint16_t>(c, src_index, dst, dst_index, n, unit, stream)
+                                     : read_rows<128, float>(c, src_index, dst, dst_index, n, unit, stream);
+  return dst->type == MK_TYPE_BF16 ? read_rows<64, uint16_t>(c, src_index, dst, dst_index, n, unit, stream)
+                                   : read_rows<64, float>(c, src_index, dst, dst_index, n, unit, stream);
 }
 
 size_t mk_kvq_workspace(const mk_kvq_cache* c, int type, int n_q_heads, int batch, int max_pages) {

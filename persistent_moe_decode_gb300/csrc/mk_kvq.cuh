@@ -103,8 +103,8 @@ __device__ __forceinline__ KvqScale kvq_scale(float lo, float hi) {
 // beyond half a step, or at it with an odd c (the limit is then the number
 // below half a step).  BF16 values with BF16 steps tie often, one in a few
 // hundred, so a branch around the correction would nearly always be taken by
-// some lane (it cost 200 us instead of 174 for a 256K prefix).  Eight patterns,
-// shifted and added, leave the codes and one constant.
+// some lane (a 256K prefix then took 200 us, not 179).  Eight patterns, shifted
+// and added, leave the codes and one constant.
 __device__ __forceinline__ uint32_t kvq_codes(const float* x, const KvqScale& s) {
   constexpr float kMagic = 12582912.f;     // 0x4b400000
   const int half = __float_as_int(0.5f * s.step);
@@ -452,12 +452,15 @@ struct KvqAttn {
       for (int n = 0; n < N; n++)
 #pragma unroll
         for (int e = 0; e < 2; e++) {
-          p[n][e][0] = ex2(x[n][e][0] - r[0]);
-          p[n][e][1] = ex2(x[n][e][1] - r[1]);
+          const float2 u = __fadd2_rn(make_float2(x[n][e][0], x[n][e][1]), make_float2(-r[0], -r[1]));
+          p[n][e][0] = ex2(u.x);
+          p[n][e][1] = ex2(u.y);
           top = fmaxf(fmaxf(top, p[n][e][0]), p[n][e][1]);
 #pragma unroll
           for (int g = 0; g < NG; g++) {
-            const float w0 = p[n][e][0] * bf16lo(vs[n][e][g]) * sc[g][0], w1 = p[n][e][1] * bf16lo(vs[n][e][g]) * sc[g][1];
+            const float st = bf16lo(vs[n][e][g]);
+            const float2 wv = __fmul2_rn(__fmul2_rn(make_float2(p[n][e][0], p[n][e][1]), make_float2(st, st)), make_float2(sc[g][0], sc[g][1]));
+            const float w0 = wv.x, w1 = wv.y;
             top = fmaxf(fmaxf(top, w0), w1);
             const uint32_t hi = pack_h2(w0, w1);
             wt[0][n][g][e] = hi;

@@ -120,8 +120,9 @@ int attention_sms(const mk_config& c, int n_sm, int batch, const int32_t* seq_le
   // branch's per-byte cost (its multi-token GEMVs) does not follow; with the
   // expert tiles claimed, 36 of 152 SMs (32 within 0.5 %) were the best
   // fixed split over whole batch-16 runs and 24 over batch-4 runs.
-  // With the 4-bit cache the best at batch 16 is 0.34, 1.5 times that.
-  if (batch > 1) ideal = std::max(ideal, (batch >= 8 ? (q4 ? 0.34 : 0.23) : (q4 ? 0.24 : 0.16)) * n_sm);
+  // With the 4-bit cache 0.34 (52 SMs) is the best at batch 16 and 0.21 (32) at
+  // batch 4 with 8K.
+  if (batch > 1) ideal = std::max(ideal, (batch >= 8 ? (q4 ? 0.34 : 0.23) : (q4 ? 0.21 : 0.16)) * n_sm);
   // in steps of 4 SMs on a large GPU: each split has its own task lists,
   // built and uploaded the first time it is used, and the contexts of a
   // continuous batch move the ideal split by a few SMs every step

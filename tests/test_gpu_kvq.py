@@ -459,13 +459,14 @@ def test_attention_with_a_bad_page_or_length_gives_nan_rows():
         assert e.value.code == mk.MK_ERR_BAD_ARG
 
 
-def test_calls_on_a_stream_and_captured_graphs_side_by_side():
+@pytest.mark.parametrize("spare", [1, 5000], ids=["cluster", "workspace"])
+def test_calls_on_a_stream_and_captured_graphs_side_by_side(spare):
     """A step of write and attention captured twice over one cache, the two graphs replayed at once on two
     streams with new contents, against plain calls."""
     rng = np.random.default_rng(9)
     hkv, grp, d = 4, 8, 128
     lens = [2000, 5000, 333]
-    pool, table, q = attention_case(rng, hkv, grp, d, lens, torch.bfloat16)
+    pool, table, q = attention_case(rng, hkv, grp, d, lens, torch.bfloat16, spare=spare)
     c = cache_over(pool, hkv, d)
     tb = torch.from_numpy(table).cuda()
     sets, graphs = [], []

@@ -69,16 +69,19 @@ def kernel_code(text: str) -> str:
     return "\n".join(ln.rstrip() for ln in text.splitlines() if ln.strip())
 
 
+# what the step kernel is compiled from
+STEP_SOURCES = ("mk_kernel.cu", "mk_kernel_q4.cu", "mk_kvq.cuh", "mk_layout.h", "mk_ptx.cuh")
+
+
 def kernel_sha() -> str:
-    """Key of the traffic record: a hash of the kernel sources' code (comments
+    """Key of the traffic record: a hash of the step kernel's code (comments
     excluded, so an edit to the documentation keeps the record)."""
     import hashlib
     h = hashlib.sha256()
     cs = os.path.join(ROOT, "persistent_moe_decode_gb300", "csrc")
-    for fn in sorted(os.listdir(cs)):
-        if fn.endswith((".cu", ".cuh", ".h")):
-            with open(os.path.join(cs, fn), encoding="utf-8") as f:
-                h.update(fn.encode() + b"\0" + kernel_code(f.read()).encode() + b"\0")
+    for fn in STEP_SOURCES:
+        with open(os.path.join(cs, fn), encoding="utf-8") as f:
+            h.update(fn.encode() + b"\0" + kernel_code(f.read()).encode() + b"\0")
     return h.hexdigest()[:16]
 
 

@@ -370,8 +370,10 @@ __global__ void __launch_bounds__(kCopyThreads) kvq_read_pages_kernel(Cache c, c
 //   few pages (no more than a segment a block): segments of kMinPages pages,
 //     one page a warp;
 //   many: block i takes units T i / G .. T (i + 1) / G of the T units of all
-//     tasks in order (a unit is a page, a task's last segment rounded up), so
-//     every block moves the same bytes whatever the mix of lengths.
+//     tasks in order, so that every block has the same work whatever the mix of
+//     lengths.  A unit is a page; a task's last segment counts as a whole one,
+//     and a task kTaskCost units more, for what a block spends on a segment
+//     beside its pages (16 sequences of 1K-32K: 51 us without, 46 with it).
 // A task that is one segment is written at once.  The segments of the others
 // leave (reference, sum, weighted sum) in workspace slots, at most two a block,
 // and a second kernel merges them in page order: no atomics, one result.
@@ -379,7 +381,7 @@ __global__ void __launch_bounds__(kCopyThreads) kvq_read_pages_kernel(Cache c, c
 // memory (three on their way: 110 KB an SM, twice what the latency needs).
 // 32 query and 4 KV heads of 128 dims, BF16: 262,144 tokens in 41 us, 39 of them
 // in the first kernel, against 22 us for its 151 MB at the measured copy rate;
-// 16 sequences of 1K-32K in 51 us (152 MB).  What bounds it is issuing
+// 16 sequences of 1K-32K in 46 us (152 MB).  What bounds it is issuing
 // instructions, about 365 a page and head (4096 codes): 40 to mask key codes,
 // 72 to mask and centre value codes, 60 for scales, 45 for weights and
 // references, 25 to fetch; ALU pipe 53 %, tensor pipe 20 %.  Slower: two pages a
@@ -394,6 +396,7 @@ constexpr int attn_per_sm(int d, int type) { return d == 128 && type == MK_TYPE_
 template <int D, class T>
 constexpr int kBlocksPerSm = attn_per_sm(D, sizeof(T) == 4 ? MK_TYPE_F32 : MK_TYPE_BF16);
 constexpr int kMinPages = kAttnWarps;
+constexpr int kTaskCost = 48;
 constexpr int kRing = 4;                   // pages of a warp, in flight and in use
 
 struct AttnArgs {
@@ -452,23 +455,27 @@ __device__ __forceinline__ int seq_pages(const AttnArgs& a, int b) {
 }
 
 // A place in the list of sequences: the pages of sequence b and what comes
-// before it, in units (kMinPages for each started kMinPages pages of one head:
-// a short task costs a block about that much) and in chunks of split tasks
+// before it, in units of one task each and in chunks of split tasks
 struct Place {
   int b, np;
-  long long units;
-  int split;
+  long long units, split;
+};
+
+// What comes before a sequence: units (kMinPages for each started kMinPages
+// pages), chunks of split tasks, sequences with a page
+struct Before {
+  long long units, split;
+  int tasks;
 };
 
 struct PlanSmem {
-  long long units[kAttnWarps];
-  int split[kAttnWarps];
+  long long units[kAttnWarps], marks[kAttnWarps];
   Place found;
-  // the window: a sequence a thread, and the units and chunks before each
-  int np[kAttnThreads], split_before[kAttnThreads];
-  long long before[kAttnThreads];
-  int b0, split_end;
-  long long end;                           // before the next window
+  // the window: a sequence a thread
+  int np[kAttnThreads];
+  Before before[kAttnThreads];
+  int b0;
+  Before end;                              // before the next window
 };
 
 __device__ __forceinline__ int seq_units(int np) { return (np + kMinPages - 1) / kMinPages * kMinPages; }
@@ -476,51 +483,55 @@ __device__ __forceinline__ int seq_units(int np) { return (np + kMinPages - 1) /
 // Sums over the sequences, a window of one sequence a thread at a time (in
 // shared memory: between segments nothing stays in registers).  All threads
 // of the block make every call together.
-__device__ void plan_window(const AttnArgs& a, PlanSmem& S, int first, long long end, int split_end) {
+__device__ void plan_window(const AttnArgs& a, PlanSmem& S, int first, Before end) {
+  constexpr int kTaskBits = 20;            // chunks and sequences are added up in one word
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int np = first + tid < a.batch ? max(seq_pages(a, first + tid), 0) : 0;
-  const int n = seq_units(np), m = n > kMinPages ? n / kMinPages : 0;
-  long long u = n;
-  int sp = m;
+  const long long n = seq_units(np);
+  const long long m = ((long long)(np > kMinPages ? n / kMinPages : 0) << kTaskBits) + (np > 0);
+  long long u = n, k = m;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, u, o);
-    const int y = __shfl_up_sync(0xffffffffu, sp, o);
-    if (lane >= o) u += x, sp += y;
+    const long long x = __shfl_up_sync(0xffffffffu, u, o), y = __shfl_up_sync(0xffffffffu, k, o);
+    if (lane >= o) u += x, k += y;
   }
-  if (lane == 31) S.units[warp] = u, S.split[warp] = sp;
+  if (lane == 31) S.units[warp] = u, S.marks[warp] = k;
   __syncthreads();
-  long long before = end + u - n;
-  int split_before = split_end + sp - m;
+  long long units = u - n, marks = k - m, all_units = 0, all_marks = 0;
   for (int w = 0; w < kAttnWarps; w++) {
-    if (w < warp) before += S.units[w], split_before += S.split[w];
-    end += S.units[w];
-    split_end += S.split[w];
+    if (w < warp) units += S.units[w], marks += S.marks[w];
+    all_units += S.units[w];
+    all_marks += S.marks[w];
   }
+  constexpr long long kMask = (1 << kTaskBits) - 1;
   S.np[tid] = np;
-  S.before[tid] = before;
-  S.split_before[tid] = split_before;
-  if (tid == 0) S.b0 = first, S.end = end, S.split_end = split_end;
+  S.before[tid] = {end.units + units, end.split + (marks >> kTaskBits), end.tasks + (int)(marks & kMask)};
+  if (tid == 0) {
+    S.b0 = first;
+    S.end = {end.units + all_units, end.split + (all_marks >> kTaskBits), end.tasks + (int)(all_marks & kMask)};
+  }
   __syncthreads();
 }
 
 // the next window, false after the last
 __device__ bool plan_next(const AttnArgs& a, PlanSmem& S) {
-  const int first = S.b0 + kAttnThreads, split_end = S.split_end;
-  const long long end = S.end;
+  const int first = S.b0 + kAttnThreads;
+  const Before end = S.end;
   __syncthreads();
   if (first >= a.batch) return false;
-  plan_window(a, S, first, end, split_end);
+  plan_window(a, S, first, end);
   return true;
 }
 
-// the sequence that holds unit `target`, not before the window; false past the last
-__device__ bool plan_find(const AttnArgs& a, PlanSmem& S, long long target, Place& at) {
-  while (target >= S.end)
+// the sequence that holds unit `target`, not before the window, where each
+// sequence has `cost` units more; false past the last
+__device__ bool plan_find(const AttnArgs& a, PlanSmem& S, int cost, long long target, Place& at) {
+  while (target >= S.end.units + (long long)cost * S.end.tasks)
     if (!plan_next(a, S)) return false;
   const int tid = threadIdx.x, np = S.np[tid];
-  const long long before = S.before[tid];
-  if (before <= target && target < before + seq_units(np)) S.found = {S.b0 + tid, np, before, S.split_before[tid]};
+  const Before b = S.before[tid];
+  const long long units = b.units + (long long)cost * b.tasks;
+  if (np > 0 && units <= target && target < units + seq_units(np) + cost) S.found = {S.b0 + tid, np, units, b.split};
   __syncthreads();
   at = S.found;
   __syncthreads();                         // the next call writes it again
@@ -686,24 +697,23 @@ __global__ void __launch_bounds__(kAttnThreads, kBlocksPerSm<D, T>) kvq_attentio
     for (int i = tid; i < a.c.hkv * a.grp * D; i += kAttnThreads)
       stf((T*)a.out + b * a.out_stride + i, np < 0 ? NAN : 0.f);
   }
-  plan_window(a, S, 0, 0, 0);
-  while (plan_next(a, S)) {}
-  const unsigned long long total = (unsigned long long)S.end * HT;
-  if (me == 0 && tid == 0) *attn_ws(a.ws, G).count = S.split_end * HT;   // changed below with whole shares
-  if (a.batch > kAttnThreads) {
-    __syncthreads();
-    plan_window(a, S, 0, 0, 0);
-  }
-
   const AttnWs ws = attn_ws(a.ws, G);
   Place at;
-  if (total <= (unsigned long long)G * kMinPages) {
+  plan_window(a, S, 0, Before{0, 0, 0});
+  while (plan_next(a, S)) {}
+  const Before all = S.end;
+  if (a.batch > kAttnThreads) {            // the plan is at its end
+    __syncthreads();
+    plan_window(a, S, 0, Before{0, 0, 0});
+  }
+  if ((unsigned long long)all.units * HT <= (unsigned long long)G * kMinPages) {
+    if (me == 0 && tid == 0) *ws.count = (int)(all.split * HT);
     // segment s is the s-th chunk of kMinPages pages
-    for (long long s = me; plan_find(a, S, s / HT * kMinPages, at); s += G) {
+    for (long long s = me; plan_find(a, S, 0, s / HT * kMinPages, at); s += G) {
       const int nc = seq_units(at.np) / kMinPages;
       const long long rem = s - at.units / kMinPages * HT;
       const int j = (int)(rem / nc), k = (int)(rem % nc);
-      const int slot = at.split * HT + (int)rem;
+      const int slot = (int)(at.split * HT + rem);
       if (nc > 1 && tid == 0) ws.slots[slot] = {at.b, j, k == 0 ? nc : 0, 1};
       B::segment(a, smem, at.b, j, k * kMinPages, min(at.np, (k + 1) * kMinPages),
                  nc > 1 ? ws.data + slot * attn_slot_floats(D) : nullptr);
@@ -711,12 +721,13 @@ __global__ void __launch_bounds__(kAttnThreads, kBlocksPerSm<D, T>) kvq_attentio
   } else {
     if (me == 0 && tid == 0) *ws.count = 2 * G;
     if (tid == 0) ws.slots[2 * me].parts = ws.slots[2 * me + 1].parts = 0;
+    const unsigned long long total = (unsigned long long)(all.units + (long long)kTaskCost * all.tasks) * HT;
     unsigned long long u = total * me / G;
     const unsigned long long end = total * (me + 1) / G;
     bool first = true;
     while (u < end) {
-      plan_find(a, S, (long long)(u / HT), at);
-      const int nu = seq_units(at.np);
+      plan_find(a, S, kTaskCost, (long long)(u / HT), at);
+      const int nu = seq_units(at.np) + kTaskCost;
       const unsigned long long rem = u - (unsigned long long)at.units * HT;
       const int j = (int)(rem / nu), p0 = (int)(rem % nu);
       const unsigned long long task = u - p0;              // first unit of the task

@@ -83,21 +83,22 @@ class QuantCache:
 
     def _rows(self, k, v, unit, out):
         """mk_kv_rows of k and v, and the tensors it points into."""
-        inner, shape = self._inner[unit], k.shape
-        for name, t in (("k", k), ("v", v)):
-            if t.dtype not in _TYPES or t.dtype is not k.dtype:
-                raise ValueError(f"{name}: BF16 or fp32, k and v alike, got {t.dtype}")
-            if t.get_device() != self._dev or t.shape[1:] != inner or t.shape != shape:
-                raise ValueError(f"{name}: [n, {', '.join(map(str, inner))}] on {self.pool.device}, "
-                                 f"got {tuple(t.shape)} on {t.device}")
-        q = 8 if k.dtype is torch.bfloat16 else 4
+        inner, shape, dtype = self._inner[unit], k.shape, k.dtype
+        if dtype not in _TYPES or v.dtype is not dtype:
+            raise ValueError(f"k, v: BF16 or fp32, both alike, got {dtype} and {v.dtype}")
+        if shape[1:] != inner or v.shape != shape or k.get_device() != self._dev or v.get_device() != self._dev:
+            raise ValueError(f"k, v: [n, {', '.join(map(str, inner))}] on {self.pool.device}, got {tuple(shape)} on "
+                             f"{k.device} and {tuple(v.shape)} on {v.device}")
         s, kp, vp = k.stride(), k.data_ptr(), v.data_ptr()
-        if s != v.stride() or s[-1] != 1 or any(x % q for x in s[:-1]) or (kp | vp) & 15:
+        odd = 0
+        for x in s[:-1]:
+            odd |= x
+        if s[-1] != 1 or odd & (7 if dtype is torch.bfloat16 else 3) or (kp | vp) & 15 or v.stride() != s:
             if out:
                 raise ValueError("k, v: rows of consecutive elements at 16-byte strides, k and v alike")
             k, v = (t.clone(memory_format=torch.contiguous_format) for t in (k, v))
             s, kp, vp = k.stride(), k.data_ptr(), v.data_ptr()
-        return mk.mk_kv_rows(kp, vp, _TYPES[k.dtype], shape[0], s[0], s[0] if unit == 1 else s[2], s[1]), (k, v)
+        return mk.mk_kv_rows(kp, vp, _TYPES[dtype], shape[0], s[0], s[0] if unit == 1 else s[2], s[1]), (k, v)
 
     def _dense(self, t):
         s = t.stride()
@@ -180,7 +181,7 @@ class QuantCache:
         if not self._dense(q):
             q = q.clone(memory_format=torch.contiguous_format)
         if out is None:
-            out = torch.empty(shape, dtype=dtype, device=q.device)
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
         elif out.shape != shape or out.dtype is not dtype or out.get_device() != dev or not self._dense(out):
             raise ValueError(f"out: {dtype} {tuple(shape)} on {self.pool.device}, rows of consecutive heads at "
                              "16-byte strides")

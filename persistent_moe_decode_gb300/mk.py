@@ -160,8 +160,8 @@ def _ptr(a: np.ndarray):
 
 
 def _stream_ptr(stream):
-    if stream is None:
-        return None
+    if stream is None or type(stream) is int:
+        return stream
     return C.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 

@@ -535,3 +535,34 @@ def test_decode_loop_of_write_and_attention_together():
         check_attention(out, mirror, idh[None], q, [n0 + s + 1], hkv)
     assert np.array_equal(c.pool.cpu().numpy(), mirror)
     c.check()
+
+
+def test_arguments_of_another_kind_are_refused():
+    hkv, d = 2, 64
+    c = QuantCache(4, hkv, d)
+    k = torch.zeros(3, hkv, d, dtype=torch.bfloat16, device="cuda")
+    slots = torch.arange(3, dtype=torch.int32, device="cuda")
+    for bad in ((k.half(), k.half(), slots), (k, k.float(), slots), (k[:, :1], k[:, :1], slots), (k, k[:2], slots),
+                (k.cpu(), k.cpu(), slots), (k, k, slots.long()), (k, k, slots[:2]), (k, k, slots.cpu()),
+                (k, k, slots[None])):
+        with pytest.raises(ValueError):
+            c.write(*bad)
+    for bad in ((slots.long(),), (slots, torch.float16), (slots.cpu(),)):
+        with pytest.raises(ValueError):
+            c.read(*bad)
+    pools = torch.zeros(4, hkv, 16, d, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError):
+        c.write_pages(pools, pools, slots, slots[:2])
+    with pytest.raises(ValueError):                  # an output is not copied behind the caller's back
+        c.read_pages(slots, pools.transpose(2, 3).contiguous().transpose(2, 3), pools, slots)
+    q = torch.zeros(1, 4, d, dtype=torch.bfloat16, device="cuda")
+    tb, ln = torch.zeros(1, 4, dtype=torch.int32, device="cuda"), torch.ones(1, dtype=torch.int32, device="cuda")
+    for bad in (dict(q=q.half()), dict(q=q[0]), dict(q=q[..., :32]), dict(q=q.cpu()), dict(page_tables=tb.long()),
+                dict(page_tables=tb[0]), dict(page_tables=torch.cat([tb, tb])), dict(seq_lens=ln.long()),
+                dict(seq_lens=torch.cat([ln, ln])), dict(out=q.float()), dict(out=q[:, :2])):
+        with pytest.raises(ValueError):
+            c.attention(**{**dict(q=q, page_tables=tb, seq_lens=ln), **bad})
+    with pytest.raises(Exception) as e:              # three query heads do not divide over two KV heads
+        c.attention(q[:, :3].contiguous(), tb, ln)
+    assert "config" in str(e.value)
+    c.check()

@@ -108,11 +108,13 @@ int attention_sms(const mk_config& c, int n_sm, int batch, const int32_t* seq_le
   // contexts of 1K-32K.
   // The 4-bit cache moves 28 % of the bytes, but its attention is bound by
   // instructions, about as many a token as over BF16: the same byte count with
-  // a fit of its own (56 attention SMs at 8K, the best of 40 .. 88; 128 at 256K,
-  // the best of 96 .. 140; 52 at batch 16, the best of 28 .. 72).
+  // a fit of its own.  Best attention SMs at batch 1: 56 at 8K (of 40 .. 88),
+  // 128 at 256K (of 96 .. 140); at batch 4: 32 at 8K, 40 at 14K; at batch 16: 28 at
+  // 4.6K, 36 at 8K, 52 at 16K, 60 at 22K, 64 at 30K on average.
   const bool q4 = c.kv_format == MK_KV_INT4;
   const double mean_ctx = keys / batch;
-  const double w = (q4 ? 2.6 : 1.6) * pow(8192.0 / mean_ctx, q4 ? 0.36 : 0.22) / pow((double)batch, 0.45);
+  const double w = q4 ? 2.6 * pow(8192.0 / mean_ctx, 0.36) / pow((double)batch, 0.6)
+                      : 1.6 * pow(8192.0 / mean_ctx, 0.22) / pow((double)batch, 0.45);
   double ideal = n_sm * w * kv / (w * kv + moe);
   // several tokens: at least 16 % of the SMs on the attention branch, 23 %
   // from 8 tokens up.  As the contexts of a continuous batch shrink (short
@@ -120,9 +122,11 @@ int attention_sms(const mk_config& c, int n_sm, int batch, const int32_t* seq_le
   // branch's per-byte cost (its multi-token GEMVs) does not follow; with the
   // expert tiles claimed, 36 of 152 SMs (32 within 0.5 %) were the best
   // fixed split over whole batch-16 runs and 24 over batch-4 runs.
-  // With the 4-bit cache 0.34 (52 SMs) is the best at batch 16 and 0.21 (32) at
-  // batch 4 with 8K.
-  if (batch > 1) ideal = std::max(ideal, (batch >= 8 ? (q4 ? 0.34 : 0.23) : (q4 ? 0.21 : 0.16)) * n_sm);
+  // With the 4-bit cache the least share grows with the contexts.
+  if (batch > 1) {
+    const double q4_min = batch >= 8 ? 0.11 + 1.39e-5 * mean_ctx : 0.13 + 1e-5 * mean_ctx;
+    ideal = std::max(ideal, (q4 ? std::max(0.13, std::min(0.42, q4_min)) : batch >= 8 ? 0.23 : 0.16) * n_sm);
+  }
   // in steps of 4 SMs on a large GPU: each split has its own task lists,
   // built and uploaded the first time it is used, and the contexts of a
   // continuous batch move the ideal split by a few SMs every step

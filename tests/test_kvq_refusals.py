@@ -179,7 +179,8 @@ def test_the_step_refuses_unknown_cache_formats_and_shapes(lib):
 def test_attention_sms_over_the_4_bit_cache(lib):
     """The measured best splits of 152 SMs on the 30B/3.3B shape; the BF16 cache's are what they were."""
     from persistent_moe_decode_gb300.configs import A3B
-    for lens, bf16, int4 in (([8192], 40, 56), ([262144], 128, 128), ([16384] * 16, 36, 52)):
+    for lens, bf16, int4 in (([8192], 40, 56), ([262144], 128, 128), ([8192] * 4, 24, 32), ([8192] * 16, 36, 36),
+                             ([16384] * 16, 36, 52), ([30000] * 16, 36, 64)):
         for fmt, want in ((mk.MK_KV_BF16, bf16), (mk.MK_KV_INT4, int4)):
             cfg = mk.make_config(A3B, len(lens), 16400, 1 << 20, kv_format=fmt)
             assert mk.mk_plan_step(cfg, 152, len(lens), np.array(lens))["n_attn"] == want

@@ -35,13 +35,18 @@ __device__ __forceinline__ void flag_bad(const Cache& c, int code) {
 //
 // Each moves 2 (or 4) bytes and 9/16 of a byte a value.  Tokens come in any
 // order, so a token's row is eight values a thread and the eight threads of a
-// scale group side by side.  Whole pages (unit 16) go a page and head a warp:
-// codes of both tokens of a pair meet in one lane, and every record is moved in
-// 16-byte pieces.  262,144 tokens of 4 heads of 128 dims in BF16, 688 MB: read 104 us
-// (98 % of the measured copy rate), written 157 us (65 %; bound by
-// instructions, about 35 a value pair: the exact rounding of every code and the
-// reduction for every scale).  8191 tokens by row: 8 us written, 6 read, bound
-// by instructions too (the indexes and addresses of short rows).
+// scale group side by side.  Whole pages (unit 16) are read a page and head a
+// warp and written a page's keys or values a warp, head after head: codes of
+// both tokens of a pair meet in one lane, every record is moved in 16-byte
+// pieces, and a writer loads the next head's half page while it computes the
+// other half.  262,144 tokens of 4 heads of 128 dims in BF16, 688 MB: read 104 us
+// (98 % of the measured copy rate), written 125 us (81 %; a third of the issue
+// slots and of the DRAM rate are left: 24 warps an SM do not hide every wait).
+// Measured of the writer: both halves of keys and values held by one warp
+// without the overlap 151 (16 warps an SM) and 136 us (32, registers spill),
+// keys or values a warp without it 133, half a page a warp 149; 64 registers
+// with the overlap 126, 48 148.  8191 tokens by row: 7 us written, 6 read, bound
+// by instructions (the indexes and addresses of short rows).
 
 // eight consecutive elements as they lie in memory, moved 16 bytes at a time
 template <class T>
@@ -239,70 +244,73 @@ __global__ void __launch_bounds__(kCopyThreads) kvq_read_kernel(Cache c, const i
 }
 
 template <int D, class T>
-__global__ void __launch_bounds__(kCopyThreads, sizeof(T) == 2 ? 3 : 1)
-    kvq_write_pages_kernel(Cache c, Rows src, const int32_t* src_index, const int32_t* dst_index, int n) {
+__global__ void __launch_bounds__(kCopyThreads, sizeof(T) == 2 ? 3 : 2)
+    kvq_write_pages_kernel(Cache c, Rows src, const int32_t* src_index, const int32_t* dst_index, int n, int heads) {
   using R = KvqRec<D>;
   constexpr int NG = R::NG;
-  const int lane = threadIdx.x & 31, head = blockIdx.y;
-  const int i = blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, val = threadIdx.x >> 5 & 1;
+  const int i = blockIdx.x * (kCopyThreads / 64) + (threadIdx.x >> 6);
+  const int h0 = blockIdx.y * heads, h1 = min(c.hkv, h0 + heads);
   int from, to;
   if (i >= n || !unit_pair(c, src_index, src.count, dst_index, c.pages, i, from, to) || from < 0) return;
-  const T* kb = (const T*)src.k + from * src.page + head * src.head;
-  const T* vb = (const T*)src.v + from * src.page + head * src.head;
-  uint8_t* rec = c.pool + ((long long)to * c.hkv + head) * R::kBytes;
   const int pr = lane >> 3, wi = lane & 7;
-  Raw8<T> kr[4][NG], vr[2][2][NG];         // tokens pr + 4 e; tokens 2 (pr + 4 e) and + 1; dims 64 g + 8 wi ..
+  // raw[e]: keys of tokens 8 e + pr and 8 e + pr + 4, or values of tokens 8 e + 2 pr and the next; dims 64 g + 8 wi ..
+  const int t0 = val ? 2 * pr : pr, dt = val ? 1 : 4;
+  const T* p = (const T*)(val ? src.v : src.k) + from * src.page + h0 * src.head + t0 * src.row + wi * 8;
+  uint8_t* rec = c.pool + ((long long)to * c.hkv + h0) * R::kBytes;
+  Raw8<T> raw[2][2][NG];
+  auto load = [&](int e) {
 #pragma unroll
-  for (int g = 0; g < NG; g++) {
+    for (int t = 0; t < 2; t++)
 #pragma unroll
-    for (int e = 0; e < 4; e++) kr[e][g].load(kb + (pr + 4 * e) * src.row + g * kKvqGroup + wi * 8);
+      for (int g = 0; g < NG; g++) raw[e][t][g].load(p + (8 * e + t * dt) * src.row + g * kKvqGroup);
+  };
+  load(0);
+  load(1);
+#pragma unroll 1
+  for (int h = h0; h < h1; h++, rec += R::kBytes) {
+    p += src.head;
 #pragma unroll
-    for (int e = 0; e < 4; e++)
-      vr[e / 2][e % 2][g].load(vb + (2 * (pr + e / 2 * 4) + e % 2) * src.row + g * kKvqGroup + wi * 8);
-  }
+    for (int e = 0; e < 2; e++) {
+      uint32_t w[2][NG], sw[2][NG];
 #pragma unroll
-  for (int e = 0; e < 4; e++) {
-    uint32_t w[NG], sw[NG];
+      for (int t = 0; t < 2; t++)
 #pragma unroll
-    for (int g = 0; g < NG; g++) {
-      float x[8];
-      kr[e][g].get(x);
-      const KvqScale s = row_scale(kr[e][g], x, 0xffffffffu);
-      w[g] = kvq_codes(x, s);
-      sw[g] = s.word();
-    }
-    const int t = pr + 4 * e;
-    if constexpr (NG == 2) {
-      // a column's 16 bytes are both words of group 0, then of group 1: two threads hold one of each
-      const uint32_t got = __shfl_xor_sync(0xffffffffu, wi & 1 ? w[0] : w[1], 1);
-      if (wi & 1)
-        w[0] = got;
-      else
-        w[1] = got;
-    }
-    store_words<NG>(rec + t * (D / 2) + wi * 4 * NG, w);
-    if (wi == 0) store_words<NG>(rec + R::kKeyScale + t * 4 * NG, sw);
-  }
+        for (int g = 0; g < NG; g++) {
+          float x[8];
+          raw[e][t][g].get(x);
+          const KvqScale s = row_scale(raw[e][t][g], x, 0xffffffffu);
+          w[t][g] = kvq_codes(x, s);
+          sw[t][g] = s.word();
+        }
+      if (h + 1 < h1) load(e);               // the next head's, while this one's other half is computed
+      if (val) {
+        const int pair = pr + 4 * e;
+        uint32_t vw[2 * NG];
 #pragma unroll
-  for (int e = 0; e < 2; e++) {
-    uint32_t w[2 * NG], sw[2 * NG];
+        for (int g = 0; g < NG; g++) {
+          vw[2 * g] = __byte_perm(w[0][g], w[1][g], 0x5410);
+          vw[2 * g + 1] = __byte_perm(w[0][g], w[1][g], 0x7632);
+        }
+        store_words<2 * NG>(rec + R::kVal + pair * D + wi * 8 * NG, vw);
+        if (wi == 0) store_words<2 * NG>(rec + R::kValScale + pair * 8 * NG, sw[0]);
+      } else {
 #pragma unroll
-    for (int g = 0; g < NG; g++) {
-      uint32_t c8[2];
-#pragma unroll
-      for (int t = 0; t < 2; t++) {
-        float x[8];
-        vr[e][t][g].get(x);
-        const KvqScale s = row_scale(vr[e][t][g], x, 0xffffffffu);
-        c8[t] = kvq_codes(x, s);
-        sw[t * NG + g] = s.word();
+        for (int k = 0; k < 2; k++) {
+          const int t = pr + 8 * e + 4 * k;
+          if constexpr (NG == 2) {
+            // a column's 16 bytes are both words of group 0, then of group 1: two threads hold one of each
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, wi & 1 ? w[k][0] : w[k][1], 1);
+            if (wi & 1)
+              w[k][0] = got;
+            else
+              w[k][1] = got;
+          }
+          store_words<NG>(rec + t * (D / 2) + wi * 4 * NG, w[k]);
+          if (wi == 0) store_words<NG>(rec + R::kKeyScale + t * 4 * NG, sw[k]);
+        }
       }
-      w[2 * g] = __byte_perm(c8[0], c8[1], 0x5410);
-      w[2 * g + 1] = __byte_perm(c8[0], c8[1], 0x7632);
     }
-    const int pair = pr + 4 * e;
-    store_words<2 * NG>(rec + R::kVal + pair * D + wi * 8 * NG, w);
-    if (wi == 0) store_words<2 * NG>(rec + R::kValScale + pair * 8 * NG, sw);
   }
 }
 
@@ -1072,8 +1080,9 @@ int write_rows(const mk_kvq_cache* c, const mk_kv_rows* src, const int32_t* src_
     kvq_write_kernel<D, T><<<copy_grid(n, kTokens, c, heads), kCopyThreads, 0, st>>>(cache_of(c), rows_of(src), src_index,
                                                                                     dst_index, n, heads);
   } else {
-    kvq_write_pages_kernel<D, T><<<copy_grid(n, kCopyThreads / 32, c), kCopyThreads, 0, st>>>(
-        cache_of(c), rows_of(src), src_index, dst_index, n);
+    const int heads = token_heads(n, kCopyThreads / 64, c, sm_count());
+    kvq_write_pages_kernel<D, T><<<copy_grid(n, kCopyThreads / 64, c, heads), kCopyThreads, 0, st>>>(
+        cache_of(c), rows_of(src), src_index, dst_index, n, heads);
   }
   return launched();
 }

@@ -96,27 +96,34 @@ __device__ __forceinline__ KvqScale kvq_scale(float lo, float hi) {
 
 // Codes of eight values, nibble i of the word that of x[i]: (x - low) / step to
 // the nearest integer, ties to even, the difference rounded to fp32.  Adding
-// 1.5 2^23 rounds diff * inv to an integer c in the low mantissa bits.  The
-// product is within 5e-6 of the quotient, so c is the nearest integer or, next
-// to a half-way point, its neighbour; diff - c step, which one FMA gives
-// exactly (c step has at most 12 bits), tells: c moves by one where that is
-// beyond half a step, or at it with an odd c (the limit is then the number
-// below half a step).  BF16 values with BF16 steps tie often, one in a few
-// hundred, so a branch around the correction would nearly always be taken by
-// some lane (a 256K prefix then took 200 us, not 179).  Eight patterns, shifted
-// and added, leave the codes and one constant.
+// 1.5 2^23 downwards leaves c, the floor of diff * inv, in the low mantissa
+// bits.  The product is within 5e-6 of the quotient, so r = diff - c step is
+// between 0 and step but for that error, and one FMA gives it exactly: c step
+// has at most 12 bits, and r is a multiple of diff's last bit no larger than
+// diff.  The code is c, or c + 1 where r is above half a step, or at it with an
+// odd c.  With H = 2 / 2^exponent(step), v = (r - step / 2) H + 1/2 held to
+// 0..1 is above, at or below 1/2 as r is above, at or below half a step (the
+// least difference is 2^-24, which v shows), so adding v to 1.5 2^23 + c
+// rounds to the code, ties included.  All this is arithmetic of the FMA pipe,
+// two values an instruction where it can be; with comparisons and selections
+// the integer pipe bound a 256K prefix at 157 us.  Eight patterns, shifted and
+// added, leave the codes and one constant.
 __device__ __forceinline__ uint32_t kvq_codes(const float* x, const KvqScale& s) {
   constexpr float kMagic = 12582912.f;     // 0x4b400000
-  const int half = __float_as_int(0.5f * s.step);
+  const float h = __uint_as_float(0x7f800000u - (__float_as_uint(s.step) & 0x7f800000u));
+  const float b = fmaf(-0.5f * h, s.step, 0.5f);
+  const float2 low = make_float2(-s.low, -s.low), inv = make_float2(s.inv, s.inv);
+  const float2 magic = make_float2(kMagic, kMagic), neg_step = make_float2(-s.step, -s.step);
   uint32_t word = 0;
 #pragma unroll
-  for (int i = 7; i >= 0; i--) {
-    const float diff = x[i] - s.low;
-    const float t = fmaf(diff, s.inv, kMagic);
-    const float r = fmaf(kMagic - t, s.step, diff);
-    const float limit = __int_as_float(half - (__float_as_int(t) & 1));
-    const float moved = fabsf(r) > limit ? t + copysignf(1.f, r) : t;
-    word = word * 16u + __float_as_uint(moved);
+  for (int i = 6; i >= 0; i -= 2) {
+    const float2 diff = __fadd2_rn(make_float2(x[i], x[i + 1]), low);
+    const float2 t = __ffma2_rd(diff, inv, magic);
+    const float2 c = __fadd2_rn(t, make_float2(-kMagic, -kMagic));
+    const float2 r = __ffma2_rn(c, neg_step, diff);
+    const float2 code = __fadd2_rn(t, make_float2(__saturatef(fmaf(r.x, h, b)), __saturatef(fmaf(r.y, h, b))));
+    word = word * 16u + __float_as_uint(code.y);
+    word = word * 16u + __float_as_uint(code.x);
   }
   return s.inv == 0.f ? 0u : word - 0x4b400000u * 0x11111111u;
 }

@@ -410,19 +410,21 @@ struct KvqAttn {
         for (int e = 0; e < 4; e++) acc[g][e] += low[e];
     }
 #pragma unroll
-    for (int e = 0; e < 2; e++)
+    for (int e = 0; e < 2; e++) {
+      float2 dot, off;                     // both heads
 #pragma unroll
-      for (int h = 0; h < 2; h++) {
-        float dot = 0.f, off = 0.f;
-#pragma unroll
-        for (int g = 0; g < NG; g++) {
-          const float step = bf16lo(ky.sc[e][g]);
-          const float base = QT == 2 ? fmaf(8.f, step, bf16hi(ky.sc[e][g])) : bf16hi(ky.sc[e][g]);
-          dot = g == 0 ? step * acc[g][2 * e + h] : fmaf(step, acc[g][2 * e + h], dot);
-          off = g == 0 ? base * sq[g][h] : fmaf(base, sq[g][h], off);
-        }
-        x[e][h] = fmaf(dot, f[h], off);
+      for (int g = 0; g < NG; g++) {
+        const float st = bf16lo(ky.sc[e][g]);
+        const float ba = QT == 2 ? fmaf(8.f, st, bf16hi(ky.sc[e][g])) : bf16hi(ky.sc[e][g]);
+        const float2 step = make_float2(st, st), base = make_float2(ba, ba);
+        const float2 s2 = make_float2(acc[g][2 * e], acc[g][2 * e + 1]), q2 = make_float2(sq[g][0], sq[g][1]);
+        dot = g == 0 ? __fmul2_rn(step, s2) : __ffma2_rn(step, s2, dot);
+        off = g == 0 ? __fmul2_rn(base, q2) : __ffma2_rn(base, q2, off);
       }
+      const float2 v = __ffma2_rn(dot, make_float2(f[0], f[1]), off);
+      x[e][0] = v.x;
+      x[e][1] = v.y;
+    }
   }
 
   // Tokens [0, valid[n]) of N pages (MASK; else all 16 of each); valid is the
@@ -518,15 +520,21 @@ struct KvqAttn {
       weights();
     }
 #pragma unroll
-    for (int n = 0; n < N; n++)
+    for (int n = 0; n < N; n++) {
+      const float2 p0 = make_float2(p[n][0][0], p[n][0][1]), p1 = make_float2(p[n][1][0], p[n][1][1]);
+      const float2 ln = __fadd2_rn(make_float2(l[0], l[1]), __fadd2_rn(p0, p1));
+      l[0] = ln.x;
+      l[1] = ln.y;
 #pragma unroll
-      for (int h = 0; h < 2; h++) {
-        l[h] += p[n][0][h] + p[n][1][h];
-#pragma unroll
-        for (int g = 0; g < NG; g++)
-          om[g][h] = fmaf(p[n][1][h], fmaf(8.f, bf16lo(vs[n][1][g]), bf16hi(vs[n][1][g])),
-                          fmaf(p[n][0][h], fmaf(8.f, bf16lo(vs[n][0][g]), bf16hi(vs[n][0][g])), om[g][h]));
+      for (int g = 0; g < NG; g++) {
+        const float m0 = fmaf(8.f, bf16lo(vs[n][0][g]), bf16hi(vs[n][0][g]));
+        const float m1 = fmaf(8.f, bf16lo(vs[n][1][g]), bf16hi(vs[n][1][g]));
+        const float2 t = __ffma2_rn(
+            p1, make_float2(m1, m1), __ffma2_rn(p0, make_float2(m0, m0), make_float2(om[g][0], om[g][1])));
+        om[g][0] = t.x;
+        om[g][1] = t.y;
       }
+    }
 #pragma unroll
     for (int n = 0; n < N; n++) {
       uint32_t v[2][NW];

@@ -40,8 +40,8 @@ __device__ __forceinline__ void flag_bad(const Cache& c, int code) {
 // both tokens of a pair meet in one lane, every record is moved in 16-byte
 // pieces, and a writer loads the next head's half page while it computes the
 // other half.  262,144 tokens of 4 heads of 128 dims in BF16, 688 MB: read 104 us
-// (98 % of the measured copy rate), written 125 us (81 %; a third of the issue
-// slots and of the DRAM rate are left: 24 warps an SM do not hide every wait).
+// (98 % of the measured copy rate), written 125 us (81 %; issue slots 69 %, DRAM
+// 66 % of its peak: 24 warps an SM do not hide every wait).
 // Measured of the writer: both halves of keys and values held by one warp
 // without the overlap 151 (16 warps an SM) and 136 us (32, registers spill),
 // keys or values a warp without it 133, half a page a warp 149; 64 registers
@@ -387,14 +387,16 @@ __global__ void __launch_bounds__(kCopyThreads) kvq_read_pages_kernel(Cache c, c
 // and a second kernel merges them in page order: no atomics, one result.
 // A warp takes every eighth page of a segment through a ring of four in shared
 // memory (three on their way: 110 KB an SM, twice what the latency needs).
-// 32 query and 4 KV heads of 128 dims, BF16: 262,144 tokens in 41 us, 39 of them
+// 32 query and 4 KV heads of 128 dims, BF16: 262,144 tokens in 42 us, 39 of them
 // in the first kernel, against 22 us for its 151 MB at the measured copy rate;
-// 16 sequences of 1K-32K in 46 us (152 MB).  What bounds it is issuing
-// instructions, about 365 a page and head (4096 codes): 40 to mask key codes,
-// 72 to mask and centre value codes, 60 for scales, 45 for weights and
-// references, 25 to fetch; ALU pipe 53 %, tensor pipe 20 %.  Slower: two pages a
-// warp at a time (49 us, registers spill), 18 warps an SM at 96 registers
-// (60 us), shifts as multiplications (43 us).
+// 16 sequences of 1K-32K in 45 us (152 MB).  About 350 instructions a page and
+// head (4096 codes): 40 to mask key codes, 72 to mask and centre value codes,
+// 50 for scales, 40 for weights and references, 25 to fetch.  Issue slots
+// 50-58 %, ALU pipe 52 %, DRAM 49 %, tensor pipe 20 %: what bounds it is a page's
+// chain (loads, products, vote, products) with 16 warps an SM.  Slower or no
+// faster: two pages a warp at a time (49 us, registers spill), the next page's
+// scores ahead of this one's values (42 us, spills too), 18 warps an SM at 96
+// registers (60 us), shifts as multiplications (43 us), a ring of five (45 us).
 
 constexpr int kAttnWarps = 8;
 constexpr int kAttnThreads = kAttnWarps * 32;

@@ -405,6 +405,44 @@ def test_pages_behind_two_gigabytes():
     c.check()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("hkv,d,n", [(5, 128, 1500), (7, 64, 1100), (1, 128, 8000)])
+def test_long_calls_store_the_same_bytes_by_page_and_by_row(hkv, d, n, dtype):
+    """Calls long enough for several heads a block, and a last block with fewer: whole pages, and the same rows in
+    calls of several lengths, leave the same bytes (those of the restatement on a sample) and read back alike."""
+    gen = torch.Generator("cuda").manual_seed(n)
+    kp, vp = (torch.randn(n, hkv, 16, d, device="cuda", generator=gen).to(dtype) for _ in range(2))
+    a, b = QuantCache(n, hkv, d), QuantCache(n, hkv, d)
+    ids = torch.randperm(n, device="cuda", generator=gen).to(torch.int32)
+    src = torch.arange(n, dtype=torch.int32, device="cuda")
+    ids[n // 3] = -1
+    src[n // 2] = -1
+    a.write_pages(kp, vp, src, ids)
+    kr, vr = (x.transpose(1, 2).reshape(n * 16, hkv, d) for x in (kp, vp))
+    dst = torch.where((src < 0) | (ids < 0), -1, ids)
+    slots = torch.where(dst[:, None] < 0, -1, dst[:, None] * 16 + torch.arange(16, device="cuda")).reshape(-1).int()
+    at = 0
+    for m in (1, 3001, 7, 9000, n * 16):
+        b.write(kr[at:at + m], vr[at:at + m], slots[at:at + m])
+        at += m
+    assert at >= n * 16 and torch.equal(a.pool, b.pool)
+    some = [0, 1, n // 3, n // 2, n // 2 + 1, n - 2, n - 1]
+    for i in some:
+        if int(dst[i]) < 0:
+            continue
+        one = np.zeros((1, hkv * 18 * d), dtype=np.uint8)
+        rows = [host(x[i].cpu()).transpose(1, 0, 2) for x in (kp, vp)]
+        _kvq.store(one, hkv, d, *rows, np.arange(16))
+        assert np.array_equal(a.pool[int(dst[i])].cpu().numpy(), one[0])
+    ko, vo = torch.zeros_like(kp), torch.zeros_like(vp)
+    a.read_pages(dst, ko, vo, torch.arange(n, dtype=torch.int32, device="cuda"))
+    kb, vb = a.read(slots, dtype)
+    for x, y in ((ko, kb), (vo, vb)):
+        assert torch.equal(x.transpose(1, 2).reshape(n * 16, hkv, d), y)
+    a.check()
+    b.check()
+
+
 # -------------------------------------------------- indexes out of range, streams, graphs
 
 def test_bad_indexes_are_flagged_and_touch_nothing():

@@ -1075,14 +1075,14 @@ int write_rows(const mk_kvq_cache* c, const mk_kv_rows* src, const int32_t* src_
                int unit, void* stream) {
   constexpr int kTokens = TokenLane<D>::kTokens;
   cudaStream_t st = (cudaStream_t)stream;
+  const int sms = sm_count();
+  if (!sms) return MK_ERR_CUDA;
   if (unit == 1) {
-    const int sms = sm_count();
-    if (!sms) return MK_ERR_CUDA;
     const int heads = token_heads(n, kTokens, c, sms);
     kvq_write_kernel<D, T><<<copy_grid(n, kTokens, c, heads), kCopyThreads, 0, st>>>(cache_of(c), rows_of(src), src_index,
                                                                                     dst_index, n, heads);
   } else {
-    const int heads = token_heads(n, kCopyThreads / 64, c, sm_count());
+    const int heads = token_heads(n, kCopyThreads / 64, c, sms);
     kvq_write_pages_kernel<D, T><<<copy_grid(n, kCopyThreads / 64, c, heads), kCopyThreads, 0, st>>>(
         cache_of(c), rows_of(src), src_index, dst_index, n, heads);
   }

@@ -396,11 +396,11 @@ class Decoder:
         if fp8 is not None:
             cfg_kw = {**cfg_kw, "expert_format": MK_EXPERTS_FP8_E4M3}
         if v_pool is None:
-            if k_pool.dim() != 3 or k_pool.element_size() != 1 \
-                    or k_pool.shape[2] != mk_kvq_page_bytes(self.dims.n_kv_heads, self.dims.head_dim):
-                raise ValueError("4-bit KV pools: uint8 [layers, pages, page bytes], got "
-                                 f"{k_pool.dtype} {tuple(k_pool.shape)}")
+            self._check_kv4(k_pool, L)
             cfg_kw = {**cfg_kw, "kv_format": MK_KV_INT4}
+        elif k_pool.element_size() == 1 or cfg_kw.get("kv_format", MK_KV_BF16) != MK_KV_BF16:
+            raise ValueError("4-bit KV pools come as k_pool with v_pool None, got "
+                             f"{k_pool.dtype} {tuple(k_pool.shape)} and a v_pool")
         self.cfg = make_config(self.dims, max_batch, max_pages_per_seq, k_pool.shape[1], **cfg_kw)
         self._keep = []
 
@@ -424,6 +424,17 @@ class Decoder:
             self.weights.s_down = arr(fp8["s_down"])
         self.h = mk_create(self.cfg, self.weights)
         self.batch = 0
+
+    def _check_kv4(self, pool, n_layers):
+        page = mk_kvq_page_bytes(self.dims.n_kv_heads, self.dims.head_dim)
+        got = f"{pool.dtype} {tuple(pool.shape)}, strides {tuple(pool.stride())}, on {pool.device}"
+        if str(pool.dtype) != "torch.uint8" or pool.dim() != 3 or pool.shape[0] != n_layers or pool.shape[1] < 1 \
+                or pool.shape[2] != page:
+            raise ValueError(f"4-bit KV pools: uint8 [{n_layers} layers, pages, {page} page bytes], got {got}")
+        if pool.stride(2) != 1 or (pool.shape[1] > 1 and pool.stride(1) != page):
+            raise ValueError(f"4-bit KV pools: the pages of a layer lie side by side (contiguous), got {got}")
+        if pool.device.type != "cuda" or pool.device != self.model.embed.device:
+            raise ValueError(f"4-bit KV pools: on the model's GPU, got {got}")
 
     def schedule(self, tokens, page_tables, seq_lens, seq_ids=None, stream=None):
         self.batch = len(tokens)

@@ -1,5 +1,5 @@
 """The 4-bit cache's calls on the host alone (no GPU): where the device cannot
-be asked, and what the shape queries answer."""
+be asked, and the pools a Decoder refuses."""
 from __future__ import annotations
 
 import os
@@ -7,6 +7,7 @@ import subprocess
 import sys
 
 import pytest
+import torch
 
 from persistent_moe_decode_gb300 import build as B
 from persistent_moe_decode_gb300 import mk
@@ -41,3 +42,38 @@ def test_calls_without_a_device_return_an_error(lib):
     env = {**os.environ, "CUDA_VISIBLE_DEVICES": "", "PYTHONPATH": ROOT}
     r = subprocess.run([sys.executable, "-c", NO_DEVICE], env=env, cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, (r.returncode, r.stderr[-2000:])
+
+
+# ------------------------------------------------ the pools a Decoder is given
+
+def decoder_error(pool, v_pool=None, **cfg):
+    from persistent_moe_decode_gb300.configs import TINY
+
+    class Model:
+        dims, fp8, embed = TINY, None, torch.zeros(1)
+        w_gate = w_up = w_down = None
+
+    with pytest.raises(ValueError) as e:
+        mk.Decoder(Model, pool, v_pool, 1, 4, **cfg)
+    return str(e.value)
+
+
+def test_a_decoder_refuses_4_bit_pools_it_would_misread(lib):
+    """Another type of one byte, pages that do not lie side by side, another number of layers, a pool that is not on
+    the GPU; 4-bit pools beside a v_pool, whose pages a BF16 step would read past their end, and BF16 pools under
+    the 4-bit format."""
+    from persistent_moe_decode_gb300.configs import TINY as d
+    page = mk.mk_kvq_page_bytes(d.n_kv_heads, d.head_dim)
+    pools = torch.zeros(d.n_layers, 8, page, dtype=torch.uint8)
+    assert "uint8" in decoder_error(pools.to(torch.int8))
+    assert "uint8" in decoder_error(pools[:1].expand(d.n_layers + 1, 8, page))
+    assert "uint8" in decoder_error(pools[:, :0])
+    assert "contiguous" in decoder_error(pools[:, ::2])
+    assert "contiguous" in decoder_error(torch.zeros(d.n_layers, 8, 2 * page, dtype=torch.uint8)[..., :page])
+    assert "contiguous" in decoder_error(torch.zeros(d.n_layers, page, 8, dtype=torch.uint8).transpose(1, 2))
+    assert "contiguous" in decoder_error(pools[:, :1].expand(-1, 8, -1))
+    # layers apart are fine, and so is a pool of one page: what remains is where they are
+    assert "GPU" in decoder_error(pools) and "GPU" in decoder_error(pools[:, :5]) and "GPU" in decoder_error(pools[:, :1])
+    assert "v_pool" in decoder_error(pools, pools)
+    bf16 = torch.zeros(d.n_layers, 8, d.n_kv_heads, 16, d.head_dim, dtype=torch.bfloat16)
+    assert "v_pool" in decoder_error(bf16, bf16, kv_format=mk.MK_KV_INT4)

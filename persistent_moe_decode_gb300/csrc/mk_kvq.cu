@@ -930,10 +930,13 @@ __global__ void __launch_bounds__(kMergeThreads) kvq_merge_kernel(AttnArgs a, in
 
 bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
+bool cache_shape(int n_kv_heads, int head_dim) {
+  return (head_dim == 64 || head_dim == 128) && n_kv_heads >= 1 && n_kv_heads <= 1024;
+}
+
 int check_cache(const mk_kvq_cache* c) {
   if (!c) return MK_ERR_BAD_ARG;
-  if ((c->head_dim != 64 && c->head_dim != 128) || c->n_kv_heads < 1 || c->n_kv_heads > 1024 || c->num_pages < 1 ||
-      c->num_pages > 0x7fffffff / kKvqPage)
+  if (!cache_shape(c->n_kv_heads, c->head_dim) || c->num_pages < 1 || c->num_pages > 0x7fffffff / kKvqPage)
     return MK_ERR_BAD_CONFIG;
   if (!c->pool || !aligned(c->pool, 16) || !aligned(c->status, 4)) return MK_ERR_BAD_ARG;
   return MK_OK;
@@ -1112,7 +1115,7 @@ int read_rows(const mk_kvq_cache* c, const int32_t* src_index, const mk_kv_rows*
 extern "C" {
 
 size_t mk_kvq_page_bytes(int n_kv_heads, int head_dim) {
-  if (n_kv_heads < 1 || (head_dim != 64 && head_dim != 128)) return 0;
+  if (!cache_shape(n_kv_heads, head_dim)) return 0;
   return (size_t)n_kv_heads * 18 * head_dim;
 }
 

@@ -28,7 +28,7 @@ def page_bytes(n_kv_heads: int, head_dim: int) -> int:
     n = mk.mk_kvq_page_bytes(n_kv_heads, head_dim)
     if n == 0:
         raise ValueError(f"4-bit cache: {n_kv_heads} KV heads of {head_dim} dims are not supported "
-                         "(head_dim must be 64 or 128)")
+                         "(1 to 1024 heads of 64 or 128 dims)")
     return n
 
 

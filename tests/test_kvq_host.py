@@ -10,7 +10,7 @@ import pytest
 import torch
 
 from persistent_moe_decode_gb300 import build as B
-from persistent_moe_decode_gb300 import mk
+from persistent_moe_decode_gb300 import kvq, mk
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -42,6 +42,19 @@ def test_calls_without_a_device_return_an_error(lib):
     env = {**os.environ, "CUDA_VISIBLE_DEVICES": "", "PYTHONPATH": ROOT}
     r = subprocess.run([sys.executable, "-c", NO_DEVICE], env=env, cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, (r.returncode, r.stderr[-2000:])
+
+
+def test_page_bytes_of_heads_the_calls_refuse(lib):
+    """mk_kvq_page_bytes supports the shapes that the calls take, and no others."""
+    c = mk.mk_kvq_cache(pool=1 << 20, num_pages=4, n_kv_heads=1, head_dim=64, status=None)
+    for hkv in (1023, 1024, 1025, 1 << 20, 2 ** 31 - 1):
+        c.n_kv_heads = hkv
+        taken = lib.mk_kvq_write(c, mk.mk_kv_rows(type=mk.MK_TYPE_BF16), None, None, 0, 1, None) == mk.MK_OK
+        assert taken == (hkv <= 1024)
+        assert mk.mk_kvq_page_bytes(hkv, 64) == (hkv * 18 * 64 if taken else 0)
+        if not taken:
+            with pytest.raises(ValueError):
+                kvq.page_bytes(hkv, 64)
 
 
 # ------------------------------------------------ the pools a Decoder is given

@@ -987,6 +987,11 @@ int check_heads(const mk_kvq_cache* c, int n_q_heads, int batch) {
   return batch < 0 || batch > 65535 ? MK_ERR_BATCH_TOO_LARGE : MK_OK;
 }
 
+int check_tables(int type, int max_pages) {
+  if (type != MK_TYPE_BF16 && type != MK_TYPE_F32) return MK_ERR_BAD_ARG;
+  return max_pages < 0 || max_pages > 0x7fffffff / kKvqPage ? MK_ERR_BAD_ARG : MK_OK;
+}
+
 // blocks that fill the GPU, two slots each
 int attn_blocks(int sms, int per_sm) { return std::min(sms * per_sm, kMaxSlots / 2); }
 
@@ -1144,7 +1149,7 @@ int mk_kvq_read(const mk_kvq_cache* c, const int32_t* src_index, const mk_kv_row
 }
 
 size_t mk_kvq_workspace(const mk_kvq_cache* c, int type, int n_q_heads, int batch, int max_pages) {
-  if (check_cache(c) || check_heads(c, n_q_heads, batch) || max_pages < 0 || batch == 0) return 0;
+  if (check_cache(c) || check_heads(c, n_q_heads, batch) || check_tables(type, max_pages) || batch == 0) return 0;
   const int sms = sm_count();
   if (!sms) return 0;
   const int grp = n_q_heads / c->n_kv_heads;
@@ -1158,9 +1163,9 @@ int mk_kvq_attention(const mk_kvq_cache* c, const void* q, int64_t q_stride, voi
                      float scale, void* workspace, size_t workspace_bytes, void* stream) {
   int rc = check_cache(c);
   if (!rc) rc = check_heads(c, n_q_heads, batch);
+  if (!rc) rc = check_tables(type, max_pages);
   if (rc) return rc;
-  if (type != MK_TYPE_BF16 && type != MK_TYPE_F32) return MK_ERR_BAD_ARG;
-  if (max_pages < 0 || max_pages > 0x7fffffff / kKvqPage || !isfinite(scale)) return MK_ERR_BAD_ARG;
+  if (!isfinite(scale)) return MK_ERR_BAD_ARG;
   if (batch == 0) return MK_OK;
   const int64_t v = type == MK_TYPE_BF16 ? 8 : 4;
   if (!q || !out || !seq_lens || (max_pages && !page_tables) || !aligned(q, 16) || !aligned(out, 16) ||

@@ -1,0 +1,40 @@
+"""The 4-bit cache's calls as a program makes them beside others: other streams,
+shared or overlapping buffers, the ends of the ranges that include/mk.h gives."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from persistent_moe_decode_gb300 import mk
+from persistent_moe_decode_gb300.kvq import QuantCache
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    from persistent_moe_decode_gb300 import build
+    build.build()
+
+
+def ints(*x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def test_the_workspace_of_arguments_that_the_attention_refuses_is_none():
+    """mk_kvq_workspace is 0 where mk_kvq_attention refuses the same type, heads, batch or page tables."""
+    c = QuantCache(4, 2, 64)
+    q = torch.zeros(1, 4, 64, device="cuda")
+    ln = ints(1)
+    fits = dict(kind=mk.MK_TYPE_F32, hq=4, batch=1, pages=1 << 20)
+    assert mk.mk_kvq_workspace(c._c, *fits.values()) > 0
+    for bad in (dict(kind=2), dict(kind=-1), dict(pages=-1), dict(pages=1 << 27), dict(pages=2 ** 31 - 1), dict(hq=3),
+                dict(batch=65536)):
+        kw = {**fits, **bad}
+        assert mk.mk_kvq_workspace(c._c, *kw.values()) == 0, bad
+        with pytest.raises(mk.MkError):              # refused before anything is read
+            mk.mk_kvq_attention(c._c, q.data_ptr(), 256, q.data_ptr(), 256, kw["kind"], kw["hq"], kw["batch"],
+                                ln.data_ptr(), kw["pages"], ln.data_ptr(), 1.0, q.data_ptr(), 1 << 40)

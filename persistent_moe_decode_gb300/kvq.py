@@ -65,11 +65,13 @@ class QuantCache:
         return self.pool.shape[0]
 
     def check(self) -> None:
-        """Raise MkError if a call so far met a page, slot or length out of range (synchronises);
-        clears the record."""
+        """Raise MkError if a call so far, on whatever stream, met a page, slot or length out of range (waits for
+        the device); clears the record."""
+        torch.cuda.synchronize(self._dev)
         code = int(self.status.item())
         if code:
             self.status.zero_()
+            torch.cuda.synchronize(self._dev)    # a later call's record, on another stream, comes after
             raise mk.MkError(code, "4-bit cache")
 
     # ------------------------------------------------------------ arguments

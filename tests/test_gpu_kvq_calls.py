@@ -38,3 +38,33 @@ def test_the_workspace_of_arguments_that_the_attention_refuses_is_none():
         with pytest.raises(mk.MkError):              # refused before anything is read
             mk.mk_kvq_attention(c._c, q.data_ptr(), 256, q.data_ptr(), 256, kw["kind"], kw["hq"], kw["batch"],
                                 ln.data_ptr(), kw["pages"], ln.data_ptr(), 1.0, q.data_ptr(), 1 << 40)
+
+
+@pytest.mark.parametrize("given", [True, False], ids=["stream argument", "current stream"])
+def test_check_sees_calls_that_have_not_run_yet_on_another_stream(given):
+    """A call behind long work on a stream of its own: check() on the current stream waits for it, and the record it
+    clears stays cleared."""
+    hkv, d = 2, 64
+    c = QuantCache(4, hkv, d)
+    k = torch.zeros(1, hkv, d, dtype=torch.bfloat16, device="cuda")
+    bad, good = ints(64), ints(5)
+    side = torch.cuda.Stream()
+    c.write(k, k, good)                              # loading a kernel may wait for the device
+    for slots in (bad, good, bad):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000_000)           # a tenth of a second
+            if not given:
+                c.write(k, k, slots)
+        if given:
+            c.write(k, k, slots, stream=side)
+        assert not side.query()
+        if slots is good:
+            c.check()
+        else:
+            with pytest.raises(mk.MkError) as e:
+                c.check()
+            assert e.value.code == mk.MK_ERR_BAD_PAGE
+        assert side.query()
+        torch.cuda.synchronize()
+        assert int(c.status.item()) == 0

@@ -48,7 +48,8 @@ __device__ __forceinline__ void flag_bad(const Cache& c, int code) {
 // with the overlap 126, 48 148.  8191 tokens by row: 7 us written, 6 read, bound
 // by instructions (the indexes and addresses of short rows).
 
-// eight consecutive elements as they lie in memory, moved 16 bytes at a time
+// eight consecutive elements as they lie in memory, moved 16 bytes at a time;
+// load() is for memory that nothing writes while the kernel runs
 template <class T>
 struct Raw8 {
   static constexpr int W = 2 * (int)sizeof(T);
@@ -92,10 +93,16 @@ __device__ __forceinline__ KvqScale row_scale(const Raw8<float>&, const float* x
   return kvq_group_scale(x, mask);
 }
 
+// eight elements of the query, by ordinary loads: out may be q, so the memory
+// is not read-only while the kernel runs
 template <class T>
 __device__ __forceinline__ void load8(float* x, const T* p) {
   Raw8<T> r;
-  r.load(p);
+#pragma unroll
+  for (int i = 0; i < Raw8<T>::W; i += 4) {
+    const uint4 t = *((const uint4*)p + i / 4);
+    r.w[i] = t.x, r.w[i + 1] = t.y, r.w[i + 2] = t.z, r.w[i + 3] = t.w;
+  }
   r.get(x);
 }
 

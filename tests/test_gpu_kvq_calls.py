@@ -68,3 +68,32 @@ def test_check_sees_calls_that_have_not_run_yet_on_another_stream(given):
         assert side.query()
         torch.cuda.synchronize()
         assert int(c.status.item()) == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("hkv,grp,d,wide", [(4, 1, 64, 8), (1, 8, 128, 8), (2, 9, 64, 3000), (4, 8, 128, 3000)],
+                         ids=["cluster64", "cluster128", "two kernels, tiles", "two kernels"])
+def test_the_output_over_the_query_where_rows_of_several_tasks_share_a_cache_line(hkv, grp, d, wide, dtype):
+    """out is q, at an offset of 16 bytes and with rows that are no multiple of 128 bytes apart: the bits are those of
+    a separate output, and what lies between and behind the rows stays."""
+    gen = torch.Generator("cuda").manual_seed(d + hkv)
+    batch, hq, pages = 9, hkv * grp, 40
+    c = QuantCache(pages, hkv, d)
+    k, v = (torch.randn(pages, hkv, 16, d, device="cuda", generator=gen).bfloat16() for _ in range(2))
+    ids = torch.arange(pages, dtype=torch.int32, device="cuda")
+    c.write_pages(k, v, ids, ids)
+    table = torch.randint(0, pages, (batch, wide), device="cuda", generator=gen).int()
+    lens = ints(1, 0, 128, 77, 16, 5, 100, 33, 64)
+    unit = 16 // dtype.itemsize
+    stride = hq * d + unit
+    flat = torch.randn(unit + batch * stride, device="cuda", generator=gen).to(dtype)
+    q = flat[unit:].view(batch, stride)[:, :hq * d].unflatten(1, (hq, d))
+    want = c.attention(q, table, lens)
+    for _ in range(5):
+        both = flat.clone()
+        same = both[unit:].view(batch, stride)[:, :hq * d].unflatten(1, (hq, d))
+        assert c.attention(same, table, lens, out=same).data_ptr() == same.data_ptr()
+        assert torch.equal(same, want)
+        same.copy_(q)
+        assert torch.equal(both, flat)
+    c.check()

@@ -10,8 +10,9 @@ read back (``read``, ``read_pages``) and attended to (``attention``).
 Every call runs on ``stream``, by default torch's current stream of the cache's
 device, and returns before the kernels have run; it can be captured into a CUDA
 graph.  Tensors last used on another stream are the caller's to order, as with
-any torch operation.  A call with tensors of another device, another type or a
-wrong shape raises; indexes and lengths are checked on the device (``check``).
+any torch operation.  A call with tensors or a stream of another device, another
+type or a wrong shape raises; indexes and lengths are checked on the device
+(``check``).
 """
 from __future__ import annotations
 
@@ -112,6 +113,8 @@ class QuantCache:
         allocations and copies too."""
         if stream is None and torch.cuda.current_device() == self._dev:
             return fn(torch._C._cuda_getCurrentRawStream(self._dev), *args)   # current_stream() costs 2 us more
+        if stream is not None and stream.device != self.pool.device:
+            raise ValueError(f"stream: one of {self.pool.device}, got one of {stream.device}")
         with torch.cuda.device(self._dev), torch.cuda.stream(stream):    # None: the device's current one
             return fn(torch.cuda.current_stream().cuda_stream, *args)
 

@@ -97,3 +97,24 @@ def test_the_output_over_the_query_where_rows_of_several_tasks_share_a_cache_lin
         same.copy_(q)
         assert torch.equal(both, flat)
     c.check()
+
+
+def test_a_stream_of_another_device_is_refused():
+    """It would make its device current, and the kernels would run there on this device's addresses."""
+    class Stream:                                    # stands in for a stream of a second GPU
+        device = torch.device("cuda", torch.cuda.current_device() + 1)
+
+    hkv, d = 2, 64
+    c = QuantCache(4, hkv, d)
+    k = torch.zeros(1, hkv, d, dtype=torch.bfloat16, device="cuda")
+    pools = torch.zeros(4, hkv, 16, d, dtype=torch.bfloat16, device="cuda")
+    one = ints(1)
+    for call in (lambda st: c.write(k, k, one, stream=st), lambda st: c.read(one, stream=st),
+                 lambda st: c.write_pages(pools, pools, one, one, stream=st),
+                 lambda st: c.read_pages(one, pools, pools, one, stream=st),
+                 lambda st: c.attention(k, one[None], one, stream=st)):
+        with pytest.raises(ValueError, match="stream"):
+            call(Stream)
+        call(torch.cuda.Stream())
+        torch.cuda.synchronize()
+    c.check()

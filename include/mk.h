@@ -506,7 +506,9 @@ int mk_kvq_write(const mk_kvq_cache* c, const mk_kv_rows* src, const int32_t* sr
  * dst_index[i] of dst, as step * code + low in fp32, rounded once to dst's
  * type.  A negative src_index[i] gives zeros, a negative dst_index[i] is
  * skipped, an index past the end is skipped and flagged in status.  No two
- * units may name the same destination.  Errors as mk_kvq_write. */
+ * units may name the same destination.  dst's rows lie apart: strides whose
+ * rows would share elements, and one place for keys and values, are
+ * MK_ERR_BAD_ARG.  Other errors as mk_kvq_write. */
 int mk_kvq_read(const mk_kvq_cache* c, const int32_t* src_index, const mk_kv_rows* dst, const int32_t* dst_index,
                 int n, int unit, void* stream);
 

@@ -964,6 +964,28 @@ int check_rows(const mk_kv_rows* r, const mk_kvq_cache* c, int n, int unit, cons
   return MK_OK;
 }
 
+// A read's rows lie apart: no two of them share an element (nested strides, in
+// whatever order), and keys and values have a place each
+bool disjoint(const mk_kv_rows* r, const mk_kvq_cache* c, int unit) {
+  struct Dim {
+    unsigned long long stride;
+    long long size;
+  };
+  auto size_of = [](int64_t s) { return s < 0 ? 0ull - (unsigned long long)s : (unsigned long long)s; };
+  Dim d[3] = {{size_of(r->head_stride), c->n_kv_heads},
+              {size_of(r->row_stride), unit == 1 ? r->count : kKvqPage},
+              {size_of(r->page_stride), unit == 1 ? 1 : r->count}};
+  std::sort(d, d + 3, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+  unsigned long long extent = (unsigned long long)c->head_dim;
+  for (const Dim& x : d) {
+    if (x.size <= 1) continue;
+    if (x.stride < extent) return false;
+    if (x.stride > (1ull << 62) / (unsigned long long)x.size) return false;   // no memory is that long
+    extent += x.stride * (unsigned long long)(x.size - 1);
+  }
+  return r->k != r->v;
+}
+
 Cache cache_of(const mk_kvq_cache* c) { return Cache{(uint8_t*)c->pool, c->status, c->num_pages, c->n_kv_heads}; }
 
 dim3 copy_grid(int n, int per_block, const mk_kvq_cache* c, int heads = 1) {
@@ -1148,6 +1170,7 @@ int mk_kvq_read(const mk_kvq_cache* c, const int32_t* src_index, const mk_kv_row
   int rc = check_cache(c);
   if (!rc) rc = check_rows(dst, c, n, unit, dst_index, src_index);
   if (rc || n == 0) return rc;
+  if (!disjoint(dst, c, unit)) return MK_ERR_BAD_ARG;
   if (c->head_dim == 128)
     return dst->type == MK_TYPE_BF16 ? read_rows<128, uint16_t>(c, src_index, dst, dst_index, n, unit, stream)
                                      : read_rows<128, float>(c, src_index, dst, dst_index, n, unit, stream);

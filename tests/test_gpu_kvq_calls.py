@@ -108,13 +108,34 @@ def test_a_stream_of_another_device_is_refused():
     c = QuantCache(4, hkv, d)
     k = torch.zeros(1, hkv, d, dtype=torch.bfloat16, device="cuda")
     pools = torch.zeros(4, hkv, 16, d, dtype=torch.bfloat16, device="cuda")
+    other = pools.clone()
     one = ints(1)
     for call in (lambda st: c.write(k, k, one, stream=st), lambda st: c.read(one, stream=st),
                  lambda st: c.write_pages(pools, pools, one, one, stream=st),
-                 lambda st: c.read_pages(one, pools, pools, one, stream=st),
+                 lambda st: c.read_pages(one, pools, other, one, stream=st),
                  lambda st: c.attention(k, one[None], one, stream=st)):
         with pytest.raises(ValueError, match="stream"):
             call(Stream)
         call(torch.cuda.Stream())
         torch.cuda.synchronize()
+    c.check()
+
+
+def test_read_pages_into_pools_that_share_memory_is_refused():
+    hkv, d = 2, 64
+    c = QuantCache(4, hkv, d)
+    k, v = (torch.full((4, hkv, 16, d), x, device="cuda") for x in (2.0, 3.0))
+    ids = ints(0, 1)
+    for a, b in ((k, k), (k[:1].expand(4, -1, -1, -1), v[:1].expand(4, -1, -1, -1)),
+                 (k[:, :1].expand(-1, hkv, -1, -1), v[:, :1].expand(-1, hkv, -1, -1))):
+        with pytest.raises(mk.MkError) as e:
+            c.read_pages(ids, a, b, ids)
+        assert e.value.code == mk.MK_ERR_BAD_ARG
+    assert (k == 2).all() and (v == 3).all()
+    both = torch.full((4, hkv, 2, 16, d), 5.0, device="cuda")    # keys and values side by side lie apart
+    c.read_pages(ids, both[:, :, 0], both[:, :, 1], ids)
+    assert (both[:2] == 0).all() and (both[2:] == 5).all()
+    c.write_pages(k[:1].expand(4, -1, -1, -1), k[:1].expand(4, -1, -1, -1), ints(0, 1, 2, 3), ints(0, 1, 2, 3))
+    c.read_pages(ints(0, 1, 2, 3), k, v, ints(0, 1, 2, 3))
+    assert (k == 2).all() and (v == 2).all()
     c.check()

@@ -28,7 +28,7 @@ L, P = mk.lib(), 1 << 20
 for d in (64, 128):
     for kind in (mk.MK_TYPE_BF16, mk.MK_TYPE_F32):
         c = mk.mk_kvq_cache(pool=P, num_pages=64, n_kv_heads=4, head_dim=d, status=None)
-        r = mk.mk_kv_rows(P, P, kind, 64, 64 * d, d, 16 * d)
+        r = mk.mk_kv_rows(P, 2 * P, kind, 16, 64 * d, d, 16 * d)
         for unit in (1, 16):
             assert L.mk_kvq_write(c, r, P, P, 3, unit, None) == mk.MK_ERR_CUDA, ("write", d, kind, unit)
             assert L.mk_kvq_read(c, P, r, P, 3, unit, None) == mk.MK_ERR_CUDA, ("read", d, kind, unit)
@@ -41,6 +41,39 @@ def test_calls_without_a_device_return_an_error(lib):
     """Valid arguments where no device answers (a child process that sees none): MK_ERR_CUDA from every call."""
     env = {**os.environ, "CUDA_VISIBLE_DEVICES": "", "PYTHONPATH": ROOT}
     r = subprocess.run([sys.executable, "-c", NO_DEVICE], env=env, cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, (r.returncode, r.stderr[-2000:])
+
+
+OVERLAP = """
+from persistent_moe_decode_gb300 import mk
+L, P, d, hkv = mk.lib(), 1 << 20, 64, 2
+def read(unit, count, page, row, head, v=2 * P, hkv=hkv, kind=mk.MK_TYPE_BF16):
+    c = mk.mk_kvq_cache(pool=P, num_pages=64, n_kv_heads=hkv, head_dim=d, status=None)
+    r = mk.mk_kv_rows(P, v, kind, count, page, row, head)
+    w = L.mk_kvq_write(c, r, P, P, 1, unit, None)
+    assert w == mk.MK_ERR_CUDA                       # a source may repeat rows; there is no device here
+    return L.mk_kvq_read(c, P, r, P, 1, unit, None)
+no, ok = mk.MK_ERR_BAD_ARG, mk.MK_ERR_CUDA
+# rows: [n][heads][d], [heads][n][d], a fused row, negative strides, one row or one head of any stride
+for row, head in ((128, 64), (64, 5 * 64), (1024, 64), (-128, 64), (128, -64), (1024, 512)):
+    assert read(1, 5, 0, row, head) == ok, (row, head)
+assert read(1, 1, 0, 0, 64) == ok and read(1, 5, 0, 64, 0, hkv=1) == ok and read(1, 0, 0, 0, 64) == ok
+for row, head in ((0, 64), (128, 0), (64, 64), (64, 128), (128, 56), (8, 64), (-64, 64), (64, 4 * 64), (2 ** 62, 2 ** 62 + 8)):
+    assert read(1, 5, 0, row, head) == no, (row, head)
+# pages: [pages][heads][16][d], [pages][16][heads][d], [16][pages][heads][d]
+for page, row, head in ((2048, 64, 1024), (2048, 128, 64), (128, 3 * 128, 64), (-2048, 64, 1024)):
+    assert read(16, 3, page, row, head) == ok, (page, row, head)
+assert read(16, 1, 0, 64, 1024) == ok
+for page, row, head in ((0, 64, 1024), (2048, 0, 1024), (2048, 64, 0), (2040, 64, 1024), (1024, 64, 1024), (2048, 64, 64)):
+    assert read(16, 3, page, row, head) == no, (page, row, head)
+assert read(1, 5, 0, 128, 64, v=P) == no and read(16, 3, 2048, 64, 1024, v=P) == no
+"""
+
+
+def test_a_read_into_rows_that_share_memory_is_refused(lib):
+    """Expanded or interleaved destinations, whose content would depend on which thread writes last."""
+    env = {**os.environ, "CUDA_VISIBLE_DEVICES": "", "PYTHONPATH": ROOT}
+    r = subprocess.run([sys.executable, "-c", OVERLAP], env=env, cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, (r.returncode, r.stderr[-2000:])
 
 

@@ -529,11 +529,16 @@ size_t mk_kvq_workspace(const mk_kvq_cache* c, int type, int n_q_heads, int batc
  *   seq_lens     [batch] tokens attended to: 0 (the row is zeros: an idle slot
  *                of a padded batch) .. 16 max_pages
  * A sequence with a page outside the cache or a length outside its range gets
- * a row of NaN and flags status.  fp32: scores and weights keep 22 bits;
- * BF16: weights are rounded to 11 bits; sums stay in fp32, one rounding at
- * the end.  A call gives the same bits every time; where a long sequence is cut
- * depends on the batch's lengths, and its sums then round differently.  out may
- * be q.  Errors: MK_ERR_BAD_CONFIG (cache shape, n_q_heads no multiple of
+ * a row of NaN and flags status.
+ * fp32: scores and weights keep 22 bits; BF16: weights are rounded to 11 bits;
+ * sums stay in fp32, one rounding at the end.  A call gives the same bits every
+ * time; where a long sequence is cut depends on the batch's lengths, and its
+ * sums then round differently.  out may be q.
+ * Range: |q|, |k| and |v| below 2^80, |scale| up to 2^20, and |scale| times
+ * sum |q_i| times max |k| of a head below 2^100, at any length.  Outside it an
+ * intermediate may overflow, and a row be Inf or NaN whose exact value is
+ * finite.
+ * Errors: MK_ERR_BAD_CONFIG (cache shape, n_q_heads no multiple of
  * n_kv_heads or above 65536), MK_ERR_BATCH_TOO_LARGE (batch outside
  * 0..65535), MK_ERR_BAD_ARG (also a workspace smaller than
  * mk_kvq_workspace), MK_ERR_CUDA. */

@@ -225,9 +225,13 @@ __device__ __forceinline__ float ex2(float x) {
 // W^T the dims as M, 16 dims a tile, so no row of M is padding.  The weight of
 // a value code is w_tg = p_t step_tg sc_g with p_t = 2^(x_t - r).  The reference
 // r and each group's power of two sc_g move only when a p or w passes 2^15
-// (one vote a page), and then so that the largest seen is 2^8: whatever the
-// sizes of scores and steps, FP16 holds 11 bits of every weight down to 2^-22
-// of the largest.
+// (one vote a page), and then so that the largest seen is 2^8: FP16 holds 11
+// bits of every weight down to 2^-22 of the largest, for all sizes of scores and
+// steps that the fp32 numbers beside it hold.  p step and the sums of p mid are
+// formed before the division by sum p, with p up to 2^15 in each of fewer than
+// 2^31 tokens: values below 2^80 cannot overflow them.  Nor can keys below that,
+// whose sum of products reaches 2^23 steps, or queries, whose factor f is up to
+// 2^11 times scale |q|; scores themselves stay below 2^100.
 // QT = 2 / PT = 2 split q and w into FP16 high and low halves (22 bits) for
 // fp32 activations, with the key codes centred too.  With one half each w is
 // rounded to 11 bits, an eighth of a BF16 result's own rounding, and BF16 q is
@@ -313,8 +317,9 @@ struct KvqAttn {
 #pragma unroll
       for (int g = 0; g < NG; g++) sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], sh);
     }
-    // a power of two takes the head's largest |q| to [2^13, 2^14): FP16 then
-    // holds every BF16 q exactly down to 2^-28 of it
+    // a power of two takes the head's largest |q| to [2^13, 2^14), its 16th part
+    // (below) to [2^9, 2^10): FP16, whose last bit is at 2^-24, then holds the 8
+    // bits of every BF16 q exactly down to 2^-26 of it (2^-17 of 2^9)
     const int e = top == 0.f ? 0 : min(126, 13 + 127 - (int)(__float_as_uint(top) >> 23));
     const float up = __uint_as_float((uint32_t)(e + 127) << 23);
     const float fh = scale_log2 * (QT == 2 ? 1.f : 16777216.f) * __uint_as_float((uint32_t)(127 - e) << 23);

@@ -113,3 +113,71 @@ def test_attention_over_262144_tokens(d, dtype, batch):
     print(f"d {d} {dtype} batch {batch}: relative error {err / norm(out):.2e}, bound {bound / norm(out):.2e}")
     assert bound <= (1e-3 if f32 else 0.04) * norm(out)      # codes 0 .. 15 in place of code - 8 would be 0.08 off
     assert err <= bound
+
+
+# ------------------------------------------------ the number range include/mk.h gives
+
+LIMITS = {
+    "query 2^79": dict(q=2.0 ** 77, k=2.0 ** -76),
+    "keys 2^79": dict(q=2.0 ** -76, k=2.0 ** 77),
+    "values 2^79": dict(v=2.0 ** 77),
+    "all": dict(q=2.0 ** -78, k=2.0 ** 77, v=2.0 ** 77),
+    "scale 2^20": dict(q=2.0 ** -19, scale=2.0 ** 16),
+    "small": dict(q=2.0 ** -100, k=2.0 ** 70, v=2.0 ** -100, scale=2.0 ** 20),
+}
+
+
+def range_case(rng, d, n, dtype, q=1.0, k=1.0, v=1.0):
+    hkv, heads, batch = 1, 8, 2
+    pages = -(-n // 16)
+    pool = rng.integers(0, 256, size=(pages, hkv * 18 * d), dtype=np.uint8)
+    kr, vr = (rng.normal(size=(n, hkv, d)).clip(-4, 4).astype(np.float32).astype(np.float64) for _ in range(2))
+    _kvq.store(pool, hkv, d, kr * k, vr * v, np.arange(n))
+    qr = torch.from_numpy(rng.normal(size=(batch, hkv * heads, d)).clip(-4, 4) * q).float().to(dtype)
+    return pool, np.arange(pages, dtype=np.int32)[None].repeat(batch, 0), qr
+
+
+def over(pool, table, q, n, **kw):
+    from persistent_moe_decode_gb300.kvq import QuantCache
+    c = QuantCache.from_pool(torch.from_numpy(pool).cuda(), 1, q.shape[-1])
+    out = c.attention(q.cuda(), torch.from_numpy(table).cuda(), torch.full((len(table),), n, dtype=torch.int32,
+                                                                          device="cuda"), **kw)
+    c.check()
+    return out.double().cpu().numpy()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("name", LIMITS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_at_the_ends_of_the_number_range(d, name, dtype):
+    rng = np.random.default_rng(d)
+    kw, n = dict(LIMITS[name]), 500
+    scale = kw.pop("scale", d ** -0.5)
+    pool, table, q = range_case(rng, d, n, dtype, **kw)
+    got = over(pool, table, q, n, scale=scale)
+    keys, values = _kvq.load(pool, 1, d, np.arange(n))
+    for b in range(len(table)):
+        ref, spread, score = _kvq.attention(q[b].double().numpy(), keys, values, 1, scale)
+        tol = _kvq.attention_tolerance(ref, spread, score, n, d, dtype == torch.float32)
+        assert (np.abs(got[b] - ref) <= tol).all(), float((np.abs(got[b] - ref) / tol).max())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("sizes", [(2.0 ** 50, 2.0 ** 44), (2.0 ** 17, 2.0 ** 77), (2.0 ** 77, 2.0 ** 17)])
+def test_scores_near_2_to_the_100_leave_the_largest_token(sizes, dtype):
+    """The gap between the two largest scores is far above their error, so all weight is one token's."""
+    rng = np.random.default_rng(16)
+    d, n = 128, 300
+    pool, table, q = range_case(rng, d, n, dtype, q=sizes[0], k=sizes[1])
+    got = over(pool, table, q, n)
+    keys, values = _kvq.load(pool, 1, d, np.arange(n))
+    for b in range(len(table)):
+        qb = q[b].double().numpy()
+        kx = (keys[1] * keys[0] + keys[2])[:, 0]
+        bound = np.abs(qb).sum(1).max() * np.abs(kx).max() * d ** -0.5
+        assert 2.0 ** 99 < bound < 2.0 ** 100
+        x = np.sort(qb @ kx.T * d ** -0.5, 1)
+        assert (x[:, -1] - x[:, -2] > 2.0 ** -9 * bound).all()
+        ref, spread, _ = _kvq.attention(qb, keys, values, 1, d ** -0.5)
+        tol = _kvq.attention_tolerance(ref, spread, np.zeros(len(qb)), n, d, dtype == torch.float32)
+        assert (np.abs(got[b] - ref) <= tol).all()

@@ -69,8 +69,21 @@ def kernel_code(text: str) -> str:
     return "\n".join(ln.rstrip() for ln in text.splitlines() if ln.strip())
 
 
-# what the step kernel is compiled from
-STEP_SOURCES = ("mk_kernel.cu", "mk_kernel_q4.cu", "mk_kvq.cuh", "mk_layout.h", "mk_ptx.cuh")
+def step_sources(cs: str) -> list[str]:
+    """What the step kernel is compiled from: its two units in the folder and
+    every file they include by name, directly or through another."""
+    import re
+    names, todo = set(), ["mk_kernel.cu", "mk_kernel_q4.cu"]
+    while todo:
+        fn = todo.pop()
+        if fn in names:
+            continue
+        names.add(fn)
+        with open(os.path.join(cs, fn), encoding="utf-8") as f:
+            code = kernel_code(f.read())
+        todo += [os.path.normpath(os.path.join(os.path.dirname(fn), inc))
+                 for inc in re.findall(r'^\s*#\s*include\s*"([^"]+)"', code, flags=re.M)]
+    return sorted(names)
 
 
 def kernel_sha() -> str:
@@ -79,7 +92,7 @@ def kernel_sha() -> str:
     import hashlib
     h = hashlib.sha256()
     cs = os.path.join(ROOT, "persistent_moe_decode_gb300", "csrc")
-    for fn in STEP_SOURCES:
+    for fn in step_sources(cs):
         with open(os.path.join(cs, fn), encoding="utf-8") as f:
             h.update(fn.encode() + b"\0" + kernel_code(f.read()).encode() + b"\0")
     return h.hexdigest()[:16]

@@ -42,6 +42,8 @@
 extern "C" {
 #endif
 
+/* Structs grow at their end without a new version: compile against the header of
+ * the library that is loaded. */
 #define MK_ABI_VERSION 1
 
 enum mk_status {
@@ -133,7 +135,10 @@ typedef struct {
  *               calls below; v_pool is not used (may be NULL).  The step
  *               quantises the new token's fp32 K (post-RoPE) and V into it and
  *               attends to what it then holds.  28 % of the BF16 cache's
- *               bytes. */
+ *               bytes.  The step's query and softmax weights are rounded to 11
+ *               bits each before their products with the codes (over BF16
+ *               pools they keep 16), and scores and sums are those of a BF16
+ *               mk_kvq_attention; its range of numbers holds too. */
 enum mk_kv_format { MK_KV_BF16 = 0, MK_KV_INT4 = 1 };
 
 /* Weight format of the routed experts (mk_config.expert_format).
@@ -530,10 +535,16 @@ size_t mk_kvq_workspace(const mk_kvq_cache* c, int type, int n_q_heads, int batc
  *                of a padded batch) .. 16 max_pages
  * A sequence with a page outside the cache or a length outside its range gets
  * a row of NaN and flags status.
- * fp32: scores and weights keep 22 bits; BF16: weights are rounded to 11 bits;
- * sums stay in fp32, one rounding at the end.  A call gives the same bits every
- * time; where a long sequence is cut depends on the batch's lengths, and its
- * sums then round differently.  out may be q.
+ * fp32: the query and the softmax weights keep 22 bits, sums round in fp32.
+ * BF16: the query is exact; weights are rounded to 11 bits, relative to
+ * themselves.  A score's products with 64 codes are summed by tensor cores that
+ * cut off what lies below a fixed bit: less than 2^-6 of scale max |q| step (of
+ * a head and a group), where a code's own rounding is half of scale |q_i| step in
+ * each dim; the sums over a sequence's pages are fp32 and cut off too, not
+ * rounded.  Both: one rounding to the type at the end.  A call gives the same
+ * bits every time; where a long sequence is cut depends on the batch's lengths,
+ * and its sums then round differently.  out may be q, and else lies apart from
+ * it.
  * Range: |q|, |k| and |v| below 2^80, |scale| up to 2^20, and |scale| times
  * sum |q_i| times max |k| of a head below 2^100, at any length.  Outside it an
  * intermediate may overflow, and a row be Inf or NaN whose exact value is

@@ -2738,8 +2738,10 @@ struct Cons {
   // goes from the QKV output to its fragments without shared memory.  q and
   // the weights are rounded to 11 bits: a score is off by at most 2^-11 of the
   // sum of its terms' sizes, an eighth of what a BF16 query costs, and the
-  // cache itself holds 4 bits.  (With q in two halves: 5.04 against 4.50 ms a
-  // step at 256K context, 30B/3.3B model.)
+  // cache itself holds 4 bits.  Key codes are FP16 subnormals, whose sums the
+  // tensor cores cut off at 2^-24 of what scaled queries and a code reach
+  // (scores() of KvqAttn).  (With q in two halves: 5.04 against 4.50 ms a step
+  // at 256K context, 30B/3.3B model, when that was decided.)
   static constexpr int kStepQTerms = 1;
   template <int D>
   __device__ __forceinline__ bool attn_q4() {

@@ -45,8 +45,10 @@ __device__ __forceinline__ void flag_bad(const Cache& c, int code) {
 // Measured of the writer: both halves of keys and values held by one warp
 // without the overlap 151 (16 warps an SM) and 136 us (32, registers spill),
 // keys or values a warp without it 133, half a page a warp 149; 64 registers
-// with the overlap 126, 48 148.  8191 tokens by row: 7 us written, 6 read, bound
-// by instructions (the indexes and addresses of short rows).
+// with the overlap 126, 48 148.  8191 tokens by row: 7 us written, 6 read (12.3 and
+// 8.2 with a cold cache, for 3.2 us of bytes each), bound by latency: a thread's
+// index, address and row are one chain of loads with nothing of another token in
+// flight (issue slots 32 %, ALU 41-49 %, DRAM 7-17 %).
 
 // eight consecutive elements as they lie in memory, moved 16 bytes at a time;
 // load() is for memory that nothing writes while the kernel runs
@@ -388,17 +390,25 @@ __global__ void __launch_bounds__(kCopyThreads) kvq_read_pages_kernel(Cache c, c
 //     tasks in order, so that every block has the same work whatever the mix of
 //     lengths.  A unit is a page; a task's last segment counts as a whole one,
 //     and a task kTaskCost units more, for what a block spends on a segment
-//     beside its pages (16 sequences of 1K-32K: 51 us without, 46 with it).
+//     beside its pages.  48 against 0, 24 and 96, 16 sequences of 1K-32K: 45.0 us
+//     against 50.3, 46.4, 46.1 (4 KV heads of 128 dims); 76.2 against 86.1, 77.5,
+//     77.1 (8 heads); 20.0 against 21.7, 20.2, 20.3 (1 head); 28.5 against 31.5,
+//     29.3, 29.6 (64 dims); fp32 54.1 against 69.3, 61.8, 55.9 (64 dims 34.9
+//     against 37.9, 35.4, 36.3); 64 of up to 9000: 46.5 against 63.0, 48.0, 51.0;
+//     one of 256K: 42.0 against 40.7, 40.9, 41.9.
 // A task that is one segment is written at once.  The segments of the others
 // leave (reference, sum, weighted sum) in workspace slots, at most two a block,
 // and a second kernel merges them in page order: no atomics, one result.
 // A warp takes every eighth page of a segment through a ring of four in shared
 // memory (three on their way: 110 KB an SM, twice what the latency needs).
 // 32 query and 4 KV heads of 128 dims, BF16: 262,144 tokens in 42 us, 39 of them
-// in the first kernel, against 22 us for its 151 MB at the measured copy rate;
-// 16 sequences of 1K-32K in 45 us (152 MB).  About 350 instructions a page and
-// head (4096 codes): 40 to mask key codes, 72 to mask and centre value codes,
-// 50 for scales, 40 for weights and references, 25 to fetch.  Issue slots
+// in the first kernel, against 22 us for its 151 MB at the measured copy rate
+// (fp32: 50 us, one block an SM; 64 dims: 25 us BF16, 32 fp32, for 75 MB);
+// 16 sequences of 1K-32K in 45 us (152 MB), fp32 54.  About 350 instructions a page
+// and head (4096 codes).  Counted in the source: 40 to mask key codes, 72 to mask
+// and centre value codes, 50 for scales, 40 for weights and references, 25 to
+// fetch; the rest are 16 matrix products, 4 transposes, 8 shared loads,
+// exponentials, packing, the vote and the loop.  Issue slots
 // 50-58 %, ALU pipe 52 %, DRAM 49 %, tensor pipe 20 %: what bounds it is a page's
 // chain (loads, products, vote, products) with 16 warps an SM.  Slower or no
 // faster: two pages a warp at a time (49 us, registers spill), the next page's
@@ -1029,11 +1039,13 @@ int attn_blocks(int sms, int per_sm) { return std::min(sms * per_sm, kMaxSlots /
 // at once (half of the slots where it spans 8 SMs or more: a GPC holds two of
 // those at best).  Its warps then have `mine` pages each of the longest
 // sequence the page tables can hold, with all blocks sharing every page evenly
-// it would be `even`; a page costs a warp about a microsecond, the second
-// kernel and the plan about seven, and a batch with one long sequence among
+// it would be `even`; a page costs a warp about half a microsecond, the second
+// kernel and the plan 1.5 to 8, and a batch with one long sequence among
 // short ones must not wait for one cluster.  Measured, cluster against two
-// kernels, 32 query and 4 KV heads of 128 dims: one sequence of 512 7.5 : 9.0 us, 8K
-// 10.2 : 12.7, 16K 12.3 : 20.4; four of 8K 17.5 : 19.6, sixteen up to 2K 12.9 : 23.2.
+// kernels in a graph, 32 query and 4 KV heads of 128 dims: one sequence of 512
+// 6.4 : 8.0 us, 8K 9.1 : 11.8, 16K 11.2 : 14.9; four of 8K 15.8 : 16.3, one of 8K
+// and three of 100 11.6 : 12.1; sixteen up to 2K 11.7 : 18.4, of 4000 15.9 : 24.1;
+// fp32, one of 12,000 11.5 : 12.0.  24,500 tokens are past the rule: 16.1.
 int attn_cluster(long long tasks, int max_pages, int sms, int per_sm) {
   const long long slots = (long long)sms * per_sm;
   int n = 1;

@@ -235,7 +235,13 @@ __device__ __forceinline__ float ex2(float x) {
 // QT = 2 / PT = 2 split q and w into FP16 high and low halves (22 bits) for
 // fp32 activations, with the key codes centred too.  With one half each w is
 // rounded to 11 bits, an eighth of a BF16 result's own rounding, and BF16 q is
-// exact.
+// exact.  The key codes are then subnormals: a product stands at up to 2^0 when it
+// is aligned, and what lies below 2^-24 is cut off each of 17 addends in 4
+// products a group, 2^-17.9 in all of sums that f = 2^11 scale |q| multiplies: a
+// score is off by less than 2^-6 scale max |q| step a group, against half of scale
+// |q_i| step in every dim that the codes' own rounding costs (centring them too
+// takes 32 instructions more a page and head).  And o takes every page in the
+// product itself, which cuts off where fp32 calls add with a rounding.
 template <int D, int QT, int PT>
 struct KvqAttn {
   using R = KvqRec<D>;

@@ -557,6 +557,115 @@ int mk_kvq_attention(const mk_kvq_cache* c, const void* q, int64_t q_stride, voi
                      int n_q_heads, int batch, const int32_t* page_tables, int max_pages, const int32_t* seq_lens,
                      float scale, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------
+ * Operators on one layer's BF16 KV pools (those of mk_weights): rotary
+ * positions, rows into the cache, attention over prompts and over a prefix
+ * that sequences share.  What fills a cache that mk_decode_step then reads.
+ *
+ * As the mk_kvq_* calls they keep no state, run on `stream`, return before the
+ * kernels have run, allocate nothing and may be captured into a graph; two of
+ * them may run at the same time unless one writes what the other uses.
+ * Pointers but the structs' own are DEVICE pointers; pools, rows, q, out and
+ * workspace are 16-byte aligned, strides multiples of 16 bytes (else
+ * MK_ERR_BAD_ARG).
+ */
+typedef struct {
+  void* k_pool;     /* [num_pages][n_kv_heads][16][head_dim] BF16               */
+  void* v_pool;     /* the same                                                 */
+  int num_pages;    /* 1 .. 2^26 - 1                                            */
+  int n_kv_heads;   /* 1 .. 1024                                                */
+  int head_dim;     /* 64 or 128                                                */
+  int32_t* status;  /* one int32, or NULL: a kernel that meets a bad page or
+                       slot stores MK_ERR_BAD_PAGE there, a bad length, prefix or
+                       start MK_ERR_BAD_ARG; never cleared by a call              */
+} mk_kv_cache;
+
+/* Rotary positions.  Of the first rotary_dim dims of a head the pairs (a, b) =
+ * (i, i + rotary_dim / 2), or (2 i, 2 i + 1) if interleaved, become
+ *   magnitude (a cos t - b sin t, a sin t + b cos t),  t = 2 pi position turns[i],
+ * i < rotary_dim / 2; the other dims stay.  turns[i] is a fraction of 2^64, so
+ * that position turns[i] modulo 2^64 is the angle's exact place in its turn at
+ * any position. */
+typedef struct {
+  const uint64_t* turns;  /* DEVICE [rotary_dim / 2]: frequency / (2 pi) 2^64   */
+  int head_dim;           /* 64 or 128                                          */
+  int rotary_dim;         /* a multiple of 16, up to head_dim                   */
+  int interleaved;        /* 0: halves, 1: neighbours                           */
+  float magnitude;        /* of cos and sin (1 without long-context scaling)    */
+} mk_rope;
+
+/* Rows of heads: element (row t, head h, dim i) at t * row_stride +
+ * h * head_stride + i (strides in elements). */
+typedef struct {
+  void* data;
+  int n_heads;            /* 0: there are none                                  */
+  int64_t row_stride, head_stride;
+} mk_head_rows;
+
+/* Rotate n rows of query and key heads (type: both of inputs and outputs) by
+ * positions[n] (any int32).  In fp32, rounded once to the type.  An output is
+ * its input (same address and strides) or lies apart from every input, and its
+ * rows and heads lie apart from one another.  q or k may have no heads.
+ * Errors: MK_ERR_BAD_CONFIG (rope's shape, a head count outside 0..65536),
+ * MK_ERR_BAD_ARG, MK_ERR_CUDA. */
+int mk_rope_apply(const mk_rope* r, int n, const int32_t* positions, int type, const mk_head_rows* q,
+                  const mk_head_rows* k, const mk_head_rows* q_out, const mk_head_rows* k_out, void* stream);
+
+/* mk_rope_apply whose rotated keys, and the values v as they are, go to the
+ * cache in BF16: row t to slots[t] = page * 16 + row.  The rotated queries go
+ * to q_out in BF16.  A negative slot skips its row's keys and values, one past
+ * the end too and flags status; no two rows may name the same slot.  q may have
+ * no heads; q_out lies apart from every input.  Errors as mk_rope_apply,
+ * MK_ERR_BAD_CONFIG also for the cache's shape. */
+int mk_kv_append(const mk_kv_cache* c, const mk_rope* r, int n, const int32_t* positions, int type,
+                 const mk_head_rows* q, const mk_head_rows* k, const mk_head_rows* v, const int32_t* slots,
+                 const mk_head_rows* q_out, void* stream);
+
+/* Workspace bytes of mk_kv_attention with these arguments on the current
+ * device, for any lengths; 0 if they are not supported.  It needs no
+ * preparation.  Calls that may run at the same time, or two captured graphs
+ * that may, need a workspace each. */
+size_t mk_kv_workspace(const mk_kv_cache* c, int n_q_heads, int total_q, int batch, int groups);
+
+/* Causal attention of packed query rows over their sequences' cached tokens.
+ *   q, out       [total_q][n_q_heads][head_dim] BF16, q_stride and out_stride
+ *                elements between rows; query head h reads KV head
+ *                h / (n_q_heads / n_kv_heads)
+ *   q_starts     [batch + 1]: the new tokens of sequence b are rows q_starts[b]
+ *                to q_starts[b + 1], which may be none; rows outside them are
+ *                left as they were
+ *   page_tables  [batch][max_pages] physical pages; entries past a sequence's
+ *                length are not read
+ *   seq_lens     [batch] cached tokens, the new ones (the last of them)
+ *                included: new token i of n sees the first seq_lens[b] - n + i
+ *                + 1, and gets a row of zeros if that is none
+ * With groups > 0 sequences group_starts[g] to group_starts[g + 1] (of
+ * group_starts [groups + 1], from 0 to batch) have their first prefix_lens[g]
+ * tokens in common: whole pages, before each one's new tokens, taken from the
+ * page table of the group's first sequence and read once for the whole group
+ * (the other tables' entries there are not read).  0: nothing in common.
+ * A sequence with a length or prefix outside its range gets rows of NaN and
+ * flags status; a page outside the cache does that to the rows that see it, and
+ * may to other rows of the sequence (the group, in a prefix).  Starts that
+ * decrease or leave their range flag status, and rows of such sequences are left
+ * as they were or get NaN.
+ * What a row does not see has no part in it, infinities and NaN included, and
+ * neither has what a page holds past the sequence.
+ * Products of BF16 values summed in fp32; softmax in fp32; weights rounded to
+ * BF16 (8 bits, relative to themselves) for their products with the values; one
+ * rounding to BF16 at the end.  A call gives the same bits every time; where a
+ * long sequence is cut depends on the batch, and its sums then round
+ * differently.  out may be q, and else lies apart from it.  Range: scores
+ * (scale times q . k) below 2^100; `scale` above 0 and below 2^20.
+ * Errors: MK_ERR_BAD_CONFIG (cache shape, n_q_heads no multiple of n_kv_heads
+ * or above 128 times it), MK_ERR_BATCH_TOO_LARGE (batch or groups outside
+ * 0..65535, total_q outside 0..2^24), MK_ERR_BAD_ARG (also a workspace smaller
+ * than mk_kv_workspace), MK_ERR_CUDA. */
+int mk_kv_attention(const mk_kv_cache* c, const void* q, int64_t q_stride, void* out, int64_t out_stride,
+                    int n_q_heads, int total_q, int batch, const int32_t* q_starts, const int32_t* page_tables,
+                    int max_pages, const int32_t* seq_lens, int groups, const int32_t* group_starts,
+                    const int32_t* prefix_lens, float scale, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Library-owned device bytes (counters, scratch, queues, task lists). */
 size_t mk_device_bytes(const mk_handle* h);
 /* SMs the persistent grid uses. */

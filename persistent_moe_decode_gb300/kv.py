@@ -1,0 +1,277 @@
+"""The BF16 paged KV cache on torch tensors: checks, allocation and streams
+around the ``mk_rope_*`` and ``mk_kv_*`` calls of include/mk.h (no arithmetic of
+theirs here but the frequencies of the rotary positions).
+
+A :class:`PagedCache` is one layer's pools, BF16 ``[pages, n_kv_heads, 16,
+head_dim]`` each, as :class:`persistent_moe_decode_gb300.mk.Decoder` takes them
+for all layers: what fills them so that a decode step can go on from there.
+``append`` rotates a projection's query and key rows and puts keys and values in
+their slots, ``attention`` is the causal attention of packed prompts (or pieces of
+prompts, or single tokens) over their sequences' pages, ``shared_attention`` the
+same where sequences have a prefix in common.  :class:`Rope` holds the
+frequencies, and rotates on its own where the rows go elsewhere (a
+:class:`persistent_moe_decode_gb300.kvq.QuantCache`, for instance).
+
+Every call runs on ``stream``, by default torch's current stream of the tensors'
+device, and returns before the kernels have run; it can be captured into a CUDA
+graph.  Tensors last used on another stream are the caller's to order, as with
+any torch operation.  A call with tensors or a stream of another device, another
+type or a wrong shape raises; indexes and lengths are checked on the device
+(``PagedCache.check``).
+"""
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import torch
+
+from . import mk
+
+PAGE_SIZE = 16
+_TYPES = {torch.bfloat16: mk.MK_TYPE_BF16, torch.float32: mk.MK_TYPE_F32}
+
+
+def _run(device, index, fn, stream, *args):
+    """fn(stream pointer, ...) with the device and the call's stream current, for torch's own allocations and copies
+    too."""
+    if stream is None and torch.cuda.current_device() == index:
+        return fn(torch._C._cuda_getCurrentRawStream(index), *args)   # current_stream() costs 2 us more
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream: one of {device}, got one of {stream.device}")
+    with torch.cuda.device(index), torch.cuda.stream(stream):         # None: the device's current one
+        return fn(torch.cuda.current_stream().cuda_stream, *args)
+
+
+def _vector(t, name, device, index, n=None):
+    if t.dtype is not torch.int32 or t.dim() != 1 or t.get_device() != index or (n is not None and t.shape[0] != n):
+        raise ValueError(f"{name}: an int32 vector{f' of {n}' if n is not None else ''} on {device}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t if t.is_contiguous() else t.contiguous()
+
+
+def _aligned(t):
+    s, q = t.stride(), 7 if t.dtype is torch.bfloat16 else 3
+    return s[2] == 1 and not (s[0] | s[1]) & q and not t.data_ptr() & 15
+
+
+def _rows(t):
+    s = t.stride()
+    return mk.mk_head_rows(t.data_ptr(), t.shape[1], s[0], s[1])
+
+
+def frequencies(rotary_dim: int, theta: float, scaling: str | None = None, factor: float = 1.0,
+                original_context: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """Angles per position of the ``rotary_dim / 2`` pairs (fp64) and the magnitude of their cos and sin.
+
+    ``theta ** (-2 i / rotary_dim)``, and for contexts ``factor`` times as long as ``original_context``:
+    ``"linear"`` divides all by the factor; ``"ntk"`` takes ``theta * factor ** (r / (r - 2))``; ``"yarn"`` divides the
+    pairs that make fewer than ``beta_slow`` turns over the original context, keeps those of more than ``beta_fast``,
+    goes over from one to the other in between, and has the magnitude ``1 + 0.1 ln(factor)``.
+    """
+    r, i = rotary_dim, np.arange(rotary_dim // 2, dtype=np.float64)
+    if not (math.isfinite(theta) and theta > 1):
+        raise ValueError(f"theta: above 1, got {theta}")
+    if scaling is None:
+        return theta ** (-2 * i / r), 1.0
+    if not (math.isfinite(factor) and factor >= 1):
+        raise ValueError(f"factor: 1 or more, got {factor}")
+    if scaling == "linear":
+        return theta ** (-2 * i / r) / factor, 1.0
+    if scaling == "ntk":
+        return (theta * factor ** (r / (r - 2))) ** (-2 * i / r), 1.0
+    if scaling != "yarn":
+        raise ValueError(f"scaling: None, 'linear', 'ntk' or 'yarn', got {scaling!r}")
+    if original_context < 1 or not 0 < beta_slow < beta_fast:
+        raise ValueError(f"yarn: an original_context of 1 or more and 0 < beta_slow < beta_fast, got {original_context}, "
+                         f"{beta_slow}, {beta_fast}")
+
+    def pair(turns):        # the pair that makes so many turns over the original context
+        return r * math.log(original_context / (turns * 2 * math.pi)) / (2 * math.log(theta))
+
+    low, high = max(0, math.floor(pair(beta_fast))), min(r - 1, math.ceil(pair(beta_slow)))
+    ramp = np.clip((i - low) / max(high - low, 1e-3), 0, 1)
+    f = theta ** (-2 * i / r)
+    return f / factor * ramp + f * (1 - ramp), 1 + 0.1 * math.log(factor)
+
+
+class Rope:
+    """Rotary positions of heads of ``head_dim`` (64 or 128) dims, the first ``rotary_dim`` (a multiple of 16; all by
+    default) of which turn: pairs ``(i, i + rotary_dim / 2)``, or ``(2 i, 2 i + 1)`` if ``interleaved``.  The other
+    arguments are those of :func:`frequencies`.  Angles are exact to fp32 at any int32 position."""
+
+    def __init__(self, head_dim: int, theta: float, rotary_dim: int | None = None, interleaved: bool = False,
+                 scaling: str | None = None, factor: float = 1.0, original_context: int = 0, beta_fast: float = 32.0,
+                 beta_slow: float = 1.0, device="cuda"):
+        r = head_dim if rotary_dim is None else rotary_dim
+        if head_dim not in (64, 128) or r < 16 or r > head_dim or r % 16:
+            raise ValueError(f"rotary positions: heads of 64 or 128 dims, a multiple of 16 of them turning, got {head_dim} "
+                             f"and {r}")
+        self.head_dim, self.rotary_dim, self.interleaved = head_dim, r, bool(interleaved)
+        freq, self.magnitude = frequencies(r, theta, scaling, factor, original_context, beta_fast, beta_slow)
+        # fractions of a turn a position, of 2^64: an angle's place in its turn is then an integer product
+        turns = np.array([int(f / (2 * math.pi) * 2.0 ** 64) for f in freq], dtype=np.uint64)
+        self.turns = torch.from_numpy(turns.view(np.int64)).to(device)
+        if self.turns.device.type != "cuda":
+            raise ValueError(f"rotary positions: a GPU, got {self.turns.device}")
+        self._dev = self.turns.get_device()
+        self._c = mk.mk_rope(self.turns.data_ptr(), head_dim, r, int(self.interleaved), self.magnitude)
+
+    def _heads(self, t, name, n, dtype):
+        if t.dim() != 3 or t.dtype is not dtype or t.shape[2] != self.head_dim or t.get_device() != self._dev \
+                or (n is not None and t.shape[0] != n) or dtype not in _TYPES:
+            raise ValueError(f"{name}: BF16 or fp32 rows [n, heads, {self.head_dim}] on {self.turns.device}, alike, got "
+                             f"{t.dtype} {tuple(t.shape)} on {t.device}")
+        return t if _aligned(t) else t.clone(memory_format=torch.contiguous_format)
+
+    def apply(self, q, k, positions, out=None, stream=None):
+        """Rows q ``[n, heads, head_dim]`` and k ``[n, kv heads, head_dim]`` (BF16 or fp32, alike) turned by
+        ``positions`` (int32 ``[n]``): ``(q, k)``, new tensors, or the pair ``out``, which may be the inputs and else
+        lies apart from them."""
+        return _run(self.turns.device, self._dev, self._apply, stream, q, k, positions, out)
+
+    def _apply(self, st, q, k, positions, out):
+        dtype, n = q.dtype, q.shape[0]
+        given = (q, k)
+        q, k = self._heads(q, "q", None, dtype), self._heads(k, "k", n, dtype)
+        positions = _vector(positions, "positions", self.turns.device, self._dev, n)
+        if out is None:
+            out = tuple(torch.empty(t.shape, dtype=dtype, device=t.device) for t in (q, k))
+        for t, like, name in zip(out, given, ("out[0]", "out[1]")):
+            if t.shape != like.shape or t.dtype is not dtype or t.get_device() != self._dev or not _aligned(t):
+                raise ValueError(f"{name}: {dtype} {tuple(like.shape)} on {self.turns.device}, rows of consecutive "
+                                 f"elements at 16-byte strides, got {t.dtype} {tuple(t.shape)} on {t.device}")
+        mk.mk_rope_apply(self._c, n, positions.data_ptr(), _TYPES[dtype], _rows(q), _rows(k), _rows(out[0]),
+                         _rows(out[1]), st)
+        return out[0], out[1]
+
+
+class PagedCache:
+    """One layer's BF16 paged KV cache: ``k_pool`` and ``v_pool``, ``[pages, n_kv_heads, 16, head_dim]``, zeros when
+    new."""
+
+    def __init__(self, n_pages: int, n_kv_heads: int, head_dim: int, device="cuda"):
+        shape = (n_pages, n_kv_heads, PAGE_SIZE, head_dim)
+        self._attach(torch.zeros(shape, dtype=torch.bfloat16, device=device),
+                     torch.zeros(shape, dtype=torch.bfloat16, device=device))
+
+    @classmethod
+    def from_pools(cls, k_pool: torch.Tensor, v_pool: torch.Tensor) -> "PagedCache":
+        """A cache over existing pools (kept referenced, not copied)."""
+        self = cls.__new__(cls)
+        self._attach(k_pool, v_pool)
+        return self
+
+    def _attach(self, k_pool, v_pool):
+        for t, name in ((k_pool, "k_pool"), (v_pool, "v_pool")):
+            if t.dtype is not torch.bfloat16 or t.dim() != 4 or not t.is_contiguous() or t.shape != k_pool.shape \
+                    or t.shape[0] < 1 or t.shape[0] >= 1 << 26 or not 1 <= t.shape[1] <= 1024 \
+                    or t.shape[2] != PAGE_SIZE or t.shape[3] not in (64, 128) or t.data_ptr() & 15:
+                raise ValueError(f"{name}: contiguous BF16 [pages, 1 to 1024 KV heads, 16, 64 or 128 dims], both alike, "
+                                 f"got {t.dtype} {tuple(t.shape)}")
+            if t.device.type != "cuda" or t.device != k_pool.device:
+                raise ValueError(f"{name}: both pools on one GPU, got {k_pool.device} and {v_pool.device}")
+        self.k_pool, self.v_pool = k_pool, v_pool
+        self.n_pages, self.n_kv_heads, _, self.head_dim = k_pool.shape
+        self._dev, self._ws_bytes = k_pool.get_device(), {}
+        self.status = torch.zeros(1, dtype=torch.int32, device=k_pool.device)
+        self._c = mk.mk_kv_cache(k_pool.data_ptr(), v_pool.data_ptr(), self.n_pages, self.n_kv_heads, self.head_dim,
+                                 self.status.data_ptr())
+
+    def check(self) -> None:
+        """Raise MkError if a call so far, on whatever stream, met a page, slot, start or length out of range (waits
+        for the device); clears the record."""
+        torch.cuda.synchronize(self._dev)
+        code = int(self.status.item())
+        if code:
+            self.status.zero_()
+            torch.cuda.synchronize(self._dev)    # a later call's record, on another stream, comes after
+            raise mk.MkError(code, "paged cache")
+
+    # ---------------------------------------------------------------- calls
+
+    def append(self, rope: Rope, q, k, v, positions, slots, out=None, stream=None):
+        """Turn rows q ``[n, heads, head_dim]`` and k ``[n, n_kv_heads, head_dim]`` by ``positions`` (int32 ``[n]``) and
+        put the turned keys and the values v (all BF16 or fp32, alike) into slots ``page * 16 + row`` (int32 ``[n]``,
+        distinct; a negative one skips its row).  Returns the turned queries in BF16: ``out``, a new tensor unless given,
+        which lies apart from the inputs."""
+        return _run(self.k_pool.device, self._dev, self._append, stream, rope, q, k, v, positions, slots, out)
+
+    def attention(self, q, q_starts, page_tables, seq_lens, scale: float | None = None, out=None, stream=None):
+        """Causal attention of packed rows q (BF16 ``[n, n_q_heads, head_dim]``): rows ``q_starts[b]`` to
+        ``q_starts[b + 1]`` (int32 ``[batch + 1]``) are the last tokens of the ``seq_lens[b]`` (int32 ``[batch]``) that
+        ``page_tables[b]`` (int32 ``[batch, max_pages]``) holds, and each sees those up to itself.  ``scale`` defaults to
+        head_dim ** -0.5.  A row that sees nothing gives zeros, rows of no sequence are left as they were (undefined in a
+        new tensor).  Returns ``out``, a new tensor like q unless given; it may be q."""
+        return _run(self.k_pool.device, self._dev, self._attention, stream, q, q_starts, page_tables, seq_lens, None, None,
+                    scale, out)
+
+    def shared_attention(self, q, q_starts, page_tables, seq_lens, group_starts, prefix_lens,
+                         scale: float | None = None, out=None, stream=None):
+        """:meth:`attention` where the sequences ``group_starts[g]`` to ``group_starts[g + 1]`` (int32 ``[groups + 1]``,
+        from 0 to the batch) share their first ``prefix_lens[g]`` tokens (int32 ``[groups]``; whole pages before each
+        one's new tokens, the first of its page table's entries; 0: nothing): these are read once a group."""
+        return _run(self.k_pool.device, self._dev, self._attention, stream, q, q_starts, page_tables, seq_lens,
+                    group_starts, prefix_lens, scale, out)
+
+    def _append(self, st, rope, q, k, v, positions, slots, out):
+        dev, device, d = self._dev, self.k_pool.device, self.head_dim
+        if rope.head_dim != d or rope._dev != dev:
+            raise ValueError(f"rope: one of heads of {d} dims on {device}, got {rope.head_dim} on {rope.turns.device}")
+        dtype, n = q.dtype, q.shape[0]
+        q, k, v = rope._heads(q, "q", None, dtype), rope._heads(k, "k", n, dtype), rope._heads(v, "v", n, dtype)
+        if k.shape[1] != self.n_kv_heads or v.shape[1] != self.n_kv_heads:
+            raise ValueError(f"k, v: {self.n_kv_heads} KV heads, got {k.shape[1]} and {v.shape[1]}")
+        positions = _vector(positions, "positions", device, dev, n)
+        slots = _vector(slots, "slots", device, dev, n)
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=device)
+        elif out.shape != q.shape or out.dtype is not torch.bfloat16 or out.get_device() != dev or not _aligned(out):
+            raise ValueError(f"out: BF16 {tuple(q.shape)} on {device}, rows of consecutive elements at 16-byte strides, "
+                             f"got {out.dtype} {tuple(out.shape)} on {out.device}")
+        mk.mk_kv_append(self._c, rope._c, n, positions.data_ptr(), _TYPES[dtype], _rows(q), _rows(k), _rows(v),
+                        slots.data_ptr(), _rows(out), st)
+        return out
+
+    def _dense(self, t):
+        s = t.stride()
+        return _aligned(t) and s[1] == self.head_dim and (t.shape[0] < 2 or s[0] >= t.shape[1] * self.head_dim)
+
+    def _attention(self, st, q, q_starts, page_tables, seq_lens, group_starts, prefix_lens, scale, out):
+        dev, device, d = self._dev, self.k_pool.device, self.head_dim
+        if q.dim() != 3 or q.dtype is not torch.bfloat16 or q.get_device() != dev or q.shape[2] != d:
+            raise ValueError(f"q: BF16 [rows, heads, {d}] on {device}, got {q.dtype} {tuple(q.shape)} on {q.device}")
+        if page_tables.dtype is not torch.int32 or page_tables.dim() != 2 or page_tables.get_device() != dev:
+            raise ValueError(f"page_tables: int32 [batch, max_pages] on {device}, got {page_tables.dtype} "
+                             f"{tuple(page_tables.shape)} on {page_tables.device}")
+        (n, hq, _), (batch, max_pages) = q.shape, page_tables.shape
+        q_starts = _vector(q_starts, "q_starts", device, dev, batch + 1)
+        seq_lens = _vector(seq_lens, "seq_lens", device, dev, batch)
+        groups = 0
+        if prefix_lens is not None:
+            prefix_lens = _vector(prefix_lens, "prefix_lens", device, dev)
+            groups = prefix_lens.shape[0]
+            group_starts = _vector(group_starts, "group_starts", device, dev, groups + 1)
+            if groups == 0 and batch:
+                raise ValueError("prefix_lens: the groups hold all sequences, got none")
+        if not page_tables.is_contiguous():
+            page_tables = page_tables.contiguous()
+        if not self._dense(q):
+            q = q.clone(memory_format=torch.contiguous_format)
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=device)
+        elif out.shape != q.shape or out.dtype is not q.dtype or out.get_device() != dev or not self._dense(out):
+            raise ValueError(f"out: BF16 {tuple(q.shape)} on {device}, rows of consecutive heads at 16-byte strides")
+        # the workspace belongs to this call's stream, or to the graph that captures it
+        key = (hq, n, batch, groups)
+        ws_bytes = self._ws_bytes.get(key)      # a function of these alone
+        if ws_bytes is None:
+            if len(self._ws_bytes) >= 1024:
+                self._ws_bytes.clear()
+            ws_bytes = self._ws_bytes[key] = mk.mk_kv_workspace(self._c, hq, n, batch, groups)
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device) if ws_bytes else None
+        mk.mk_kv_attention(self._c, q.data_ptr(), q.stride(0), out.data_ptr(), out.stride(0), hq, n, batch,
+                           q_starts.data_ptr(), page_tables.data_ptr(), max_pages, seq_lens.data_ptr(), groups,
+                           group_starts.data_ptr() if groups else None, prefix_lens.data_ptr() if groups else None,
+                           d ** -0.5 if scale is None else scale, ws.data_ptr() if ws_bytes else None, ws_bytes, st)
+        return out

@@ -43,7 +43,8 @@ EXPORTS = ("mk_create", "mk_schedule_step", "mk_decode_step", "mk_step_status", 
            "mk_decode_step_static", "mk_plan_step", "mk_read_debug", "mk_service_create",
            "mk_service_submit", "mk_service_run", "mk_service_wait", "mk_service_result",
            "mk_service_batch", "mk_service_destroy", "mk_kvq_page_bytes", "mk_kvq_write", "mk_kvq_read",
-           "mk_kvq_workspace", "mk_kvq_attention")
+           "mk_kvq_workspace", "mk_kvq_attention", "mk_rope_apply", "mk_kv_append", "mk_kv_workspace",
+           "mk_kv_attention")
 
 
 class mk_config(C.Structure):
@@ -84,6 +85,20 @@ class mk_kvq_cache(C.Structure):
 class mk_kv_rows(C.Structure):
     _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("type", C.c_int), ("count", C.c_int),
                 ("page_stride", C.c_int64), ("row_stride", C.c_int64), ("head_stride", C.c_int64)]
+
+
+class mk_kv_cache(C.Structure):
+    _fields_ = [("k_pool", C.c_void_p), ("v_pool", C.c_void_p), ("num_pages", C.c_int), ("n_kv_heads", C.c_int),
+                ("head_dim", C.c_int), ("status", C.c_void_p)]
+
+
+class mk_rope(C.Structure):
+    _fields_ = [("turns", C.c_void_p), ("head_dim", C.c_int), ("rotary_dim", C.c_int), ("interleaved", C.c_int),
+                ("magnitude", C.c_float)]
+
+
+class mk_head_rows(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("n_heads", C.c_int), ("row_stride", C.c_int64), ("head_stride", C.c_int64)]
 
 
 class MkError(RuntimeError):
@@ -132,6 +147,13 @@ def lib():
             L.mk_kvq_workspace.restype = C.c_size_t
             L.mk_kvq_attention.argtypes = [kvc, vp, C.c_int64, vp, C.c_int64, i32, i32, i32, vp, i32, vp,
                                            C.c_float, vp, C.c_size_t, vp]
+            rope, hr, kv = C.POINTER(mk_rope), C.POINTER(mk_head_rows), C.POINTER(mk_kv_cache)
+            L.mk_rope_apply.argtypes = [rope, i32, vp, i32, hr, hr, hr, hr, vp]
+            L.mk_kv_append.argtypes = [kv, rope, i32, vp, i32, hr, hr, hr, vp, hr, vp]
+            L.mk_kv_workspace.argtypes = [kv, i32, i32, i32, i32]
+            L.mk_kv_workspace.restype = C.c_size_t
+            L.mk_kv_attention.argtypes = [kv, vp, C.c_int64, vp, C.c_int64, i32, i32, i32, vp, vp, i32, vp, i32, vp, vp,
+                                          C.c_float, vp, C.c_size_t, vp]
             L.mk_device_bytes.argtypes = [vp]
             L.mk_device_bytes.restype = C.c_size_t
             L.mk_num_sms.argtypes = [vp]
@@ -360,6 +382,32 @@ def mk_kvq_attention(cache: mk_kvq_cache, q_ptr: int, q_stride: int, out_ptr: in
     return _check(lib().mk_kvq_attention(cache, q_ptr, q_stride, out_ptr, out_stride, dtype, n_q_heads, batch,
                                          page_tables_ptr, max_pages, seq_lens_ptr, scale, workspace_ptr,
                                          workspace_bytes, _stream_ptr(stream)), "mk_kvq_attention")
+
+
+def mk_rope_apply(rope: mk_rope, n: int, positions_ptr, dtype: int, q: mk_head_rows, k: mk_head_rows,
+                  q_out: mk_head_rows, k_out: mk_head_rows, stream=None) -> int:
+    return _check(lib().mk_rope_apply(rope, n, positions_ptr, dtype, q, k, q_out, k_out, _stream_ptr(stream)),
+                  "mk_rope_apply")
+
+
+def mk_kv_append(cache: mk_kv_cache, rope: mk_rope, n: int, positions_ptr, dtype: int, q: mk_head_rows,
+                 k: mk_head_rows, v: mk_head_rows, slots_ptr, q_out: mk_head_rows, stream=None) -> int:
+    return _check(lib().mk_kv_append(cache, rope, n, positions_ptr, dtype, q, k, v, slots_ptr, q_out,
+                                     _stream_ptr(stream)), "mk_kv_append")
+
+
+def mk_kv_workspace(cache: mk_kv_cache, n_q_heads: int, total_q: int, batch: int, groups: int) -> int:
+    return int(lib().mk_kv_workspace(cache, n_q_heads, total_q, batch, groups))
+
+
+def mk_kv_attention(cache: mk_kv_cache, q_ptr: int, q_stride: int, out_ptr: int, out_stride: int, n_q_heads: int,
+                    total_q: int, batch: int, q_starts_ptr, page_tables_ptr, max_pages: int, seq_lens_ptr,
+                    groups: int, group_starts_ptr, prefix_lens_ptr, scale: float, workspace_ptr=None,
+                    workspace_bytes: int = 0, stream=None) -> int:
+    return _check(lib().mk_kv_attention(cache, q_ptr, q_stride, out_ptr, out_stride, n_q_heads, total_q, batch,
+                                        q_starts_ptr, page_tables_ptr, max_pages, seq_lens_ptr, groups,
+                                        group_starts_ptr, prefix_lens_ptr, scale, workspace_ptr, workspace_bytes,
+                                        _stream_ptr(stream)), "mk_kv_attention")
 
 
 # ---------------------------------------------------------- convenience

@@ -35,7 +35,7 @@ def _cuda_home() -> str:
 
 
 def _sources():
-    return [os.path.join(CSRC, f) for f in ("mk_kernel.cu", "mk_kernel_q4.cu", "mk_static.cu", "mk_service.cu", "mk_kvq.cu", "mk_kv.cu",
+    return [os.path.join(CSRC, f) for f in ("mk_kernel.cu", "mk_kernel_q4.cu", "mk_static.cu", "mk_service.cu", "mk_kvq.cu", "mk_kv.cu", "mk_kv_attn.cu",
                                              "mk_sched.cpp", "mk_api.cpp")]
 
 

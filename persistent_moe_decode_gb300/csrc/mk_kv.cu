@@ -8,13 +8,14 @@
 #include <cuda_runtime.h>
 
 #include "mk.h"
+#include "mk_kv.cuh"
 #include "mk_ptx.cuh"
 
 using namespace mk;
 
 namespace {
 
-constexpr int kPage = 16;
+constexpr int kPage = kKvPage;
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ void flag(int32_t* status, int code) {
@@ -145,77 +146,6 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
       store8(out + lo, x);
       store8(out + hi, y);
     }
-  }
-}
-
-// ------------------------------------------------------------------- attention
-
-struct AttnArgs {
-  const uint16_t *q, *k_pool, *v_pool;
-  uint16_t* out;
-  const int32_t *q_starts, *page_tables, *seq_lens, *group_starts, *prefix_lens;
-  int32_t* status;
-  int64_t q_stride, out_stride;
-  int hq, hkv, grp, total_q, batch, groups, max_pages, num_pages;
-  float scale_log2;
-};
-
-// One warp per query row and head, keys one after the other.
-template <int D>
-__global__ void __launch_bounds__(256) kv_attention_simple(const AttnArgs a) {
-  const int b = blockIdx.y, lane = threadIdx.x & 31;
-  const int t0 = a.q_starts[b], t1 = a.q_starts[b + 1];
-  if (t0 < 0 || t1 < t0 || t1 > a.total_q) {
-    flag(a.status, MK_ERR_BAD_ARG);
-    return;
-  }
-  const int len = a.seq_lens[b], n = t1 - t0;
-  bool bad = len < 0 || len > a.max_pages * kPage;
-  int prefix = 0, first = b;
-  if (a.groups) {
-    int g = 0;
-    while (g < a.groups && !(a.group_starts[g] <= b && b < a.group_starts[g + 1])) g++;
-    if (g == a.groups) {
-      bad = true;
-    } else {
-      prefix = a.prefix_lens[g], first = a.group_starts[g];
-      if (prefix < 0 || prefix % kPage || (prefix > 0 && n > 0 && prefix > len - n) || first < 0) bad = true;
-    }
-  }
-  if (bad) flag(a.status, MK_ERR_BAD_ARG);
-  for (int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); w < (int64_t)n * a.hq; w += (int64_t)gridDim.x * 8) {
-    const int i = (int)(w / a.hq), h = (int)(w % a.hq), kvh = h / a.grp;
-    const uint16_t* q = a.q + (int64_t)(t0 + i) * a.q_stride + (int64_t)h * D;
-    uint16_t* out = a.out + (int64_t)(t0 + i) * a.out_stride + (int64_t)h * D;
-    float qf[D / 32], o[D / 32], m = -INFINITY, l = 0.f;
-    bool nan = bad;
-#pragma unroll
-    for (int c = 0; c < D / 32; c++) qf[c] = bf16f(q[lane + 32 * c]), o[c] = 0.f;
-    const int seen = len - n + i + 1;
-    for (int j = 0; !nan && j < seen; j++) {
-      const int page = a.page_tables[(int64_t)(j < prefix ? first : b) * a.max_pages + j / kPage];
-      if (page < 0 || page >= a.num_pages) {
-        flag(a.status, MK_ERR_BAD_PAGE);
-        nan = true;
-        break;
-      }
-      const int64_t at = (((int64_t)page * a.hkv + kvh) * kPage + j % kPage) * D + lane;
-      float s = 0.f;
-#pragma unroll
-      for (int c = 0; c < D / 32; c++) s = fmaf(qf[c], bf16f(a.k_pool[at + 32 * c]), s);
-#pragma unroll
-      for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-      s *= a.scale_log2;
-      const float mn = fmaxf(m, s);
-      const float keep = m == mn ? 1.f : exp2f(m - mn), p = exp2f(s - mn);
-      l = l * keep + p;
-#pragma unroll
-      for (int c = 0; c < D / 32; c++) o[c] = fmaf(p, bf16f(a.v_pool[at + 32 * c]), o[c] * keep);
-      m = mn;
-    }
-#pragma unroll
-    for (int c = 0; c < D / 32; c++)
-      out[lane + 32 * c] = f2bf(nan ? NAN : seen <= 0 ? 0.f : o[c] / l);
   }
 }
 
@@ -363,7 +293,8 @@ int mk_kv_append(const mk_kv_cache* c, const mk_rope* r, int n, const int32_t* p
 
 size_t mk_kv_workspace(const mk_kv_cache* c, int n_q_heads, int total_q, int batch, int groups) {
   if (check_attention(c, n_q_heads, total_q, batch, groups) || total_q == 0 || batch == 0) return 0;
-  return 0;
+  const int sms = sm_count();
+  return sms ? kv_attention_ws(c->head_dim, n_q_heads, total_q, groups, sms) : 0;
 }
 
 int mk_kv_attention(const mk_kv_cache* c, const void* q, int64_t q_stride, void* out, int64_t out_stride,
@@ -381,7 +312,12 @@ int mk_kv_attention(const mk_kv_cache* c, const void* q, int64_t q_stride, void*
     return MK_ERR_BAD_ARG;
   const int sms = sm_count();
   if (!sms) return MK_ERR_CUDA;
-  AttnArgs a{};
+  if (!workspace || !aligned(workspace, 16) ||
+      workspace_bytes < kv_attention_ws(c->head_dim, n_q_heads, total_q, groups, sms))
+    return MK_ERR_BAD_ARG;
+  KvAttnArgs a{};
+  a.ws = (uint8_t*)workspace;
+  a.head_dim = c->head_dim;
   a.q = (const uint16_t*)q;
   a.k_pool = (const uint16_t*)c->k_pool;
   a.v_pool = (const uint16_t*)c->v_pool;
@@ -393,11 +329,7 @@ int mk_kv_attention(const mk_kv_cache* c, const void* q, int64_t q_stride, void*
   a.hq = n_q_heads, a.hkv = c->n_kv_heads, a.grp = n_q_heads / c->n_kv_heads;
   a.total_q = total_q, a.batch = batch, a.groups = groups, a.max_pages = max_pages, a.num_pages = c->num_pages;
   a.scale_log2 = scale * kLog2e;
-  cudaStream_t st = (cudaStream_t)stream;
-  const dim3 grid(256, (unsigned)batch);
-  if (c->head_dim == 128) kv_attention_simple<128><<<grid, 256, 0, st>>>(a);
-  else kv_attention_simple<64><<<grid, 256, 0, st>>>(a);
-  return cudaGetLastError() == cudaSuccess ? MK_OK : MK_ERR_CUDA;
+  return kv_attention_launch(a, sms, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,30 @@
+// What the BF16 paged cache's attention (mk_kv_attn.cu) and its entry points
+// (mk_kv.cu) share.
+#pragma once
+#include <stddef.h>
+#include <stdint.h>
+
+
+
+namespace mk {
+
+constexpr int kKvPage = 16;
+
+struct KvAttnArgs {
+  const uint16_t *q, *k_pool, *v_pool;
+  uint16_t* out;
+  const int32_t *q_starts, *page_tables, *seq_lens, *group_starts, *prefix_lens;
+  int32_t* status;
+  uint8_t* ws;
+  int64_t q_stride, out_stride;
+  int head_dim, hq, hkv, grp, total_q, batch, groups, max_pages, num_pages;
+  float scale_log2;
+};
+
+// workspace bytes on a device of `sms` multiprocessors
+size_t kv_attention_ws(int head_dim, int hq, int total_q, int groups, int sms);
+
+// checked arguments; returns an mk_status
+int kv_attention_launch(const KvAttnArgs& a, int sms, void* stream);
+
+}  // namespace mk

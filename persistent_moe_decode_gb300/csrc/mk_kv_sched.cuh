@@ -1,0 +1,217 @@
+// How the blocks of the paged cache's attention share its work: tasks, row
+// blocks, key tiles, and the stretch that each block takes.  Compiled for the
+// host too, where a test walks every block's stretch.
+#pragma once
+#include <stdint.h>
+
+#include "mk.h"
+#include "mk_kv.cuh"
+
+#ifdef __CUDACC__
+#define MK_HD __host__ __device__
+#else
+#define MK_HD
+#endif
+
+namespace mk {
+
+constexpr int kTile = 128;               // keys a step, rows a tile
+constexpr int kStart = 3;                // an item's start and end, in key tiles
+constexpr int kMinShare = 4;             // no block takes less (in the same units)
+constexpr int kMinPart = 2;              // no part of an item has fewer key tiles
+
+enum : int { kCausal = 1, kNan = 2, kPrefix = 4 };
+
+template <class T>
+MK_HD inline T hd_min(T a, T b) { return a < b ? a : b; }
+template <class T>
+MK_HD inline T hd_max(T a, T b) { return a > b ? a : b; }
+
+MK_HD inline void flag(int32_t* status, int code) {
+  if (status) *(volatile int32_t*)status = code;
+}
+
+// a stretch of key tiles [k0, k1) of n of one row block of one KV head
+struct Part {
+  int tok0, ntok;          // packed rows of q
+  int head, table;         // KV head; page table row
+  int kbeg, kend;          // keys of the block
+  int lim;                 // keys that its first token sees end here; a causal one's next token sees one more
+  int k0, k1, n;
+  int flags;
+  int slot;                // workspace slot of a part, -1: the whole item
+};
+
+struct Task {
+  int tok0, ntok, nb;      // rows, row blocks
+  int table, kbeg, kend;
+  int c0;                  // causal: token i sees keys below c0 + i + 1
+  int flags;
+};
+
+MK_HD inline Task load_task(const KvAttnArgs& a, int t, int tb, bool report) {
+  Task k{};
+  if (t < a.groups) {
+    const int s0 = a.group_starts[t], s1 = a.group_starts[t + 1], prefix = a.prefix_lens[t];
+    k.flags = kPrefix;
+    bool ok = 0 <= s0 && s0 <= s1 && s1 <= a.batch &&
+              (s0 == s1 || (prefix >= 0 && prefix % kKvPage == 0 && prefix <= a.max_pages * kKvPage));
+    int q0 = 0, q1 = 0;
+    if (ok) {
+      q0 = a.q_starts[s0], q1 = a.q_starts[s1];
+      ok = 0 <= q0 && q0 <= q1 && q1 <= a.total_q;
+    }
+    if (!ok) {
+      if (report) flag(a.status, MK_ERR_BAD_ARG);
+      q0 = q1 = 0;
+    }
+    k.tok0 = q0, k.ntok = q1 - q0;
+    k.table = s0, k.kbeg = 0, k.kend = prefix;
+  } else {
+    const int b = t - a.groups;
+    const int q0 = a.q_starts[b], q1 = a.q_starts[b + 1], len = a.seq_lens[b];
+    k.flags = kCausal;
+    bool ok = 0 <= q0 && q0 <= q1 && q1 <= a.total_q;
+    k.tok0 = ok ? q0 : 0, k.ntok = ok ? q1 - q0 : 0;
+    int prefix = 0;
+    bool fit = len >= 0 && len <= a.max_pages * kKvPage;
+    if (a.groups) {
+      int lo = 0, hi = a.groups;          // the last group that starts at or before b
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (a.group_starts[mid] <= b) lo = mid; else hi = mid;
+      }
+      // groups without sequences start there too
+      prefix = a.prefix_lens[lo];
+      const int s0 = a.group_starts[lo], s1 = a.group_starts[lo + 1];
+      if (!(0 <= s0 && s0 <= b && b < s1 && s1 <= a.batch)) fit = false;
+      // its rows are among the group's, or the group leaves them out
+      if (fit && !(0 <= a.q_starts[s0] && a.q_starts[s0] <= q0 && q1 <= a.q_starts[s1] && a.q_starts[s1] <= a.total_q))
+        fit = false;
+      if (prefix < 0 || prefix % kKvPage || (fit && prefix > 0 && k.ntok > 0 && prefix > len - k.ntok)) fit = false;
+    }
+    if (!(ok && fit) && report) flag(a.status, MK_ERR_BAD_ARG);
+    k.table = b;
+    if (fit) k.kbeg = prefix, k.kend = len, k.c0 = len - k.ntok;
+    else k.flags |= kNan;
+  }
+  k.nb = (k.ntok + tb - 1) / tb;
+  return k;
+}
+
+MK_HD inline int block_end(const Task& k, int b, int tb) {      // end of a row block's keys
+  if (k.flags & kNan) return k.kbeg;
+  return k.flags & kCausal ? hd_max(k.kbeg, k.c0 + hd_min(k.ntok, (b + 1) * tb)) : k.kend;
+}
+
+MK_HD inline int block_tiles(const Task& k, int b, int tb) {
+  return (block_end(k, b, tb) - k.kbeg + kTile - 1) / kTile;
+}
+
+// sum over i < n of floor((a i + b) / m), by Euclid's steps on (a, m)
+MK_HD inline long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
+  long long s = 0;
+  while (n) {
+    if (a >= m) s += (long long)n * (n - 1) / 2 * (a / m), a %= m;
+    if (b >= m) s += (long long)n * (b / m), b %= m;
+    const unsigned y = a * n + b;
+    if (y < m) break;
+    n = y / m, b = y % m;
+    const unsigned t = a;
+    a = m, m = t;
+  }
+  return s;
+}
+
+// key tiles of the row blocks before b, b <= nb
+MK_HD inline long long tiles_before(const Task& k, int b, int tb) {
+  if (k.flags & kNan || b == 0) return 0;
+  if (!(k.flags & kCausal)) return (long long)b * block_tiles(k, 0, tb);
+  long long s = b == k.nb ? block_tiles(k, b - 1, tb) : 0;
+  const int full = hd_min(b, k.nb - 1);
+  if (full <= 4) {
+    for (int i = 0; i < full; i++) s += block_tiles(k, i, tb);
+    return s;
+  }
+  const int base = k.c0 - k.kbeg;                        // block i: ceil((base + tb (i + 1)) / 128) if positive
+  const int skip = base >= 0 ? 0 : hd_min(full, -base / tb);
+  return s + floor_sum(full - skip, kTile, tb, base + tb * (skip + 1) + kTile - 1);
+}
+
+MK_HD inline long long cost_before(const Task& k, int b, int tb) {
+  return tiles_before(k, b, tb) + (long long)b * kStart;
+}
+
+// Where a border x units into an item of n tiles cuts it: the same for the
+// block before and the block after.
+MK_HD inline int cut(long long x, int n) {
+  int k = (int)hd_min(x, (long long)n);
+  if (k < kMinPart) k = 0;
+  return n - k < kMinPart ? n : k;
+}
+
+// The parts of one block: its stretch [pos, stop) of all items laid end to end,
+// from task t, which begins at `at`.  On the GPU a warp walks it together.
+struct Stretch {
+  const KvAttnArgs& a;
+  const int tb;
+  int t, head, b;
+  long long at;
+  const long long pos, stop;
+  Task k;
+
+  MK_HD Stretch(const KvAttnArgs& args, int tt, int task, long long start, long long pos, long long stop, int lane)
+      : a(args), tb(2 * tt), t(task), at(start), pos(pos), stop(stop) {
+    k = load_task(a, t, tb, false);
+    const long long per = cost_before(k, k.nb, tb);
+    head = (int)((pos - at) / per);
+    const long long r = pos - at - head * per;
+    int lo = 0, hi = k.nb;               // the last row block that begins at or before pos
+    while (hi - lo > 1) {
+#ifdef __CUDA_ARCH__
+      const int step = (hi - lo + 31) / 32, c = lo + step * lane;
+      const int n = __popc(__ballot_sync(0xffffffffu, c < hi && cost_before(k, c, tb) <= r));
+#else
+      const int step = (hi - lo + 31) / 32;
+      int n = 0;
+      for (int i = 0; i < 32; i++) n += lo + step * i < hi && cost_before(k, lo + step * i, tb) <= r;
+#endif
+      lo += step * (n - 1);
+      hi = hd_min(hi, lo + step);
+    }
+    b = lo;
+    at += head * per + cost_before(k, b, tb);
+  }
+
+  // the next part with anything to do; slots 2 c and 2 c + 1 are the block's
+  MK_HD bool next(Part* m, int slot) {
+    while (t < a.groups + a.batch && at < stop) {
+      const int n = block_tiles(k, b, tb), len = n + kStart;
+      const int k0 = at < pos ? cut(pos - at, n) : 0, k1 = at + len <= stop ? n : cut(stop - at, n);
+      const bool some = k1 > k0 || (n == 0 && at >= pos);
+      if (some) {
+        m->tok0 = k.tok0 + b * tb, m->ntok = hd_min(tb, k.ntok - b * tb);
+        m->head = head, m->table = k.table;
+        m->kbeg = k.kbeg, m->kend = block_end(k, b, tb);
+        m->lim = k.flags & kCausal ? k.c0 + b * tb + 1 : k.kend;
+        m->k0 = k0, m->k1 = k1, m->n = n, m->flags = k.flags;
+        m->slot = k0 == 0 && k1 == n ? -1 : slot + (k0 == 0);
+      }
+      at += len;
+      if (++b == k.nb) {
+        b = 0;
+        if (++head == a.hkv) {
+          head = 0;
+          while (++t < a.groups + a.batch) {
+            k = load_task(a, t, tb, false);
+            if (k.nb) break;
+          }
+        }
+      }
+      if (some) return true;
+    }
+    return false;
+  }
+};
+
+}  // namespace mk

@@ -19,6 +19,7 @@ struct KvAttnArgs {
   int64_t q_stride, out_stride;
   int head_dim, hq, hkv, grp, total_q, batch, groups, max_pages, num_pages;
   float scale_log2;
+  unsigned long long per_block;   // 2^64 / blocks of the grid, set by the launch
 };
 
 // workspace bytes on a device of `sms` multiprocessors

@@ -37,9 +37,9 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kItems = 4;                // ring of work items
-constexpr int kReaders = 11;             // warps that read an item: 8 softmax, MMA, Q, clear
+constexpr int kReaders = 11;             // warps that read an item: 8 softmax, 2 MMA, Q and clearing
 constexpr unsigned long long kWaitNs = 4000000000ull;
-constexpr int kRegsSoftmax = 216, kRegsOther = 72;
+constexpr int kRegsSoftmax = 200, kRegsOther = 104;
 static_assert(256 * kRegsSoftmax + 128 * kRegsOther == kThreads * 168, "register split");
 
 template <int D>
@@ -85,24 +85,27 @@ __host__ __device__ __forceinline__ Ws ws_of(uint8_t* p, int d, int hq, int tota
 struct Sync {
   uint64_t kv_full[10], kv_empty[10];
   uint64_t raw_full[10];                 // a tile that is cleared before it counts as full
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2];
+  uint64_t q_full[2], q_empty[2], s_full[2], o_full[2];
+  uint64_t p_full[2], turn[2];           // weights are there; wide items: the other warp has issued its products
+  uint64_t pair_full, pair_empty;        // narrow items: the second warpgroup's sums are there, are read
   uint64_t item_full[kItems], item_empty[kItems];
-  uint64_t drain;
+  uint64_t drain[2];
   uint32_t tmem;
   volatile int stop;
   long long scan[kThreads / 32];
-  long long total, start;
-  int task;
+  Begin begin;
+  float pair[2][kTile];
+  int work;                              // this block has a stretch
 };
 
 // Waits for the phase of this parity; false once the block gives up, or after
 // kWaitNs, which makes it give up.
 __device__ __forceinline__ bool wait(Sync& s, uint64_t* bar, uint32_t parity, int32_t* status) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (mbar_wait_some(bar, parity)) return true;
   unsigned long long t0 = 0;
   for (int i = 1;; i++) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 255) == 0) {
+    if (mbar_wait_some(bar, parity)) return true;
+    if ((i & 15) == 0) {
       if (s.stop) return false;
       const unsigned long long t = gtime_ns();
       if (!t0) t0 = t;
@@ -133,157 +136,193 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7f80
 
 // ----------------------------------------------------------------------- kernel
 
-// Softmax of one tile of rows (a warpgroup), item after item
+// Softmax (a warpgroup), item after item: of one of its two tiles of rows, over
+// all its keys; or, where its rows fit one tile, of every second key tile, the
+// two sums being added at the end.
 template <int D>
-__device__ void softmax_role(const KvAttnArgs& a, Sync& s, Item* items, const Ws& ws, int tile, int tt) {
+__device__ void softmax_role(const KvAttnArgs& a, Sync& s, Item* items, const Ws& ws, int group, int tt) {
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, row = 32 * warp + lane;
   const uint32_t tm = s.tmem + ((uint32_t)(32 * warp) << 16);
-  const uint32_t tm_s = tm + 128 * tile, tm_o = tm + 256 + D * tile;
+  const uint32_t tm_s = tm + 128 * group, tm_o = tm + 256 + D * group;
   const float scale = a.scale_log2;
   const int my_tok = row / a.grp, my_head = row - my_tok * a.grp;
-  uint32_t steps = 0, parts = 0;
+  uint32_t steps = 0, parts = 0, pairs = 0;
   for (int it = 0;; it++) {
     Item* slot = &items[it % kItems];
     if (!wait_warp(s, &s.item_full[it % kItems], (it / kItems) & 1, a.status)) return;
     const Part m = *slot;
     if (m.flags & kEnd) return;
-    const int tok = tile * tt + my_tok;
+    const bool narrow = m.ntok <= tt;
+    const int tok = narrow ? my_tok : group * tt + my_tok, every = narrow ? 2 : 1;
     const bool mine = my_tok < tt && tok < m.ntok;
-    if (m.ntok > tile * tt) {
-      const int lim = m.flags & kCausal ? m.lim + tok : m.kend;
-      const int least = __reduce_min_sync(0xffffffffu, mine ? lim : 0x7fffffff);
-      float top = -INFINITY, sum = 0.f;
-      for (int j = m.k0; j < m.k1; j++, steps++) {
-        if (!wait_warp(s, &s.s_full[tile], steps & 1, a.status)) return;
-        tc_fence_after();
-        float x[kTile];
+    const int lim = m.flags & kCausal ? m.lim + tok : m.kend;
+    const int least = __reduce_min_sync(0xffffffffu, mine ? lim : 0x7fffffff);
+    const int j0 = narrow ? m.k0 + group : m.k0;
+    float top = -INFINITY, sum = 0.f;
+    for (int j = j0; j < m.k1; j += every, steps++) {
+      if (!wait_warp(s, &s.s_full[group], steps & 1, a.status)) return;
+      tc_fence_after();
+      float x[kTile];
 #pragma unroll
-        for (int c = 0; c < 4; c++) tc_ld32(tm_s + 32 * c, (uint32_t*)x + 32 * c);
-        tc_wait_ld();
-        const int t0 = m.kbeg + kTile * j;
-        if (t0 + kTile > least) {
-          const int seen = lim - t0;
+      for (int c = 0; c < 4; c++) tc_ld32(tm_s + 32 * c, (uint32_t*)x + 32 * c);
+      tc_wait_ld();
+      const int t0 = m.kbeg + kTile * j;
+      if (t0 + kTile > least) {
+        const int seen = lim - t0;
 #pragma unroll
-          for (int c = 0; c < kTile; c++) x[c] = c < seen ? x[c] : -INFINITY;
-        }
-        float mx[4] = {x[0], x[1], x[2], x[3]};
+        for (int c = 0; c < kTile; c++) x[c] = c < seen ? x[c] : -INFINITY;
+      }
+      float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-        for (int c = 4; c < kTile; c += 8) {
+      for (int c = 4; c < kTile; c += 8) {
 #pragma unroll
-          for (int u = 0; u < 4; u++)
-            mx[u] = c + 4 + u < kTile ? fmaxf(fmaxf(mx[u], x[c + u]), x[c + 4 + u]) : fmaxf(mx[u], x[c + u]);
-        }
-        const float high = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        // The reference moves only when a weight would pass 2^8: sums and
-        // products stay within 2^8 of their size, and O is rarely rescaled.
-        const bool move = high > top && (high - top) * scale > 8.f;
-        if (j == m.k0) {
-          if (high > top) top = high;
-        } else if (__any_sync(0xffffffffu, move)) {
-          // S of this step is complete, so P V of the step before is too
-          const float keep = move ? tc_ex2((top - high) * scale) : 1.f;
-          if (move) top = high;
-          sum *= keep;
+        for (int u = 0; u < 4; u++)
+          mx[u] = c + 4 + u < kTile ? fmaxf(fmaxf(mx[u], x[c + u]), x[c + 4 + u]) : fmaxf(mx[u], x[c + u]);
+      }
+      const float high = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      // The reference moves only when a weight would pass 2^8: sums and
+      // products stay within 2^8 of their size, and O is rarely rescaled.
+      const bool move = high > top && (high - top) * scale > 8.f;
+      if (j == j0) {
+        if (high > top) top = high;
+      } else if (__any_sync(0xffffffffu, move)) {
+        // S of this step is complete, so P V of the step before is too
+        const float keep = move ? tc_ex2((top - high) * scale) : 1.f;
+        if (move) top = high;
+        sum *= keep;
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tc_ld32(tm_o + c, o);
-            tc_wait_ld();
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tc_ld32(tm_o + c, o);
+          tc_wait_ld();
 #pragma unroll
-            for (int u = 0; u < 32; u++) o[u] = __float_as_uint(__uint_as_float(o[u]) * keep);
-            tc_st32(tm_o + c, o);
-          }
+          for (int u = 0; u < 32; u++) o[u] = __float_as_uint(__uint_as_float(o[u]) * keep);
+          tc_st32(tm_o + c, o);
         }
-        const float off = top == -INFINITY ? 0.f : -top * scale;
-        const float2 sc2 = make_float2(scale, scale), off2 = make_float2(off, off);
-        float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      }
+      const float off = top == -INFINITY ? 0.f : -top * scale;
+      const float2 sc2 = make_float2(scale, scale), off2 = make_float2(off, off);
+      float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-          uint32_t p[32];
+      for (int h = 0; h < 2; h++) {
+        uint32_t p[32];
 #pragma unroll
-          for (int u = 0; u < 32; u++) {
-            float2 e = __ffma2_rn(make_float2(x[64 * h + 2 * u], x[64 * h + 2 * u + 1]), sc2, off2);
-            e.x = tc_ex2(e.x), e.y = tc_ex2(e.y);
-            acc[u & 1] = __fadd2_rn(acc[u & 1], e);
-            p[u] = cvt_bf2(e.x, e.y);
-          }
-          tc_st32(tm_s + 32 * h, p);
+        for (int u = 0; u < 32; u++) {
+          float2 e = __ffma2_rn(make_float2(x[64 * h + 2 * u], x[64 * h + 2 * u + 1]), sc2, off2);
+          e.x = tc_ex2(e.x), e.y = tc_ex2(e.y);
+          acc[u & 1] = __fadd2_rn(acc[u & 1], e);
+          p[u] = cvt_bf2(e.x, e.y);
         }
-        sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
-        tc_wait_st();
+        tc_st32(tm_s + 32 * h, p);
+      }
+      tc_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.p_full[group]);
+      sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+    }
+    // -------------------------------------------------------------- the result
+    if (m.k1 > j0) {
+      if (!wait_warp(s, &s.o_full[group], parts & 1, a.status)) return;
+      parts++;
+      tc_fence_after();
+    }
+    float keep0 = 1.f, keep1 = 0.f;
+    if (narrow) {
+      if (group == 1) {
+        s.pair[0][row] = top, s.pair[1][row] = sum;
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&s.p_full[tile]);
+        if (lane == 0) mbar_arrive(&s.pair_full);
+        if (!wait_warp(s, &s.pair_empty, pairs++ & 1, a.status)) return;
+        if (lane == 0) mbar_arrive(&s.item_empty[it % kItems]);
+        continue;
       }
-      // ------------------------------------------------------------ the result
-      const int first = m.kbeg + kTile * m.k0, last = min(m.kend, m.kbeg + kTile * m.k1);
-      const bool some = m.k1 > m.k0;
-      if (some) {
-        if (!wait_warp(s, &s.o_full[tile], parts & 1, a.status)) return;
-        parts++;
-        tc_fence_after();
+      if (!wait_warp(s, &s.pair_full, pairs++ & 1, a.status)) return;
+      tc_fence_after();
+      const float top1 = s.pair[0][row], sum1 = s.pair[1][row], high = fmaxf(top, top1);
+      if (high > -INFINITY) {
+        keep0 = top == high ? 1.f : tc_ex2((top - high) * scale);
+        keep1 = top1 == high ? 1.f : tc_ex2((top1 - high) * scale);
       }
-      const bool nan = (m.flags & kNan) || ((volatile Item*)slot)->bad;
-      const bool dirty = ((volatile Item*)slot)->dirty;
-      const bool sees = lim > first;                         // something in this part
-      float ref = top == -INFINITY ? (sees && some ? -FLT_MAX : -INFINITY) : top * scale;
-      const bool whole = m.slot < 0, parted = a.groups > 0;
-      float mul = 1.f;
-      if (whole) mul = sees && some ? 1.f / sum : 0.f;       // all weights zero: 1 / 0, NaN below
-      const int64_t token = m.tok0 + tok;
-      const int head = m.head * a.grp + my_head;
-      const size_t at = ((m.flags & kPrefix ? 0 : (size_t)a.total_q) + token) * a.hq + head;
+      sum = (keep0 == 0.f ? 0.f : keep0 * sum) + (keep1 == 0.f ? 0.f : keep1 * sum1);
+      top = high;
+    }
+    const int first = m.kbeg + kTile * m.k0, last = min(m.kend, m.kbeg + kTile * m.k1);
+    const bool some = m.k1 > m.k0, second = narrow && m.k1 > m.k0 + 1;
+    const bool nan = (m.flags & kNan) || ((volatile Item*)slot)->bad;
+    const bool dirty = ((volatile Item*)slot)->dirty;
+    const bool sees = some && lim > first;                   // something in this part
+    const float ref = top == -INFINITY ? (sees ? -FLT_MAX : -INFINITY) : top * scale;
+    const bool whole = m.slot < 0, parted = a.groups > 0;
+    const float mul = !whole ? 1.f : sees ? 1.f / sum : 0.f;
+    const bool lost = nan || (sees && sum == 0.f);           // every score is -infinity
+    const int64_t token = m.tok0 + tok;
+    const int head = m.head * a.grp + my_head;
+    const size_t at = ((m.flags & kPrefix ? 0 : (size_t)a.total_q) + token) * a.hq + head;
+    float* data = ws.data + (whole ? 0 : m.slot) * slot_floats(D);
+    const int line = narrow ? row : 128 * group + row;
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        uint32_t r[32];
-        float* o = (float*)r;
-        if (some) {
-          tc_ld32(tm_o + c, r);
-          tc_wait_ld();
-        } else {
+    for (int c = 0; c < D; c += 32) {
+      uint32_t r[32];
+      float* o = (float*)r;
+      tc_ld32(tm_o + c, r);
+      if (second) {
+        uint32_t r1[32];
+        tc_ld32(tm_o + D + c, r1);
+        tc_wait_ld();
+#pragma unroll
+        for (int u = 0; u < 32; u++) {
+          const float y = keep1 == 0.f ? 0.f : keep1 * __uint_as_float(r1[u]);
+          o[u] = keep0 == 0.f ? y : fmaf(keep0, o[u], y);
+        }
+      } else {
+        tc_wait_ld();
+        if (!some) {
 #pragma unroll
           for (int u = 0; u < 32; u++) o[u] = 0.f;
         }
-        if (dirty && mine) {
-          // values that were not finite and that this row sees: whatever their weight, they are in its sum
-          for (int t = max(first, m.flags & kCausal ? m.lim : m.kend); t < min(lim, last); t++) {
-            const int page = a.page_tables[(int64_t)m.table * a.max_pages + t / kKvPage];
-            if (page < 0 || page >= a.num_pages) continue;
-            const uint16_t* v = a.v_pool + (((int64_t)page * a.hkv + m.head) * kKvPage + t % kKvPage) * D + c;
+      }
+      if (dirty && mine) {
+        // values that were not finite and that this row sees: whatever their weight, they are in its sum
+        for (int t = max(first, m.flags & kCausal ? m.lim : m.kend); t < min(lim, last); t++) {
+          const int page = a.page_tables[(int64_t)m.table * a.max_pages + t / kKvPage];
+          if (page < 0 || page >= a.num_pages) continue;
+          const uint16_t* v = a.v_pool + (((int64_t)page * a.hkv + m.head) * kKvPage + t % kKvPage) * D + c;
 #pragma unroll
-            for (int u = 0; u < 32; u++) {
-              const float f = bf16f(v[u]);
-              if (!(fabsf(f) <= FLT_MAX)) o[u] += f;
-            }
+          for (int u = 0; u < 32; u++) {
+            const float f = bf16f(v[u]);
+            if (!(fabsf(f) <= FLT_MAX)) o[u] += f;
           }
         }
-        if (mine && whole) {
-#pragma unroll
-          for (int u = 0; u < 32; u++) o[u] = nan || (sees && some && sum == 0.f) ? NAN : o[u] * mul;
-        }
-        if (mine && whole && !parted) {
-          uint4* out = (uint4*)(a.out + token * a.out_stride + (int64_t)head * D + c);
-#pragma unroll
-          for (int u = 0; u < 4; u++)
-            out[u] = make_uint4(cvt_bf2(o[8 * u], o[8 * u + 1]), cvt_bf2(o[8 * u + 2], o[8 * u + 3]),
-                                cvt_bf2(o[8 * u + 4], o[8 * u + 5]), cvt_bf2(o[8 * u + 6], o[8 * u + 7]));
-        } else if (mine) {
-          float4* out = (float4*)(whole ? ws.part_o + at * D + c
-                                        : ws.data + m.slot * slot_floats(D) + (size_t)(128 * tile + row) * D + c);
-#pragma unroll
-          for (int u = 0; u < 8; u++) out[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
-        }
-        __syncwarp();          // the next tensor memory load is the whole warp's
       }
-      if (mine && whole && parted) ws.part_m[at] = nan ? NAN : ref == -INFINITY || ref == -FLT_MAX ? ref : ref + log2f(sum);
-      if (mine && !whole) {
-        float* d = ws.data + m.slot * slot_floats(D) + 256 * D + 128 * tile + row;
-        d[0] = ref, d[256] = sum;
+      if (mine && whole) {
+#pragma unroll
+        for (int u = 0; u < 32; u++) o[u] = lost ? NAN : o[u] * mul;
       }
-      tc_fence_before();       // O has been read before the next item's first P is announced
+      if (mine && whole && !parted) {
+        uint4* out = (uint4*)(a.out + token * a.out_stride + (int64_t)head * D + c);
+#pragma unroll
+        for (int u = 0; u < 4; u++)
+          out[u] = make_uint4(cvt_bf2(o[8 * u], o[8 * u + 1]), cvt_bf2(o[8 * u + 2], o[8 * u + 3]),
+                              cvt_bf2(o[8 * u + 4], o[8 * u + 5]), cvt_bf2(o[8 * u + 6], o[8 * u + 7]));
+      } else if (mine) {
+        // a part's slot holds four dims of all rows side by side: a warp writes 512 bytes
+        float4* out = whole ? (float4*)(ws.part_o + at * D + c) : (float4*)data + 64 * c + line;
+#pragma unroll
+        for (int u = 0; u < 8; u++)
+          out[whole ? u : 256 * u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+      }
+      __syncwarp();          // the next tensor memory load is the whole warp's
     }
+    if (mine && whole && parted) ws.part_m[at] = nan ? NAN : ref == -INFINITY || ref == -FLT_MAX ? ref : ref + log2f(sum);
+    if (mine && !whole) data[256 * D + line] = ref, data[256 * D + 256 + line] = sum;
+    tc_fence_before();       // O has been read before the next item's first P is announced
     __syncwarp();
-    if (lane == 0) mbar_arrive(&s.item_empty[it % kItems]);
+    if (lane == 0) {
+      if (narrow) mbar_arrive(&s.pair_empty);
+      mbar_arrive(&s.item_empty[it % kItems]);
+    }
   }
 }
 
@@ -292,32 +331,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     kv_attention_kernel(const KvAttnArgs a, const __grid_constant__ CUtensorMap map_q,
                         const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
   using S = Shape<D>;
-  extern __shared__ uint8_t raw[];
+  extern __shared__ uint8_t raw_smem[];
   __shared__ Sync s;
   __shared__ Item items[kItems];
-  const uint32_t q_smem = (smem_u32(raw) + 1023u) & ~1023u, kv_smem = q_smem + 2 * S::kTileBytes;
+  const uint32_t q_smem = (smem_u32(raw_smem) + 1023u) & ~1023u, kv_smem = q_smem + 2 * S::kTileBytes;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tt = kTile / a.grp, tb = 2 * tt, tasks = a.groups + a.batch;
   const Ws ws = ws_of(a.ws, D, a.hq, a.total_q, gridDim.x);
 
   if (tid == 0) {
-    for (int i = 0; i < S::kStages; i++) mbar_init(&s.kv_full[i], 1), mbar_init(&s.kv_empty[i], 1), mbar_init(&s.raw_full[i], 1);
+    for (int i = 0; i < S::kStages; i++) mbar_init(&s.kv_full[i], 1), mbar_init(&s.kv_empty[i], 2), mbar_init(&s.raw_full[i], 1);
     for (int t = 0; t < 2; t++) {
-      mbar_init(&s.q_full[t], 1), mbar_init(&s.q_empty[t], 1), mbar_init(&s.s_full[t], 1);
-      mbar_init(&s.p_full[t], 4), mbar_init(&s.o_full[t], 1);
+      mbar_init(&s.q_full[t], 1), mbar_init(&s.q_empty[t], t ? 1 : 2), mbar_init(&s.s_full[t], 1);
+      mbar_init(&s.p_full[t], 4), mbar_init(&s.turn[t], 1), mbar_init(&s.o_full[t], 1);
     }
     for (int i = 0; i < kItems; i++) mbar_init(&s.item_full[i], 1), mbar_init(&s.item_empty[i], kReaders);
-    mbar_init(&s.drain, 1);
-    s.stop = 0, s.task = -1;
+    mbar_init(&s.pair_full, 4), mbar_init(&s.pair_empty, 4), mbar_init(&s.drain[0], 1), mbar_init(&s.drain[1], 1);
+    s.stop = 0, s.work = 0;
     mbar_fence_init();
   }
   if (warp == 8) tc_alloc(&s.tmem, 512);
 
-  // all tasks' cost, and the task that this block's stretch begins in
-  const int chunk = (tasks + kThreads - 1) / kThreads, first = min(tasks, tid * chunk), end = min(tasks, first + chunk);
+  if (warp == 11 && lane < 3) tma_prefetch_map(lane == 0 ? &map_k : lane == 1 ? &map_v : &map_q);
+
+  // all tasks' cost, and the item that this block's stretch begins in
+  const int chunk = tasks <= kThreads ? 1 : (tasks + kThreads - 1) / kThreads;
+  const int first = min(tasks, tid * chunk), end = min(tasks, first + chunk);
   long long mine = 0;
+  Task k{};
   for (int t = first; t < end; t++) {
-    const Task k = load_task(a, t, tb, blockIdx.x == 0);
+    k = load_task(a, t, tb, blockIdx.x == 0);
     mine += cost_before(k, k.nb, tb) * a.hkv;
   }
   long long incl = mine;
@@ -331,23 +374,32 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   long long before = incl - mine, total = 0;
+#pragma unroll
   for (int w = 0; w < kThreads / 32; w++) {
-    if (w < warp) before += s.scan[w];
-    total += s.scan[w];
+    const long long x = s.scan[w];
+    if (w < warp) before += x;
+    total += x;
   }
-  const long long share = max((total + gridDim.x - 1) / gridDim.x, (long long)kMinShare);
+  // about an equal share: total / blocks, from above
+  const long long share = max((long long)__umul64hi((unsigned long long)total, a.per_block) + 1, (long long)kMinShare);
   const long long pos = share * blockIdx.x, stop = min(total, pos + share);
-  if (pos < total && before <= pos && pos < before + mine) {
-    long long at = before;
-    for (int t = first; t < end; t++) {
-      const Task k = load_task(a, t, tb, false);
-      const long long c = cost_before(k, k.nb, tb) * a.hkv;
-      if (pos < at + c) {
-        s.task = t, s.start = at;
-        break;
+  const bool owner = pos < total && before <= pos && pos < before + mine;
+  if (__any_sync(0xffffffffu, owner)) {          // the warp that found the task finds the item
+    int t = first;
+    if (owner && chunk > 1)
+      for (; t < end; t++) {
+        k = load_task(a, t, tb, false);
+        const long long c = cost_before(k, k.nb, tb) * a.hkv;
+        if (pos < before + c) break;
+        before += c;
       }
-      at += c;
-    }
+    const int from = __ffs(__ballot_sync(0xffffffffu, owner)) - 1;
+    Task o;
+#pragma unroll
+    for (int w = 0; w < (int)(sizeof(Task) / 4); w++)
+      reinterpret_cast<int*>(&o)[w] = __shfl_sync(0xffffffffu, reinterpret_cast<const int*>(&k)[w], from);
+    const Begin g = begin_of(o, __shfl_sync(0xffffffffu, t, from), tb, __shfl_sync(0xffffffffu, before, from), pos, lane);
+    if (lane == 0) s.begin = g, s.work = 1;
   }
   __syncthreads();
   const uint32_t tmem = s.tmem;
@@ -363,61 +415,82 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t loads = 0, raw = 0, raw_use = 0;    // stages whose last tile goes through raw_full; its uses, modulo 2
       int it = 0;
       bool ok = true;
-      if (s.task >= 0) {
-        Stretch w(a, tt, s.task, s.start, pos, stop, lane);
-        Part m;
-        while (ok && w.next(&m, 2 * (int)blockIdx.x)) {
-          {
-            const int k0 = m.k0, k1 = m.k1, head = m.head;
-            Item* dst = &items[it % kItems];
-            ok = wait_warp(s, &s.item_empty[it % kItems], ((it / kItems) & 1) ^ 1, a.status);
-            if (!ok) break;
-            if (lane == 0) {
-              *static_cast<Part*>(dst) = m;
-              dst->bad = dst->dirty = 0;
-              mbar_arrive(&s.item_full[it % kItems]);
-            }
-            it++;
-            bool bad = false;
-            const int i = S::kHalves == 2 ? lane >> 1 : lane, half = S::kHalves == 2 ? lane & 1 : 0;
-            const int32_t* table = a.page_tables + (int64_t)m.table * a.max_pages + m.kbeg / kKvPage + i;
-            // pages of tile j for this lane; none past the keys
-            auto pages_of = [&](int j) { return min(8, (m.kend - m.kbeg - kTile * j + kKvPage - 1) / kKvPage); };
-            auto page_of = [&](int j) { return j < k1 && i < pages_of(j) ? table[8 * j] : 0; };
-            const int clear = (m.flags & kCausal ? m.lim : m.kend) - m.kbeg;
-            auto load = [&](const CUtensorMap& map, int j, int page, bool value) {
-              const uint32_t st = loads % S::kStages;
-              if (!wait_warp(s, &s.kv_empty[st], ((loads / S::kStages) & 1) ^ 1, a.status)) return false;
-              const int np = pages_of(j);
-              const bool out = i < np && (page < 0 || page >= a.num_pages);
-              if (__any_sync(0xffffffffu, out)) {
-                bad = true;
-                if (lane == 0) ((volatile Item*)dst)->bad = 1, flag(a.status, MK_ERR_BAD_PAGE);
-              }
-              const bool through = value && kTile * (j + 1) > clear;
-              raw = (raw & ~(1u << st)) | (uint32_t)through << st;
-              raw_use ^= (uint32_t)through << st;
-              uint64_t* bar = through ? &s.raw_full[st] : &s.kv_full[st];
-              if (lane == 0) mbar_arrive_expect_tx(bar, np * S::kHalves * 2048);
-              __syncwarp();
-              // a page outside the cache: past the last one, which the copy fills with zeros
-              if (i < np)
-                tma_load_3d(kv_smem + st * S::kTileBytes + half * 16384 + i * 2048, &map, 64 * half, kKvPage * head,
-                            out ? a.num_pages : page, bar);
-              loads++;
-              return true;
-            };
-            int cur = page_of(k0), next = page_of(k0 + 1);
-            ok = k1 == k0 || load(map_k, k0, cur, false);
-            for (int j = k0; ok && j < k1; j++) {
-              const int later = page_of(j + 2);
-              ok = load(map_v, j, cur, true);
-              if (ok && j + 1 < k1) ok = load(map_k, j + 1, next, false);
-              cur = next, next = later;
-            }
-            if (m.slot >= 0)
-              desc[k0 == 0] = Slot{k1 < m.n ? 1 : 2, m.tok0, m.ntok, head, m.kbeg, m.lim, m.flags, bad};
+      if (s.work) {
+        auto pages_of = [&](const Part& p, int j) { return min(8, (p.kend - p.kbeg - kTile * j + kKvPage - 1) / kKvPage); };
+        auto page_of = [&](const Part& p, int j) {
+          return j < p.k1 && lane < pages_of(p, j)
+                     ? a.page_tables[(int64_t)p.table * a.max_pages + p.kbeg / kKvPage + 8 * j + lane] : 0;
+        };
+        Stretch w(a, tt, s.begin, pos, stop);
+        Part m, nx;
+        bool have = w.next(&m, 2 * (int)blockIdx.x);
+        int page[3], npage[3] = {0, 0, 0};
+        if (have)
+          for (int x = 0; x < 3; x++) page[x] = page_of(m, m.k0 + x);
+        while (have) {
+          Item* dst = &items[it % kItems];
+          ok = wait_warp(s, &s.item_empty[it % kItems], ((it / kItems) & 1) ^ 1, a.status);
+          if (!ok) break;
+          if (lane == 0) {
+            *static_cast<Part*>(dst) = m;
+            dst->bad = dst->dirty = 0;
+            mbar_arrive(&s.item_full[it % kItems]);
           }
+          it++;
+          bool bad = false;
+          const int clear = (m.flags & kCausal ? m.lim : m.kend) - m.kbeg;
+          auto load = [&](const CUtensorMap& map, int j, int pg, bool value) {
+            const uint32_t st = loads % S::kStages;
+            if (!wait_warp(s, &s.kv_empty[st], ((loads / S::kStages) & 1) ^ 1, a.status)) return false;
+            const int np = pages_of(m, j);
+            const bool out = lane < np && (pg < 0 || pg >= a.num_pages);
+            if (__any_sync(0xffffffffu, out)) {
+              bad = true;
+              if (lane == 0) ((volatile Item*)dst)->bad = 1, flag(a.status, MK_ERR_BAD_PAGE);
+            }
+            const bool through = value && kTile * (j + 1) > clear;
+            raw = (raw & ~(1u << st)) | (uint32_t)through << st;
+            raw_use ^= (uint32_t)through << st;
+            uint64_t* bar = through ? &s.raw_full[st] : &s.kv_full[st];
+            // a page outside the cache: past the last one, which the copy fills with zeros
+            const int from = out ? a.num_pages : pg;
+            int ids[8];
+#pragma unroll
+            for (int i = 0; i < 8; i++) ids[i] = __shfl_sync(0xffffffffu, from, i);
+            // one lane issues: sixteen lanes at once took 2500 cycles a tile, each copy on its own
+            if (tc_elect()) {
+              mbar_arrive_expect_tx(bar, np * S::kHalves * 2048);
+#pragma unroll
+              for (int i = 0; i < 8; i++)
+                if (i < np)
+#pragma unroll
+                  for (int h = 0; h < S::kHalves; h++)
+                    tma_load_3d(kv_smem + st * S::kTileBytes + h * 16384 + i * 2048, &map, 64 * h, kKvPage * m.head, ids[i], bar);
+            }
+            __syncwarp();
+            loads++;
+            return true;
+          };
+          // in the order of their use: K of the first step (narrow: two), then V of one and K of a later one
+          const bool narrow = m.ntok <= tt;
+          ok = m.k1 == m.k0 || load(map_k, m.k0, page[0], false);
+          if (ok && narrow && m.k1 > m.k0 + 1) ok = load(map_k, m.k0 + 1, page[1], false);
+          // the next part and its first pages, while this one's copies are under way
+          const bool more = w.next(&nx, 2 * (int)blockIdx.x);
+          if (more)
+            for (int x = 0; x < 3; x++) npage[x] = page_of(nx, nx.k0 + x);
+          for (int j = m.k0; ok && j < m.k1; j++) {
+            const int later = page_of(m, j + 3);
+            ok = load(map_v, j, page[0], true);
+            if (ok && !narrow && j + 1 < m.k1) ok = load(map_k, j + 1, page[1], false);
+            if (ok && narrow && j + 2 < m.k1) ok = load(map_k, j + 2, page[2], false);
+            page[0] = page[1], page[1] = page[2], page[2] = later;
+          }
+          if (m.slot >= 0)
+            desc[m.k0 == 0] = Slot{m.k1 < m.n ? 1 : 2, m.tok0, m.ntok, m.head, m.kbeg, m.lim, m.flags, bad};
+          if (!ok) break;
+          have = more, m = nx;
+          for (int x = 0; x < 3; x++) page[x] = npage[x];
         }
       }
       if (ok && wait_warp(s, &s.item_empty[it % kItems], ((it / kItems) & 1) ^ 1, a.status) && lane == 0) {
@@ -432,108 +505,126 @@ __global__ void __launch_bounds__(kThreads, 1)
           else settle(&s.kv_full[st], (i / S::kStages) & 1);
         }
       }
-    } else if (warp == 9) {
-      // -------------------------------------------------- MMAs (one thread)
-      if (lane == 0) {
-        constexpr uint32_t idesc_s = tc_idesc(kTile, false), idesc_o = tc_idesc(D, true);
-        uint32_t loads = 0, items_q[2] = {0, 0}, steps[2] = {0, 0};
-        bool ok = true;
-        auto qk = [&](int t, uint32_t st) {
-          const uint32_t qa = q_smem + t * S::kTileBytes, kb = kv_smem + st * S::kTileBytes;
+    } else if (warp < 11) {
+      // ---------- MMAs, a warp each for the two softmax warpgroups: together,
+      // one lane issues.  Wide items: stream t is a tile of rows, and each step's
+      // K and V serve both.  Narrow ones: the streams take key tiles in turn.
+      // Either way a warp sees every load of the ring, in order.
+      constexpr uint32_t idesc_s = tc_idesc(kTile, false), idesc_o = tc_idesc(D, true);
+      const int t = __shfl_sync(0xffffffffu, warp - 9, 0);
+      uint32_t loads = 0, used_q[2] = {0, 0}, steps = 0, turns = 0;
+      bool ok = true;
+      const uint64_t k_desc = tc_desc(kv_smem), v_desc = tc_desc(kv_smem, 16384);
+      auto commit = [&](uint64_t* bar) {
+        if (tc_elect()) tc_commit(bar);
+        __syncwarp();
+      };
+      auto full = [&](uint32_t load) {
+        ok = ok && wait_warp(s, &s.kv_full[load % S::kStages], (load / S::kStages) & 1, a.status);
+        tc_fence_after();
+        return ok;
+      };
+      auto used = [&](bool by_me) {                          // this load's stage; on to the next
+        uint64_t* bar = &s.kv_empty[loads++ % S::kStages];
+        if (tc_elect()) {
+          if (by_me) tc_commit(bar);
+          else mbar_arrive(bar);
+        }
+        __syncwarp();
+      };
+      for (int it = 0; ok; it++) {
+        ok = wait_warp(s, &s.item_full[it % kItems], (it / kItems) & 1, a.status);
+        if (!ok) break;
+        const Item& m = items[it % kItems];
+        const int flags = m.flags, n = m.k1 - m.k0;
+        const bool narrow = m.ntok <= tt;
+        if (flags & kEnd) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.item_empty[it % kItems]);
+        if (n == 0) continue;
+        const int tile = narrow ? 0 : t, every = narrow ? 2 : 1;
+        const uint64_t q_desc = tc_desc(q_smem + tile * S::kTileBytes);
+        auto mine = [&](int j) { return !narrow || (j & 1) == t; };
+        auto last = [&](int j) { return j + every >= n; };   // of this stream
+        auto qk = [&](int j, uint32_t load) {                // one lane: S of key tile j
+          const uint64_t kd = k_desc + load % S::kStages * (S::kTileBytes / 16);
 #pragma unroll
           for (int c = 0; c < D / 16; c++) {
-            const uint32_t off = c / 4 * 16384 + c % 4 * 32;
-            tc_mma_ss(tmem + 128 * t, tc_desc(qa + off), tc_desc(kb + off), idesc_s, c > 0);
+            const int off = (c / 4 * 16384 + c % 4 * 32) / 16;
+            tc_mma_ss(tmem + 128 * t, q_desc + off, kd + off, idesc_s, c > 0);
           }
+          tc_commit(&s.s_full[t]);
+          if (last(j)) tc_commit(&s.q_empty[tile]);
         };
-        auto pv = [&](int t, uint32_t st, bool acc) {
-          const uint32_t vb = kv_smem + st * S::kTileBytes;
+        auto pv = [&](int j, uint32_t load) {                // one lane: O of key tile j
+          const uint64_t vd = v_desc + load % S::kStages * (S::kTileBytes / 16);
 #pragma unroll
           for (int c = 0; c < kTile / 16; c++)
-            tc_mma_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * c, tc_desc(vb + 2048 * c, 16384), idesc_o, acc || c > 0);
+            tc_mma_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * c, vd + c * (2048 / 16), idesc_o, j >= every || c > 0);
+          if (last(j)) tc_commit(&s.o_full[t]);
         };
-        auto full = [&](uint32_t i) {
-          ok = ok && wait(s, &s.kv_full[i % S::kStages], (i / S::kStages) & 1, a.status);
+        auto weights = [&] {
+          ok = ok && wait_warp(s, &s.p_full[t], steps++ & 1, a.status);
           tc_fence_after();
+          return ok;
         };
-        for (int it = 0; ok; it++) {
-          ok = wait(s, &s.item_full[it % kItems], (it / kItems) & 1, a.status);
-          if (!ok) break;
-          const Item& m = items[it % kItems];
-          const int flags = m.flags, k0 = m.k0, k1 = m.k1, tiles = m.ntok > tt ? 2 : 1;
-          if (flags & kEnd) break;
-          mbar_arrive(&s.item_empty[it % kItems]);
-          if (k1 == k0) continue;
-          full(loads);
-          for (int t = 0; ok && t < tiles; t++) {
-            ok = wait(s, &s.q_full[t], items_q[t]++ & 1, a.status);
+        ok = wait_warp(s, &s.q_full[0], used_q[0]++ & 1, a.status);
+        if (ok && !narrow && t == 1) ok = wait_warp(s, &s.q_full[1], used_q[1]++ & 1, a.status);
+        // tile 0 of Q is free when both have done with it
+        if (t == 1 && (!narrow || n == 1) && lane == 0) mbar_arrive(&s.q_empty[0]);
+        __syncwarp();
+        for (int j = 0; ok && j < min(n, every); j++) {
+          if (!full(loads)) break;
+          if (mine(j) && tc_elect()) qk(j, loads);
+          __syncwarp();
+          used(mine(j));
+        }
+        if (!narrow) {
+          // The warps take turns, products of one stream after those of the
+          // other: in step with each other both softmaxes would run at once, and
+          // then both products (32K prompt: 6.66 ms without turns).
+          for (int j = 0; ok && j < n; j++) {
+            const bool more = j + 1 < n;
+            if (!full(loads) || !weights() || (more && !full(loads + 1))) break;
+            ok = wait_warp(s, &s.turn[t], (turns++ & 1) ^ (t == 0), a.status);
             if (!ok) break;
-            tc_fence_after();
-            qk(t, loads % S::kStages);
-            tc_commit(&s.s_full[t]);
-            if (k1 == k0 + 1) tc_commit(&s.q_empty[t]);
-          }
-          tc_commit(&s.kv_empty[loads % S::kStages]);
-          loads++;
-          for (int j = k0; ok && j < k1; j++) {
-            const uint32_t sv = loads % S::kStages, sk = (loads + 1) % S::kStages;
-            const bool more = j + 1 < k1;
-            full(loads);
-            for (int t = 0; ok && t < tiles; t++) {
-              ok = wait(s, &s.p_full[t], steps[t]++ & 1, a.status);
-              if (!ok) break;
-              tc_fence_after();
-              pv(t, sv, j > k0);
+            if (tc_elect()) {
+              pv(j, loads);
+              tc_commit(&s.kv_empty[loads % S::kStages]);
               if (more) {
-                if (t == 0) full(loads + 1);
-                if (!ok) break;
-                qk(t, sk);
-                tc_commit(&s.s_full[t]);
-                if (j + 2 == k1) tc_commit(&s.q_empty[t]);
-              } else {
-                tc_commit(&s.o_full[t]);
+                qk(j + 1, loads + 1);
+                tc_commit(&s.kv_empty[(loads + 1) % S::kStages]);
               }
+              mbar_arrive(&s.turn[t ^ 1]);
             }
-            tc_commit(&s.kv_empty[sv]);
-            if (more) tc_commit(&s.kv_empty[sk]);
+            __syncwarp();
             loads += more ? 2 : 1;
           }
-        }
-        // nothing may arrive on a barrier after the block's end
-        tc_commit(&s.drain);
-        settle(&s.drain, 0);
-      }
-    } else if (warp == 10) {
-      // --------------------------------------------------- Q (one thread)
-      if (lane == 0) {
-        uint32_t loads[2] = {0, 0};
-        bool ok = true;
-        const uint32_t bytes = (uint32_t)(tt * a.grp) * 128 * S::kHalves;
-        for (int it = 0; ok; it++) {
-          ok = wait(s, &s.item_full[it % kItems], (it / kItems) & 1, a.status);
-          if (!ok) break;
-          const Part m = items[it % kItems];
-          if (m.flags & kEnd) break;
-          mbar_arrive(&s.item_empty[it % kItems]);
-          for (int t = 0; ok && m.k1 > m.k0 && t < 2 && m.ntok > t * tt; t++) {
-            ok = wait(s, &s.q_empty[t], (loads[t] & 1) ^ 1, a.status);
-            if (!ok) break;
-            loads[t]++;
-            mbar_arrive_expect_tx(&s.q_full[t], bytes);
-            for (int h = 0; h < S::kHalves; h++)
-              tma_load_3d(q_smem + t * S::kTileBytes + h * 16384, &map_q, 64 * h, m.head * a.grp, m.tok0 + t * tt,
-                          &s.q_full[t]);
+        } else {
+          for (int j = 0; ok && j < n; j++) {
+            if (!full(loads) || (mine(j) && !weights())) break;
+            if (mine(j) && tc_elect()) pv(j, loads);
+            __syncwarp();
+            used(mine(j));
+            if (j + 2 < n) {
+              if (!full(loads)) break;
+              if (mine(j) && tc_elect()) qk(j + 2, loads);
+              __syncwarp();
+              used(mine(j));
+            }
           }
         }
-        if (s.stop)
-          for (int t = 0; t < 2; t++)
-            if (loads[t]) settle(&s.q_full[t], (loads[t] - 1) & 1);
       }
+      // nothing may arrive on a barrier after the block's end
+      commit(&s.drain[t]);
+      settle(&s.drain[t], 0);
     } else {
-      // ---------------- values that some row does not see (whole warp): a
+      // ---------------- Q, and values that some row does not see (whole warp): a
       // weight of zero times NaN or an infinity is no zero, so those are taken
       // out, and what a page holds past the sequence with them
-      uint32_t loads = 0, uses = 0;
+      uint8_t* kv = raw_smem + (kv_smem - smem_u32(raw_smem));
+      uint32_t loads = 0, uses = 0, q_loads[2] = {0, 0};
+      const uint32_t q_bytes = (uint32_t)(tt * a.grp) * 128 * S::kHalves;
       bool ok = true;
       for (int it = 0; ok; it++) {
         ok = wait_warp(s, &s.item_full[it % kItems], (it / kItems) & 1, a.status);
@@ -541,36 +632,58 @@ __global__ void __launch_bounds__(kThreads, 1)
         Item* slot = &items[it % kItems];
         const Part m = *slot;
         if (m.flags & kEnd) break;
+        for (int t = 0; ok && m.k1 > m.k0 && t < 2 && m.ntok > t * tt; t++) {
+          ok = wait_warp(s, &s.q_empty[t], (q_loads[t] & 1) ^ 1, a.status);
+          if (!ok) break;
+          q_loads[t]++;
+          if (tc_elect()) {
+            mbar_arrive_expect_tx(&s.q_full[t], q_bytes);
+#pragma unroll
+            for (int h = 0; h < S::kHalves; h++)
+              tma_load_3d(q_smem + t * S::kTileBytes + h * 16384, &map_q, 64 * h, m.head * a.grp, m.tok0 + t * tt,
+                          &s.q_full[t]);
+          }
+          __syncwarp();
+        }
         const int clear = (m.flags & kCausal ? m.lim : m.kend) - m.kbeg;
         for (int j = m.k0; ok && j < m.k1; j++) {
           if (kTile * (j + 1) <= clear) continue;
-          const uint32_t i = loads + 2 * (j - m.k0) + 1, st = i % S::kStages;
+          const uint32_t i = loads + (j - m.k0) + min(j - m.k0 + (m.ntok <= tt ? 2 : 1), m.k1 - m.k0), st = i % S::kStages;
           ok = wait_warp(s, &s.raw_full[st], uses >> st & 1, a.status);
           if (!ok) break;
           uses ^= 1u << st;
-          const int lo = max(0, clear - kTile * j), held = m.kend - m.kbeg - kTile * j;
-          const uint32_t base = kv_smem + st * S::kTileBytes;
+          const int lo = max(0, clear - kTile * j), held = min(kTile, m.kend - m.kbeg - kTile * j);
           bool found = false;
-#pragma unroll 4
-          for (int c = 8 * lo + lane; c < 8 * kTile; c += 32) {
+          // 16 bytes a lane, eight loads at a time: rows [lo, held) are looked over, those after them zeroed
+          for (int c = 8 * lo + lane; c < 8 * held; c += 4 * 32) {
+            uint4 w[4][S::kHalves];
 #pragma unroll
-            for (int h = 0; h < S::kHalves; h++) {
-              const uint32_t at = base + 16384 * h + 16 * c;
-              uint32_t w[4];
-              asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at));
-              const bool past = c / 8 >= held;
-              const uint32_t nf = not_finite(w[0]) | not_finite(w[1]) | not_finite(w[2]) | not_finite(w[3]);
-              if (past || nf) {
-                found |= !past;
+            for (int u = 0; u < 4; u++)
 #pragma unroll
-                for (int u = 0; u < 4; u++) {
-                  const uint32_t b = not_finite(w[u]);
-                  w[u] = past ? 0u : w[u] & ~((b & 0x8000u ? 0xffffu : 0u) | (b & 0x80000000u ? 0xffff0000u : 0u));
-                }
-                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+              for (int h = 0; h < S::kHalves; h++) {
+                w[u][h] = make_uint4(0, 0, 0, 0);
+                if (c + 32 * u < 8 * held) w[u][h] = *(const uint4*)(kv + st * S::kTileBytes + 16384 * h + 16 * (c + 32 * u));
               }
-            }
+#pragma unroll
+            for (int u = 0; u < 4; u++)
+#pragma unroll
+              for (int h = 0; h < S::kHalves; h++) {
+                uint32_t* x = reinterpret_cast<uint32_t*>(&w[u][h]);
+                if (not_finite(x[0]) | not_finite(x[1]) | not_finite(x[2]) | not_finite(x[3])) {
+                  found = true;
+#pragma unroll
+                  for (int e = 0; e < 4; e++) {
+                    const uint32_t b = not_finite(x[e]);
+                    x[e] &= ~((b & 0x8000u ? 0xffffu : 0u) | (b & 0x80000000u ? 0xffff0000u : 0u));
+                  }
+                  *(uint4*)(kv + st * S::kTileBytes + 16384 * h + 16 * (c + 32 * u)) = w[u][h];
+                }
+              }
           }
+          for (int c = 8 * max(held, 0) + lane; c < 8 * kTile; c += 32)
+#pragma unroll
+            for (int h = 0; h < S::kHalves; h++)
+              *(uint4*)(kv + st * S::kTileBytes + 16384 * h + 16 * c) = make_uint4(0, 0, 0, 0);
           if (found) ((volatile Item*)slot)->dirty = 1;
           fence_proxy_async_smem();
           __syncwarp();
@@ -580,6 +693,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.item_empty[it % kItems]);
       }
+      if (s.stop)
+        for (int t = 0; t < 2; t++)
+          if (q_loads[t]) settle(&s.q_full[t], (q_loads[t] - 1) & 1);
     }
   }
   __syncwarp();
@@ -591,18 +707,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------------ merge
 
-// Adds up an item's parts in key order, a warp a row: part c's first item (if
-// it goes on) and the first slots of the blocks after it.
-constexpr int kMergeRows = 16;             // blocks of rows (gridDim.y)
-
+// Adds up an item's parts in key order: block c's item, if it goes on, and the
+// first slots of the blocks after it.  A warp takes 8 rows and 32 of their dims.
 template <int D>
 __global__ void __launch_bounds__(256) kv_merge_kernel(const KvAttnArgs a) {
-  constexpr int V = D / 32, kBatch = 8;
+  constexpr int kBatch = 8;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x, blocks = gridDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Ws ws = ws_of(a.ws, D, a.hq, a.total_q, blocks);
   const Slot m = ws.slots[2 * c + 1];
   if (m.state != 1) return;
+  const int job = blockIdx.y * 8 + warp, r = job / (D / 32) * 8 + (lane & 7), c4 = job % (D / 32) * 8 + (lane >> 3);
+  if (r - (lane & 7) >= m.ntok * a.grp) return;
   int parts = 1;
   bool nan = m.nan;
   for (int i0 = c + 1; i0 < blocks; i0 += 32) {
@@ -614,61 +730,62 @@ __global__ void __launch_bounds__(256) kv_merge_kernel(const KvAttnArgs a) {
     parts += n;
     if (last) break;
   }
-  const int tt = kTile / a.grp;
-  for (int r = blockIdx.y + gridDim.y * warp; r < m.ntok * a.grp; r += gridDim.y * 8) {
-    const int tok = r / a.grp, h = r - tok * a.grp, tile = tok / tt;
-    const int row = 128 * tile + (tok - tile * tt) * a.grp + h;
-    float top = -INFINITY, den = 0.f, num[V];
+  if (r >= m.ntok * a.grp) return;
+  const int tt = kTile / a.grp, tok = r / a.grp, h = r - tok * a.grp, tile = tok / tt;
+  const int row = 128 * tile + (tok - tile * tt) * a.grp + h;
+  float top = -INFINITY, den = 0.f;
+  float4 num[2] = {};
+  for (int i0 = 0; i0 < parts; i0 += kBatch) {
+    float ref[kBatch], l[kBatch];
+    float4 o[kBatch][2];
 #pragma unroll
-    for (int v = 0; v < V; v++) num[v] = 0.f;
-    for (int i0 = 0; i0 < parts; i0 += kBatch) {
-      float ref[kBatch], l[kBatch], o[kBatch][V];
+    for (int u = 0; u < kBatch; u++) {
+      ref[u] = -INFINITY, l[u] = 0.f;
+      o[u][0] = o[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i0 + u < parts) {
+        const float* d = ws.data + (i0 + u ? 2 * (c + i0 + u) : 2 * c + 1) * slot_floats(D);
+        ref[u] = d[256 * D + row], l[u] = d[256 * D + 256 + row];
 #pragma unroll
-      for (int u = 0; u < kBatch; u++) {
-        ref[u] = -INFINITY, l[u] = 0.f;
-#pragma unroll
-        for (int v = 0; v < V; v++) o[u][v] = 0.f;
-        if (i0 + u < parts) {
-          const float* d = ws.data + (i0 + u ? 2 * (c + i0 + u) : 2 * c + 1) * slot_floats(D);
-          ref[u] = d[256 * D + row], l[u] = d[256 * D + 256 + row];
-#pragma unroll
-          for (int v = 0; v < V; v++) o[u][v] = d[(size_t)row * D + 32 * v + lane];
-        }
+        for (int v = 0; v < 2; v++) o[u][v] = ((const float4*)d)[(c4 + 4 * v) * 256 + row];
       }
-      float high = top;
+    }
+    float high = top;
 #pragma unroll
-      for (int u = 0; u < kBatch; u++) high = fmaxf(high, ref[u]);
-      if (high == -INFINITY) continue;
-      const float keep = top == high ? 1.f : tc_ex2(top - high);
-      den = keep == 0.f ? 0.f : den * keep;
+    for (int u = 0; u < kBatch; u++) high = fmaxf(high, ref[u]);
+    if (high == -INFINITY) continue;
+    const float keep = top == high ? 1.f : tc_ex2(top - high);
+    if (keep == 0.f) den = 0.f, num[0] = num[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+    den *= keep;
 #pragma unroll
-      for (int v = 0; v < V; v++) num[v] = keep == 0.f ? 0.f : num[v] * keep;
+    for (int v = 0; v < 2; v++) num[v].x *= keep, num[v].y *= keep, num[v].z *= keep, num[v].w *= keep;
 #pragma unroll
-      for (int u = 0; u < kBatch; u++) {
-        const float w = ref[u] == high ? 1.f : tc_ex2(ref[u] - high);
-        if (w == 0.f) continue;            // nothing of it is left, whatever it holds
-        den = fmaf(l[u], w, den);
+    for (int u = 0; u < kBatch; u++) {
+      const float w = ref[u] == high ? 1.f : tc_ex2(ref[u] - high);
+      if (w == 0.f) continue;            // nothing of it is left, whatever it holds
+      den = fmaf(l[u], w, den);
 #pragma unroll
-        for (int v = 0; v < V; v++) num[v] = fmaf(o[u][v], w, num[v]);
+      for (int v = 0; v < 2; v++) {
+        num[v].x = fmaf(o[u][v].x, w, num[v].x), num[v].y = fmaf(o[u][v].y, w, num[v].y);
+        num[v].z = fmaf(o[u][v].z, w, num[v].z), num[v].w = fmaf(o[u][v].w, w, num[v].w);
       }
-      top = high;
     }
-    const int64_t token = m.tok0 + tok;
-    const int head = m.head * a.grp + h;
-    const bool sees = (m.flags & kCausal ? m.lim + tok : m.lim) > m.kbeg;
-#pragma unroll
-    for (int v = 0; v < V; v++) num[v] = nan ? NAN : sees ? num[v] / den : 0.f;
-    if (a.groups) {
-      const size_t at = ((m.flags & kPrefix ? 0 : (size_t)a.total_q) + token) * a.hq + head;
-#pragma unroll
-      for (int v = 0; v < V; v++) ws.part_o[at * D + 32 * v + lane] = num[v];
-      if (lane == 0) ws.part_m[at] = nan ? NAN : !sees ? -INFINITY : top == -FLT_MAX ? top : top + log2f(den);
-    } else {
-      uint16_t* out = a.out + token * a.out_stride + (int64_t)head * D;
-#pragma unroll
-      for (int v = 0; v < V; v++) out[32 * v + lane] = f2bf(num[v]);
-    }
+    top = high;
   }
+  const int64_t token = m.tok0 + tok;
+  const int head = m.head * a.grp + h;
+  const bool sees = (m.flags & kCausal ? m.lim + tok : m.lim) > m.kbeg;
+  const float inv = 1.f / den;
+  const size_t at = ((m.flags & kPrefix ? 0 : (size_t)a.total_q) + token) * a.hq + head;
+#pragma unroll
+  for (int v = 0; v < 2; v++) {
+    float4 o = make_float4(num[v].x * inv, num[v].y * inv, num[v].z * inv, num[v].w * inv);
+    if (!sees) o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (nan || (sees && den == 0.f)) o = make_float4(NAN, NAN, NAN, NAN);
+    const int d = 4 * (c4 + 4 * v);
+    if (a.groups) *(float4*)(ws.part_o + at * D + d) = o;
+    else *(uint2*)(a.out + token * a.out_stride + (int64_t)head * D + d) = make_uint2(cvt_bf2(o.x, o.y), cvt_bf2(o.z, o.w));
+  }
+  if (a.groups && c4 == 0) ws.part_m[at] = nan ? NAN : !sees ? -INFINITY : top == -FLT_MAX ? top : top + log2f(den);
 }
 
 // Groups: a row's common and own keys together
@@ -762,7 +879,9 @@ int launch(const KvAttnArgs& a, int sms, cudaStream_t st) {
       !make_map(&mk_, a.k_pool, D, (uint64_t)a.hkv * kKvPage, a.num_pages, D, page, kKvPage, 1) ||
       !make_map(&mv, a.v_pool, D, (uint64_t)a.hkv * kKvPage, a.num_pages, D, page, kKvPage, 1))
     return MK_ERR_CUDA;
-  kv_attention_kernel<D><<<sms, kThreads, Shape<D>::kSmem, st>>>(a, mq, mk_, mv);
+  KvAttnArgs b = a;
+  b.per_block = ~0ull / (unsigned)sms;
+  kv_attention_kernel<D><<<sms, kThreads, Shape<D>::kSmem, st>>>(b, mq, mk_, mv);
   int rc = launched(cudaGetLastError());
   if (rc) return rc;
   // the next kernels are launched while the one before runs, and wait for its end
@@ -772,7 +891,7 @@ int launch(const KvAttnArgs& a, int sms, cudaStream_t st) {
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.stream = st, cfg.attrs = &at, cfg.numAttrs = 1;
   cfg.blockDim = dim3(256);
-  cfg.gridDim = dim3(sms, kMergeRows);
+  cfg.gridDim = dim3(sms, D / 8);       // 256 rows: 32 groups of 8 rows, D / 32 of dims, 8 warps a block
   rc = launched(cudaLaunchKernelEx(&cfg, kv_merge_kernel<D>, a));
   if (rc || !a.groups) return rc;
   cfg.gridDim = dim3((unsigned)std::min<long long>(8 * sms, ((long long)a.total_q * a.hq + 7) / 8));

@@ -16,9 +16,13 @@
 namespace mk {
 
 constexpr int kTile = 128;               // keys a step, rows a tile
-constexpr int kStart = 3;                // an item's start and end, in key tiles
-constexpr int kMinShare = 4;             // no block takes less (in the same units)
-constexpr int kMinPart = 2;              // no part of an item has fewer key tiles
+
+// Cost of a row block, in units: kWide a key where its rows fill two tiles,
+// kNarrow where they fill one, and its start and end.
+constexpr int kWide = 4, kNarrow = 3;
+constexpr int kStart = 3 * kTile * kWide;
+constexpr int kMinShare = 4 * kTile * kWide;      // no block takes less
+constexpr int kMinPart = 2;                       // no part of an item has fewer key tiles
 
 enum : int { kCausal = 1, kNan = 2, kPrefix = 4 };
 
@@ -108,50 +112,82 @@ MK_HD inline int block_tiles(const Task& k, int b, int tb) {
   return (block_end(k, b, tb) - k.kbeg + kTile - 1) / kTile;
 }
 
-// sum over i < n of floor((a i + b) / m), by Euclid's steps on (a, m)
-MK_HD inline long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
-  long long s = 0;
-  while (n) {
-    if (a >= m) s += (long long)n * (n - 1) / 2 * (a / m), a %= m;
-    if (b >= m) s += (long long)n * (b / m), b %= m;
-    const unsigned y = a * n + b;
-    if (y < m) break;
-    n = y / m, b = y % m;
-    const unsigned t = a;
-    a = m, m = t;
-  }
-  return s;
+// units a key of row block b: all but a task's last have two tiles of rows
+MK_HD inline int block_rate(const Task& k, int b, int tb) {
+  return b < k.nb - 1 || 2 * (k.ntok - b * tb) > tb ? kWide : kNarrow;
 }
 
-// key tiles of the row blocks before b, b <= nb
-MK_HD inline long long tiles_before(const Task& k, int b, int tb) {
-  if (k.flags & kNan || b == 0) return 0;
-  if (!(k.flags & kCausal)) return (long long)b * block_tiles(k, 0, tb);
-  long long s = b == k.nb ? block_tiles(k, b - 1, tb) : 0;
-  const int full = hd_min(b, k.nb - 1);
-  if (full <= 4) {
-    for (int i = 0; i < full; i++) s += block_tiles(k, i, tb);
-    return s;
-  }
-  const int base = k.c0 - k.kbeg;                        // block i: ceil((base + tb (i + 1)) / 128) if positive
-  const int skip = base >= 0 ? 0 : hd_min(full, -base / tb);
-  return s + floor_sum(full - skip, kTile, tb, base + tb * (skip + 1) + kTile - 1);
-}
-
+// cost of the row blocks before b, b <= nb
 MK_HD inline long long cost_before(const Task& k, int b, int tb) {
-  return tiles_before(k, b, tb) + (long long)b * kStart;
+  if (b == 0) return 0;
+  const int full = hd_min(b, k.nb - 1);
+  long long keys = 0;
+  if (full > 0) {
+    if (k.flags & kCausal && !(k.flags & kNan)) {      // the sum of base + tb (i + 1) where that is positive
+      const int base = k.c0 - k.kbeg, skip = base >= 0 ? 0 : hd_min(full, -base / tb);
+      keys = (long long)(full - skip) * base +
+             ((long long)full * (full + 1) - (long long)skip * (skip + 1)) / 2 * tb;
+    } else if (!(k.flags & kNan)) {
+      keys = (long long)full * (k.kend - k.kbeg);
+    }
+  }
+  long long cost = keys * kWide + (long long)b * kStart;
+  if (b > full) cost += (long long)(block_end(k, b - 1, tb) - k.kbeg) * block_rate(k, b - 1, tb);
+  return cost;
 }
 
-// Where a border x units into an item of n tiles cuts it: the same for the
+// Where a border x units into an item of n key tiles cuts it: the same for the
 // block before and the block after.
-MK_HD inline int cut(long long x, int n) {
-  int k = (int)hd_min(x, (long long)n);
+MK_HD inline int cut(long long x, int rate, int n) {
+  static_assert(kTile * kWide == 512 && kTile * kNarrow == 384, "units of a tile");
+  int k = rate == kWide ? (int)((x + 256) >> 9) : (int)((unsigned)((x + 192) >> 7) / 3);
   if (k < kMinPart) k = 0;
   return n - k < kMinPart ? n : k;
 }
 
-// The parts of one block: its stretch [pos, stop) of all items laid end to end,
-// from task t, which begins at `at`.  On the GPU a warp walks it together.
+// floor(x / y) of 0 <= x, 0 < y whose quotient is small: a float's guess, put right
+MK_HD inline int quotient(long long x, long long y) {
+  int q = (int)((float)x / (float)y);
+  while (q > 0 && q * y > x) q--;
+  while ((q + 1) * y <= x) q++;
+  return q;
+}
+
+// Where a block begins: in row block b of KV head `head` of task t, whose items
+// begin at `at`.
+struct Begin {
+  Task k;
+  int t, head, b;
+  long long at;
+};
+
+// The item that holds position r of task k, which begins at `start`.  On the
+// GPU a warp finds it together.
+MK_HD inline Begin begin_of(const Task& k, int t, int tb, long long start, long long pos, int lane) {
+  Begin g{k, t, 0, 0, start};
+  const long long per = cost_before(k, k.nb, tb);
+  g.head = quotient(pos - start, per);
+  const long long r = pos - start - g.head * per;
+  int lo = 0, hi = k.nb;                 // the last row block that begins at or before pos
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+#ifdef __CUDA_ARCH__
+    const int c = lo + step * lane;
+    const int n = __popc(__ballot_sync(0xffffffffu, c < hi && cost_before(k, c, tb) <= r));
+#else
+    int n = 0;
+    for (int i = 0; i < 32; i++) n += lo + step * i < hi && cost_before(k, lo + step * i, tb) <= r;
+#endif
+    lo += step * (n - 1);
+    hi = hd_min(hi, lo + step);
+  }
+  g.b = lo;
+  g.at = start + g.head * per + cost_before(k, lo, tb);
+  return g;
+}
+
+// The parts of one block: its stretch [pos, stop) of all items laid end to end.
+// On the GPU a warp walks it together.
 struct Stretch {
   const KvAttnArgs& a;
   const int tb;
@@ -160,39 +196,20 @@ struct Stretch {
   const long long pos, stop;
   Task k;
 
-  MK_HD Stretch(const KvAttnArgs& args, int tt, int task, long long start, long long pos, long long stop, int lane)
-      : a(args), tb(2 * tt), t(task), at(start), pos(pos), stop(stop) {
-    k = load_task(a, t, tb, false);
-    const long long per = cost_before(k, k.nb, tb);
-    head = (int)((pos - at) / per);
-    const long long r = pos - at - head * per;
-    int lo = 0, hi = k.nb;               // the last row block that begins at or before pos
-    while (hi - lo > 1) {
-#ifdef __CUDA_ARCH__
-      const int step = (hi - lo + 31) / 32, c = lo + step * lane;
-      const int n = __popc(__ballot_sync(0xffffffffu, c < hi && cost_before(k, c, tb) <= r));
-#else
-      const int step = (hi - lo + 31) / 32;
-      int n = 0;
-      for (int i = 0; i < 32; i++) n += lo + step * i < hi && cost_before(k, lo + step * i, tb) <= r;
-#endif
-      lo += step * (n - 1);
-      hi = hd_min(hi, lo + step);
-    }
-    b = lo;
-    at += head * per + cost_before(k, b, tb);
-  }
+  MK_HD Stretch(const KvAttnArgs& args, int tt, const Begin& g, long long pos, long long stop)
+      : a(args), tb(2 * tt), t(g.t), head(g.head), b(g.b), at(g.at), pos(pos), stop(stop), k(g.k) {}
 
   // the next part with anything to do; slots 2 c and 2 c + 1 are the block's
   MK_HD bool next(Part* m, int slot) {
     while (t < a.groups + a.batch && at < stop) {
-      const int n = block_tiles(k, b, tb), len = n + kStart;
-      const int k0 = at < pos ? cut(pos - at, n) : 0, k1 = at + len <= stop ? n : cut(stop - at, n);
+      const int end = block_end(k, b, tb), n = (end - k.kbeg + kTile - 1) / kTile, rate = block_rate(k, b, tb);
+      const long long len = (long long)(end - k.kbeg) * rate + kStart;
+      const int k0 = at < pos ? cut(pos - at, rate, n) : 0, k1 = at + len <= stop ? n : cut(stop - at, rate, n);
       const bool some = k1 > k0 || (n == 0 && at >= pos);
       if (some) {
         m->tok0 = k.tok0 + b * tb, m->ntok = hd_min(tb, k.ntok - b * tb);
         m->head = head, m->table = k.table;
-        m->kbeg = k.kbeg, m->kend = block_end(k, b, tb);
+        m->kbeg = k.kbeg, m->kend = end;
         m->lim = k.flags & kCausal ? k.c0 + b * tb + 1 : k.kend;
         m->k0 = k0, m->k1 = k1, m->n = n, m->flags = k.flags;
         m->slot = k0 == 0 && k1 == n ? -1 : slot + (k0 == 0);

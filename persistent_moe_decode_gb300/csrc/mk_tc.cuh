@@ -18,6 +18,13 @@ __device__ __forceinline__ uint64_t tc_desc(uint32_t smem, uint32_t lead = 16) {
          2ull << 61;
 }
 
+// one lane of a converged warp
+__device__ __forceinline__ bool tc_elect() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // kind::f16 instruction descriptor: fp32 accumulator, BF16 operands, M 128,
 // B K-major or (b_mn) MN-major
 __host__ __device__ constexpr uint32_t tc_idesc(int n, bool b_mn) {
@@ -105,6 +112,24 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, int x
           dst),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
+}
+
+// true once the phase of this parity has completed; may suspend the thread for a
+// while instead of answering at once
+__device__ __forceinline__ bool mbar_wait_some(uint64_t* b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(b)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+__device__ __forceinline__ void tma_prefetch_map(const void* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
 }  // namespace mk

@@ -34,11 +34,12 @@ static void walk(const KvAttnArgs& a, int blocks, bool sound) {
     CHECK(k.ntok >= 0 && k.tok0 >= 0 && (k.ntok == 0 || k.tok0 + k.ntok <= a.total_q));
     long long n = 0;
     for (int b = 0; b < k.nb; b++) {
-      if (k.nb < 300) CHECK(tiles_before(k, b, tb) == n);
-      n += block_tiles(k, b, tb);
+      CHECK(cost_before(k, b, tb) == n);
+      n += (long long)(block_end(k, b, tb) - k.kbeg) * block_rate(k, b, tb) + kStart;
+      CHECK(block_rate(k, b, tb) == (std::min(tb, k.ntok - b * tb) > tt ? kWide : kNarrow));
     }
-    CHECK(tiles_before(k, k.nb, tb) == n);
-    at[t + 1] = at[t] + (n + (long long)k.nb * kStart) * a.hkv;
+    CHECK(cost_before(k, k.nb, tb) == n);
+    at[t + 1] = at[t] + n * a.hkv;
   }
   const long long total = at[tasks], share = std::max((total + blocks - 1) / blocks, (long long)kMinShare);
   // (tok0, head, prefix) of an item -> its tiles taken so far
@@ -53,9 +54,11 @@ static void walk(const KvAttnArgs& a, int blocks, bool sound) {
     }
     int t = 0;
     while (!(at[t] <= pos && pos < at[t + 1])) t++;
-    Stretch w(a, tt, t, at[t], pos, stop, 0);
+    const Task k = load_task(a, t, tb, false);
+    Stretch w(a, tt, begin_of(k, t, tb, at[t], pos, 0), pos, stop);
     Part m;
-    int units = 0, used[2] = {0, 0};
+    long long units = 0;
+    int used[2] = {0, 0};
     bool first = true, leaves = false;
     while (w.next(&m, 2 * c)) {
       CHECK(!leaves);                            // what is left open is the last
@@ -76,10 +79,10 @@ static void walk(const KvAttnArgs& a, int blocks, bool sound) {
       if (first && open) CHECK(m.k0 > 0);
       if (leaves) open_key = key;
       first = false;
-      units += m.k1 - m.k0 + kStart;
+      units += (long long)(std::min(kTile * m.k1, m.kend - m.kbeg) - kTile * m.k0) * (m.ntok > tt ? kWide : kNarrow) + kStart;
     }
     open = leaves;
-    CHECK(units <= share + 2 * kStart + 2 * kMinPart);
+    CHECK(units <= share + 2 * kStart + (2 * kMinPart + 2) * kTile * kWide);
   }
   CHECK(!open);
   if (!sound) return;

@@ -169,8 +169,13 @@ __device__ void softmax_role(const KvAttnArgs& a, Sync& s, Item* items, const Ws
       const int t0 = m.kbeg + kTile * j;
       if (t0 + kTile > least) {
         const int seen = lim - t0;
+        if (narrow && D == 128) {            // first 8 keys of all pages, then the last 8
 #pragma unroll
-        for (int c = 0; c < kTile; c++) x[c] = c < seen ? x[c] : -INFINITY;
+          for (int c = 0; c < kTile; c++) x[c] = c % 64 / 8 * 16 + c / 64 * 8 + c % 8 < seen ? x[c] : -INFINITY;
+        } else {
+#pragma unroll
+          for (int c = 0; c < kTile; c++) x[c] = c < seen ? x[c] : -INFINITY;
+        }
       }
       float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
@@ -329,7 +334,8 @@ __device__ void softmax_role(const KvAttnArgs& a, Sync& s, Item* items, const Ws
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     kv_attention_kernel(const KvAttnArgs a, const __grid_constant__ CUtensorMap map_q,
-                        const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
+                        const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap page_k,
+                        const __grid_constant__ CUtensorMap page_v) {
   using S = Shape<D>;
   extern __shared__ uint8_t raw_smem[];
   __shared__ Sync s;
@@ -339,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tt = kTile / a.grp, tb = 2 * tt, tasks = a.groups + a.batch;
   const Ws ws = ws_of(a.ws, D, a.hq, a.total_q, gridDim.x);
 
-  if (tid == 0) {
+  if (tid == kThreads - 32) {
     for (int i = 0; i < S::kStages; i++) mbar_init(&s.kv_full[i], 1), mbar_init(&s.kv_empty[i], 2), mbar_init(&s.raw_full[i], 1);
     for (int t = 0; t < 2; t++) {
       mbar_init(&s.q_full[t], 1), mbar_init(&s.q_empty[t], t ? 1 : 2), mbar_init(&s.s_full[t], 1);
@@ -352,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 8) tc_alloc(&s.tmem, 512);
 
-  if (warp == 11 && lane < 3) tma_prefetch_map(lane == 0 ? &map_k : lane == 1 ? &map_v : &map_q);
+  if (warp == 10 && lane < 4) tma_prefetch_map(lane == 0 ? &map_k : lane == 1 ? &page_v : lane == 2 ? &map_q : &page_k);
 
   // all tasks' cost, and the item that this block's stretch begins in
   const int chunk = tasks <= kThreads ? 1 : (tasks + kThreads - 1) / kThreads;
@@ -438,8 +444,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           it++;
           bool bad = false;
+          const bool narrow = m.ntok <= tt;
           const int clear = (m.flags & kCausal ? m.lim : m.kend) - m.kbeg;
-          auto load = [&](const CUtensorMap& map, int j, int pg, bool value) {
+          auto load = [&](bool value, int j, int pg) {
             const uint32_t st = loads % S::kStages;
             if (!wait_warp(s, &s.kv_empty[st], ((loads / S::kStages) & 1) ^ 1, a.status)) return false;
             const int np = pages_of(m, j);
@@ -457,34 +464,46 @@ __global__ void __launch_bounds__(kThreads, 1)
             int ids[8];
 #pragma unroll
             for (int i = 0; i < 8; i++) ids[i] = __shfl_sync(0xffffffffu, from, i);
-            // one lane issues: sixteen lanes at once took 2500 cycles a tile, each copy on its own
+            // One lane issues, about 60 cycles a copy (sixteen lanes at once: 150
+            // each), so whole pages where their layout serves: all but the keys
+            // of wide items, whose product wants 16 atoms at one stride.
             if (tc_elect()) {
+              const uint32_t to = kv_smem + st * S::kTileBytes;
               mbar_arrive_expect_tx(bar, np * S::kHalves * 2048);
+              if (value || narrow || S::kHalves == 1) {
+                const CUtensorMap* map = value ? &page_v : &page_k;
 #pragma unroll
-              for (int i = 0; i < 8; i++)
-                if (i < np)
+                for (int i = 0; i < 8; i++)
+                  if (i < np) tma_load_4d(to + i * S::kHalves * 2048, map, 0, kKvPage * m.head, 0, ids[i], bar);
+              } else {
 #pragma unroll
-                  for (int h = 0; h < S::kHalves; h++)
-                    tma_load_3d(kv_smem + st * S::kTileBytes + h * 16384 + i * 2048, &map, 64 * h, kKvPage * m.head, ids[i], bar);
+                for (int i = 0; i < 8; i++)
+                  if (i < np)
+#pragma unroll
+                    for (int h = 0; h < S::kHalves; h++)
+                      tma_load_3d(to + h * 16384 + i * 2048, &map_k, 64 * h, kKvPage * m.head, ids[i], bar);
+              }
             }
             __syncwarp();
             loads++;
             return true;
           };
           // in the order of their use: K of the first step (narrow: two), then V of one and K of a later one
-          const bool narrow = m.ntok <= tt;
-          ok = m.k1 == m.k0 || load(map_k, m.k0, page[0], false);
-          if (ok && narrow && m.k1 > m.k0 + 1) ok = load(map_k, m.k0 + 1, page[1], false);
-          // the next part and its first pages, while this one's copies are under way
-          const bool more = w.next(&nx, 2 * (int)blockIdx.x);
-          if (more)
-            for (int x = 0; x < 3; x++) npage[x] = page_of(nx, nx.k0 + x);
-          for (int j = m.k0; ok && j < m.k1; j++) {
+          ok = m.k1 == m.k0 || load(false, m.k0, page[0]);
+          if (ok && narrow && m.k1 > m.k0 + 1) ok = load(false, m.k0 + 1, page[1]);
+          bool more = false;
+          for (int j = m.k0; ok && (j < m.k1 || j == m.k0); j++) {
             const int later = page_of(m, j + 3);
-            ok = load(map_v, j, page[0], true);
-            if (ok && !narrow && j + 1 < m.k1) ok = load(map_k, j + 1, page[1], false);
-            if (ok && narrow && j + 2 < m.k1) ok = load(map_k, j + 2, page[2], false);
+            if (j < m.k1) ok = load(true, j, page[0]);
+            if (ok && !narrow && j + 1 < m.k1) ok = load(false, j + 1, page[1]);
+            if (ok && narrow && j + 2 < m.k1) ok = load(false, j + 2, page[2]);
             page[0] = page[1], page[1] = page[2], page[2] = later;
+            if (j == m.k0) {
+              // the next part and its first pages, while this one's copies are under way
+              more = w.next(&nx, 2 * (int)blockIdx.x);
+              if (more)
+                for (int x = 0; x < 3; x++) npage[x] = page_of(nx, nx.k0 + x);
+            }
           }
           if (m.slot >= 0)
             desc[m.k0 == 0] = Slot{m.k1 < m.n ? 1 : 2, m.tok0, m.ntok, m.head, m.kbeg, m.lim, m.flags, bad};
@@ -510,11 +529,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // one lane issues.  Wide items: stream t is a tile of rows, and each step's
       // K and V serve both.  Narrow ones: the streams take key tiles in turn.
       // Either way a warp sees every load of the ring, in order.
-      constexpr uint32_t idesc_s = tc_idesc(kTile, false), idesc_o = tc_idesc(D, true);
+      constexpr uint32_t idesc_s = tc_idesc(kTile, false), idesc_half = tc_idesc(64, false), idesc_o = tc_idesc(D, true);
       const int t = __shfl_sync(0xffffffffu, warp - 9, 0);
       uint32_t loads = 0, used_q[2] = {0, 0}, steps = 0, turns = 0;
       bool ok = true;
-      const uint64_t k_desc = tc_desc(kv_smem), v_desc = tc_desc(kv_smem, 16384);
       auto commit = [&](uint64_t* bar) {
         if (tc_elect()) tc_commit(bar);
         __syncwarp();
@@ -544,14 +562,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (n == 0) continue;
         const int tile = narrow ? 0 : t, every = narrow ? 2 : 1;
         const uint64_t q_desc = tc_desc(q_smem + tile * S::kTileBytes);
+        // Keys of a narrow item lie page by page, both halves of the dims in each:
+        // their atoms (8 keys) are 4096 apart, so S takes the first 8 keys of all
+        // pages, then the last 8 (two products of 64 keys), and the values follow
+        // that order.  Values of a wide item are taken page by page.
+        const bool paged = narrow && S::kHalves == 2;
+        const uint64_t k_desc = tc_desc(kv_smem, paged ? 4096 : 1024);
+        const uint64_t v_desc = tc_desc(kv_smem, paged ? 4096 : 1024, 2048);
         auto mine = [&](int j) { return !narrow || (j & 1) == t; };
         auto last = [&](int j) { return j + every >= n; };   // of this stream
         auto qk = [&](int j, uint32_t load) {                // one lane: S of key tile j
           const uint64_t kd = k_desc + load % S::kStages * (S::kTileBytes / 16);
+          if (paged) {
 #pragma unroll
-          for (int c = 0; c < D / 16; c++) {
-            const int off = (c / 4 * 16384 + c % 4 * 32) / 16;
-            tc_mma_ss(tmem + 128 * t, q_desc + off, kd + off, idesc_s, c > 0);
+            for (int h = 0; h < 2; h++)
+#pragma unroll
+              for (int c = 0; c < D / 16; c++)
+                tc_mma_ss(tmem + 128 * t + 64 * h, q_desc + (c / 4 * 16384 + c % 4 * 32) / 16,
+                          kd + (1024 * h + c / 4 * 2048 + c % 4 * 32) / 16, idesc_half, c > 0);
+          } else {
+#pragma unroll
+            for (int c = 0; c < D / 16; c++) {
+              const int off = (c / 4 * 16384 + c % 4 * 32) / 16;
+              tc_mma_ss(tmem + 128 * t, q_desc + off, kd + off, idesc_s, c > 0);
+            }
           }
           tc_commit(&s.s_full[t]);
           if (last(j)) tc_commit(&s.q_empty[tile]);
@@ -559,8 +593,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto pv = [&](int j, uint32_t load) {                // one lane: O of key tile j
           const uint64_t vd = v_desc + load % S::kStages * (S::kTileBytes / 16);
 #pragma unroll
-          for (int c = 0; c < kTile / 16; c++)
-            tc_mma_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * c, vd + c * (2048 / 16), idesc_o, j >= every || c > 0);
+          for (int c = 0; c < kTile / 16; c++) {
+            const int at = paged ? c % 4 * 8192 + c / 4 * 1024 : c * S::kHalves * 2048;
+            tc_mma_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * c, vd + at / 16, idesc_o, j >= every || c > 0);
+          }
           if (last(j)) tc_commit(&s.o_full[t]);
         };
         auto weights = [&] {
@@ -655,6 +691,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int lo = max(0, clear - kTile * j), held = min(kTile, m.kend - m.kbeg - kTile * j);
           bool found = false;
           // 16 bytes a lane, eight loads at a time: rows [lo, held) are looked over, those after them zeroed
+          auto chunk = [&](int c, int h) {           // 16 bytes c % 8 of half h of row c / 8
+            return (uint4*)(kv + st * S::kTileBytes + (c >> 7) * (S::kHalves * 2048) + h * 2048 + (c & 127) * 16);
+          };
           for (int c = 8 * lo + lane; c < 8 * held; c += 4 * 32) {
             uint4 w[4][S::kHalves];
 #pragma unroll
@@ -662,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int h = 0; h < S::kHalves; h++) {
                 w[u][h] = make_uint4(0, 0, 0, 0);
-                if (c + 32 * u < 8 * held) w[u][h] = *(const uint4*)(kv + st * S::kTileBytes + 16384 * h + 16 * (c + 32 * u));
+                if (c + 32 * u < 8 * held) w[u][h] = *chunk(c + 32 * u, h);
               }
 #pragma unroll
             for (int u = 0; u < 4; u++)
@@ -676,14 +715,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t b = not_finite(x[e]);
                     x[e] &= ~((b & 0x8000u ? 0xffffu : 0u) | (b & 0x80000000u ? 0xffff0000u : 0u));
                   }
-                  *(uint4*)(kv + st * S::kTileBytes + 16384 * h + 16 * (c + 32 * u)) = w[u][h];
+                  *chunk(c + 32 * u, h) = w[u][h];
                 }
               }
           }
           for (int c = 8 * max(held, 0) + lane; c < 8 * kTile; c += 32)
 #pragma unroll
-            for (int h = 0; h < S::kHalves; h++)
-              *(uint4*)(kv + st * S::kTileBytes + 16384 * h + 16 * c) = make_uint4(0, 0, 0, 0);
+            for (int h = 0; h < S::kHalves; h++) *chunk(c, h) = make_uint4(0, 0, 0, 0);
           if (found) ((volatile Item*)slot)->dirty = 1;
           fence_proxy_async_smem();
           __syncwarp();
@@ -840,15 +878,16 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return (PFN_cuTensorMapEncodeTiled_v12000)f;
 }
 
-// [n2][n1][D] BF16, rows of D elements at stride1 elements, planes at stride2;
-// boxes of 64 dims x box1 x box2
-bool make_map(CUtensorMap* map, const void* p, int d, uint64_t n1, uint64_t n2, uint64_t stride1, uint64_t stride2,
-              uint32_t box1, uint32_t box2) {
+// BF16 tensor of `rank` dims (innermost first; strides of the others in
+// elements), 128-byte swizzle
+bool make_map(CUtensorMap* map, const void* p, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+              const cuuint32_t* box) {
   auto enc = encoder();
   if (!enc) return false;
-  const cuuint64_t dims[3] = {(cuuint64_t)d, n1, n2}, strides[2] = {stride1 * 2, stride2 * 2};
-  const cuuint32_t box[3] = {64, box1, box2}, one[3] = {1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, one,
+  cuuint64_t bytes[3];
+  for (int i = 0; i < rank - 1; i++) bytes[i] = 2 * strides[i];
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(p), dims, bytes, box, one,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -872,16 +911,24 @@ int launch(const KvAttnArgs& a, int sms, cudaStream_t st) {
     }
     raised[dev / 64].fetch_or(1ull << (dev % 64), std::memory_order_relaxed);
   }
-  CUtensorMap mq, mk_, mv;
-  const uint64_t page = (uint64_t)a.hkv * kKvPage * D;
-  const uint64_t q_stride = a.total_q > 1 ? (uint64_t)a.q_stride : (uint64_t)a.hq * D;
-  if (!make_map(&mq, a.q, D, a.hq, a.total_q, D, q_stride, a.grp, kTile / a.grp) ||
-      !make_map(&mk_, a.k_pool, D, (uint64_t)a.hkv * kKvPage, a.num_pages, D, page, kKvPage, 1) ||
-      !make_map(&mv, a.v_pool, D, (uint64_t)a.hkv * kKvPage, a.num_pages, D, page, kKvPage, 1))
+  CUtensorMap map_q, map_k, page_k, page_v;
+  const cuuint64_t page = (cuuint64_t)a.hkv * kKvPage * D;
+  const cuuint64_t q_stride = a.total_q > 1 ? (cuuint64_t)a.q_stride : (cuuint64_t)a.hq * D;
+  // q: 64 dims of a group's heads of a tile's tokens; pools: 64 dims of a page
+  // of a head, and all its dims as halves of 64
+  const cuuint64_t q_dims[3] = {D, (cuuint64_t)a.hq, (cuuint64_t)a.total_q}, q_strides[2] = {D, q_stride};
+  const cuuint64_t k_dims[3] = {D, (cuuint64_t)a.hkv * kKvPage, (cuuint64_t)a.num_pages}, k_strides[2] = {D, page};
+  const cuuint64_t p_dims[4] = {64, (cuuint64_t)a.hkv * kKvPage, D / 64, (cuuint64_t)a.num_pages};
+  const cuuint64_t p_strides[3] = {D, 64, page};
+  const cuuint32_t q_box[3] = {64, (cuuint32_t)a.grp, (cuuint32_t)(kTile / a.grp)}, k_box[3] = {64, kKvPage, 1};
+  const cuuint32_t p_box[4] = {64, kKvPage, D / 64, 1};
+  if (!make_map(&map_q, a.q, 3, q_dims, q_strides, q_box) || !make_map(&map_k, a.k_pool, 3, k_dims, k_strides, k_box) ||
+      !make_map(&page_k, a.k_pool, 4, p_dims, p_strides, p_box) ||
+      !make_map(&page_v, a.v_pool, 4, p_dims, p_strides, p_box))
     return MK_ERR_CUDA;
   KvAttnArgs b = a;
   b.per_block = ~0ull / (unsigned)sms;
-  kv_attention_kernel<D><<<sms, kThreads, Shape<D>::kSmem, st>>>(b, mq, mk_, mv);
+  kv_attention_kernel<D><<<sms, kThreads, Shape<D>::kSmem, st>>>(b, map_q, map_k, page_k, page_v);
   int rc = launched(cudaGetLastError());
   if (rc) return rc;
   // the next kernels are launched while the one before runs, and wait for its end

@@ -9,12 +9,12 @@ namespace mk {
 
 // Shared-memory operand descriptor, 128-byte swizzle: start address, leading
 // and stride byte offsets in units of 16 bytes, version 1, swizzle mode 2.
-//   K-major   rows of 128 bytes (64 BF16 of K), eight rows an atom: stride 1024;
-//             the next 16 of K are 32 bytes on
+//   K-major   rows of 128 bytes (64 BF16 of K), eight rows an atom, `stride` from
+//             one atom to the next; the next 16 of K are 32 bytes on
 //   MN-major  rows of 128 bytes (64 BF16 of N) of one k each, eight k an atom:
-//             stride 1024 between atoms of k, `lead` between blocks of 64 of N
-__device__ __forceinline__ uint64_t tc_desc(uint32_t smem, uint32_t lead = 16) {
-  return (uint64_t)((smem & 0x3ffff) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 |
+//             `stride` between atoms of k, `lead` between blocks of 64 of N
+__device__ __forceinline__ uint64_t tc_desc(uint32_t smem, uint32_t stride = 1024, uint32_t lead = 16) {
+  return (uint64_t)((smem & 0x3ffff) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(stride >> 4) << 32 | 1ull << 46 |
          2ull << 61;
 }
 
@@ -111,6 +111,15 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, int x
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
           dst),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// 4-D
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, int x, int y, int z, int w, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+          dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
       : "memory");
 }
 

@@ -20,6 +20,7 @@ struct KvAttnArgs {
   int head_dim, hq, hkv, grp, total_q, batch, groups, max_pages, num_pages;
   float scale_log2;
   unsigned long long per_block;   // 2^64 / blocks of the grid, set by the launch
+  int aligned32;                  // out and its rows lie at 32 bytes, likewise
 };
 
 // workspace bytes on a device of `sms` multiprocessors

@@ -65,8 +65,10 @@ struct alignas(16) Slot {
 struct Ws {
   Slot* slots;             // [2 blocks]: 2 c the part that block c did not begin, 2 c + 1 that it did
   float* data;             // [2 blocks][kSlotFloats]
-  float* part_o;           // groups: [2][total_q][hq][D], common keys, own keys
-  float* part_m;           // [2][total_q][hq] log2 of the sum of exponentials
+  // groups: a row's sums over common keys and over own ones; line l of total_q *
+  // hq is (KV head, token, head of its group)
+  float* part_o;           // [2][D / 4][lines][4]
+  float* part_m;           // [2][lines] log2 of the sum of exponentials
 };
 
 __host__ __device__ __forceinline__ size_t slot_floats(int d) { return (size_t)256 * d + 512; }
@@ -264,9 +266,12 @@ __device__ void softmax_role(const KvAttnArgs& a, Sync& s, Item* items, const Ws
     const bool lost = nan || (sees && sum == 0.f);           // every score is -infinity
     const int64_t token = m.tok0 + tok;
     const int head = m.head * a.grp + my_head;
-    const size_t at = ((m.flags & kPrefix ? 0 : (size_t)a.total_q) + token) * a.hq + head;
+    const size_t lines = (size_t)a.total_q * a.hq, at = ((size_t)m.head * a.total_q + token) * a.grp + my_head;
+    const int own = m.flags & kPrefix ? 0 : 1, line = narrow ? row : 128 * group + row;
+    // four dims of all rows lie side by side: a warp writes 512 bytes
     float* data = ws.data + (whole ? 0 : m.slot) * slot_floats(D);
-    const int line = narrow ? row : 128 * group + row;
+    float4* quads = whole ? (float4*)ws.part_o + own * (D / 4) * lines + at : (float4*)data + line;
+    const size_t quad_step = whole ? lines : 256;
 #pragma unroll 1
     for (int c = 0; c < D; c += 32) {
       uint32_t r[32];
@@ -306,21 +311,19 @@ __device__ void softmax_role(const KvAttnArgs& a, Sync& s, Item* items, const Ws
         for (int u = 0; u < 32; u++) o[u] = lost ? NAN : o[u] * mul;
       }
       if (mine && whole && !parted) {
-        uint4* out = (uint4*)(a.out + token * a.out_stride + (int64_t)head * D + c);
+        uint32_t b[16];
 #pragma unroll
-        for (int u = 0; u < 4; u++)
-          out[u] = make_uint4(cvt_bf2(o[8 * u], o[8 * u + 1]), cvt_bf2(o[8 * u + 2], o[8 * u + 3]),
-                              cvt_bf2(o[8 * u + 4], o[8 * u + 5]), cvt_bf2(o[8 * u + 6], o[8 * u + 7]));
+        for (int u = 0; u < 16; u++) b[u] = cvt_bf2(o[2 * u], o[2 * u + 1]);
+        uint16_t* out = a.out + token * a.out_stride + (int64_t)head * D + c;
+        st_32(out, b, a.aligned32), st_32(out + 16, b + 8, a.aligned32);
       } else if (mine) {
-        // a part's slot holds four dims of all rows side by side: a warp writes 512 bytes
-        float4* out = whole ? (float4*)(ws.part_o + at * D + c) : (float4*)data + 64 * c + line;
 #pragma unroll
         for (int u = 0; u < 8; u++)
-          out[whole ? u : 256 * u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+          quads[(c / 4 + u) * quad_step] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
       }
-      __syncwarp();          // the next tensor memory load is the whole warp's
+      __syncwarp();        // the next tensor memory load is the whole warp's
     }
-    if (mine && whole && parted) ws.part_m[at] = nan ? NAN : ref == -INFINITY || ref == -FLT_MAX ? ref : ref + log2f(sum);
+    if (mine && whole && parted) ws.part_m[own * lines + at] = nan ? NAN : ref == -INFINITY || ref == -FLT_MAX ? ref : ref + log2f(sum);
     if (mine && !whole) data[256 * D + line] = ref, data[256 * D + 256 + line] = sum;
     tc_fence_before();       // O has been read before the next item's first P is announced
     __syncwarp();
@@ -813,51 +816,50 @@ __global__ void __launch_bounds__(256) kv_merge_kernel(const KvAttnArgs a) {
   const int head = m.head * a.grp + h;
   const bool sees = (m.flags & kCausal ? m.lim + tok : m.lim) > m.kbeg;
   const float inv = 1.f / den;
-  const size_t at = ((m.flags & kPrefix ? 0 : (size_t)a.total_q) + token) * a.hq + head;
+  const size_t lines = (size_t)a.total_q * a.hq, at = ((size_t)m.head * a.total_q + token) * a.grp + h;
+  const int own = m.flags & kPrefix ? 0 : 1;
 #pragma unroll
   for (int v = 0; v < 2; v++) {
     float4 o = make_float4(num[v].x * inv, num[v].y * inv, num[v].z * inv, num[v].w * inv);
     if (!sees) o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (nan || (sees && den == 0.f)) o = make_float4(NAN, NAN, NAN, NAN);
     const int d = 4 * (c4 + 4 * v);
-    if (a.groups) *(float4*)(ws.part_o + at * D + d) = o;
+    if (a.groups) ((float4*)ws.part_o)[(own * (D / 4) + d / 4) * lines + at] = o;
     else *(uint2*)(a.out + token * a.out_stride + (int64_t)head * D + d) = make_uint2(cvt_bf2(o.x, o.y), cvt_bf2(o.z, o.w));
   }
-  if (a.groups && c4 == 0) ws.part_m[at] = nan ? NAN : !sees ? -INFINITY : top == -FLT_MAX ? top : top + log2f(den);
+  if (a.groups && c4 == 0) ws.part_m[own * lines + at] = nan ? NAN : !sees ? -INFINITY : top == -FLT_MAX ? top : top + log2f(den);
 }
 
-// Groups: a row's common and own keys together
+// Groups: a row's common and own keys together.  A warp takes 8 lines and 32 of
+// their dims.
 template <int D>
 __global__ void __launch_bounds__(256) kv_join_kernel(const KvAttnArgs a, int blocks) {
-  constexpr int V = D / 32;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
   const Ws ws = ws_of(a.ws, D, a.hq, a.total_q, blocks);
-  const int t0 = max(0, a.q_starts[0]), t1 = min(a.total_q, a.q_starts[a.batch]);
-  const int64_t rows = (int64_t)a.total_q * a.hq;
-  for (int64_t r = (int64_t)t0 * a.hq + blockIdx.x * 8 + (threadIdx.x >> 5); r < (int64_t)t1 * a.hq; r += gridDim.x * 8) {
-    const float m0 = ws.part_m[r], m1 = ws.part_m[rows + r];
-    const float high = fmaxf(m0, m1);
-    float o[V];
-    if (m0 != m0 || m1 != m1) {
+  const int t0 = a.q_starts[0], t1 = a.q_starts[a.batch];
+  const int64_t lines = (int64_t)a.total_q * a.hq;
+  const float4* o = (const float4*)ws.part_o;
+  for (int64_t job = blockIdx.x * 8 + (threadIdx.x >> 5); job < (lines + 7) / 8 * (D / 32); job += gridDim.x * 8) {
+    const int64_t r = job / (D / 32) * 8 + (lane & 7);
+    const int c4 = (int)(job % (D / 32)) * 8 + (lane >> 3);
+    if (r >= lines) continue;
+    const int64_t per = (int64_t)a.total_q * a.grp;
+    const int kv = (int)(r / per), in = (int)(r - kv * per), token = in / a.grp, head = kv * a.grp + in % a.grp;
+    if (token < t0 || token >= t1) continue;               // of no sequence
+    const float m0 = ws.part_m[r], m1 = ws.part_m[lines + r], high = fmaxf(m0, m1);
+    const bool nan = m0 != m0 || m1 != m1, none = high == -INFINITY;
+    const float w0 = m0 == high ? 1.f : tc_ex2(m0 - high), w1 = m1 == high ? 1.f : tc_ex2(m1 - high), inv = 1.f / (w0 + w1);
 #pragma unroll
-      for (int v = 0; v < V; v++) o[v] = NAN;
-    } else if (high == -INFINITY) {
-#pragma unroll
-      for (int v = 0; v < V; v++) o[v] = 0.f;
-    } else {
-      const float w0 = m0 == high ? 1.f : tc_ex2(m0 - high), w1 = m1 == high ? 1.f : tc_ex2(m1 - high);
-      const float inv = 1.f / (w0 + w1);
-#pragma unroll
-      for (int v = 0; v < V; v++) {
-        const float x = w0 == 0.f ? 0.f : w0 * ws.part_o[r * D + 32 * v + lane];
-        const float y = w1 == 0.f ? 0.f : w1 * ws.part_o[(rows + r) * D + 32 * v + lane];
-        o[v] = (x + y) * inv;
-      }
+    for (int v = 0; v < 2; v++) {
+      const float4 x = o[(int64_t)(c4 + 4 * v) * lines + r], y = o[(int64_t)(D / 4 + c4 + 4 * v) * lines + r];
+      auto both = [&](float p, float q) {
+        const float s = (w0 == 0.f ? 0.f : w0 * p) + (w1 == 0.f ? 0.f : w1 * q);
+        return nan ? NAN : none ? 0.f : s * inv;
+      };
+      *(uint2*)(a.out + token * a.out_stride + (int64_t)head * D + 4 * (c4 + 4 * v)) =
+          make_uint2(cvt_bf2(both(x.x, y.x), both(x.y, y.y)), cvt_bf2(both(x.z, y.z), both(x.w, y.w)));
     }
-    uint16_t* out = a.out + r / a.hq * a.out_stride + r % a.hq * D;
-#pragma unroll
-    for (int v = 0; v < V; v++) out[32 * v + lane] = f2bf(o[v]);
   }
 }
 
@@ -928,6 +930,7 @@ int launch(const KvAttnArgs& a, int sms, cudaStream_t st) {
     return MK_ERR_CUDA;
   KvAttnArgs b = a;
   b.per_block = ~0ull / (unsigned)sms;
+  b.aligned32 = (((uintptr_t)a.out | 2 * (uintptr_t)a.out_stride) & 31) == 0;
   kv_attention_kernel<D><<<sms, kThreads, Shape<D>::kSmem, st>>>(b, map_q, map_k, page_k, page_v);
   int rc = launched(cudaGetLastError());
   if (rc) return rc;
@@ -941,7 +944,7 @@ int launch(const KvAttnArgs& a, int sms, cudaStream_t st) {
   cfg.gridDim = dim3(sms, D / 8);       // 256 rows: 32 groups of 8 rows, D / 32 of dims, 8 warps a block
   rc = launched(cudaLaunchKernelEx(&cfg, kv_merge_kernel<D>, a));
   if (rc || !a.groups) return rc;
-  cfg.gridDim = dim3((unsigned)std::min<long long>(8 * sms, ((long long)a.total_q * a.hq + 7) / 8));
+  cfg.gridDim = dim3((unsigned)std::min<long long>(8 * sms, ((long long)a.total_q * a.hq + 7) / 8 * (D / 32) / 8 + 1));
   return launched(cudaLaunchKernelEx(&cfg, kv_join_kernel<D>, a, sms));
 }
 

@@ -92,6 +92,17 @@ __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t* r) {
       : "memory");
 }
 
+// 32 bytes to global memory, one whole sector a lane, where the address allows
+__device__ __forceinline__ void st_32(void* p, const uint32_t* r, bool aligned) {
+  if (aligned)
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+                 "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+  else
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(r[0], r[1], r[2], r[3]),
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(r[4], r[5], r[6], r[7]);
+}
+
 // two fp32 -> a BF16 pair (lo in the low half), to nearest even
 __device__ __forceinline__ uint32_t cvt_bf2(float lo, float hi) {
   uint32_t d;

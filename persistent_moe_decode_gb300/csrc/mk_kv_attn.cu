@@ -88,7 +88,8 @@ struct Sync {
   uint64_t kv_full[10], kv_empty[10];
   uint64_t raw_full[10];                 // a tile that is cleared before it counts as full
   uint64_t q_full[2], q_empty[2], s_full[2], o_full[2];
-  uint64_t p_full[2], turn[2];           // weights are there; wide items: the other warp has issued its products
+  uint64_t p_full[2][2];                 // a stream's weights of the first, the last 64 columns
+  uint64_t turn[2];                      // wide items: the other warp has issued its products
   uint64_t pair_full, pair_empty;        // narrow items: the second warpgroup's sums are there, are read
   uint64_t item_full[kItems], item_empty[kItems];
   uint64_t drain[2];
@@ -221,11 +222,11 @@ __device__ void softmax_role(const KvAttnArgs& a, Sync& s, Item* items, const Ws
           p[u] = cvt_bf2(e.x, e.y);
         }
         tc_st32(tm_s + 32 * h, p);
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.p_full[group][h]);     // its product starts while the other half is made
       }
-      tc_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s.p_full[group]);
       sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
     }
     // -------------------------------------------------------------- the result
@@ -352,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < S::kStages; i++) mbar_init(&s.kv_full[i], 1), mbar_init(&s.kv_empty[i], 2), mbar_init(&s.raw_full[i], 1);
     for (int t = 0; t < 2; t++) {
       mbar_init(&s.q_full[t], 1), mbar_init(&s.q_empty[t], t ? 1 : 2), mbar_init(&s.s_full[t], 1);
-      mbar_init(&s.p_full[t], 4), mbar_init(&s.turn[t], 1), mbar_init(&s.o_full[t], 1);
+      mbar_init(&s.p_full[t][0], 4), mbar_init(&s.p_full[t][1], 4), mbar_init(&s.turn[t], 1), mbar_init(&s.o_full[t], 1);
     }
     for (int i = 0; i < kItems; i++) mbar_init(&s.item_full[i], 1), mbar_init(&s.item_empty[i], kReaders);
     mbar_init(&s.pair_full, 4), mbar_init(&s.pair_empty, 4), mbar_init(&s.drain[0], 1), mbar_init(&s.drain[1], 1);
@@ -593,19 +594,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_commit(&s.s_full[t]);
           if (last(j)) tc_commit(&s.q_empty[tile]);
         };
-        auto pv = [&](int j, uint32_t load) {                // one lane: O of key tile j
+        auto pv = [&](int j, uint32_t load) {                // O of key tile j, half by half
           const uint64_t vd = v_desc + load % S::kStages * (S::kTileBytes / 16);
+          const uint32_t par = steps++ & 1;
 #pragma unroll
-          for (int c = 0; c < kTile / 16; c++) {
-            const int at = paged ? c % 4 * 8192 + c / 4 * 1024 : c * S::kHalves * 2048;
-            tc_mma_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * c, vd + at / 16, idesc_o, j >= every || c > 0);
+          for (int h = 0; h < 2; h++) {
+            ok = ok && wait_warp(s, &s.p_full[t][h], par, a.status);
+            if (!ok) return;
+            tc_fence_after();
+            if (tc_elect()) {
+#pragma unroll
+              for (int c = 4 * h; c < 4 * h + 4; c++) {
+                const int at = paged ? c % 4 * 8192 + c / 4 * 1024 : c * S::kHalves * 2048;
+                tc_mma_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * c, vd + at / 16, idesc_o, j >= every || c > 0);
+              }
+              if (h == 1 && last(j)) tc_commit(&s.o_full[t]);
+            }
+            __syncwarp();
           }
-          if (last(j)) tc_commit(&s.o_full[t]);
-        };
-        auto weights = [&] {
-          ok = ok && wait_warp(s, &s.p_full[t], steps++ & 1, a.status);
-          tc_fence_after();
-          return ok;
         };
         ok = wait_warp(s, &s.q_full[0], used_q[0]++ & 1, a.status);
         if (ok && !narrow && t == 1) ok = wait_warp(s, &s.q_full[1], used_q[1]++ & 1, a.status);
@@ -623,12 +629,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           // other: in step with each other both softmaxes would run at once, and
           // then both products (32K prompt: 6.66 ms without turns).
           for (int j = 0; ok && j < n; j++) {
+            // all else first: the weights come last
             const bool more = j + 1 < n;
-            if (!full(loads) || !weights() || (more && !full(loads + 1))) break;
+            if (!full(loads) || (more && !full(loads + 1))) break;
             ok = wait_warp(s, &s.turn[t], (turns++ & 1) ^ (t == 0), a.status);
+            pv(j, loads);
             if (!ok) break;
             if (tc_elect()) {
-              pv(j, loads);
               tc_commit(&s.kv_empty[loads % S::kStages]);
               if (more) {
                 qk(j + 1, loads + 1);
@@ -641,9 +648,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         } else {
           for (int j = 0; ok && j < n; j++) {
-            if (!full(loads) || (mine(j) && !weights())) break;
-            if (mine(j) && tc_elect()) pv(j, loads);
-            __syncwarp();
+            if (!full(loads)) break;
+            if (mine(j)) pv(j, loads);
+            if (!ok) break;
             used(mine(j));
             if (j + 2 < n) {
               if (!full(loads)) break;

@@ -97,6 +97,7 @@ struct Sync {
   volatile int stop;
   long long scan[kThreads / 32];
   Begin begin;
+  long long pos, end, share;
   float pair[2][kTile];
   int work;                              // this block has a stretch
 };
@@ -349,6 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tt = kTile / a.grp, tb = 2 * tt, tasks = a.groups + a.batch;
   const Ws ws = ws_of(a.ws, D, a.hq, a.total_q, gridDim.x);
 
+  if (tid == 0) s.work = 0;
   if (tid == kThreads - 32) {
     for (int i = 0; i < S::kStages; i++) mbar_init(&s.kv_full[i], 1), mbar_init(&s.kv_empty[i], 2), mbar_init(&s.raw_full[i], 1);
     for (int t = 0; t < 2; t++) {
@@ -357,61 +359,69 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kItems; i++) mbar_init(&s.item_full[i], 1), mbar_init(&s.item_empty[i], kReaders);
     mbar_init(&s.pair_full, 4), mbar_init(&s.pair_empty, 4), mbar_init(&s.drain[0], 1), mbar_init(&s.drain[1], 1);
-    s.stop = 0, s.work = 0;
+    s.stop = 0;
     mbar_fence_init();
   }
   if (warp == 8) tc_alloc(&s.tmem, 512);
 
   if (warp == 10 && lane < 4) tma_prefetch_map(lane == 0 ? &map_k : lane == 1 ? &page_v : lane == 2 ? &map_q : &page_k);
 
-  // all tasks' cost, and the item that this block's stretch begins in
-  const int chunk = tasks <= kThreads ? 1 : (tasks + kThreads - 1) / kThreads;
+  // All tasks' cost, and the item that this block's stretch begins in.  Few
+  // tasks are one warp's work: the others need not be waited for.
+  const bool few = tasks <= 32;
+  const int chunk = few || tasks <= kThreads ? 1 : (tasks + kThreads - 1) / kThreads;
   const int first = min(tasks, tid * chunk), end = min(tasks, first + chunk);
-  long long mine = 0;
+  long long mine = 0, incl = 0;
   Task k{};
-  for (int t = first; t < end; t++) {
-    k = load_task(a, t, tb, blockIdx.x == 0);
-    mine += cost_before(k, k.nb, tb) * a.hkv;
-  }
-  long long incl = mine;
+  if (!few || warp == 0) {
+    for (int t = first; t < end; t++) {
+      k = load_task(a, t, tb, blockIdx.x == 0);
+      mine += cost_before(k, k.nb, tb) * a.hkv;
+    }
+    incl = mine;
 #pragma unroll
-  for (int x = 1; x < 32; x <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, incl, x);
-    if (lane >= x) incl += y;
+    for (int x = 1; x < 32; x <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, x);
+      if (lane >= x) incl += y;
+    }
   }
-  if (lane == 31) s.scan[warp] = incl;
+  long long before = incl - mine, total = __shfl_sync(0xffffffffu, incl, 31);
+  if (!few) {
+    if (lane == 31) s.scan[warp] = incl;
+    __syncthreads();
+    total = 0;
+    for (int w = 0; w < kThreads / 32; w++) {
+      const long long x = s.scan[w];
+      if (w < warp) before += x;
+      total += x;
+    }
+  }
+  if (!few || warp == 0) {
+    // about an equal share: total / blocks, from above
+    const long long share = max((long long)__umul64hi((unsigned long long)total, a.per_block) + 1, (long long)kMinShare);
+    const long long pos = share * blockIdx.x;
+    const bool owner = pos < total && before <= pos && pos < before + mine;
+    if (__any_sync(0xffffffffu, owner)) {        // the warp that found the task finds the item
+      int t = first;
+      if (owner && chunk > 1)
+        for (; t < end; t++) {
+          k = load_task(a, t, tb, false);
+          const long long c = cost_before(k, k.nb, tb) * a.hkv;
+          if (pos < before + c) break;
+          before += c;
+        }
+      const int from = __ffs(__ballot_sync(0xffffffffu, owner)) - 1;
+      Task o;
+#pragma unroll
+      for (int w = 0; w < (int)(sizeof(Task) / 4); w++)
+        reinterpret_cast<int*>(&o)[w] = __shfl_sync(0xffffffffu, reinterpret_cast<const int*>(&k)[w], from);
+      const Begin g = begin_of(o, __shfl_sync(0xffffffffu, t, from), tb, __shfl_sync(0xffffffffu, before, from), pos, lane);
+      if (lane == 0) s.begin = g, s.pos = pos, s.end = min(total, pos + share), s.share = share, s.work = 1;
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  long long before = incl - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; w++) {
-    const long long x = s.scan[w];
-    if (w < warp) before += x;
-    total += x;
-  }
-  // about an equal share: total / blocks, from above
-  const long long share = max((long long)__umul64hi((unsigned long long)total, a.per_block) + 1, (long long)kMinShare);
-  const long long pos = share * blockIdx.x, stop = min(total, pos + share);
-  const bool owner = pos < total && before <= pos && pos < before + mine;
-  if (__any_sync(0xffffffffu, owner)) {          // the warp that found the task finds the item
-    int t = first;
-    if (owner && chunk > 1)
-      for (; t < end; t++) {
-        k = load_task(a, t, tb, false);
-        const long long c = cost_before(k, k.nb, tb) * a.hkv;
-        if (pos < before + c) break;
-        before += c;
-      }
-    const int from = __ffs(__ballot_sync(0xffffffffu, owner)) - 1;
-    Task o;
-#pragma unroll
-    for (int w = 0; w < (int)(sizeof(Task) / 4); w++)
-      reinterpret_cast<int*>(&o)[w] = __shfl_sync(0xffffffffu, reinterpret_cast<const int*>(&k)[w], from);
-    const Begin g = begin_of(o, __shfl_sync(0xffffffffu, t, from), tb, __shfl_sync(0xffffffffu, before, from), pos, lane);
-    if (lane == 0) s.begin = g, s.work = 1;
-  }
-  __syncthreads();
   const uint32_t tmem = s.tmem;
 
   if (warp < 8) {
@@ -431,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           return j < p.k1 && lane < pages_of(p, j)
                      ? a.page_tables[(int64_t)p.table * a.max_pages + p.kbeg / kKvPage + 8 * j + lane] : 0;
         };
-        Stretch w(a, tt, s.begin, pos, stop);
+        Stretch w(a, tt, s.begin, s.pos, s.end, s.share);
         Part m, nx;
         bool have = w.next(&m, 2 * (int)blockIdx.x);
         int page[3], npage[3] = {0, 0, 0};
@@ -758,8 +768,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Adds up an item's parts in key order: block c's item, if it goes on, and the
 // first slots of the blocks after it.  A warp takes 8 rows and 32 of their dims.
 template <int D>
-__global__ void __launch_bounds__(256) kv_merge_kernel(const KvAttnArgs a) {
-  constexpr int kBatch = 8;
+__global__ void __launch_bounds__(256, 4) kv_merge_kernel(const KvAttnArgs a) {
+  constexpr int kBatch = 4;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x, blocks = gridDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Ws ws = ws_of(a.ws, D, a.hq, a.total_q, blocks);

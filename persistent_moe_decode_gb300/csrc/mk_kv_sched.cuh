@@ -18,11 +18,14 @@ namespace mk {
 constexpr int kTile = 128;               // keys a step, rows a tile
 
 // Cost of a row block, in units: kWide a key where its rows fill two tiles,
-// kNarrow where they fill one, and its start and end.
+// kNarrow where they fit one, and its start and end, about 5 key tiles
+// (10,000 and 8,000 cycles beside 2,300 and 1,800 a tile).
 constexpr int kWide = 4, kNarrow = 3;
-constexpr int kStart = 3 * kTile * kWide;
+constexpr int kWideStart = 5 * kTile * kWide, kNarrowStart = 5 * kTile * kNarrow;
 constexpr int kMinShare = 4 * kTile * kWide;      // no block takes less
-constexpr int kMinPart = 2;                       // no part of an item has fewer key tiles
+// No part of an item has fewer key tiles: a part costs an end and its share of
+// the merge, so that a wide one of less is better left where it is.
+constexpr int kMinWidePart = 6, kMinPart = 2;
 
 enum : int { kCausal = 1, kNan = 2, kPrefix = 4 };
 
@@ -117,6 +120,8 @@ MK_HD inline int block_rate(const Task& k, int b, int tb) {
   return b < k.nb - 1 || 2 * (k.ntok - b * tb) > tb ? kWide : kNarrow;
 }
 
+MK_HD inline int start_cost(int rate) { return rate == kWide ? kWideStart : kNarrowStart; }
+
 // cost of the row blocks before b, b <= nb
 MK_HD inline long long cost_before(const Task& k, int b, int tb) {
   if (b == 0) return 0;
@@ -131,18 +136,22 @@ MK_HD inline long long cost_before(const Task& k, int b, int tb) {
       keys = (long long)full * (k.kend - k.kbeg);
     }
   }
-  long long cost = keys * kWide + (long long)b * kStart;
-  if (b > full) cost += (long long)(block_end(k, b - 1, tb) - k.kbeg) * block_rate(k, b - 1, tb);
+  long long cost = keys * kWide + (long long)full * kWideStart;
+  if (b > full) {
+    const int rate = block_rate(k, b - 1, tb);
+    cost += (long long)(block_end(k, b - 1, tb) - k.kbeg) * rate + start_cost(rate);
+  }
   return cost;
 }
 
 // Where a border x units into an item of n key tiles cuts it: the same for the
-// block before and the block after.
-MK_HD inline int cut(long long x, int rate, int n) {
+// block before and the block after.  Small shares are cut as they fall.
+MK_HD inline int cut(long long x, int rate, int n, long long share) {
   static_assert(kTile * kWide == 512 && kTile * kNarrow == 384, "units of a tile");
   int k = rate == kWide ? (int)((x + 256) >> 9) : (int)((unsigned)((x + 192) >> 7) / 3);
-  if (k < kMinPart) k = 0;
-  return n - k < kMinPart ? n : k;
+  const int least = rate == kWide ? (int)hd_max(hd_min(share >> 12, (long long)kMinWidePart), (long long)kMinPart) : kMinPart;
+  if (k < least) k = 0;
+  return n - k < least ? n : k;
 }
 
 // floor(x / y) of 0 <= x, 0 < y whose quotient is small: a float's guess, put right
@@ -193,18 +202,19 @@ struct Stretch {
   const int tb;
   int t, head, b;
   long long at;
-  const long long pos, stop;
+  const long long pos, stop, share;
   Task k;
 
-  MK_HD Stretch(const KvAttnArgs& args, int tt, const Begin& g, long long pos, long long stop)
-      : a(args), tb(2 * tt), t(g.t), head(g.head), b(g.b), at(g.at), pos(pos), stop(stop), k(g.k) {}
+  MK_HD Stretch(const KvAttnArgs& args, int tt, const Begin& g, long long pos, long long stop, long long share)
+      : a(args), tb(2 * tt), t(g.t), head(g.head), b(g.b), at(g.at), pos(pos), stop(stop), share(share), k(g.k) {}
 
   // the next part with anything to do; slots 2 c and 2 c + 1 are the block's
   MK_HD bool next(Part* m, int slot) {
     while (t < a.groups + a.batch && at < stop) {
       const int end = block_end(k, b, tb), n = (end - k.kbeg + kTile - 1) / kTile, rate = block_rate(k, b, tb);
-      const long long len = (long long)(end - k.kbeg) * rate + kStart;
-      const int k0 = at < pos ? cut(pos - at, rate, n) : 0, k1 = at + len <= stop ? n : cut(stop - at, rate, n);
+      const long long len = (long long)(end - k.kbeg) * rate + start_cost(rate);
+      const int k0 = at < pos ? cut(pos - at, rate, n, share) : 0;
+      const int k1 = at + len <= stop ? n : cut(stop - at, rate, n, share);
       const bool some = k1 > k0 || (n == 0 && at >= pos);
       if (some) {
         m->tok0 = k.tok0 + b * tb, m->ntok = hd_min(tb, k.ntok - b * tb);

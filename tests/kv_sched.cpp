@@ -35,7 +35,7 @@ static void walk(const KvAttnArgs& a, int blocks, bool sound) {
     long long n = 0;
     for (int b = 0; b < k.nb; b++) {
       CHECK(cost_before(k, b, tb) == n);
-      n += (long long)(block_end(k, b, tb) - k.kbeg) * block_rate(k, b, tb) + kStart;
+      n += (long long)(block_end(k, b, tb) - k.kbeg) * block_rate(k, b, tb) + start_cost(block_rate(k, b, tb));
       CHECK(block_rate(k, b, tb) == (std::min(tb, k.ntok - b * tb) > tt ? kWide : kNarrow));
     }
     CHECK(cost_before(k, k.nb, tb) == n);
@@ -55,7 +55,7 @@ static void walk(const KvAttnArgs& a, int blocks, bool sound) {
     int t = 0;
     while (!(at[t] <= pos && pos < at[t + 1])) t++;
     const Task k = load_task(a, t, tb, false);
-    Stretch w(a, tt, begin_of(k, t, tb, at[t], pos, 0), pos, stop);
+    Stretch w(a, tt, begin_of(k, t, tb, at[t], pos, 0), pos, stop, share);
     Part m;
     long long units = 0;
     int used[2] = {0, 0};
@@ -79,10 +79,10 @@ static void walk(const KvAttnArgs& a, int blocks, bool sound) {
       if (first && open) CHECK(m.k0 > 0);
       if (leaves) open_key = key;
       first = false;
-      units += (long long)(std::min(kTile * m.k1, m.kend - m.kbeg) - kTile * m.k0) * (m.ntok > tt ? kWide : kNarrow) + kStart;
+      units += (long long)(std::min(kTile * m.k1, m.kend - m.kbeg) - kTile * m.k0) * (m.ntok > tt ? kWide : kNarrow) + start_cost(m.ntok > tt ? kWide : kNarrow);
     }
     open = leaves;
-    CHECK(units <= share + 2 * kStart + (2 * kMinPart + 2) * kTile * kWide);
+    CHECK(units <= share + 2 * kWideStart + 2 * (kMinWidePart + 1) * kTile * kWide);
   }
   CHECK(!open);
   if (!sound) return;

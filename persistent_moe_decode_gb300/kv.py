@@ -32,11 +32,15 @@ PAGE_SIZE = 16
 _TYPES = {torch.bfloat16: mk.MK_TYPE_BF16, torch.float32: mk.MK_TYPE_F32}
 
 
+# the calls' own cost matters beside kernels of a few microseconds: torch's accessors are called once each
+_current_device, _raw_stream = torch.cuda.current_device, torch._C._cuda_getCurrentRawStream
+
+
 def _run(device, index, fn, stream, *args):
     """fn(stream pointer, ...) with the device and the call's stream current, for torch's own allocations and copies
     too."""
-    if stream is None and torch.cuda.current_device() == index:
-        return fn(torch._C._cuda_getCurrentRawStream(index), *args)   # current_stream() costs 2 us more
+    if stream is None and _current_device() == index:
+        return fn(_raw_stream(index), *args)                          # current_stream() costs 2 us more
     if stream is not None and stream.device != device:
         raise ValueError(f"stream: one of {device}, got one of {stream.device}")
     with torch.cuda.device(index), torch.cuda.stream(stream):         # None: the device's current one
@@ -50,14 +54,16 @@ def _vector(t, name, device, index, n=None):
     return t if t.is_contiguous() else t.contiguous()
 
 
-def _aligned(t):
-    s, q = t.stride(), 7 if t.dtype is torch.bfloat16 else 3
-    return s[2] == 1 and not (s[0] | s[1]) & q and not t.data_ptr() & 15
+def _new(like, dtype=None):
+    return torch.empty_like(like, dtype=dtype, memory_format=torch.contiguous_format)
 
 
-def _rows(t):
-    s = t.stride()
-    return mk.mk_head_rows(t.data_ptr(), t.shape[1], s[0], s[1])
+def _rows(t, shape, odd):
+    """mk_head_rows of a tensor [n, heads, dims] of this shape, or None where its rows do not lie 16-byte aligned
+    (``odd``: the strides' bits that may not be set)."""
+    s0, s1, s2 = t.stride()
+    p = t.data_ptr()
+    return None if s2 != 1 or (s0 | s1) & odd or p & 15 else mk.mk_head_rows(p, shape[1], s0, s1)
 
 
 def frequencies(rotary_dim: int, theta: float, scaling: str | None = None, factor: float = 1.0,
@@ -118,11 +124,28 @@ class Rope:
         self._c = mk.mk_rope(self.turns.data_ptr(), head_dim, r, int(self.interleaved), self.magnitude)
 
     def _heads(self, t, name, n, dtype):
-        if t.dim() != 3 or t.dtype is not dtype or t.shape[2] != self.head_dim or t.get_device() != self._dev \
-                or (n is not None and t.shape[0] != n) or dtype not in _TYPES:
-            raise ValueError(f"{name}: BF16 or fp32 rows [n, heads, {self.head_dim}] on {self.turns.device}, alike, got "
-                             f"{t.dtype} {tuple(t.shape)} on {t.device}")
-        return t if _aligned(t) else t.clone(memory_format=torch.contiguous_format)
+        """The tensor, aligned, and its mk_head_rows."""
+        shape = t.shape
+        if len(shape) != 3 or t.dtype is not dtype or shape[2] != self.head_dim or t.get_device() != self._dev \
+                or shape[0] != n or dtype not in _TYPES:
+            raise ValueError(f"{name}: BF16 or fp32 rows [{n}, heads, {self.head_dim}] on {self.turns.device}, q, k and v "
+                             f"alike, got {t.dtype} {tuple(shape)} on {t.device}")
+        odd = 7 if dtype is torch.bfloat16 else 3
+        rows = _rows(t, shape, odd)
+        if rows is None:
+            t = t.clone(memory_format=torch.contiguous_format)
+            rows = _rows(t, shape, odd)
+        return t, rows
+
+    def _out(self, t, name, like, dtype):
+        """mk_head_rows of a given output."""
+        rows = None
+        if t.shape == like.shape and t.dtype is dtype and t.get_device() == self._dev:
+            rows = _rows(t, like.shape, 7 if dtype is torch.bfloat16 else 3)
+        if rows is None:
+            raise ValueError(f"{name}: {dtype} {tuple(like.shape)} on {self.turns.device}, rows of consecutive elements "
+                             f"at 16-byte strides, got {t.dtype} {tuple(t.shape)} on {t.device}")
+        return rows
 
     def apply(self, q, k, positions, out=None, stream=None):
         """Rows q ``[n, heads, head_dim]`` and k ``[n, kv heads, head_dim]`` (BF16 or fp32, alike) turned by
@@ -131,19 +154,20 @@ class Rope:
         return _run(self.turns.device, self._dev, self._apply, stream, q, k, positions, out)
 
     def _apply(self, st, q, k, positions, out):
-        dtype, n = q.dtype, q.shape[0]
+        dtype, n, d = q.dtype, q.shape[0], self.head_dim
         given = (q, k)
-        q, k = self._heads(q, "q", None, dtype), self._heads(k, "k", n, dtype)
+        q, q_rows = self._heads(q, "q", n, dtype)
+        k, k_rows = self._heads(k, "k", n, dtype)
         positions = _vector(positions, "positions", self.turns.device, self._dev, n)
         if out is None:
-            out = tuple(torch.empty(t.shape, dtype=dtype, device=t.device) for t in (q, k))
-        for t, like, name in zip(out, given, ("out[0]", "out[1]")):
-            if t.shape != like.shape or t.dtype is not dtype or t.get_device() != self._dev or not _aligned(t):
-                raise ValueError(f"{name}: {dtype} {tuple(like.shape)} on {self.turns.device}, rows of consecutive "
-                                 f"elements at 16-byte strides, got {t.dtype} {tuple(t.shape)} on {t.device}")
-        mk.mk_rope_apply(self._c, n, positions.data_ptr(), _TYPES[dtype], _rows(q), _rows(k), _rows(out[0]),
-                         _rows(out[1]), st)
-        return out[0], out[1]
+            qo, ko = _new(q), _new(k)
+            hq, hk = q_rows.n_heads, k_rows.n_heads
+            q_to, k_to = mk.mk_head_rows(qo.data_ptr(), hq, hq * d, d), mk.mk_head_rows(ko.data_ptr(), hk, hk * d, d)
+        else:
+            qo, ko = out
+            q_to, k_to = self._out(qo, "out[0]", given[0], dtype), self._out(ko, "out[1]", given[1], dtype)
+        mk.mk_rope_apply(self._c, n, positions.data_ptr(), _TYPES[dtype], q_rows, k_rows, q_to, k_to, st)
+        return qo, ko
 
 
 class PagedCache:
@@ -219,49 +243,65 @@ class PagedCache:
         if rope.head_dim != d or rope._dev != dev:
             raise ValueError(f"rope: one of heads of {d} dims on {device}, got {rope.head_dim} on {rope.turns.device}")
         dtype, n = q.dtype, q.shape[0]
-        q, k, v = rope._heads(q, "q", None, dtype), rope._heads(k, "k", n, dtype), rope._heads(v, "v", n, dtype)
-        if k.shape[1] != self.n_kv_heads or v.shape[1] != self.n_kv_heads:
-            raise ValueError(f"k, v: {self.n_kv_heads} KV heads, got {k.shape[1]} and {v.shape[1]}")
+        q, q_rows = rope._heads(q, "q", n, dtype)
+        k, k_rows = rope._heads(k, "k", n, dtype)
+        v, v_rows = rope._heads(v, "v", n, dtype)
+        hkv = self.n_kv_heads
+        if k_rows.n_heads != hkv or v_rows.n_heads != hkv:
+            raise ValueError(f"k, v: {hkv} KV heads, got {k.shape[1]} and {v.shape[1]}")
         positions = _vector(positions, "positions", device, dev, n)
         slots = _vector(slots, "slots", device, dev, n)
         if out is None:
-            out = torch.empty(q.shape, dtype=torch.bfloat16, device=device)
-        elif out.shape != q.shape or out.dtype is not torch.bfloat16 or out.get_device() != dev or not _aligned(out):
-            raise ValueError(f"out: BF16 {tuple(q.shape)} on {device}, rows of consecutive elements at 16-byte strides, "
-                             f"got {out.dtype} {tuple(out.shape)} on {out.device}")
-        mk.mk_kv_append(self._c, rope._c, n, positions.data_ptr(), _TYPES[dtype], _rows(q), _rows(k), _rows(v),
-                        slots.data_ptr(), _rows(out), st)
+            out = _new(q, torch.bfloat16)
+            hq = q_rows.n_heads
+            to = mk.mk_head_rows(out.data_ptr(), hq, hq * d, d)
+        else:
+            to = rope._out(out, "out", q, torch.bfloat16)
+        mk.mk_kv_append(self._c, rope._c, n, positions.data_ptr(), _TYPES[dtype], q_rows, k_rows, v_rows,
+                        slots.data_ptr(), to, st)
         return out
 
-    def _dense(self, t):
-        s = t.stride()
-        return _aligned(t) and s[1] == self.head_dim and (t.shape[0] < 2 or s[0] >= t.shape[1] * self.head_dim)
+    def _dense(self, t, shape):
+        """Elements between rows of consecutive heads, 16-byte aligned; 0 if they do not lie so."""
+        s0, s1, s2 = t.stride()
+        n, heads, d = shape
+        if s2 != 1 or (heads > 1 and s1 != d) or s0 & 7 or t.data_ptr() & 15 or (n > 1 and s0 < heads * d):
+            return 0
+        return s0 if n > 1 else heads * d
 
     def _attention(self, st, q, q_starts, page_tables, seq_lens, group_starts, prefix_lens, scale, out):
         dev, device, d = self._dev, self.k_pool.device, self.head_dim
-        if q.dim() != 3 or q.dtype is not torch.bfloat16 or q.get_device() != dev or q.shape[2] != d:
-            raise ValueError(f"q: BF16 [rows, heads, {d}] on {device}, got {q.dtype} {tuple(q.shape)} on {q.device}")
+        shape = q.shape
+        if len(shape) != 3 or q.dtype is not torch.bfloat16 or q.get_device() != dev or shape[2] != d:
+            raise ValueError(f"q: BF16 [rows, heads, {d}] on {device}, got {q.dtype} {tuple(shape)} on {q.device}")
         if page_tables.dtype is not torch.int32 or page_tables.dim() != 2 or page_tables.get_device() != dev:
             raise ValueError(f"page_tables: int32 [batch, max_pages] on {device}, got {page_tables.dtype} "
                              f"{tuple(page_tables.shape)} on {page_tables.device}")
-        (n, hq, _), (batch, max_pages) = q.shape, page_tables.shape
+        (n, hq, _), (batch, max_pages) = shape, page_tables.shape
         q_starts = _vector(q_starts, "q_starts", device, dev, batch + 1)
         seq_lens = _vector(seq_lens, "seq_lens", device, dev, batch)
-        groups = 0
+        groups, gs, pl = 0, None, None
         if prefix_lens is not None:
             prefix_lens = _vector(prefix_lens, "prefix_lens", device, dev)
             groups = prefix_lens.shape[0]
             group_starts = _vector(group_starts, "group_starts", device, dev, groups + 1)
             if groups == 0 and batch:
                 raise ValueError("prefix_lens: the groups hold all sequences, got none")
+            gs, pl = group_starts.data_ptr(), prefix_lens.data_ptr()
         if not page_tables.is_contiguous():
             page_tables = page_tables.contiguous()
-        if not self._dense(q):
+        q_stride = self._dense(q, shape)
+        if not q_stride:
             q = q.clone(memory_format=torch.contiguous_format)
+            q_stride = hq * d
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=device)
-        elif out.shape != q.shape or out.dtype is not q.dtype or out.get_device() != dev or not self._dense(out):
-            raise ValueError(f"out: BF16 {tuple(q.shape)} on {device}, rows of consecutive heads at 16-byte strides")
+            out, out_stride = _new(q), hq * d
+        else:
+            out_stride = 0
+            if out.shape == shape and out.dtype is torch.bfloat16 and out.get_device() == dev:
+                out_stride = self._dense(out, shape)
+            if not out_stride and n * hq:
+                raise ValueError(f"out: BF16 {tuple(shape)} on {device}, rows of consecutive heads at 16-byte strides")
         # the workspace belongs to this call's stream, or to the graph that captures it
         key = (hq, n, batch, groups)
         ws_bytes = self._ws_bytes.get(key)      # a function of these alone
@@ -269,9 +309,8 @@ class PagedCache:
             if len(self._ws_bytes) >= 1024:
                 self._ws_bytes.clear()
             ws_bytes = self._ws_bytes[key] = mk.mk_kv_workspace(self._c, hq, n, batch, groups)
-        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=device) if ws_bytes else None
-        mk.mk_kv_attention(self._c, q.data_ptr(), q.stride(0), out.data_ptr(), out.stride(0), hq, n, batch,
-                           q_starts.data_ptr(), page_tables.data_ptr(), max_pages, seq_lens.data_ptr(), groups,
-                           group_starts.data_ptr() if groups else None, prefix_lens.data_ptr() if groups else None,
+        ws = self.status.new_empty((ws_bytes + 3) // 4) if ws_bytes else None
+        mk.mk_kv_attention(self._c, q.data_ptr(), q_stride, out.data_ptr(), out_stride, hq, n, batch, q_starts.data_ptr(),
+                           page_tables.data_ptr(), max_pages, seq_lens.data_ptr(), groups, gs, pl,
                            d ** -0.5 if scale is None else scale, ws.data_ptr() if ws_bytes else None, ws_bytes, st)
         return out

@@ -110,6 +110,8 @@ class MkError(RuntimeError):
 def lib():
     """Load libmk.so; raise if it is missing (no CPU fallback exists)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(_LIB_PATH):

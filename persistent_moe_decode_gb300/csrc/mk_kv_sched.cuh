@@ -17,15 +17,15 @@ namespace mk {
 
 constexpr int kTile = 128;               // keys a step, rows a tile
 
-// Cost of a row block, in units: kWide a key where its rows fill two tiles,
-// kNarrow where they fit one, and its start and end, about 5 key tiles
-// (10,000 and 8,000 cycles beside 2,300 and 1,800 a tile).
-constexpr int kWide = 4, kNarrow = 3;
-constexpr int kWideStart = 5 * kTile * kWide, kNarrowStart = 5 * kTile * kNarrow;
-constexpr int kMinShare = 4 * kTile * kWide;      // no block takes less
+// Cost of a row block, in keys: its own, and its start and end.  A key tile
+// takes 2,300 cycles where the rows fill two tiles (wide: the products), 2,000
+// where they fit one (narrow: the copies of its pages); a start and an end 11,000
+// and 6,000, a little more where they follow each other.
+constexpr int kWideStart = 5 * kTile, kNarrowStart = 4 * kTile;
+constexpr int kMinShare = 4 * kTile;              // no block takes less
 // No part of an item has fewer key tiles: a part costs an end and its share of
 // the merge, so that a wide one of less is better left where it is.
-constexpr int kMinWidePart = 6, kMinPart = 2;
+constexpr int kMinWidePart = 4, kMinPart = 2;
 
 enum : int { kCausal = 1, kNan = 2, kPrefix = 4 };
 
@@ -115,12 +115,12 @@ MK_HD inline int block_tiles(const Task& k, int b, int tb) {
   return (block_end(k, b, tb) - k.kbeg + kTile - 1) / kTile;
 }
 
-// units a key of row block b: all but a task's last have two tiles of rows
-MK_HD inline int block_rate(const Task& k, int b, int tb) {
-  return b < k.nb - 1 || 2 * (k.ntok - b * tb) > tb ? kWide : kNarrow;
-}
+// all row blocks but a task's last are wide
+MK_HD inline bool wide(const Task& k, int b, int tb) { return b < k.nb - 1 || 2 * (k.ntok - b * tb) > tb; }
 
-MK_HD inline int start_cost(int rate) { return rate == kWide ? kWideStart : kNarrowStart; }
+MK_HD inline int block_cost(const Task& k, int b, int tb) {
+  return block_end(k, b, tb) - k.kbeg + (wide(k, b, tb) ? kWideStart : kNarrowStart);
+}
 
 // cost of the row blocks before b, b <= nb
 MK_HD inline long long cost_before(const Task& k, int b, int tb) {
@@ -136,22 +136,15 @@ MK_HD inline long long cost_before(const Task& k, int b, int tb) {
       keys = (long long)full * (k.kend - k.kbeg);
     }
   }
-  long long cost = keys * kWide + (long long)full * kWideStart;
-  if (b > full) {
-    const int rate = block_rate(k, b - 1, tb);
-    cost += (long long)(block_end(k, b - 1, tb) - k.kbeg) * rate + start_cost(rate);
-  }
-  return cost;
+  return keys + (long long)full * kWideStart + (b > full ? block_cost(k, b - 1, tb) : 0);
 }
 
-// Where a border x units into an item of n key tiles cuts it: the same for the
+// Where a border x keys into an item of n key tiles cuts it: the same for the
 // block before and the block after.  Small shares are cut as they fall.
-MK_HD inline int cut(long long x, int rate, int n, long long share) {
-  static_assert(kTile * kWide == 512 && kTile * kNarrow == 384, "units of a tile");
-  int k = rate == kWide ? (int)((x + 256) >> 9) : (int)((unsigned)((x + 192) >> 7) / 3);
-  const int least = rate == kWide ? (int)hd_max(hd_min(share >> 12, (long long)kMinWidePart), (long long)kMinPart) : kMinPart;
-  if (k < least) k = 0;
-  return n - k < least ? n : k;
+MK_HD inline int cut(long long x, bool wide, int n, long long share) {
+  const int least = wide ? (int)hd_max(hd_min(share >> 10, (long long)kMinWidePart), (long long)kMinPart) : kMinPart;
+  const int k = (int)((x + kTile / 2) / kTile);
+  return k < least ? 0 : n - k < least ? n : k;
 }
 
 // floor(x / y) of 0 <= x, 0 < y whose quotient is small: a float's guess, put right
@@ -211,10 +204,9 @@ struct Stretch {
   // the next part with anything to do; slots 2 c and 2 c + 1 are the block's
   MK_HD bool next(Part* m, int slot) {
     while (t < a.groups + a.batch && at < stop) {
-      const int end = block_end(k, b, tb), n = (end - k.kbeg + kTile - 1) / kTile, rate = block_rate(k, b, tb);
-      const long long len = (long long)(end - k.kbeg) * rate + start_cost(rate);
-      const int k0 = at < pos ? cut(pos - at, rate, n, share) : 0;
-      const int k1 = at + len <= stop ? n : cut(stop - at, rate, n, share);
+      const int end = block_end(k, b, tb), n = (end - k.kbeg + kTile - 1) / kTile, len = block_cost(k, b, tb);
+      const bool w = wide(k, b, tb);
+      const int k0 = at < pos ? cut(pos - at, w, n, share) : 0, k1 = at + len <= stop ? n : cut(stop - at, w, n, share);
       const bool some = k1 > k0 || (n == 0 && at >= pos);
       if (some) {
         m->tok0 = k.tok0 + b * tb, m->ntok = hd_min(tb, k.ntok - b * tb);

@@ -35,8 +35,8 @@ static void walk(const KvAttnArgs& a, int blocks, bool sound) {
     long long n = 0;
     for (int b = 0; b < k.nb; b++) {
       CHECK(cost_before(k, b, tb) == n);
-      n += (long long)(block_end(k, b, tb) - k.kbeg) * block_rate(k, b, tb) + start_cost(block_rate(k, b, tb));
-      CHECK(block_rate(k, b, tb) == (std::min(tb, k.ntok - b * tb) > tt ? kWide : kNarrow));
+      n += block_cost(k, b, tb);
+      CHECK(block_cost(k, b, tb) == block_end(k, b, tb) - k.kbeg + (std::min(tb, k.ntok - b * tb) > tt ? kWideStart : kNarrowStart));
     }
     CHECK(cost_before(k, k.nb, tb) == n);
     at[t + 1] = at[t] + n * a.hkv;
@@ -79,10 +79,10 @@ static void walk(const KvAttnArgs& a, int blocks, bool sound) {
       if (first && open) CHECK(m.k0 > 0);
       if (leaves) open_key = key;
       first = false;
-      units += (long long)(std::min(kTile * m.k1, m.kend - m.kbeg) - kTile * m.k0) * (m.ntok > tt ? kWide : kNarrow) + start_cost(m.ntok > tt ? kWide : kNarrow);
+      units += std::min(kTile * m.k1, m.kend - m.kbeg) - kTile * m.k0 + (m.ntok > tt ? kWideStart : kNarrowStart);
     }
     open = leaves;
-    CHECK(units <= share + 2 * kWideStart + 2 * (kMinWidePart + 1) * kTile * kWide);
+    CHECK(units <= share + 2 * kWideStart + 2 * (kMinWidePart + 1) * kTile);
   }
   CHECK(!open);
   if (!sound) return;

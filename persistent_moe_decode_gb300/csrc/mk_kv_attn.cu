@@ -84,6 +84,13 @@ __host__ __device__ __forceinline__ Ws ws_of(uint8_t* p, int d, int hq, int tota
 
 // ------------------------------------------------------------------------ waits
 
+// a block's stretch and the item it begins in
+struct Plan {
+  Begin begin;
+  long long pos, end, share;
+  int work;                              // there is one
+};
+
 struct Sync {
   uint64_t kv_full[10], kv_empty[10];
   uint64_t raw_full[10];                 // a tile that is cleared before it counts as full
@@ -96,10 +103,8 @@ struct Sync {
   uint32_t tmem;
   volatile int stop;
   long long scan[kThreads / 32];
-  Begin begin;
-  long long pos, end, share;
+  Plan plan;
   float pair[2][kTile];
-  int work;                              // this block has a stretch
 };
 
 // Waits for the phase of this parity; false once the block gives up, or after
@@ -138,6 +143,33 @@ __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.
 // one BF16 pair's elements that are not finite: bit 15, bit 31
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
 
+// One warp: this block's stretch, if it begins in a task of this warp.  Each lane
+// has a task k (number t) or none, of `mine` keys after `before` others.
+__device__ __forceinline__ void find_plan(const KvAttnArgs& a, Plan& plan, const Task& k, int t, long long before,
+                                          long long mine, long long total, int tb, int lane) {
+  // about an equal share: total / blocks, from above
+  const long long share = max((long long)__umul64hi((unsigned long long)total, a.per_block) + 1, (long long)kMinShare);
+  const long long pos = share * blockIdx.x;
+  const unsigned owner = __ballot_sync(0xffffffffu, pos < total && before <= pos && pos < before + mine);
+  if (!owner) return;
+  const int from = __ffs(owner) - 1;
+  Task o;
+#pragma unroll
+  for (int w = 0; w < (int)(sizeof(Task) / 4); w++)
+    reinterpret_cast<int*>(&o)[w] = __shfl_sync(0xffffffffu, reinterpret_cast<const int*>(&k)[w], from);
+  const Begin g = begin_of(o, __shfl_sync(0xffffffffu, t, from), tb, __shfl_sync(0xffffffffu, before, from), pos, lane);
+  if (lane == 0) plan.begin = g, plan.pos = pos, plan.end = min(total, pos + share), plan.share = share, plan.work = 1;
+}
+
+__device__ __forceinline__ long long scan(long long x, int lane) {
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += y;
+  }
+  return x;
+}
+
 // ----------------------------------------------------------------------- kernel
 
 // Softmax (a warpgroup), item after item: of one of its two tiles of rows, over
@@ -172,13 +204,17 @@ __device__ void softmax_role(const KvAttnArgs& a, Sync& s, Item* items, const Ws
       tc_wait_ld();
       const int t0 = m.kbeg + kTile * j;
       if (t0 + kTile > least) {
-        const int seen = lim - t0;
-        if (narrow && D == 128) {            // first 8 keys of all pages, then the last 8
+        // columns that are seen: the first of each 64 (a narrow item's pages have
+        // their first 8 keys in the first 64 columns, the others in the last)
+        const int seen = min(max(lim - t0, 0), kTile);
+        const bool paged = narrow && D == 128;
 #pragma unroll
-          for (int c = 0; c < kTile; c++) x[c] = c % 64 / 8 * 16 + c / 64 * 8 + c % 8 < seen ? x[c] : -INFINITY;
-        } else {
+        for (int c = 0; c < kTile; c += 32) {
+          const int h = c / 64;
+          const int n = (paged ? 8 * (seen >> 4) + min(max((seen & 15) - 8 * h, 0), 8) : seen - 64 * h) - c % 64;
+          const uint32_t bits = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1;
 #pragma unroll
-          for (int c = 0; c < kTile; c++) x[c] = c < seen ? x[c] : -INFINITY;
+          for (int u = 0; u < 32; u++) x[c + u] = bits >> u & 1 ? x[c + u] : -INFINITY;
         }
       }
       float mx[4] = {x[0], x[1], x[2], x[3]};
@@ -350,7 +386,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tt = kTile / a.grp, tb = 2 * tt, tasks = a.groups + a.batch;
   const Ws ws = ws_of(a.ws, D, a.hq, a.total_q, gridDim.x);
 
-  if (tid == 0) s.work = 0;
   if (tid == kThreads - 32) {
     for (int i = 0; i < S::kStages; i++) mbar_init(&s.kv_full[i], 1), mbar_init(&s.kv_empty[i], 2), mbar_init(&s.raw_full[i], 1);
     for (int t = 0; t < 2; t++) {
@@ -359,70 +394,53 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kItems; i++) mbar_init(&s.item_full[i], 1), mbar_init(&s.item_empty[i], kReaders);
     mbar_init(&s.pair_full, 4), mbar_init(&s.pair_empty, 4), mbar_init(&s.drain[0], 1), mbar_init(&s.drain[1], 1);
-    s.stop = 0;
+    s.stop = 0, s.plan.work = 0;
     mbar_fence_init();
   }
   if (warp == 8) tc_alloc(&s.tmem, 512);
 
   if (warp == 10 && lane < 4) tma_prefetch_map(lane == 0 ? &map_k : lane == 1 ? &page_v : lane == 2 ? &map_q : &page_k);
 
-  // All tasks' cost, and the item that this block's stretch begins in.  Few
-  // tasks are one warp's work: the others need not be waited for.
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s.tmem;
+
+  // All tasks' cost, and the item that this block's stretch begins in.  Up to 32
+  // tasks are left to the warp that copies pages, while the others get ready.
   const bool few = tasks <= 32;
-  const int chunk = few || tasks <= kThreads ? 1 : (tasks + kThreads - 1) / kThreads;
-  const int first = min(tasks, tid * chunk), end = min(tasks, first + chunk);
-  long long mine = 0, incl = 0;
-  Task k{};
-  if (!few || warp == 0) {
-    for (int t = first; t < end; t++) {
-      k = load_task(a, t, tb, blockIdx.x == 0);
+  if (!few) {
+    const int chunk = (tasks + kThreads - 1) / kThreads;
+    int t = min(tasks, tid * chunk);
+    const int end = min(tasks, t + chunk);
+    long long mine = 0, total = 0;
+    Task k{};
+    for (int i = t; i < end; i++) {
+      k = load_task(a, i, tb, blockIdx.x == 0);
       mine += cost_before(k, k.nb, tb) * a.hkv;
     }
-    incl = mine;
-#pragma unroll
-    for (int x = 1; x < 32; x <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, incl, x);
-      if (lane >= x) incl += y;
-    }
-  }
-  long long before = incl - mine, total = __shfl_sync(0xffffffffu, incl, 31);
-  if (!few) {
+    const long long incl = scan(mine, lane);
+    long long before = incl - mine;
     if (lane == 31) s.scan[warp] = incl;
     __syncthreads();
-    total = 0;
     for (int w = 0; w < kThreads / 32; w++) {
       const long long x = s.scan[w];
       if (w < warp) before += x;
       total += x;
     }
-  }
-  if (!few || warp == 0) {
-    // about an equal share: total / blocks, from above
-    const long long share = max((long long)__umul64hi((unsigned long long)total, a.per_block) + 1, (long long)kMinShare);
-    const long long pos = share * blockIdx.x;
-    const bool owner = pos < total && before <= pos && pos < before + mine;
-    if (__any_sync(0xffffffffu, owner)) {        // the warp that found the task finds the item
-      int t = first;
-      if (owner && chunk > 1)
-        for (; t < end; t++) {
+    if (chunk > 1) {                       // the thread that holds the position finds its task
+      const long long pos = max((long long)__umul64hi((unsigned long long)total, a.per_block) + 1, (long long)kMinShare) * blockIdx.x;
+      if (before <= pos && pos < before + mine)
+        for (;; t++) {
           k = load_task(a, t, tb, false);
-          const long long c = cost_before(k, k.nb, tb) * a.hkv;
-          if (pos < before + c) break;
-          before += c;
+          mine = cost_before(k, k.nb, tb) * a.hkv;
+          if (pos < before + mine) break;
+          before += mine;
         }
-      const int from = __ffs(__ballot_sync(0xffffffffu, owner)) - 1;
-      Task o;
-#pragma unroll
-      for (int w = 0; w < (int)(sizeof(Task) / 4); w++)
-        reinterpret_cast<int*>(&o)[w] = __shfl_sync(0xffffffffu, reinterpret_cast<const int*>(&k)[w], from);
-      const Begin g = begin_of(o, __shfl_sync(0xffffffffu, t, from), tb, __shfl_sync(0xffffffffu, before, from), pos, lane);
-      if (lane == 0) s.begin = g, s.pos = pos, s.end = min(total, pos + share), s.share = share, s.work = 1;
     }
+    find_plan(a, s.plan, k, t, before, mine, total, tb, lane);
+    __syncthreads();
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = s.tmem;
 
   if (warp < 8) {
     regs_up<kRegsSoftmax>();
@@ -435,13 +453,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t loads = 0, raw = 0, raw_use = 0;    // stages whose last tile goes through raw_full; its uses, modulo 2
       int it = 0;
       bool ok = true;
-      if (s.work) {
+      if (few) {
+        Task k{};
+        long long mine = 0;
+        if (lane < tasks) {
+          k = load_task(a, lane, tb, blockIdx.x == 0);
+          mine = cost_before(k, k.nb, tb) * a.hkv;
+        }
+        const long long incl = scan(mine, lane), total = __shfl_sync(0xffffffffu, incl, 31);
+        find_plan(a, s.plan, k, lane, incl - mine, mine, total, tb, lane);
+        __syncwarp();
+      }
+      if (s.plan.work) {
         auto pages_of = [&](const Part& p, int j) { return min(8, (p.kend - p.kbeg - kTile * j + kKvPage - 1) / kKvPage); };
         auto page_of = [&](const Part& p, int j) {
           return j < p.k1 && lane < pages_of(p, j)
                      ? a.page_tables[(int64_t)p.table * a.max_pages + p.kbeg / kKvPage + 8 * j + lane] : 0;
         };
-        Stretch w(a, tt, s.begin, s.pos, s.end, s.share);
+        Stretch w(a, tt, s.plan.begin, s.plan.pos, s.plan.end, s.plan.share);
         Part m, nx;
         bool have = w.next(&m, 2 * (int)blockIdx.x);
         int page[3], npage[3] = {0, 0, 0};
@@ -951,6 +980,10 @@ int launch(const KvAttnArgs& a, int sms, cudaStream_t st) {
   kv_attention_kernel<D><<<sms, kThreads, Shape<D>::kSmem, st>>>(b, map_q, map_k, page_k, page_v);
   int rc = launched(cudaGetLastError());
   if (rc) return rc;
+  // no item of up to three key tiles is cut (two parts have two each): nothing to merge
+  static_assert(kMinPart == 2 && kMinWidePart >= kMinPart, "least parts");
+  const bool merge = a.max_pages * kKvPage > 3 * kTile;
+  if (!merge && !a.groups) return MK_OK;
   // the next kernels are launched while the one before runs, and wait for its end
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute at{};
@@ -959,7 +992,7 @@ int launch(const KvAttnArgs& a, int sms, cudaStream_t st) {
   cfg.stream = st, cfg.attrs = &at, cfg.numAttrs = 1;
   cfg.blockDim = dim3(256);
   cfg.gridDim = dim3(sms, D / 8);       // 256 rows: 32 groups of 8 rows, D / 32 of dims, 8 warps a block
-  rc = launched(cudaLaunchKernelEx(&cfg, kv_merge_kernel<D>, a));
+  if (merge) rc = launched(cudaLaunchKernelEx(&cfg, kv_merge_kernel<D>, a));
   if (rc || !a.groups) return rc;
   cfg.gridDim = dim3((unsigned)std::min<long long>(8 * sms, ((long long)a.total_q * a.hq + 7) / 8 * (D / 32) / 8 + 1));
   return launched(cudaLaunchKernelEx(&cfg, kv_join_kernel<D>, a, sms));

@@ -72,7 +72,7 @@ static void walk(const KvAttnArgs& a, int blocks, bool sound) {
       CHECK((m.slot < 0) == (m.k0 == 0 && m.k1 == m.n));
       if (m.slot >= 0) {
         CHECK(m.slot == 2 * c + (m.k0 == 0) && !used[m.k0 == 0]++);
-        CHECK(m.k1 - m.k0 >= kMinPart);
+        CHECK(m.k1 - m.k0 >= kMinPart && m.n > 3);        // three key tiles are never cut
       }
       if (m.k0 > 0) CHECK(first && open && key == open_key);
       leaves = m.k1 < m.n;

@@ -891,7 +891,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const KvAttnArgs a, int bl
     const int c4 = (int)(job % (D / 32)) * 8 + (lane >> 3);
     if (r >= lines) continue;
     const int64_t per = (int64_t)a.total_q * a.grp;
-    const int kv = (int)(r / per), in = (int)(r - kv * per), token = in / a.grp, head = kv * a.grp + in % a.grp;
+    const int kv = (int)(r / per), token = (int)((r - kv * per) / a.grp), head = kv * a.grp + (int)(r % a.grp);
     if (token < t0 || token >= t1) continue;               // of no sequence
     const float m0 = ws.part_m[r], m1 = ws.part_m[lines + r], high = fmaxf(m0, m1);
     const bool nan = m0 != m0 || m1 != m1, none = high == -INFINITY;

@@ -304,6 +304,70 @@ def test_attention_strided_rows_and_in_place():
     assert torch.equal(out, got) and torch.equal(wide[:, :8], got) and torch.equal(wide[:, 8:], keep)
 
 
+def test_attention_many_sequences():
+    """More tasks than a warp has lanes, than a block has threads, and several to a thread."""
+    import random
+    rng = random.Random(2)
+    for batch in (33, 390, 1500):
+        news = [rng.choice([0, 1, 1, 1, 2, 37]) for _ in range(batch)]
+        lens = [n + rng.choice([0, 3, 130, 500]) for n in news]
+        lens[batch // 2] = 6000
+        st = _kv.batch(news, lens, 1, 64, seed=batch, hq=4)
+        want, size = _kv.attention(st["q"], st["k"], st["v"], news, lens, st["tables"])
+        assert _kv.attention_off(run(st), want, size) <= 1
+
+
+def test_attention_without_pages():
+    st = _kv.batch([3, 1], [0, 0], 2, 64, seed=1, hq=4, spare=0)
+    assert st["tables"].shape == (2, 0)
+    assert (run(st) == 0).all()
+    empty = dict(st, q=st["q"][:0], starts=torch.zeros(3, dtype=torch.int32, device="cuda"))
+    assert run(empty).shape == (0, 4, 64)
+
+
+def test_attention_far_pages():
+    """Pages whose elements lie past 2^31: the last ones of a cache of 4.5 GB each of keys and values."""
+    hkv, d, pages = 8, 128, 140_000
+    k = torch.empty(pages, hkv, 16, d, dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    n = 700
+    ids = torch.cat([torch.arange(pages - 40, pages), torch.arange(0, 4)]).int().cuda()
+    for p in (k, v):
+        p[ids.long()] = torch.randn(44, hkv, 16, d, generator=g, device="cuda").bfloat16()
+    assert k.numel() > 1 << 31
+    st = dict(k=k, v=v, q=torch.randn(100, 16, d, generator=g, device="cuda").bfloat16(), tables=ids[None].contiguous(),
+              starts=torch.tensor([0, 100], dtype=torch.int32, device="cuda"),
+              lens=torch.tensor([n], dtype=torch.int32, device="cuda"))
+    want, size = _kv.attention(st["q"], k, v, [100], [n], st["tables"])
+    assert _kv.attention_off(run(st), want, size) <= 1
+    # the cache's rows there, written
+    cache = kv().PagedCache.from_pools(k, v)
+    x = torch.randn(2, 3 * hkv, d, generator=g, device="cuda").bfloat16()
+    pos = torch.tensor([5, 6], dtype=torch.int32, device="cuda")
+    slots = torch.tensor([pages * 16 - 1, 17], dtype=torch.int32, device="cuda")
+    cache.append(kv().Rope(d, 1e4), *x.split(hkv, 1), pos, slots)
+    cache.check()
+    assert torch.equal(v[pages - 1, :, 15], x[0, 2 * hkv:]) and torch.equal(v[1, :, 1], x[1, 2 * hkv:])
+
+
+def test_far_strides():
+    """Rows 2^30 elements apart."""
+    wide = torch.empty((2 << 30) + 4096, dtype=torch.bfloat16, device="cuda")
+    rows = wide.as_strided((3, 4, 64), (1 << 30, 64, 1))
+    st = _kv.batch([3], [150], 2, 64, seed=4, hq=4)
+    want, size = _kv.attention(st["q"], st["k"], st["v"], [3], [150], st["tables"])
+    rows.copy_(st["q"])
+    out = wide.as_strided((3, 4, 64), (1 << 30, 64, 1), 1024)
+    run(dict(st, q=rows), out=out)
+    assert _kv.attention_off(out.clone(), want, size) <= 1
+    pos = torch.tensor([3, 70000, 9], dtype=torch.int32, device="cuda")
+    got, _ = kv().Rope(64, 1e4).apply(rows, rows[:, :1], pos)
+    want, size = _kv.turned(st["q"], pos, 64, 1e4, False)
+    assert _kv.rope_off(got, want, size) <= 1
+
+
 # ------------------------------------------------------------------ shared
 
 SHARED = [
@@ -355,7 +419,7 @@ def test_shared_attention_bad_groups():
     from persistent_moe_decode_gb300 import mk
     groups = [(64, [(1, 81), (2, 66)]), (32, [(5, 50), (1, 33)])]
 
-    def case(change, code, nan_rows):
+    def case(change, code, nan_rows, only=None):
         st, want, size = shared_batch(4, 2, 64, groups, seed=17)
         change(st)
         q = st["q"]
@@ -364,7 +428,7 @@ def test_shared_attention_bad_groups():
             cache.check()
         assert e.value.code == code
         assert got[nan_rows].isnan().all()
-        rest = [i for i in range(9) if i not in range(9)[nan_rows]]
+        rest = only or [i for i in range(9) if i not in range(9)[nan_rows]]
         assert _kv.attention_off(got[rest], want[rest], size[rest]) <= 1
 
     def put(name, i, x):
@@ -378,6 +442,10 @@ def test_shared_attention_bad_groups():
     case(put("group_starts", 2, 3), mk.MK_ERR_BAD_ARG, slice(8, 9))          # the last sequence is in no group
     case(put("tables", (0, 1), 1 << 20), mk.MK_ERR_BAD_PAGE, slice(0, 3))    # a common page
     case(put("tables", (2, 2), -1), mk.MK_ERR_BAD_PAGE, slice(3, 8))         # one sequence's own page
+    case(put("group_starts", 2, 7), mk.MK_ERR_BAD_ARG, slice(3, 9))          # past the batch
+    case(put("group_starts", 1, -1), mk.MK_ERR_BAD_ARG, slice(0, 9))         # no groups left
+    # starts that go up and down again: the rows of the sequence before them hold
+    case(put("starts", 2, 9), mk.MK_ERR_BAD_ARG, slice(9, 9), only=[0])
 
 
 # ---------------------------------------------------- streams, graphs, devices
@@ -421,6 +489,97 @@ def test_calls_on_a_side_stream_and_in_a_graph():
     # the rotated rows differ from the kernel's by a rounding where they lie next to a border
     assert float((first.double() - want).norm() / want.norm()) < 2.0 ** -7
     cache.check()
+
+
+def test_lengths_may_change_between_replays():
+    """A captured call reads its lengths, starts, tables and groups when it runs."""
+    news, lens = [1, 9, 1], [3000, 700, 40]
+    st = _kv.batch(news, lens, 2, 128, seed=31, hq=16, junk=False)
+    cache = kv().PagedCache.from_pools(st["k"], st["v"])
+    groups = torch.tensor([0, 1, 3], dtype=torch.int32, device="cuda")
+    common = torch.zeros(2, dtype=torch.int32, device="cuda")
+
+    def both():
+        return (cache.attention(st["q"], st["starts"], st["tables"], st["lens"]),
+                cache.shared_attention(st["q"], st["starts"], st["tables"], st["lens"], groups, common))
+    both()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = both()
+    for lens2, news2, prefix in (([2999, 650, 33], [4, 0, 7], [2992, 0]), ([17, 9, 1], [1, 9, 1], [16, 0]),
+                                 ([0, 700, 40], [0, 9, 2], [0, 16])):
+        st["lens"].copy_(torch.tensor(lens2))
+        st["starts"].copy_(torch.tensor([0, *torch.tensor(news2).cumsum(0).tolist()]))
+        common.copy_(torch.tensor(prefix))
+        st["tables"][2, 0] = st["tables"][1, 0]
+        graph.replay()
+        torch.cuda.synchronize()
+        cache.check()
+        n = sum(news2)
+        want, size = _kv.attention(st["q"][:n], st["k"], st["v"], news2, lens2, st["tables"])
+        for got in out:
+            assert _kv.attention_off(got[:n], want, size) <= 1
+
+
+def test_two_calls_at_once():
+    a = _kv.batch([300, 1], [2000, 9000], 2, 128, seed=41, hq=16)
+    b = _kv.batch([1, 1, 64], [5000, 70, 64], 4, 64, seed=42, hq=8)
+    first = [run(a), run(b)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    caches = [kv().PagedCache.from_pools(x["k"], x["v"]) for x in (a, b)]
+    got = [[], []]
+    for _ in range(20):
+        for i, x in enumerate((a, b)):
+            got[i].append(caches[i].attention(x["q"], x["starts"], x["tables"], x["lens"], stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(y, first[i]) for y in got[i])
+
+
+def test_refusals():
+    m = kv()
+    st = _kv.batch([2], [40], 2, 64, seed=1, hq=4)
+    c = m.PagedCache.from_pools(st["k"], st["v"])
+    q, s, t, n = st["q"], st["starts"], st["tables"], st["lens"]
+    rope = m.Rope(64, 1e4)
+    pos = torch.arange(2, device="cuda").int()
+    for args in ((q.float(), s, t, n), (q[0], s, t, n), (q[..., :32], s, t, n), (q.cpu(), s, t, n), (q, s[:1], t, n),
+                 (q, s.long(), t, n), (q, s, t.long(), n), (q, s, t[0], n), (q, s, t, n.float()), (q, s, t.cpu(), n),
+                 (q, s, t, torch.cat([n, n]))):
+        with pytest.raises(ValueError):
+            c.attention(*args)
+    for out in (q.float(), q[:1], torch.empty(2, 8, 64, dtype=q.dtype, device="cuda")[:, ::2], q.cpu()):
+        with pytest.raises(ValueError):
+            c.attention(q, s, t, n, out=out)
+    g = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    p = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for args in ((g[:1], p), (g, p[:0]), (g.long(), p), (g, p.cpu())):
+        with pytest.raises(ValueError):
+            c.shared_attention(q, s, t, n, *args)
+    from persistent_moe_decode_gb300 import mk
+    for scale in (0.0, -1.0, math.inf, math.nan):
+        with pytest.raises(mk.MkError):
+            c.attention(q, s, t, n, scale=scale)
+    with pytest.raises(mk.MkError):
+        c.attention(q[:, :3], s, t, n)                       # query heads no multiple of the KV heads
+    k = q[:, :2]
+    for args in ((q.half(), k.half(), pos), (q, k.float(), pos), (q, k[:1], pos), (q, k, pos[:1]), (q, k, pos.long()),
+                 (q[..., :32], k[..., :32], pos), (q.cpu(), k.cpu(), pos)):
+        with pytest.raises(ValueError):
+            rope.apply(*args)
+    with pytest.raises(ValueError):
+        rope.apply(q, k, pos, out=(q.float(), k))
+    with pytest.raises(mk.MkError):
+        rope.apply(q, k, pos, out=(q[:1].expand(2, 4, 64), k))      # rows of one place
+    slots = pos.clone()
+    for args in ((m.Rope(128, 1e4), q, k, k, pos, slots), (rope, q, q, q, pos, slots), (rope, q, k, k.float(), pos, slots),
+                 (rope, q, k, k, pos, slots[:1]), (rope, q, k, k, pos, slots.cpu())):
+        with pytest.raises(ValueError):
+            c.append(*args)
+    with pytest.raises(ValueError):
+        c.append(rope, q, k, k, pos, slots, out=q.float())
 
 
 def test_a_prompt_filled_here_decodes_like_the_oracle():

@@ -1,24 +1,51 @@
 // Attention of packed query rows over the BF16 paged cache (mk_kv_attention).
 //
+// Mathematics.  A row's running reference r (of its scores' maximum) and sum
+// l = sum exp(s - r), with O = sum exp(s - r) v beside it, a key tile of 128 at a
+// time; parts of a row over different keys add up as (r, l, O) again.  Scores and
+// O are fp32 sums of BF16 products, weights BF16.
+//
 // Rows.  A block of work is 2 tiles of 128 rows of one KV head: the query heads
 // of its group, token after token (row = token * grp + head), so that few tokens
 // of many heads fill a tile as many tokens of few heads do.  A tile holds
-// floor(128 / grp) whole tokens.  Its keys are taken 128 at a time.
+// floor(128 / grp) whole tokens.  Rows that fit one tile are `narrow`: the two
+// softmax warpgroups then take key tiles in turn, and add up at the end.
 //
 // Shares.  Lengths are on the device only, so the blocks cut the work
 // themselves: all (task, KV head, row block) items laid end to end, an item as
-// long as its key tiles and kStart for its start and end, and each block of the
-// grid takes an equal stretch.  A task is a sequence's own keys (causal), or a
-// group's common ones (all of them seen).  A block meets at most one item that
-// it does not begin and one that it does not end; these leave their sums in the
-// workspace, and the merge kernel adds them up in order.  No atomics.
+// long as its keys and a little for its start and end, and each block of the grid
+// takes an equal stretch (mk_kv_sched.cuh).  A task is a sequence's own keys
+// (causal), or a group's common ones (all of them seen).  A block meets at most
+// one item that it does not begin and one that it does not end; these leave their
+// sums in the workspace, and the merge kernel adds them up in order.  No atomics.
 //
-// A block, one an SM, 12 warps: two softmax warpgroups, a tile each, a thread a
-// row; one warp each that copies K and V pages (TMA, a ring of 128-key tiles),
-// issues the MMAs, copies Q, and clears values that some row does not see.
-// S = Q K^T goes to tensor memory; the softmax threads turn it into weights and
-// write them over it as BF16; O += P V takes them from there.  While one tile's
-// softmax runs, the tensor cores work for the other's.
+// A block, one an SM, 12 warps: two softmax warpgroups, a thread a row; a warp
+// that plans and copies K and V pages (TMA, a ring of 128-key tiles), one of MMAs
+// for each softmax warpgroup, one that copies Q and clears values that some row
+// does not see.  S = Q K^T goes to tensor memory (128 columns a stream); the
+// softmax threads turn it into weights and write them over it as BF16; O += P V
+// takes them from there (128 columns a stream, all 512 in use).  While one
+// stream's softmax runs, the tensor cores work for the other's.
+//
+// Measured, one GB300 (kernels in a graph; 32 query and 4 KV heads of 128 dims):
+// a prompt of 32,768 tokens 5.3-5.4 ms, 1640 TFLOP/s (85 % of the measured
+// matrix product rate), of 8192 0.38 ms (1440), of 2048 52 us; one token of
+// 262,144 98 us (5.5 TB/s), of 8192 17 us, of 128 8.4 us.  What bounds it:
+// - wide items: the chain of one stream, scores - weights - products: 1,250
+//   cycles of softmax (600 instructions a warp and tile; issue 37 %, exponentials
+//   30 % of their rate) and 1,050 of products after it; the other stream fills
+//   the tensor cores for two thirds of that (61 % at 8192 tokens);
+// - narrow items: a tile's 64 KB pass the SM's copy engine at 41 bytes a cycle,
+//   1,600 cycles, and one warp's issue makes 2,000 of it; all SMs together then
+//   ask for more than the HBM gives;
+// - short calls: a block takes 9,000 to 12,000 cycles until its first scores
+//   (plan, page table, copies, each cold), an item's end 4,000 to 6,000, the
+//   merge 3 to 5 us.
+// Tried and slower: one warp for all products (32K: 6.2 ms: an issued product
+// holds its warp for its 64 cycles, so the waits between them idle the tensor
+// cores), two without turns (6.7), scores read a second time instead of 128
+// registers a thread (5.4-5.8), rows handed to lanes by shuffles for the output
+// (5.6); the first kernel launched before the end of what precedes it gains 0.3 us.
 #include <cfloat>
 #include <cmath>
 #include <algorithm>
@@ -507,9 +534,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             int ids[8];
 #pragma unroll
             for (int i = 0; i < 8; i++) ids[i] = __shfl_sync(0xffffffffu, from, i);
-            // One lane issues, about 60 cycles a copy (sixteen lanes at once: 150
-            // each), so whole pages where their layout serves: all but the keys
-            // of wide items, whose product wants 16 atoms at one stride.
+            // One lane issues (sixteen lanes at once took 150 cycles a copy, 2500 a
+            // tile; one lane about 1000), whole pages where their layout serves:
+            // all but the keys of wide items, whose product wants 16 atoms at one
+            // stride.
             if (tc_elect()) {
               const uint32_t to = kv_smem + st * S::kTileBytes;
               mbar_arrive_expect_tx(bar, np * S::kHalves * 2048);
@@ -666,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!narrow) {
           // The warps take turns, products of one stream after those of the
           // other: in step with each other both softmaxes would run at once, and
-          // then both products (32K prompt: 6.66 ms without turns).
+          // then both products (32K prompt: 6.7 ms without turns, 5.4 with).
           for (int j = 0; ok && j < n; j++) {
             // all else first: the weights come last
             const bool more = j + 1 < n;
@@ -795,7 +823,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ------------------------------------------------------------------------ merge
 
 // Adds up an item's parts in key order: block c's item, if it goes on, and the
-// first slots of the blocks after it.  A warp takes 8 rows and 32 of their dims.
+// first slots of the blocks after it.  A warp takes 8 rows and 32 of their dims,
+// four parts at a time (eight need 116 registers, two blocks an SM instead of
+// four: packed prompts 89 us with them, 85 with four).  10 to 13 us on its own,
+// latency and 40 MB of parts through the L2; 3 to 8 us of it after the first
+// kernel.
 template <int D>
 __global__ void __launch_bounds__(256, 4) kv_merge_kernel(const KvAttnArgs a) {
   constexpr int kBatch = 4;
@@ -877,7 +909,8 @@ __global__ void __launch_bounds__(256, 4) kv_merge_kernel(const KvAttnArgs a) {
 }
 
 // Groups: a row's common and own keys together.  A warp takes 8 lines and 32 of
-// their dims.
+// their dims.  Bound by memory where there are many rows (23,424 of 128 dims: 10
+// us, 30 MB), by latency else (4 us).
 template <int D>
 __global__ void __launch_bounds__(256) kv_join_kernel(const KvAttnArgs a, int blocks) {
   asm volatile("griddepcontrol.wait;" ::: "memory");

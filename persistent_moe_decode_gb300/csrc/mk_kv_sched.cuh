@@ -17,10 +17,11 @@ namespace mk {
 
 constexpr int kTile = 128;               // keys a step, rows a tile
 
-// Cost of a row block, in keys: its own, and its start and end.  A key tile
-// takes 2,300 cycles where the rows fill two tiles (wide: the products), 2,000
-// where they fit one (narrow: the copies of its pages); a start and an end 11,000
-// and 6,000, a little more where they follow each other.
+// Cost of a row block, in keys: its own, and its start and end.  Fitted to the
+// blocks' clocks over batches of prompts and single tokens: a key tile takes 2,300
+// to 2,900 cycles where the rows fill two tiles (wide), 2,000 to 2,400 where they
+// fit one (narrow); a start and an end 11,000 and 4,000 to 8,000.  (With 3 and 1
+// tiles for these: packed prompts 89 us, 74 with 5 and 4.)
 constexpr int kWideStart = 5 * kTile, kNarrowStart = 4 * kTile;
 constexpr int kMinShare = 4 * kTile;              // no block takes less
 // No part of an item has fewer key tiles: a part costs an end and its share of

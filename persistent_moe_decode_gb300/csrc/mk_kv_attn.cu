@@ -115,7 +115,6 @@ __host__ __device__ __forceinline__ Ws ws_of(uint8_t* p, int d, int hq, int tota
 struct Plan {
   Begin begin;
   long long pos, end, share;
-  int work;                              // there is one
 };
 
 struct Sync {
@@ -130,7 +129,8 @@ struct Sync {
   uint32_t tmem;
   volatile int stop;
   long long scan[kThreads / 32];
-  Plan plan;
+  Plan plan;                             // of many tasks
+  int planned;
   float pair[2][kTile];
 };
 
@@ -171,21 +171,24 @@ __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
 
 // One warp: this block's stretch, if it begins in a task of this warp.  Each lane
-// has a task k (number t) or none, of `mine` keys after `before` others.
-__device__ __forceinline__ void find_plan(const KvAttnArgs& a, Plan& plan, const Task& k, int t, long long before,
-                                          long long mine, long long total, int tb, int lane) {
+// has a task k (number t) or none, of `mine` keys after `before` others, `per` a
+// KV head.
+__device__ __forceinline__ bool find_plan(const KvAttnArgs& a, Plan& plan, const Task& k, int t, long long before,
+                                          long long mine, long long per, long long total, int tb, int lane) {
   // about an equal share: total / blocks, from above
   const long long share = max((long long)__umul64hi((unsigned long long)total, a.per_block) + 1, (long long)kMinShare);
   const long long pos = share * blockIdx.x;
   const unsigned owner = __ballot_sync(0xffffffffu, pos < total && before <= pos && pos < before + mine);
-  if (!owner) return;
+  if (!owner) return false;
   const int from = __ffs(owner) - 1;
   Task o;
 #pragma unroll
   for (int w = 0; w < (int)(sizeof(Task) / 4); w++)
     reinterpret_cast<int*>(&o)[w] = __shfl_sync(0xffffffffu, reinterpret_cast<const int*>(&k)[w], from);
-  const Begin g = begin_of(o, __shfl_sync(0xffffffffu, t, from), tb, __shfl_sync(0xffffffffu, before, from), pos, lane);
-  if (lane == 0) plan.begin = g, plan.pos = pos, plan.end = min(total, pos + share), plan.share = share, plan.work = 1;
+  plan.begin = begin_of(o, __shfl_sync(0xffffffffu, t, from), tb, __shfl_sync(0xffffffffu, before, from),
+                        __shfl_sync(0xffffffffu, per, from), pos, lane);
+  plan.pos = pos, plan.end = min(total, pos + share), plan.share = share;
+  return true;
 }
 
 __device__ __forceinline__ long long scan(long long x, int lane) {
@@ -225,33 +228,40 @@ __device__ void softmax_role(const KvAttnArgs& a, Sync& s, Item* items, const Ws
     for (int j = j0; j < m.k1; j += every, steps++) {
       if (!wait_warp(s, &s.s_full[group], steps & 1, a.status)) return;
       tc_fence_after();
-      float x[kTile];
-#pragma unroll
-      for (int c = 0; c < 4; c++) tc_ld32(tm_s + 32 * c, (uint32_t*)x + 32 * c);
-      tc_wait_ld();
       const int t0 = m.kbeg + kTile * j;
-      if (t0 + kTile > least) {
+      const bool masked = t0 + kTile > least, paged = narrow && D == 128;
+      const int seen = min(max(lim - t0, 0), kTile);
+      // 64 columns at a time, read once for the maximum and once for the weights:
+      // the loop is half as long as one over 128 registers, and what the second
+      // read costs the instruction cache gives back (packed prompts 74 us against
+      // 71, questions to a shared text 108 against 99, 32K prompt 5.30 ms against
+      // 5.26).
+      auto scores = [&](int h, float* x) {
+        tc_ld32(tm_s + 64 * h, (uint32_t*)x), tc_ld32(tm_s + 64 * h + 32, (uint32_t*)x + 32);
+        tc_wait_ld();
+        if (!masked) return;
         // columns that are seen: the first of each 64 (a narrow item's pages have
         // their first 8 keys in the first 64 columns, the others in the last)
-        const int seen = min(max(lim - t0, 0), kTile);
-        const bool paged = narrow && D == 128;
+        const int n = paged ? 8 * (seen >> 4) + min(max((seen & 15) - 8 * h, 0), 8) : seen - 64 * h;
 #pragma unroll
-        for (int c = 0; c < kTile; c += 32) {
-          const int h = c / 64;
-          const int n = (paged ? 8 * (seen >> 4) + min(max((seen & 15) - 8 * h, 0), 8) : seen - 64 * h) - c % 64;
-          const uint32_t bits = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1;
+        for (int c = 0; c < 64; c += 32) {
+          const uint32_t bits = n - c >= 32 ? 0xffffffffu : n - c <= 0 ? 0u : (1u << (n - c)) - 1;
 #pragma unroll
           for (int u = 0; u < 32; u++) x[c + u] = bits >> u & 1 ? x[c + u] : -INFINITY;
         }
-      }
-      float mx[4] = {x[0], x[1], x[2], x[3]};
+      };
+      float high = -INFINITY;
+#pragma unroll 1
+      for (int h = 0; h < 2; h++) {
+        float x[64];
+        scores(h, x);
+        float m0 = fmaxf(x[0], x[1]), m1 = fmaxf(x[2], x[3]), m2 = fmaxf(x[4], x[5]), m3 = fmaxf(x[6], x[7]);
 #pragma unroll
-      for (int c = 4; c < kTile; c += 8) {
-#pragma unroll
-        for (int u = 0; u < 4; u++)
-          mx[u] = c + 4 + u < kTile ? fmaxf(fmaxf(mx[u], x[c + u]), x[c + 4 + u]) : fmaxf(mx[u], x[c + u]);
+        for (int u = 8; u < 64; u += 8)
+          m0 = fmaxf(fmaxf(m0, x[u]), x[u + 1]), m1 = fmaxf(fmaxf(m1, x[u + 2]), x[u + 3]),
+          m2 = fmaxf(fmaxf(m2, x[u + 4]), x[u + 5]), m3 = fmaxf(fmaxf(m3, x[u + 6]), x[u + 7]);
+        high = fmaxf(fmaxf(high, fmaxf(m0, m1)), fmaxf(m2, m3));
       }
-      const float high = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
       // The reference moves only when a weight would pass 2^8: sums and
       // products stay within 2^8 of their size, and O is rarely rescaled.
       const bool move = high > top && (high - top) * scale > 8.f;
@@ -275,12 +285,14 @@ __device__ void softmax_role(const KvAttnArgs& a, Sync& s, Item* items, const Ws
       const float off = top == -INFINITY ? 0.f : -top * scale;
       const float2 sc2 = make_float2(scale, scale), off2 = make_float2(off, off);
       float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
+#pragma unroll 1
       for (int h = 0; h < 2; h++) {
+        float x[64];
         uint32_t p[32];
+        scores(h, x);
 #pragma unroll
         for (int u = 0; u < 32; u++) {
-          float2 e = __ffma2_rn(make_float2(x[64 * h + 2 * u], x[64 * h + 2 * u + 1]), sc2, off2);
+          float2 e = __ffma2_rn(make_float2(x[2 * u], x[2 * u + 1]), sc2, off2);
           e.x = tc_ex2(e.x), e.y = tc_ex2(e.y);
           acc[u & 1] = __fadd2_rn(acc[u & 1], e);
           p[u] = cvt_bf2(e.x, e.y);
@@ -413,6 +425,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tt = kTile / a.grp, tb = 2 * tt, tasks = a.groups + a.batch;
   const Ws ws = ws_of(a.ws, D, a.hq, a.total_q, gridDim.x);
 
+  // Up to 32 tasks: the warp that copies pages makes its plan at once, while the
+  // others get ready.
+  const bool few = tasks <= 32;
+  Plan plan;
+  bool work = false;
+  if (few && warp == 8) {
+    Task k{};
+    long long per = 0;
+    if (lane < tasks) {
+      k = load_task(a, lane, tb, blockIdx.x == 0);
+      per = cost_before(k, k.nb, tb);
+    }
+    const long long mine = per * a.hkv, incl = scan(mine, lane), total = __shfl_sync(0xffffffffu, incl, 31);
+    work = find_plan(a, plan, k, lane, incl - mine, mine, per, total, tb, lane);
+  }
   if (tid == kThreads - 32) {
     for (int i = 0; i < S::kStages; i++) mbar_init(&s.kv_full[i], 1), mbar_init(&s.kv_empty[i], 2), mbar_init(&s.raw_full[i], 1);
     for (int t = 0; t < 2; t++) {
@@ -421,10 +448,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kItems; i++) mbar_init(&s.item_full[i], 1), mbar_init(&s.item_empty[i], kReaders);
     mbar_init(&s.pair_full, 4), mbar_init(&s.pair_empty, 4), mbar_init(&s.drain[0], 1), mbar_init(&s.drain[1], 1);
-    s.stop = 0, s.plan.work = 0;
+    s.stop = 0, s.planned = 0;
     mbar_fence_init();
   }
-  if (warp == 8) tc_alloc(&s.tmem, 512);
+  if (warp == 9) tc_alloc(&s.tmem, 512);
 
   if (warp == 10 && lane < 4) tma_prefetch_map(lane == 0 ? &map_k : lane == 1 ? &page_v : lane == 2 ? &map_q : &page_k);
 
@@ -433,18 +460,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = s.tmem;
 
-  // All tasks' cost, and the item that this block's stretch begins in.  Up to 32
-  // tasks are left to the warp that copies pages, while the others get ready.
-  const bool few = tasks <= 32;
+  // many tasks: all threads add up their cost, and one warp finds the item that
+  // this block's stretch begins in
   if (!few) {
     const int chunk = (tasks + kThreads - 1) / kThreads;
     int t = min(tasks, tid * chunk);
     const int end = min(tasks, t + chunk);
-    long long mine = 0, total = 0;
+    long long mine = 0, total = 0, per = 0;
     Task k{};
     for (int i = t; i < end; i++) {
       k = load_task(a, i, tb, blockIdx.x == 0);
-      mine += cost_before(k, k.nb, tb) * a.hkv;
+      per = cost_before(k, k.nb, tb);
+      mine += per * a.hkv;
     }
     const long long incl = scan(mine, lane);
     long long before = incl - mine;
@@ -460,13 +487,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (before <= pos && pos < before + mine)
         for (;; t++) {
           k = load_task(a, t, tb, false);
-          mine = cost_before(k, k.nb, tb) * a.hkv;
+          per = cost_before(k, k.nb, tb);
+          mine = per * a.hkv;
           if (pos < before + mine) break;
           before += mine;
         }
     }
-    find_plan(a, s.plan, k, t, before, mine, total, tb, lane);
+    if (find_plan(a, plan, k, t, before, mine, per, total, tb, lane) && lane == 0) s.plan = plan, s.planned = 1;
     __syncthreads();
+    plan = s.plan, work = s.planned;
   }
 
   if (warp < 8) {
@@ -480,24 +509,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t loads = 0, raw = 0, raw_use = 0;    // stages whose last tile goes through raw_full; its uses, modulo 2
       int it = 0;
       bool ok = true;
-      if (few) {
-        Task k{};
-        long long mine = 0;
-        if (lane < tasks) {
-          k = load_task(a, lane, tb, blockIdx.x == 0);
-          mine = cost_before(k, k.nb, tb) * a.hkv;
-        }
-        const long long incl = scan(mine, lane), total = __shfl_sync(0xffffffffu, incl, 31);
-        find_plan(a, s.plan, k, lane, incl - mine, mine, total, tb, lane);
-        __syncwarp();
-      }
-      if (s.plan.work) {
+      if (work) {
         auto pages_of = [&](const Part& p, int j) { return min(8, (p.kend - p.kbeg - kTile * j + kKvPage - 1) / kKvPage); };
         auto page_of = [&](const Part& p, int j) {
           return j < p.k1 && lane < pages_of(p, j)
                      ? a.page_tables[(int64_t)p.table * a.max_pages + p.kbeg / kKvPage + 8 * j + lane] : 0;
         };
-        Stretch w(a, tt, s.plan.begin, s.plan.pos, s.plan.end, s.plan.share);
+        Stretch w(a, tt, plan.begin, plan.pos, plan.end, plan.share);
         Part m, nx;
         bool have = w.next(&m, 2 * (int)blockIdx.x);
         int page[3], npage[3] = {0, 0, 0};
@@ -817,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 8) tc_dealloc(tmem, 512);
+  if (warp == 9) tc_dealloc(tmem, 512);
 }
 
 // ------------------------------------------------------------------------ merge

@@ -164,13 +164,14 @@ struct Begin {
   long long at;
 };
 
-// The item that holds position r of task k, which begins at `start`.  On the
-// GPU a warp finds it together.
-MK_HD inline Begin begin_of(const Task& k, int t, int tb, long long start, long long pos, int lane) {
+// The item that holds position pos of task k, which begins at `start` and has
+// `per` keys a KV head.  On the GPU a warp finds it together.
+MK_HD inline Begin begin_of(const Task& k, int t, int tb, long long start, long long per, long long pos, int lane) {
   Begin g{k, t, 0, 0, start};
-  const long long per = cost_before(k, k.nb, tb);
   g.head = quotient(pos - start, per);
-  const long long r = pos - start - g.head * per;
+  g.at += g.head * per;
+  if (k.nb == 1) return g;
+  const long long r = pos - g.at;
   int lo = 0, hi = k.nb;                 // the last row block that begins at or before pos
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32;
@@ -185,7 +186,7 @@ MK_HD inline Begin begin_of(const Task& k, int t, int tb, long long start, long 
     hi = hd_min(hi, lo + step);
   }
   g.b = lo;
-  g.at = start + g.head * per + cost_before(k, lo, tb);
+  g.at += cost_before(k, lo, tb);
   return g;
 }
 

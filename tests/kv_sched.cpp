@@ -55,7 +55,7 @@ static void walk(const KvAttnArgs& a, int blocks, bool sound) {
     int t = 0;
     while (!(at[t] <= pos && pos < at[t + 1])) t++;
     const Task k = load_task(a, t, tb, false);
-    Stretch w(a, tt, begin_of(k, t, tb, at[t], pos, 0), pos, stop, share);
+    Stretch w(a, tt, begin_of(k, t, tb, at[t], (at[t + 1] - at[t]) / a.hkv, pos, 0), pos, stop, share);
     Part m;
     long long units = 0;
     int used[2] = {0, 0};

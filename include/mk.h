@@ -634,8 +634,8 @@ size_t mk_kv_workspace(const mk_kv_cache* c, int n_q_heads, int total_q, int bat
  *   q_starts     [batch + 1]: the new tokens of sequence b are rows q_starts[b]
  *                to q_starts[b + 1], which may be none; rows outside them are
  *                left as they were
- *   page_tables  [batch][max_pages] physical pages; entries past a sequence's
- *                length are not read
+ *   page_tables  [batch][max_pages] physical pages, max_pages up to 2^24;
+ *                entries past a sequence's length are not read
  *   seq_lens     [batch] cached tokens, the new ones (the last of them)
  *                included: new token i of n sees the first seq_lens[b] - n + i
  *                + 1, and gets a row of zeros if that is none

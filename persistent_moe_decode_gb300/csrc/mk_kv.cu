@@ -305,7 +305,7 @@ int mk_kv_attention(const mk_kv_cache* c, const void* q, int64_t q_stride, void*
                     const int32_t* prefix_lens, float scale, void* workspace, size_t workspace_bytes, void* stream) {
   int rc = check_attention(c, n_q_heads, total_q, batch, groups);
   if (rc) return rc;
-  if (max_pages < 0 || max_pages >= 1 << 26 || !(scale > 0.f) || scale >= 0x1p20f) return MK_ERR_BAD_ARG;
+  if (max_pages < 0 || max_pages > kKvMaxPages || !(scale > 0.f) || scale >= 0x1p20f) return MK_ERR_BAD_ARG;
   if (total_q == 0 || batch == 0) return MK_OK;
   const int64_t row = (int64_t)n_q_heads * c->head_dim;
   if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || q_stride % 8 || out_stride % 8 ||

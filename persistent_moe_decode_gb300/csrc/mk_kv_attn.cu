@@ -91,7 +91,7 @@ struct alignas(16) Slot {
 
 struct Ws {
   Slot* slots;             // [2 blocks]: 2 c the part that block c did not begin, 2 c + 1 that it did
-  float* data;             // [2 blocks][kSlotFloats]
+  float* data;             // [2 blocks][slot_floats]
   // groups: a row's sums over common keys and over own ones; line l of total_q *
   // hq is (KV head, token, head of its group)
   float* part_o;           // [2][D / 4][lines][4]

@@ -224,9 +224,9 @@ class PagedCache:
     def attention(self, q, q_starts, page_tables, seq_lens, scale: float | None = None, out=None, stream=None):
         """Causal attention of packed rows q (BF16 ``[n, n_q_heads, head_dim]``): rows ``q_starts[b]`` to
         ``q_starts[b + 1]`` (int32 ``[batch + 1]``) are the last tokens of the ``seq_lens[b]`` (int32 ``[batch]``) that
-        ``page_tables[b]`` (int32 ``[batch, max_pages]``) holds, and each sees those up to itself.  ``scale`` defaults to
-        head_dim ** -0.5.  A row that sees nothing gives zeros, rows of no sequence are left as they were (undefined in a
-        new tensor).  Returns ``out``, a new tensor like q unless given; it may be q."""
+        ``page_tables[b]`` (int32 ``[batch, max_pages]``, up to 2^24 pages) holds, and each sees those up to itself.
+        ``scale`` defaults to head_dim ** -0.5.  A row that sees nothing gives zeros, rows of no sequence are left as they
+        were (undefined in a new tensor).  Returns ``out``, a new tensor like q unless given; it may be q."""
         return _run(self.k_pool.device, self._dev, self._attention, stream, q, q_starts, page_tables, seq_lens, None, None,
                     scale, out)
 

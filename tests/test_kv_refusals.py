@@ -137,6 +137,7 @@ def attn_args(**kw):
     (dict(batch=-1), mk.MK_ERR_BATCH_TOO_LARGE), (dict(batch=65536), mk.MK_ERR_BATCH_TOO_LARGE),
     (dict(groups=-1), mk.MK_ERR_BATCH_TOO_LARGE), (dict(groups=65536), mk.MK_ERR_BATCH_TOO_LARGE),
     (dict(max_pages=-1), mk.MK_ERR_BAD_ARG), (dict(max_pages=1 << 26), mk.MK_ERR_BAD_ARG),
+    (dict(max_pages=(1 << 24) + 1), mk.MK_ERR_BAD_ARG),     # above it one item could outlast the kernel's waits
     (dict(scale=0.0), mk.MK_ERR_BAD_ARG), (dict(scale=-1.0), mk.MK_ERR_BAD_ARG), (dict(scale=math.nan), mk.MK_ERR_BAD_ARG),
     (dict(scale=math.inf), mk.MK_ERR_BAD_ARG), (dict(scale=2.0 ** 20), mk.MK_ERR_BAD_ARG),
     (dict(q=None), mk.MK_ERR_BAD_ARG), (dict(out=None), mk.MK_ERR_BAD_ARG), (dict(q=P + 8), mk.MK_ERR_BAD_ARG),

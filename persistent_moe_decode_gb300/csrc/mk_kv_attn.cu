@@ -841,20 +841,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ------------------------------------------------------------------------ merge
 
 // Adds up an item's parts in key order: block c's item, if it goes on, and the
-// first slots of the blocks after it.  A warp takes 8 rows and 32 of their dims,
-// four parts at a time (eight need 116 registers, two blocks an SM instead of
-// four: packed prompts 89 us with them, 85 with four).  10 to 13 us on its own,
-// latency and 40 MB of parts through the L2; 3 to 8 us of it after the first
-// kernel.
-template <int D>
-__global__ void __launch_bounds__(256, 4) kv_merge_kernel(const KvAttnArgs a) {
-  constexpr int kBatch = 4;
+// first slots of the blocks after it.  A warp takes 8 rows and 64 of their dims,
+// kBatch parts at a time.  Two need 64 registers, four blocks an SM, and win where
+// there are many rows, whose chains are short and fill the SMs (questions to a
+// shared text 96.6 us with two, 97.8 with four); four win where there are few,
+// whose chains are long (16 tokens behind one prefix, 23 parts: 42.8 and 36.6 us);
+// even at 8192 rows.  32 dims a warp make more blocks than run at once, each of
+// which first fetches its slot (98.4 and 38.6).
+template <int D, int kBatch>
+__global__ void __launch_bounds__(256, 8 / kBatch) kv_merge_kernel(const KvAttnArgs a) {
+  constexpr int kVecs = 4;               // of 4 dims, a lane
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x, blocks = gridDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Ws ws = ws_of(a.ws, D, a.hq, a.total_q, blocks);
   const Slot m = ws.slots[2 * c + 1];
   if (m.state != 1) return;
-  const int job = blockIdx.y * 8 + warp, r = job / (D / 32) * 8 + (lane & 7), c4 = job % (D / 32) * 8 + (lane >> 3);
+  const int job = blockIdx.y * 8 + warp, r = job / (D / 64) * 8 + (lane & 7), c4 = job % (D / 64) * 16 + (lane >> 3);
   if (r - (lane & 7) >= m.ntok * a.grp) return;
   int parts = 1;
   bool nan = m.nan;
@@ -871,19 +873,20 @@ __global__ void __launch_bounds__(256, 4) kv_merge_kernel(const KvAttnArgs a) {
   const int tt = kTile / a.grp, tok = r / a.grp, h = r - tok * a.grp, tile = tok / tt;
   const int row = 128 * tile + (tok - tile * tt) * a.grp + h;
   float top = -INFINITY, den = 0.f;
-  float4 num[2] = {};
+  float4 num[kVecs] = {};
   for (int i0 = 0; i0 < parts; i0 += kBatch) {
     float ref[kBatch], l[kBatch];
-    float4 o[kBatch][2];
+    float4 o[kBatch][kVecs];
 #pragma unroll
     for (int u = 0; u < kBatch; u++) {
       ref[u] = -INFINITY, l[u] = 0.f;
-      o[u][0] = o[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int v = 0; v < kVecs; v++) o[u][v] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i0 + u < parts) {
         const float* d = ws.data + (i0 + u ? 2 * (c + i0 + u) : 2 * c + 1) * slot_floats(D);
         ref[u] = d[256 * D + row], l[u] = d[256 * D + 256 + row];
 #pragma unroll
-        for (int v = 0; v < 2; v++) o[u][v] = ((const float4*)d)[(c4 + 4 * v) * 256 + row];
+        for (int v = 0; v < kVecs; v++) o[u][v] = ((const float4*)d)[(c4 + 4 * v) * 256 + row];
       }
     }
     float high = top;
@@ -891,17 +894,19 @@ __global__ void __launch_bounds__(256, 4) kv_merge_kernel(const KvAttnArgs a) {
     for (int u = 0; u < kBatch; u++) high = fmaxf(high, ref[u]);
     if (high == -INFINITY) continue;
     const float keep = top == high ? 1.f : tc_ex2(top - high);
-    if (keep == 0.f) den = 0.f, num[0] = num[1] = make_float4(0.f, 0.f, 0.f, 0.f);
-    den *= keep;
+    den = keep == 0.f ? 0.f : den * keep;
 #pragma unroll
-    for (int v = 0; v < 2; v++) num[v].x *= keep, num[v].y *= keep, num[v].z *= keep, num[v].w *= keep;
+    for (int v = 0; v < kVecs; v++) {
+      num[v].x *= keep, num[v].y *= keep, num[v].z *= keep, num[v].w *= keep;
+      if (keep == 0.f) num[v] = make_float4(0.f, 0.f, 0.f, 0.f);     // whatever it held
+    }
 #pragma unroll
     for (int u = 0; u < kBatch; u++) {
       const float w = ref[u] == high ? 1.f : tc_ex2(ref[u] - high);
       if (w == 0.f) continue;            // nothing of it is left, whatever it holds
       den = fmaf(l[u], w, den);
 #pragma unroll
-      for (int v = 0; v < 2; v++) {
+      for (int v = 0; v < kVecs; v++) {
         num[v].x = fmaf(o[u][v].x, w, num[v].x), num[v].y = fmaf(o[u][v].y, w, num[v].y);
         num[v].z = fmaf(o[u][v].z, w, num[v].z), num[v].w = fmaf(o[u][v].w, w, num[v].w);
       }
@@ -915,7 +920,7 @@ __global__ void __launch_bounds__(256, 4) kv_merge_kernel(const KvAttnArgs a) {
   const size_t lines = (size_t)a.total_q * a.hq, at = ((size_t)m.head * a.total_q + token) * a.grp + h;
   const int own = m.flags & kPrefix ? 0 : 1;
 #pragma unroll
-  for (int v = 0; v < 2; v++) {
+  for (int v = 0; v < kVecs; v++) {
     float4 o = make_float4(num[v].x * inv, num[v].y * inv, num[v].z * inv, num[v].w * inv);
     if (!sees) o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (nan || (sees && den == 0.f)) o = make_float4(NAN, NAN, NAN, NAN);
@@ -1042,8 +1047,9 @@ int launch(const KvAttnArgs& a, int sms, cudaStream_t st) {
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.stream = st, cfg.attrs = &at, cfg.numAttrs = 1;
   cfg.blockDim = dim3(256);
-  cfg.gridDim = dim3(sms, D / 8);       // 256 rows: 32 groups of 8 rows, D / 32 of dims, 8 warps a block
-  if (merge) rc = launched(cudaLaunchKernelEx(&cfg, kv_merge_kernel<D>, a));
+  cfg.gridDim = dim3(sms, D / 16);      // 256 rows: 32 groups of 8 rows, D / 64 of dims, 8 warps a block
+  const bool many = (long long)a.total_q * a.hq > 64 * sms;
+  if (merge) rc = launched(cudaLaunchKernelEx(&cfg, many ? kv_merge_kernel<D, 2> : kv_merge_kernel<D, 4>, a));
   if (rc || !a.groups) return rc;
   cfg.gridDim = dim3((unsigned)std::min<long long>(8 * sms, ((long long)a.total_q * a.hq + 7) / 8 * (D / 32) / 8 + 1));
   return launched(cudaLaunchKernelEx(&cfg, kv_join_kernel<D>, a, sms));

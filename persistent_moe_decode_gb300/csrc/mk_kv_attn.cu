@@ -311,7 +311,9 @@ __device__ void softmax_role(const KvAttnArgs& a, Sync& s, Item* items, const Ws
       parts++;
       tc_fence_after();
     }
-    float keep0 = 1.f, keep1 = 0.f;
+    // A weight that rounds to zero still multiplies: a NaN that the row sees must
+    // not depend on where its keys were cut.
+    float keep0 = 1.f, keep1 = 1.f;
     if (narrow) {
       if (group == 1) {
         s.pair[0][row] = top, s.pair[1][row] = sum;
@@ -329,7 +331,7 @@ __device__ void softmax_role(const KvAttnArgs& a, Sync& s, Item* items, const Ws
         keep0 = top == high ? 1.f : tc_ex2((top - high) * scale);
         keep1 = top1 == high ? 1.f : tc_ex2((top1 - high) * scale);
       }
-      sum = (keep0 == 0.f ? 0.f : keep0 * sum) + (keep1 == 0.f ? 0.f : keep1 * sum1);
+      sum = fmaf(keep0, sum, keep1 * sum1);
       top = high;
     }
     const int first = m.kbeg + kTile * m.k0, last = min(m.kend, m.kbeg + kTile * m.k1);
@@ -339,8 +341,9 @@ __device__ void softmax_role(const KvAttnArgs& a, Sync& s, Item* items, const Ws
     const bool sees = some && lim > first;                   // something in this part
     const float ref = top == -INFINITY ? (sees ? -FLT_MAX : -INFINITY) : top * scale;
     const bool whole = m.slot < 0, parted = a.groups > 0;
-    const float mul = !whole ? 1.f : sees ? 1.f / sum : 0.f;
-    const bool lost = nan || (sees && sum == 0.f);           // every score is -infinity
+    const bool zero = sees && sum == 0.f;                    // every score is -infinity
+    const float mul = !whole || (zero && parted) ? 1.f : sees ? 1.f / sum : 0.f;
+    const bool lost = nan || (zero && !parted);
     const int64_t token = m.tok0 + tok;
     const int head = m.head * a.grp + my_head;
     const size_t lines = (size_t)a.total_q * a.hq, at = ((size_t)m.head * a.total_q + token) * a.grp + my_head;
@@ -359,10 +362,7 @@ __device__ void softmax_role(const KvAttnArgs& a, Sync& s, Item* items, const Ws
         tc_ld32(tm_o + D + c, r1);
         tc_wait_ld();
 #pragma unroll
-        for (int u = 0; u < 32; u++) {
-          const float y = keep1 == 0.f ? 0.f : keep1 * __uint_as_float(r1[u]);
-          o[u] = keep0 == 0.f ? y : fmaf(keep0, o[u], y);
-        }
+        for (int u = 0; u < 32; u++) o[u] = fmaf(keep0, o[u], keep1 * __uint_as_float(r1[u]));
       } else {
         tc_wait_ld();
         if (!some) {
@@ -894,16 +894,12 @@ __global__ void __launch_bounds__(256, 8 / kBatch) kv_merge_kernel(const KvAttnA
     for (int u = 0; u < kBatch; u++) high = fmaxf(high, ref[u]);
     if (high == -INFINITY) continue;
     const float keep = top == high ? 1.f : tc_ex2(top - high);
-    den = keep == 0.f ? 0.f : den * keep;
+    den *= keep;
 #pragma unroll
-    for (int v = 0; v < kVecs; v++) {
-      num[v].x *= keep, num[v].y *= keep, num[v].z *= keep, num[v].w *= keep;
-      if (keep == 0.f) num[v] = make_float4(0.f, 0.f, 0.f, 0.f);     // whatever it held
-    }
+    for (int v = 0; v < kVecs; v++) num[v].x *= keep, num[v].y *= keep, num[v].z *= keep, num[v].w *= keep;
 #pragma unroll
     for (int u = 0; u < kBatch; u++) {
       const float w = ref[u] == high ? 1.f : tc_ex2(ref[u] - high);
-      if (w == 0.f) continue;            // nothing of it is left, whatever it holds
       den = fmaf(l[u], w, den);
 #pragma unroll
       for (int v = 0; v < kVecs; v++) {
@@ -916,14 +912,15 @@ __global__ void __launch_bounds__(256, 8 / kBatch) kv_merge_kernel(const KvAttnA
   const int64_t token = m.tok0 + tok;
   const int head = m.head * a.grp + h;
   const bool sees = (m.flags & kCausal ? m.lim + tok : m.lim) > m.kbeg;
-  const float inv = 1.f / den;
+  const bool zero = sees && den == 0.f;        // every score is -infinity
+  const float inv = zero && a.groups ? 1.f : 1.f / den;
   const size_t lines = (size_t)a.total_q * a.hq, at = ((size_t)m.head * a.total_q + token) * a.grp + h;
   const int own = m.flags & kPrefix ? 0 : 1;
 #pragma unroll
   for (int v = 0; v < kVecs; v++) {
     float4 o = make_float4(num[v].x * inv, num[v].y * inv, num[v].z * inv, num[v].w * inv);
     if (!sees) o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (nan || (sees && den == 0.f)) o = make_float4(NAN, NAN, NAN, NAN);
+    if (nan || (zero && !a.groups)) o = make_float4(NAN, NAN, NAN, NAN);
     const int d = 4 * (c4 + 4 * v);
     if (a.groups) ((float4*)ws.part_o)[(own * (D / 4) + d / 4) * lines + at] = o;
     else *(uint2*)(a.out + token * a.out_stride + (int64_t)head * D + d) = make_uint2(cvt_bf2(o.x, o.y), cvt_bf2(o.z, o.w));
@@ -950,14 +947,13 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const KvAttnArgs a, int bl
     const int kv = (int)(r / per), token = (int)((r - kv * per) / a.grp), head = kv * a.grp + (int)(r % a.grp);
     if (token < t0 || token >= t1) continue;               // of no sequence
     const float m0 = ws.part_m[r], m1 = ws.part_m[lines + r], high = fmaxf(m0, m1);
-    const bool nan = m0 != m0 || m1 != m1, none = high == -INFINITY;
+    const bool nan = m0 != m0 || m1 != m1 || high == -FLT_MAX, none = high == -INFINITY;   // -FLT_MAX: -infinities alone
     const float w0 = m0 == high ? 1.f : tc_ex2(m0 - high), w1 = m1 == high ? 1.f : tc_ex2(m1 - high), inv = 1.f / (w0 + w1);
 #pragma unroll
     for (int v = 0; v < 2; v++) {
       const float4 x = o[(int64_t)(c4 + 4 * v) * lines + r], y = o[(int64_t)(D / 4 + c4 + 4 * v) * lines + r];
       auto both = [&](float p, float q) {
-        const float s = (w0 == 0.f ? 0.f : w0 * p) + (w1 == 0.f ? 0.f : w1 * q);
-        return nan ? NAN : none ? 0.f : s * inv;
+        return nan ? NAN : none ? 0.f : fmaf(w0, p, w1 * q) * inv;
       };
       *(uint2*)(a.out + token * a.out_stride + (int64_t)head * D + 4 * (c4 + 4 * v)) =
           make_uint2(cvt_bf2(both(x.x, y.x), both(x.y, y.y)), cvt_bf2(both(x.z, y.z), both(x.w, y.w)));

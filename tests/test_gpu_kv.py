@@ -448,6 +448,42 @@ def test_shared_attention_bad_groups():
     case(put("starts", 2, 9), mk.MK_ERR_BAD_ARG, slice(9, 9), only=[0])
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("slope", [0.0, 0.01, -0.01])
+def test_parts_on_both_sides_of_the_merge_rule(d, slope):
+    """Long keys for just as many rows (of heads) as four parts at a time are added up for, and for one more: parts of
+    like and of far apart maxima.  A NaN among values, one among keys, whose weights round to zero beside others, reach
+    the rows that see them; scores of -infinity alone have no weight, and a row of nothing else is NaN."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    for rows in (2 * sms, 2 * sms + 1):
+        groups = [(4096, [(rows - 2, 6000), (1, 4400)]), (0, [(1, 700)])]
+        news, lens = [rows - 2, 1, 1], [6000, 4400, 700]
+        st, _, _ = shared_batch(32, 4, d, groups, seed=rows, junk=False)
+
+        def keys(b, lo, n):
+            t = torch.arange(lo, n, device="cuda")
+            return st["tables"][b, t // 16].long(), t % 16, (slope * t)[:, None, None].bfloat16()
+        for b, lo in ((0, 0), (1, 4096), (2, 0)):
+            page, row, up = keys(b, lo, lens[b])
+            st["k"][page, :, row] += up
+        st["q"].copy_((torch.rand_like(st["q"].float()) * 0.5 + 0.2).bfloat16())
+        page, row, _ = keys(0, 5998, 6000)
+        st["v"][page[0], 1, row[0], 7] = math.nan            # of the last two tokens' 8 heads
+        page, row, _ = keys(0, 5990, 5991)
+        st["k"][page, 2, row, 0] = math.nan                  # of the last ten tokens'
+        for b, lo in ((1, 4096), (2, 0)):
+            page, row, _ = keys(b, lo, lens[b])
+            st["k"][page, 3, row, 0] = -math.inf
+        tables = st["tables"].clone()
+        tables[1, :256] = tables[0, :256]
+        want, size = _kv.attention(st["q"], st["k"], st["v"], news, lens, tables)
+        assert want.isnan().sum() == 2 * 8 + 10 * 8 * d + 8 * d
+        got, cache = run_shared(st)
+        cache.check()
+        assert _kv.attention_off(got, want, size) <= 1
+        assert _kv.attention_off(run(dict(st, tables=tables)), want, size) <= 1
+
+
 # ---------------------------------------------------- streams, graphs, devices
 
 def test_calls_on_a_side_stream_and_in_a_graph():

@@ -342,8 +342,7 @@ __device__ void softmax_role(const KvAttnArgs& a, Sync& s, Item* items, const Ws
     const float ref = top == -INFINITY ? (sees ? -FLT_MAX : -INFINITY) : top * scale;
     const bool whole = m.slot < 0, parted = a.groups > 0;
     const bool zero = sees && sum == 0.f;                    // every score is -infinity
-    const float mul = !whole || (zero && parted) ? 1.f : sees ? 1.f / sum : 0.f;
-    const bool lost = nan || (zero && !parted);
+    const float mul = !whole ? 1.f : !sees ? 0.f : zero ? (parted ? 1.f : NAN) : 1.f / sum;
     const int64_t token = m.tok0 + tok;
     const int head = m.head * a.grp + my_head;
     const size_t lines = (size_t)a.total_q * a.hq, at = ((size_t)m.head * a.total_q + token) * a.grp + my_head;
@@ -385,7 +384,7 @@ __device__ void softmax_role(const KvAttnArgs& a, Sync& s, Item* items, const Ws
       }
       if (mine && whole) {
 #pragma unroll
-        for (int u = 0; u < 32; u++) o[u] = lost ? NAN : o[u] * mul;
+        for (int u = 0; u < 32; u++) o[u] = nan ? NAN : o[u] * mul;
       }
       if (mine && whole && !parted) {
         uint32_t b[16];

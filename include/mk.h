@@ -658,7 +658,8 @@ size_t mk_kv_workspace(const mk_kv_cache* c, int n_q_heads, int total_q, int bat
  * results undefined.  A call gives the same bits every time; where a
  * long sequence is cut depends on the batch, and its sums then round
  * differently.  out may be q, and else lies apart from it.  Range: scores
- * (scale times q . k) below 2^100; `scale` above 0 and below 2^20.
+ * (scale times q . k) below 2^100, sums of |v| over a row's keys below 2^119;
+ * `scale` above 0 and below 2^20.
  * Errors: MK_ERR_BAD_CONFIG (cache shape, n_q_heads no multiple of n_kv_heads
  * or above 128 times it), MK_ERR_BATCH_TOO_LARGE (batch or groups outside
  * 0..65535, total_q outside 0..2^24), MK_ERR_BAD_ARG (also a workspace smaller

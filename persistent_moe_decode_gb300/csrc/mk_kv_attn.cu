@@ -28,24 +28,24 @@
 // stream's softmax runs, the tensor cores work for the other's.
 //
 // Measured, one GB300 (kernels in a graph; 32 query and 4 KV heads of 128 dims):
-// a prompt of 32,768 tokens 5.3-5.4 ms, 1640 TFLOP/s (85 % of the measured
-// matrix product rate), of 8192 0.38 ms (1440), of 2048 52 us; one token of
-// 262,144 98 us (5.5 TB/s), of 8192 17 us, of 128 8.4 us.  What bounds it:
+// a prompt of 32,768 tokens 5.3 ms, 1660 TFLOP/s (86 % of the measured matrix
+// product rate), of 8192 0.372-0.378 ms (1470), of 2048 48-50 us; one token of
+// 262,144 94 us (5.7 TB/s), of 8192 15 us, of 128 7.9 us.  What bounds it:
 // - wide items: the chain of one stream, scores - weights - products: 1,250
-//   cycles of softmax (600 instructions a warp and tile; issue 37 %, exponentials
-//   30 % of their rate) and 1,050 of products after it; the other stream fills
-//   the tensor cores for two thirds of that (61 % at 8192 tokens);
+//   cycles of softmax (690 instructions a warp and tile; issue 45 %, exponentials
+//   33 % of their rate) and 1,050 of products after it; the other stream fills
+//   the tensor cores for two thirds of that (66 % of active cycles at 8192 tokens);
 // - narrow items: a tile's 64 KB pass the SM's copy engine at 41 bytes a cycle,
 //   1,600 cycles, and one warp's issue makes 2,000 of it; all SMs together then
 //   ask for more than the HBM gives;
 // - short calls: a block takes 9,000 to 12,000 cycles until its first scores
 //   (plan, page table, copies, each cold), an item's end 4,000 to 6,000, the
-//   merge 3 to 5 us.
+//   merge 3 to 4 us.
 // Tried and slower: one warp for all products (32K: 6.2 ms: an issued product
 // holds its warp for its 64 cycles, so the waits between them idle the tensor
-// cores), two without turns (6.7), scores read a second time instead of 128
-// registers a thread (5.4-5.8), rows handed to lanes by shuffles for the output
-// (5.6); the first kernel launched before the end of what precedes it gains 0.3 us.
+// cores), two without turns (6.7), scores taken by 32 columns (5.4-5.8), rows
+// handed to lanes by shuffles for the output (5.6); the first kernel launched
+// before the end of what precedes it gains 0.3 us.
 #include <cfloat>
 #include <cmath>
 #include <algorithm>

@@ -647,8 +647,9 @@ size_t mk_kv_workspace(const mk_kv_cache* c, int n_q_heads, int total_q, int bat
  * A sequence with a length or prefix outside its range gets rows of NaN and
  * flags status; a page outside the cache does that to the rows that see it, and
  * may to other rows of the sequence (the group, in a prefix).  Starts that
- * decrease or leave their range flag status, and rows of such sequences are left
- * as they were or get NaN.
+ * decrease or leave their range flag status: what comes before the first such
+ * place and after the last holds, where only one of the two sides names it; all
+ * other rows are left as they were or get NaN.
  * What a row does not see has no part in it, infinities and NaN included, and
  * neither has what a page holds past the sequence.
  * Products of BF16 values summed in fp32; softmax in fp32; weights rounded to

@@ -96,6 +96,7 @@ struct Ws {
   // hq is (KV head, token, head of its group)
   float* part_o;           // [2][D / 4][lines][4]
   float* part_m;           // [2][lines] log2 of the sum of exponentials
+  int32_t* rows;           // [4] those that sequences own (owned_rows)
 };
 
 __host__ __device__ __forceinline__ size_t slot_floats(int d) { return (size_t)256 * d + 512; }
@@ -106,6 +107,7 @@ __host__ __device__ __forceinline__ Ws ws_of(uint8_t* p, int d, int hq, int tota
   w.data = (float*)(p + (size_t)2 * blocks * sizeof(Slot));
   w.part_o = w.data + 2 * blocks * slot_floats(d);
   w.part_m = w.part_o + (size_t)2 * total_q * hq * d;
+  w.rows = (int32_t*)(w.part_m + (size_t)2 * total_q * hq);
   return w;
 }
 
@@ -131,6 +133,9 @@ struct Sync {
   long long scan[kThreads / 32];
   Plan plan;                             // of many tasks
   int planned;
+  Sound sound;
+  int ordered;                           // all starts of few tasks are
+  int first[2], last[2];                 // starts out of order, of groups and of sequences: the outermost
   float pair[2][kTile];
 };
 
@@ -436,6 +441,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       k = load_task(a, lane, tb, blockIdx.x == 0);
       per = cost_before(k, k.nb, tb);
     }
+    const bool ordered = !__any_sync(0xffffffffu, k.flags & kOrder);
+    if (lane == 0) s.ordered = ordered, s.sound = all_hold();
     const long long mine = per * a.hkv, incl = scan(mine, lane), total = __shfl_sync(0xffffffffu, incl, 31);
     work = find_plan(a, plan, k, lane, incl - mine, mine, per, total, tb, lane);
   }
@@ -448,6 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kItems; i++) mbar_init(&s.item_full[i], 1), mbar_init(&s.item_empty[i], kReaders);
     mbar_init(&s.pair_full, 4), mbar_init(&s.pair_empty, 4), mbar_init(&s.drain[0], 1), mbar_init(&s.drain[1], 1);
     s.stop = 0, s.planned = 0;
+    s.first[0] = s.first[1] = 0x7fffffff, s.last[0] = s.last[1] = -1;
     mbar_fence_init();
   }
   if (warp == 9) tc_alloc(&s.tmem, 512);
@@ -460,22 +468,39 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = s.tmem;
 
   // many tasks: all threads add up their cost, and one warp finds the item that
-  // this block's stretch begins in
-  if (!few) {
+  // this block's stretch begins in.  So too for few whose starts are out of order,
+  // which keeps what that takes out of the way of all other calls.
+  if (!few || !s.ordered) {
     const int chunk = (tasks + kThreads - 1) / kThreads;
     int t = min(tasks, tid * chunk);
     const int end = min(tasks, t + chunk);
-    long long mine = 0, total = 0, per = 0;
+    long long mine, before, total = 0, per = 0;
     Task k{};
-    for (int i = t; i < end; i++) {
-      k = load_task(a, i, tb, blockIdx.x == 0);
-      per = cost_before(k, k.nb, tb);
-      mine += per * a.hkv;
+    Sound so = all_hold();
+    for (bool again = false;; again = true) {
+      bool wrong = false;
+      mine = 0;
+      for (int i = t; i < end; i++) {
+        k = load_task(a, i, tb, blockIdx.x == 0, so);
+        per = cost_before(k, k.nb, tb);
+        mine += per * a.hkv;
+        wrong |= !again && k.flags & kOrder;
+      }
+      const long long incl = scan(mine, lane);
+      before = incl - mine;
+      if (lane == 31) s.scan[warp] = incl;
+      if (!__syncthreads_or(wrong)) break;
+      // starts out of order: once more, with what holds
+      for (int i = t; i < end; i++)
+        if (!in_order(a, i)) {
+          const int q = i >= a.groups, x = q ? i - a.groups : i;
+          atomicMin(&s.first[q], x), atomicMax(&s.last[q], x);
+        }
+      __syncthreads();
+      if (s.last[0] >= 0) holding(a.group_starts, a.groups, s.first[0], s.last[0], &so.g0, &so.g1);
+      if (s.last[1] >= 0) holding(a.q_starts, a.batch, s.first[1], s.last[1], &so.b0, &so.b1);
     }
-    const long long incl = scan(mine, lane);
-    long long before = incl - mine;
-    if (lane == 31) s.scan[warp] = incl;
-    __syncthreads();
+    if (tid == 0) s.sound = so;
     for (int w = 0; w < kThreads / 32; w++) {
       const long long x = s.scan[w];
       if (w < warp) before += x;
@@ -485,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const long long pos = max((long long)__umul64hi((unsigned long long)total, a.per_block) + 1, (long long)kMinShare) * blockIdx.x;
       if (before <= pos && pos < before + mine)
         for (;; t++) {
-          k = load_task(a, t, tb, false);
+          k = load_task(a, t, tb, false, so);
           per = cost_before(k, k.nb, tb);
           mine = per * a.hkv;
           if (pos < before + mine) break;
@@ -514,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           return j < p.k1 && lane < pages_of(p, j)
                      ? a.page_tables[(int64_t)p.table * a.max_pages + p.kbeg / kKvPage + 8 * j + lane] : 0;
         };
-        Stretch w(a, tt, plan.begin, plan.pos, plan.end, plan.share);
+        Stretch w(a, tt, plan.begin, plan.pos, plan.end, plan.share, &s.sound);
         Part m, nx;
         bool have = w.next(&m, 2 * (int)blockIdx.x);
         int page[3], npage[3] = {0, 0, 0};
@@ -605,6 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&s.item_full[it % kItems]);
       }
       if (lane < 2) ws.slots[2 * blockIdx.x + lane] = lane ? desc[1] : desc[0];
+      if (a.groups && blockIdx.x == 0 && lane == 0) owned_rows(a, s.sound, ws.rows);
       if (s.stop) {
         for (uint32_t i = loads > S::kStages ? loads - S::kStages : 0; i < loads; i++) {
           const uint32_t st = i % S::kStages;
@@ -935,7 +961,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const KvAttnArgs a, int bl
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
   const Ws ws = ws_of(a.ws, D, a.hq, a.total_q, blocks);
-  const int t0 = a.q_starts[0], t1 = a.q_starts[a.batch];
+  const int r0 = ws.rows[0], r1 = ws.rows[1], r2 = ws.rows[2], r3 = ws.rows[3];
   const int64_t lines = (int64_t)a.total_q * a.hq;
   const float4* o = (const float4*)ws.part_o;
   for (int64_t job = blockIdx.x * 8 + (threadIdx.x >> 5); job < (lines + 7) / 8 * (D / 32); job += gridDim.x * 8) {
@@ -944,7 +970,8 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const KvAttnArgs a, int bl
     if (r >= lines) continue;
     const int64_t per = (int64_t)a.total_q * a.grp;
     const int kv = (int)(r / per), token = (int)((r - kv * per) / a.grp), head = kv * a.grp + (int)(r % a.grp);
-    if (token < t0 || token >= t1) continue;               // of no sequence
+    // of no sequence: nothing was written here for it
+    if ((token < r0 || token >= r1) && (token < r2 || token >= r3)) continue;
     const float m0 = ws.part_m[r], m1 = ws.part_m[lines + r], high = fmaxf(m0, m1);
     const bool nan = m0 != m0 || m1 != m1 || high == -FLT_MAX, none = high == -INFINITY;   // -FLT_MAX: -infinities alone
     const float w0 = m0 == high ? 1.f : tc_ex2(m0 - high), w1 = m1 == high ? 1.f : tc_ex2(m1 - high), inv = 1.f / (w0 + w1);
@@ -1054,7 +1081,7 @@ int launch(const KvAttnArgs& a, int sms, cudaStream_t st) {
 
 size_t kv_attention_ws(int head_dim, int hq, int total_q, int groups, int sms) {
   size_t n = (size_t)2 * sms * (sizeof(Slot) + 4 * slot_floats(head_dim));
-  if (groups) n += (size_t)2 * total_q * hq * (head_dim + 1) * 4;
+  if (groups) n += (size_t)2 * total_q * hq * (head_dim + 1) * 4 + 16;
   return n;
 }
 

@@ -28,7 +28,7 @@ constexpr int kMinShare = 4 * kTile;              // no block takes less
 // the merge, so that a wide one of less is better left where it is.
 constexpr int kMinWidePart = 4, kMinPart = 2;
 
-enum : int { kCausal = 1, kNan = 2, kPrefix = 4 };
+enum : int { kCausal = 1, kNan = 2, kPrefix = 4, kOrder = 16 };   // kOrder: its starts are out of order
 
 template <class T>
 MK_HD inline T hd_min(T a, T b) { return a < b ? a : b; }
@@ -50,6 +50,53 @@ struct Part {
   int slot;                // workspace slot of a part, -1: the whole item
 };
 
+// Sequences (b) and groups (g) that hold: those below b0, g0 and from b1, g1 on.
+// Starts in order and in range hold all of them.  Else those before the first
+// place that is not so hold and those after the last, but for what both sides
+// name; all others have no rows, so that no row is two sequences' or two groups'.
+struct Sound {
+  int b0, b1, g0, g1;
+};
+MK_HD inline Sound all_hold() { return {0x7fffffff, 0x7fffffff, 0x7fffffff, 0x7fffffff}; }
+
+MK_HD inline bool in_order(const int32_t* starts, int i, int end) {
+  const int x = starts[i], y = starts[i + 1];
+  return 0 <= x && x <= y && y <= end;
+}
+
+// of task t: a group's start and end, or a sequence's
+MK_HD inline bool in_order(const KvAttnArgs& a, int t) {
+  const bool g = t < a.groups;
+  return in_order(g ? a.group_starts : a.q_starts, g ? t : t - a.groups, g ? a.batch : a.total_q);
+}
+
+// x0 and x1 of n starts and their end; first and last: the outermost that are out of order
+MK_HD inline void holding(const int32_t* starts, int n, int first, int last, int* x0, int* x1) {
+  int lo = first, hi = last + 1;
+  if (first > 0 && last + 1 < n) {           // both sides are in order, each by itself
+    const int to = starts[first], from = starts[last + 1];
+    int a = -1, b = first;                   // the last start of the one side that is not past the other's first
+    while (b > a) {
+      const int mid = a + (b - a + 1) / 2;
+      if (starts[mid] <= from) a = mid; else b = mid - 1;
+    }
+    lo = a < 0 ? 0 : a;
+    a = last + 1, b = n;                     // the first of the other that is not before the one's last
+    while (a < b) {
+      const int mid = a + (b - a) / 2;
+      if (starts[mid] >= to) b = mid; else a = mid + 1;
+    }
+    hi = a;
+  }
+  *x0 = lo, *x1 = hi;
+}
+
+// The packed rows that sequences own, as ends of two ranges.
+MK_HD inline void owned_rows(const KvAttnArgs& a, const Sound& so, int32_t* rows) {
+  rows[0] = a.q_starts[0], rows[1] = a.q_starts[so.b0 < a.batch ? so.b0 : a.batch];
+  rows[2] = a.q_starts[so.b1 < a.batch ? so.b1 : a.batch], rows[3] = a.q_starts[a.batch];
+}
+
 struct Task {
   int tok0, ntok, nb;      // rows, row blocks
   int table, kbeg, kend;
@@ -57,16 +104,18 @@ struct Task {
   int flags;
 };
 
-MK_HD inline Task load_task(const KvAttnArgs& a, int t, int tb, bool report) {
+MK_HD inline Task load_task(const KvAttnArgs& a, int t, int tb, bool report, const Sound& so = all_hold()) {
   Task k{};
   if (t < a.groups) {
     const int s0 = a.group_starts[t], s1 = a.group_starts[t + 1], prefix = a.prefix_lens[t];
-    k.flags = kPrefix;
-    bool ok = 0 <= s0 && s0 <= s1 && s1 <= a.batch &&
+    const bool order = 0 <= s0 && s0 <= s1 && s1 <= a.batch;
+    k.flags = order ? kPrefix : kPrefix | kOrder;
+    bool ok = order && (t < so.g0 || t >= so.g1) &&
               (s0 == s1 || (prefix >= 0 && prefix % kKvPage == 0 && prefix <= a.max_pages * kKvPage));
     int q0 = 0, q1 = 0;
-    if (ok) {
-      q0 = a.q_starts[s0], q1 = a.q_starts[s1];
+    if (ok) {                              // rows of those sequences that hold, and between them
+      const int b0 = s0 < so.b0 ? s0 : hd_max(s0, so.b1), b1 = s1 > so.b1 ? s1 : hd_min(s1, so.b0);
+      if (b0 < b1) q0 = a.q_starts[b0], q1 = a.q_starts[b1];
       ok = 0 <= q0 && q0 <= q1 && q1 <= a.total_q;
     }
     if (!ok) {
@@ -78,13 +127,17 @@ MK_HD inline Task load_task(const KvAttnArgs& a, int t, int tb, bool report) {
   } else {
     const int b = t - a.groups;
     const int q0 = a.q_starts[b], q1 = a.q_starts[b + 1], len = a.seq_lens[b];
-    k.flags = kCausal;
-    bool ok = 0 <= q0 && q0 <= q1 && q1 <= a.total_q;
+    const bool order = 0 <= q0 && q0 <= q1 && q1 <= a.total_q, ok = order && (b < so.b0 || b >= so.b1);
+    k.flags = order ? kCausal : kCausal | kOrder;
     k.tok0 = ok ? q0 : 0, k.ntok = ok ? q1 - q0 : 0;
     int prefix = 0;
     bool fit = len >= 0 && len <= a.max_pages * kKvPage;
     if (a.groups) {
-      int lo = 0, hi = a.groups;          // the last group that starts at or before b
+      int lo = 0, hi = a.groups;          // the last group that starts at or before b, of those that hold on its side
+      if (so.g0 < a.groups) {
+        if (so.g0 > 0 && b < a.group_starts[so.g0]) hi = so.g0;
+        else lo = hd_min(so.g1, hi - 1);
+      }
       while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
         if (a.group_starts[mid] <= b) lo = mid; else hi = mid;
@@ -92,10 +145,7 @@ MK_HD inline Task load_task(const KvAttnArgs& a, int t, int tb, bool report) {
       // groups without sequences start there too
       prefix = a.prefix_lens[lo];
       const int s0 = a.group_starts[lo], s1 = a.group_starts[lo + 1];
-      if (!(0 <= s0 && s0 <= b && b < s1 && s1 <= a.batch)) fit = false;
-      // its rows are among the group's, or the group leaves them out
-      if (fit && !(0 <= a.q_starts[s0] && a.q_starts[s0] <= q0 && q1 <= a.q_starts[s1] && a.q_starts[s1] <= a.total_q))
-        fit = false;
+      if (!(0 <= s0 && s0 <= b && b < s1 && s1 <= a.batch && (lo < so.g0 || lo >= so.g1))) fit = false;
       if (prefix < 0 || prefix % kKvPage || (fit && prefix > 0 && k.ntok > 0 && prefix > len - k.ntok)) fit = false;
     }
     if (!(ok && fit) && report) flag(a.status, MK_ERR_BAD_ARG);
@@ -194,14 +244,16 @@ MK_HD inline Begin begin_of(const Task& k, int t, int tb, long long start, long 
 // On the GPU a warp walks it together.
 struct Stretch {
   const KvAttnArgs& a;
+  const Sound* so;         // NULL: all hold
   const int tb;
   int t, head, b;
   long long at;
   const long long pos, stop, share;
   Task k;
 
-  MK_HD Stretch(const KvAttnArgs& args, int tt, const Begin& g, long long pos, long long stop, long long share)
-      : a(args), tb(2 * tt), t(g.t), head(g.head), b(g.b), at(g.at), pos(pos), stop(stop), share(share), k(g.k) {}
+  MK_HD Stretch(const KvAttnArgs& args, int tt, const Begin& g, long long pos, long long stop, long long share,
+                const Sound* sound = nullptr)
+      : a(args), so(sound), tb(2 * tt), t(g.t), head(g.head), b(g.b), at(g.at), pos(pos), stop(stop), share(share), k(g.k) {}
 
   // the next part with anything to do; slots 2 c and 2 c + 1 are the block's
   MK_HD bool next(Part* m, int slot) {
@@ -224,7 +276,7 @@ struct Stretch {
         if (++head == a.hkv) {
           head = 0;
           while (++t < a.groups + a.batch) {
-            k = load_task(a, t, tb, false);
+            k = load_task(a, t, tb, false, so ? *so : all_hold());
             if (k.nb) break;
           }
         }

@@ -566,8 +566,8 @@ int mk_kvq_attention(const mk_kvq_cache* c, const void* q, int64_t q_stride, voi
  * kernels have run, allocate nothing and may be captured into a graph; two of
  * them may run at the same time unless one writes what the other uses.
  * Pointers but the structs' own are DEVICE pointers; pools, rows, q, out and
- * workspace are 16-byte aligned, strides multiples of 16 bytes (else
- * MK_ERR_BAD_ARG).
+ * workspace are 16-byte aligned, arrays of int32 4-byte aligned, strides
+ * multiples of 16 bytes (else MK_ERR_BAD_ARG).
  */
 typedef struct {
   void* k_pool;     /* [num_pages][n_kv_heads][16][head_dim] BF16               */

@@ -310,7 +310,9 @@ class PagedCache:
         if ws_bytes is None:
             if len(self._ws_bytes) >= 1024:
                 self._ws_bytes.clear()
-            ws_bytes = self._ws_bytes[key] = mk.mk_kv_workspace(self._c, hq, n, batch, groups)
+            ws_bytes = mk.mk_kv_workspace(self._c, hq, n, batch, groups)
+            if ws_bytes:                        # 0: nothing to do, refused, or a device that could not be asked
+                self._ws_bytes[key] = ws_bytes
         ws = self.status.new_empty((ws_bytes + 3) // 4) if ws_bytes else None
         mk.mk_kv_attention(self._c, q.data_ptr(), q_stride, out.data_ptr(), out_stride, hq, n, batch, q_starts.data_ptr(),
                            page_tables.data_ptr(), max_pages, seq_lens.data_ptr(), groups, gs, pl,

@@ -65,7 +65,10 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kItems = 4;                // ring of work items
 constexpr int kReaders = 11;             // warps that read an item: 8 softmax, 2 MMA, Q and clearing
-constexpr unsigned long long kWaitNs = 4000000000ull;
+#ifndef MK_KV_WAIT_NS                    // a test builds these kernels with waits that run out
+#define MK_KV_WAIT_NS 4000000000ull
+#endif
+constexpr unsigned long long kWaitNs = MK_KV_WAIT_NS, kSettleNs = 4000000000ull;
 constexpr int kRegsSoftmax = 200, kRegsOther = 104;
 static_assert(256 * kRegsSoftmax + 128 * kRegsOther == kThreads * 168, "register split");
 
@@ -130,6 +133,7 @@ struct Sync {
   uint64_t drain[2];
   uint32_t tmem;
   volatile int stop;
+  uint32_t kv_loads, kv_raw, kv_raw_use, q_loads[2];     // copies that were issued, for a block that gives up
   long long scan[kThreads / 32];
   Plan plan;                             // of many tasks
   int planned;
@@ -142,11 +146,14 @@ struct Sync {
 // Waits for the phase of this parity; false once the block gives up, or after
 // kWaitNs, which makes it give up.
 __device__ __forceinline__ bool wait(Sync& s, uint64_t* bar, uint32_t parity, int32_t* status) {
-  if (mbar_wait_some(bar, parity)) return true;
+  // a look may last as long as the hardware likes: a limit of microseconds takes short ones
+  constexpr bool kShort = kWaitNs < 1000000;
+  auto done = [&] { return kShort ? mbar_try_wait(bar, parity) : mbar_wait_some(bar, parity); };
+  if (done()) return true;
   unsigned long long t0 = 0;
   for (int i = 1;; i++) {
-    if (mbar_wait_some(bar, parity)) return true;
-    if ((i & 15) == 0) {
+    if (done()) return true;
+    if (kShort || (i & 15) == 0) {
       if (s.stop) return false;
       const unsigned long long t = gtime_ns();
       if (!t0) t0 = t;
@@ -161,10 +168,10 @@ __device__ __forceinline__ bool wait(Sync& s, uint64_t* bar, uint32_t parity, in
 __device__ __forceinline__ bool wait_warp(Sync& s, uint64_t* bar, uint32_t parity, int32_t* status) {
   return __all_sync(0xffffffffu, wait(s, bar, parity, status));
 }
-// after giving up: what is in flight must have landed before the block ends
+// what is in flight must have landed before the block ends
 __device__ __forceinline__ void settle(uint64_t* bar, uint32_t parity) {
   const unsigned long long t0 = gtime_ns();
-  while (!mbar_try_wait(bar, parity) && gtime_ns() - t0 < kWaitNs) {}
+  while (!mbar_try_wait(bar, parity) && gtime_ns() - t0 < kSettleNs) {}
 }
 
 template <int R>
@@ -631,13 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (lane < 2) ws.slots[2 * blockIdx.x + lane] = lane ? desc[1] : desc[0];
       if (a.groups && blockIdx.x == 0 && lane == 0) owned_rows(a, s.sound, ws.rows);
-      if (s.stop) {
-        for (uint32_t i = loads > S::kStages ? loads - S::kStages : 0; i < loads; i++) {
-          const uint32_t st = i % S::kStages;
-          if (raw >> st & 1) settle(&s.raw_full[st], (raw_use >> st & 1) ^ 1);
-          else settle(&s.kv_full[st], (i / S::kStages) & 1);
-        }
-      }
+      if (lane == 0) s.kv_loads = loads, s.kv_raw = raw, s.kv_raw_use = raw_use;
     } else if (warp < 11) {
       // ---------- MMAs, a warp each for the two softmax warpgroups: together,
       // one lane issues.  Wide items: stream t is a tile of rows, and each step's
@@ -851,15 +852,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.item_empty[it % kItems]);
       }
-      if (s.stop)
-        for (int t = 0; t < 2; t++)
-          if (q_loads[t]) settle(&s.q_full[t], (q_loads[t] - 1) & 1);
+      if (lane == 0) s.q_loads[0] = q_loads[0], s.q_loads[1] = q_loads[1];
     }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // A block that gave up: the warps that copy may have ended well before the wait
+  // that ran out, so their copies are waited for here, where no warp goes on.
+  if (s.stop) {
+    if (warp == 8) {
+      const uint32_t loads = s.kv_loads;
+      for (uint32_t i = loads > S::kStages ? loads - S::kStages : 0; i < loads; i++) {
+        const uint32_t st = i % S::kStages;
+        if (s.kv_raw >> st & 1) settle(&s.raw_full[st], (s.kv_raw_use >> st & 1) ^ 1);
+        else settle(&s.kv_full[st], (i / S::kStages) & 1);
+      }
+    } else if (warp == 11) {
+      for (int t = 0; t < 2; t++)
+        if (s.q_loads[t]) settle(&s.q_full[t], (s.q_loads[t] - 1) & 1);
+    }
+    __syncthreads();
+  }
   if (warp == 9) tc_dealloc(tmem, 512);
 }
 

@@ -654,8 +654,8 @@ size_t mk_kv_workspace(const mk_kv_cache* c, int n_q_heads, int total_q, int bat
  * neither has what a page holds past the sequence.
  * Products of BF16 values summed in fp32; softmax in fp32; weights rounded to
  * BF16 (8 bits, relative to themselves) for their products with the values; one
- * rounding to BF16 at the end.  A kernel that waits for its own copies or products
- * for more than 4 seconds gives up, stores MK_ERR_TIMEOUT in status and leaves the
+ * rounding to BF16 at the end.  A kernel that waits for a copy or a product of its
+ * own for more than 4 seconds gives up, stores MK_ERR_TIMEOUT in status and leaves the
  * results undefined.  A call gives the same bits every time; where a
  * long sequence is cut depends on the batch, and its sums then round
  * differently.  out may be q, and else lies apart from it.  Range: scores

@@ -7,9 +7,13 @@
 namespace mk {
 
 constexpr int kKvPage = 16;
-// A block's warps wait for one another over an item at most, which is one sequence's
-// keys: 2^28 tokens take 2.7 s of the 4 s after which a wait gives up.
+// A sequence's pages, at most.  An item is all of its keys for one block of rows:
+// 2^21 key tiles of up to 2,900 cycles, 4.2 s at the 1455 MHz of long matrix products.
 constexpr int kKvMaxPages = 1 << 24;
+// A wait of the attention kernel for a key tile gives up after so long; one that may
+// last over an item after so many times that.
+constexpr unsigned long long kKvWaitNs = 4000000000ull;
+constexpr int kKvItemWaits = 16;
 
 struct KvAttnArgs {
   const uint16_t *q, *k_pool, *v_pool;

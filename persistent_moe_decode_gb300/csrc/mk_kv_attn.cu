@@ -66,9 +66,9 @@ constexpr int kThreads = 384;
 constexpr int kItems = 4;                // ring of work items
 constexpr int kReaders = 11;             // warps that read an item: 8 softmax, 2 MMA, Q and clearing
 #ifndef MK_KV_WAIT_NS                    // a test builds these kernels with waits that run out
-#define MK_KV_WAIT_NS 4000000000ull
+#define MK_KV_WAIT_NS kKvWaitNs
 #endif
-constexpr unsigned long long kWaitNs = MK_KV_WAIT_NS, kSettleNs = 4000000000ull;
+constexpr unsigned long long kWaitNs = MK_KV_WAIT_NS, kSettleNs = kKvWaitNs;
 constexpr int kRegsSoftmax = 200, kRegsOther = 104;
 static_assert(256 * kRegsSoftmax + 128 * kRegsOther == kThreads * 168, "register split");
 
@@ -144,7 +144,9 @@ struct Sync {
 };
 
 // Waits for the phase of this parity; false once the block gives up, or after
-// kWaitNs, which makes it give up.
+// kWaitNs (ITEM: of a wait that lasts over a whole item, kKvItemWaits times that),
+// which makes it give up.
+template <bool ITEM = false>
 __device__ __forceinline__ bool wait(Sync& s, uint64_t* bar, uint32_t parity, int32_t* status) {
   // a look may last as long as the hardware likes: a limit of microseconds takes short ones
   constexpr bool kShort = kWaitNs < 1000000;
@@ -157,7 +159,7 @@ __device__ __forceinline__ bool wait(Sync& s, uint64_t* bar, uint32_t parity, in
       if (s.stop) return false;
       const unsigned long long t = gtime_ns();
       if (!t0) t0 = t;
-      if (t - t0 > kWaitNs) {
+      if (t - t0 > (ITEM ? kKvItemWaits : 1) * kWaitNs) {
         s.stop = 1;
         flag(status, MK_ERR_TIMEOUT);
         return false;
@@ -165,8 +167,9 @@ __device__ __forceinline__ bool wait(Sync& s, uint64_t* bar, uint32_t parity, in
     }
   }
 }
+template <bool ITEM = false>
 __device__ __forceinline__ bool wait_warp(Sync& s, uint64_t* bar, uint32_t parity, int32_t* status) {
-  return __all_sync(0xffffffffu, wait(s, bar, parity, status));
+  return __all_sync(0xffffffffu, wait<ITEM>(s, bar, parity, status));
 }
 // what is in flight must have landed before the block ends
 __device__ __forceinline__ void settle(uint64_t* bar, uint32_t parity) {
@@ -779,18 +782,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------- Q, and values that some row does not see (whole warp): a
       // weight of zero times NaN or an infinity is no zero, so those are taken
       // out, and what a page holds past the sequence with them
+      // All of its waits may last over an item; what they wait for the other warps
+      // wait for too, tile by tile.
       uint8_t* kv = raw_smem + (kv_smem - smem_u32(raw_smem));
       uint32_t loads = 0, uses = 0, q_loads[2] = {0, 0};
       const uint32_t q_bytes = (uint32_t)(tt * a.grp) * 128 * S::kHalves;
       bool ok = true;
       for (int it = 0; ok; it++) {
-        ok = wait_warp(s, &s.item_full[it % kItems], (it / kItems) & 1, a.status);
+        ok = wait_warp<true>(s, &s.item_full[it % kItems], (it / kItems) & 1, a.status);
         if (!ok) break;
         Item* slot = &items[it % kItems];
         const Part m = *slot;
         if (m.flags & kEnd) break;
         for (int t = 0; ok && m.k1 > m.k0 && t < 2 && m.ntok > t * tt; t++) {
-          ok = wait_warp(s, &s.q_empty[t], (q_loads[t] & 1) ^ 1, a.status);
+          ok = wait_warp<true>(s, &s.q_empty[t], (q_loads[t] & 1) ^ 1, a.status);
           if (!ok) break;
           q_loads[t]++;
           if (tc_elect()) {
@@ -806,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = m.k0; ok && j < m.k1; j++) {
           if (kTile * (j + 1) <= clear) continue;
           const uint32_t i = loads + (j - m.k0) + min(j - m.k0 + (m.ntok <= tt ? 2 : 1), m.k1 - m.k0), st = i % S::kStages;
-          ok = wait_warp(s, &s.raw_full[st], uses >> st & 1, a.status);
+          ok = wait_warp<true>(s, &s.raw_full[st], uses >> st & 1, a.status);
           if (!ok) break;
           uses ^= 1u << st;
           const int lo = max(0, clear - kTile * j), held = min(kTile, m.kend - m.kbeg - kTile * j);

@@ -70,7 +70,7 @@ def test_a_wait_that_runs_out(libraries, ns, hq, hkv, d, news, lens, groups, pre
     assert (ws[size:] == 77).all()
     code = int(cache.status.item())
     assert code in (0, mk.MK_ERR_TIMEOUT)
-    assert code or ns > 3_000                    # the first rows' wait for their scores is longer
+    assert code or ns > 1_000                    # a block plans longer before it copies anything
     # the same call as it is meant, right after
     cache.status.zero_()
     args = (q, st["starts"], st["tables"], st["lens"])

@@ -190,8 +190,7 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7f80
 // KV head.
 __device__ __forceinline__ bool find_plan(const KvAttnArgs& a, Plan& plan, const Task& k, int t, long long before,
                                           long long mine, long long per, long long total, int tb, int lane) {
-  // about an equal share: total / blocks, from above
-  const long long share = max((long long)__umul64hi((unsigned long long)total, a.per_block) + 1, (long long)kMinShare);
+  const long long share = share_of(total, a.per_block);
   const long long pos = share * blockIdx.x;
   const unsigned owner = __ballot_sync(0xffffffffu, pos < total && before <= pos && pos < before + mine);
   if (!owner) return false;
@@ -517,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       total += x;
     }
     if (chunk > 1) {                       // the thread that holds the position finds its task
-      const long long pos = max((long long)__umul64hi((unsigned long long)total, a.per_block) + 1, (long long)kMinShare) * blockIdx.x;
+      const long long pos = share_of(total, a.per_block) * blockIdx.x;
       if (before <= pos && pos < before + mine)
         for (;; t++) {
           k = load_task(a, t, tb, false, so);
@@ -1073,7 +1072,7 @@ int launch(const KvAttnArgs& a, int sms, cudaStream_t st) {
       !make_map(&page_v, a.v_pool, 4, p_dims, p_strides, p_box))
     return MK_ERR_CUDA;
   KvAttnArgs b = a;
-  b.per_block = ~0ull / (unsigned)sms;
+  b.per_block = per_block(sms);
   b.aligned32 = (((uintptr_t)a.out | 2 * (uintptr_t)a.out_stride) & 31) == 0;
   kv_attention_kernel<D><<<sms, kThreads, Shape<D>::kSmem, st>>>(b, map_q, map_k, page_k, page_v);
   int rc = launched(cudaGetLastError());

@@ -190,6 +190,19 @@ MK_HD inline long long cost_before(const Task& k, int b, int tb) {
   return keys + (long long)full * kWideStart + (b > full ? block_cost(k, b - 1, tb) : 0);
 }
 
+// An equal share of `total` for each block, from above, and no less than the least:
+// total / blocks by a product with the blocks' reciprocal, which the host makes.
+inline unsigned long long per_block(int blocks) { return ~0ull / (unsigned)blocks; }
+
+MK_HD inline long long share_of(long long total, unsigned long long per) {
+#ifdef __CUDA_ARCH__
+  const unsigned long long high = __umul64hi((unsigned long long)total, per);
+#else
+  const unsigned long long high = (unsigned long long)((unsigned __int128)total * per >> 64);
+#endif
+  return hd_max((long long)high + 1, (long long)kMinShare);
+}
+
 // Where a border x keys into an item of n key tiles cuts it: the same for the
 // block before and the block after.  Small shares are cut as they fall.
 MK_HD inline int cut(long long x, bool wide, int n, long long share) {

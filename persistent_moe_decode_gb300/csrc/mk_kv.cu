@@ -18,10 +18,6 @@ namespace {
 constexpr int kPage = kKvPage;
 constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ void flag(int32_t* status, int code) {
-  if (status) *(volatile int32_t*)status = code;
-}
-
 // ------------------------------------------------------------ rotary positions
 //
 // A block takes a few rows.  Its threads first put cos and sin of every (row,

@@ -4,7 +4,17 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#ifdef __CUDACC__
+#define MK_HD __host__ __device__
+#else
+#define MK_HD
+#endif
+
 namespace mk {
+
+MK_HD inline void flag(int32_t* status, int code) {
+  if (status) *(volatile int32_t*)status = code;
+}
 
 constexpr int kKvPage = 16;
 // A sequence's pages, at most.  An item is all of its keys for one block of rows:

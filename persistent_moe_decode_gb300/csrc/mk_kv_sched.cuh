@@ -7,12 +7,6 @@
 #include "mk.h"
 #include "mk_kv.cuh"
 
-#ifdef __CUDACC__
-#define MK_HD __host__ __device__
-#else
-#define MK_HD
-#endif
-
 namespace mk {
 
 constexpr int kTile = 128;               // keys a step, rows a tile
@@ -34,10 +28,6 @@ template <class T>
 MK_HD inline T hd_min(T a, T b) { return a < b ? a : b; }
 template <class T>
 MK_HD inline T hd_max(T a, T b) { return a > b ? a : b; }
-
-MK_HD inline void flag(int32_t* status, int code) {
-  if (status) *(volatile int32_t*)status = code;
-}
 
 // a stretch of key tiles [k0, k1) of n of one row block of one KV head
 struct Part {
@@ -297,7 +287,7 @@ struct Stretch {
   // the next part with anything to do; slots 2 c and 2 c + 1 are the block's
   MK_HD bool next(Part* m, int slot) {
     while (t < a.groups + a.batch && at < stop) {
-      const int end = block_end(k, b, tb), n = (end - k.kbeg + kTile - 1) / kTile, len = block_cost(k, b, tb);
+      const int end = block_end(k, b, tb), n = block_tiles(k, b, tb), len = block_cost(k, b, tb);
       const bool w = wide(k, b, tb);
       const int k0 = at < pos ? cut(pos - at, w, n, share) : 0, k1 = at + len <= stop ? n : cut(stop - at, w, n, share);
       const bool some = k1 > k0 || (n == 0 && at >= pos);

@@ -103,7 +103,9 @@ __device__ __forceinline__ void st_32(void* p, const uint32_t* r, bool aligned) 
     reinterpret_cast<uint4*>(p)[1] = make_uint4(r[4], r[5], r[6], r[7]);
 }
 
-// two fp32 -> a BF16 pair (lo in the low half), to nearest even
+// two fp32 -> a BF16 pair (lo in the low half), to nearest even: one instruction.
+// (pack_bf2's two conversions give the same and make a softmax's weights the
+// attention's bound: a prompt of 8192 tokens 593 us against 377.)
 __device__ __forceinline__ uint32_t cvt_bf2(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));

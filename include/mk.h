@@ -622,9 +622,10 @@ int mk_kv_append(const mk_kv_cache* c, const mk_rope* r, int n, const int32_t* p
                  const mk_head_rows* q_out, void* stream);
 
 /* Workspace bytes of mk_kv_attention with these arguments on the current
- * device, for any lengths; 0 if they are not supported.  It needs no
- * preparation.  Calls that may run at the same time, or two captured graphs
- * that may, need a workspace each. */
+ * device, for any lengths; 0 if they are not supported.  With groups it holds
+ * two sums a row of heads, 8 (head_dim + 1) bytes.  It needs no preparation.
+ * Calls that may run at the same time, or two captured graphs that may, need a
+ * workspace each. */
 size_t mk_kv_workspace(const mk_kv_cache* c, int n_q_heads, int total_q, int batch, int groups);
 
 /* Causal attention of packed query rows over their sequences' cached tokens.
@@ -653,7 +654,8 @@ size_t mk_kv_workspace(const mk_kv_cache* c, int n_q_heads, int total_q, int bat
  * What a row does not see has no part in it, infinities and NaN included, and
  * neither has what a page holds past the sequence.
  * Products of BF16 values summed in fp32; softmax in fp32; weights rounded to
- * BF16 (8 bits, relative to themselves) for their products with the values; one
+ * BF16 (8 bits, relative to themselves; mk_decode_step keeps about 16,
+ * mk_kvq_attention 11 of BF16 queries) for their products with the values; one
  * rounding to BF16 at the end.  A kernel that waits for a copy or a product of its
  * own for more than 4 seconds gives up, stores MK_ERR_TIMEOUT in status and leaves the
  * results undefined.  A call gives the same bits every time; where a

@@ -3,7 +3,10 @@
 // Mathematics.  A row's running reference r (of its scores' maximum) and sum
 // l = sum exp(s - r), with O = sum exp(s - r) v beside it, a key tile of 128 at a
 // time; parts of a row over different keys add up as (r, l, O) again.  Scores and
-// O are fp32 sums of BF16 products, weights BF16.
+// O are fp32 sums of BF16 products.  Weights are rounded to BF16 for theirs with the
+// values (not in l): the tensor cores take both operands of one type, and a second
+// product for the weights' low halves would double that half of the work.  It costs
+// 0.4 to 0.7e-3 of the results' norm beside 1.4 to 1.7e-3 of their own rounding.
 //
 // Rows.  A block of work is 2 tiles of 128 rows of one KV head: the query heads
 // of its group, token after token (row = token * grp + head), so that few tokens
@@ -29,8 +32,9 @@
 //
 // Measured, one GB300 (kernels in a graph; 32 query and 4 KV heads of 128 dims):
 // a prompt of 32,768 tokens 5.3 ms, 1660 TFLOP/s (86 % of the measured matrix
-// product rate), of 8192 0.372-0.378 ms (1470), of 2048 48-50 us; one token of
-// 262,144 94 us (5.7 TB/s), of 8192 15 us, of 128 7.9 us.  What bounds it:
+// product rate; 5.7 ms a call among others, at a lower clock), of 8192 0.374-0.396 ms
+// (1390-1470), of 2048 49-51 us; one token of 262,144 94 us (5.7 TB/s), of 8192 15-17
+// us, of 128 8-9 us; 8192 tokens of 16 heads of 64 dims 186 us.  What bounds it:
 // - wide items: the chain of one stream, scores - weights - products: 1,250
 //   cycles of softmax (690 instructions a warp and tile; issue 45 %, exponentials
 //   33 % of their rate) and 1,050 of products after it; the other stream fills

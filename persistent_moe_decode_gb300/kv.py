@@ -236,7 +236,8 @@ class PagedCache:
                          scale: float | None = None, out=None, stream=None):
         """:meth:`attention` where the sequences ``group_starts[g]`` to ``group_starts[g + 1]`` (int32 ``[groups + 1]``,
         from 0 to the batch) share their first ``prefix_lens[g]`` tokens (int32 ``[groups]``; whole pages before each
-        one's new tokens, the first of its page table's entries; 0: nothing): these are read once a group."""
+        one's new tokens, the first of its page table's entries; 0: nothing): these are read once a group.  For the call
+        it takes ``8 * (head_dim + 1)`` bytes a row and query head, whatever is shared."""
         return _run(self.k_pool.device, self._dev, self._attention, stream, q, q_starts, page_tables, seq_lens,
                     group_starts, prefix_lens, scale, out)
 

@@ -305,9 +305,9 @@ int mk_kv_attention(const mk_kv_cache* c, const void* q, int64_t q_stride, void*
   if (total_q == 0 || batch == 0) return MK_OK;
   const int64_t row = (int64_t)n_q_heads * c->head_dim;
   if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || q_stride % 8 || out_stride % 8 ||
-      (total_q > 1 && (q_stride < row || out_stride < row)) || !q_starts || !seq_lens || (max_pages && !page_tables) ||
-      (groups && (!group_starts || !prefix_lens)) || !aligned(q_starts, 4) || !aligned(page_tables, 4) ||
-      !aligned(seq_lens, 4) || !aligned(group_starts, 4) || !aligned(prefix_lens, 4))
+      (total_q > 1 && (q_stride < row || out_stride < row)) || !q_starts || !aligned(q_starts, 4) || !seq_lens ||
+      !aligned(seq_lens, 4) || (max_pages && (!page_tables || !aligned(page_tables, 4))) ||
+      (groups && (!group_starts || !aligned(group_starts, 4) || !prefix_lens || !aligned(prefix_lens, 4))))
     return MK_ERR_BAD_ARG;
   const int sms = sm_count();
   if (!sms) return MK_ERR_CUDA;

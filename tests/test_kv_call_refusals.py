@@ -52,3 +52,11 @@ def test_a_workspace_size_that_could_not_be_asked_is_asked_again(monkeypatch):
         call()
     assert call().shape == q.shape and call().shape == q.shape
     assert len(asked) == 2 and [a[-2] for a in called] == [0, 64, 64]
+
+
+def test_arrays_that_are_not_read_may_be_anything(lib):
+    """Without groups or pages their arrays are not looked at: the refusal is for want of a device, or of a workspace."""
+    import torch
+    code = mk.MK_ERR_BAD_ARG if torch.cuda.is_available() else mk.MK_ERR_CUDA
+    refused(mk.mk_kv_attention, code, *attn_args(group_starts=P + 2, prefix_lens=P + 1))
+    refused(mk.mk_kv_attention, code, *attn_args(max_pages=0, tables=P + 2))

@@ -198,9 +198,7 @@ class PagedCache:
         self.k_pool, self.v_pool = k_pool, v_pool
         self.n_pages, self.n_kv_heads, _, self.head_dim = k_pool.shape
         self._dev, self._ws_bytes = k_pool.get_device(), {}
-        self.status = torch.zeros(1, dtype=torch.int32, device=k_pool.device)
-        if not torch.cuda.is_current_stream_capturing():      # zero before a call on another stream may store there
-            torch.cuda.current_stream(k_pool.device).synchronize()
+        self.status = mk.status_word(k_pool.device)
         self._c = mk.mk_kv_cache(k_pool.data_ptr(), v_pool.data_ptr(), self.n_pages, self.n_kv_heads, self.head_dim,
                                  self.status.data_ptr())
 

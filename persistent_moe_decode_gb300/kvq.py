@@ -57,9 +57,7 @@ class QuantCache:
         self.pool, self.n_kv_heads, self.head_dim = pool, n_kv_heads, head_dim
         self._dev, self._ws_bytes = pool.get_device(), {}
         self._inner = {1: (n_kv_heads, head_dim), PAGE_SIZE: (n_kv_heads, PAGE_SIZE, head_dim)}
-        self.status = torch.zeros(1, dtype=torch.int32, device=pool.device)
-        if not torch.cuda.is_current_stream_capturing():      # zero before a call on another stream may store there
-            torch.cuda.current_stream(pool.device).synchronize()
+        self.status = mk.status_word(pool.device)
         self._c = mk.mk_kvq_cache(pool=pool.data_ptr(), num_pages=pool.shape[0], n_kv_heads=n_kv_heads,
                                   head_dim=head_dim, status=self.status.data_ptr())
 

@@ -414,6 +414,27 @@ def mk_kv_attention(cache: mk_kv_cache, q_ptr: int, q_stride: int, out_ptr: int,
 
 # ---------------------------------------------------------- convenience
 
+_words = {}     # device index -> (words that are zero, of which so many are taken)
+
+
+def status_word(device):
+    """An int32 tensor ``[1]`` for a cache's status, zero already: a call on any stream may store there before the
+    current stream gets on.  Words come a thousand at a time, each for one cache ever, so that few caches wait for their
+    zeros."""
+    import torch
+    # whatever the caller's mode: another cache's check() may clear its word in another
+    with torch.cuda.device(device), torch.inference_mode(False):
+        if torch.cuda.is_current_stream_capturing():       # nothing is waited for, and the graph's memory is its own
+            return torch.zeros(1, dtype=torch.int32, device=device)
+        with _lock:
+            words, taken = _words.get(torch.cuda.current_device(), (None, 0))
+            if words is None or taken == words.shape[0]:
+                words, taken = torch.zeros(1024, dtype=torch.int32, device=device), 0
+                torch.cuda.current_stream().synchronize()
+            _words[torch.cuda.current_device()] = words, taken + 1
+            return words[taken:taken + 1]
+
+
 def make_config(dims, max_batch: int, max_pages_per_seq: int, num_kv_pages: int, **kw) -> mk_config:
     """mk_config from a ModelDims plus capacity / schedule fields."""
     c = mk_config(n_layers=dims.n_layers, hidden=dims.hidden, n_q_heads=dims.n_q_heads,
